@@ -469,6 +469,130 @@ hum_status hum_moe_grouped_gemm(const hum_weight_desc* w, const void* packed, in
                                 float* out_swiglu_f32, const hum_tile_config* cfg, void* workspace,
                                 size_t ws_bytes, void* stream);
 
+/* ---- attention side of a decode step -------------------------------------
+ * What runs between a layer's qkv product and its output product: rotary
+ * positions, the paged key-value cache in the activation formats of
+ * hum_quant_act, and the attention of each sequence's newest token over that
+ * cache.  The device of every pointer must be the current one. */
+
+typedef enum hum_rope_layout {
+  HUM_ROPE_HALF = 0,        /* pair i = elements i and i + rotary_dim / 2 */
+  HUM_ROPE_INTERLEAVED = 1  /* pair i = elements 2 i and 2 i + 1 */
+} hum_rope_layout;
+
+typedef enum hum_rope_scaling {
+  HUM_ROPE_NONE = 0,
+  HUM_ROPE_LINEAR = 1,  /* every frequency divided by factor */
+  HUM_ROPE_NTK = 2,     /* base' = base * factor^(R / (R - 2)): the slowest pair divided by factor, the fastest kept */
+  HUM_ROPE_YARN = 3     /* YaRN (Peng et al. 2023): pairs that turn fast_turns times or more over original_len keep
+                           their frequency, those that turn slow_turns times or less have it divided by factor, a
+                           linear ramp over the pair index between; cos and sin times 0.1 ln(factor) + 1 */
+} hum_rope_scaling;
+
+typedef struct hum_rotary_desc {
+  int32_t dtype;         /* HUM_BF16 | HUM_F32: elements of q and k */
+  int32_t layout;        /* hum_rope_layout */
+  int32_t head_dim;      /* elements per head, 1 .. 1024 */
+  int32_t rotary_dim;    /* the first rotary_dim elements turn (even, 2 .. head_dim); the rest are copied */
+  int32_t num_q_heads;   /* >= 0 */
+  int32_t num_kv_heads;  /* >= 0 */
+  int32_t inverse;       /* 1: turn by minus the angle (with the same factor: the gradient of the turn) */
+  float factor;          /* multiplies cos and sin (YaRN's attention factor; 1 for none) */
+} hum_rotary_desc;
+
+/* Host function: float64 frequencies inv_freq[i] = base^(-2i/R), i < R / 2 =
+ * rotary_dim / 2, scaled, into HOST memory, and the factor for cos and sin.
+ * original_len, fast_turns and slow_turns are read for HUM_ROPE_YARN only,
+ * factor for every scaling but HUM_ROPE_NONE (factor >= 1). */
+hum_status hum_rotary_inv_freq(int32_t rotary_dim, double base, int32_t scaling, double factor,
+                               double original_len, double fast_turns, double slow_turns,
+                               double* inv_freq_host, float* factor_out);
+
+/* q [T][num_q_heads][head_dim] and k [T][num_kv_heads][head_dim] turned by
+ * positions[t] * inv_freq[i], both in one launch:
+ *   y0 = x0 cos - x1 sin, y1 = x0 sin + x1 cos, in f32, rounded once.
+ * The angle is reduced in float64, so far positions keep their precision.
+ *   positions : i64 [T]; inv_freq : f64 [rotary_dim / 2] (device)
+ *   strides   : elements from token to token and from head to head (head
+ *               elements are contiguous); any, as long as the rows of an
+ *               output do not overlap
+ *   out       : may be the input itself (same pointer and strides), but may
+ *               not overlap it otherwise
+ * q (with q_out) or k (with k_out) may be NULL where its head count is 0. */
+hum_status hum_rotary(const hum_rotary_desc* desc, int64_t num_tokens, const int64_t* positions,
+                      const double* inv_freq, const void* q, int64_t q_token_stride, int64_t q_head_stride,
+                      void* q_out, int64_t q_out_token_stride, int64_t q_out_head_stride, const void* k,
+                      int64_t k_token_stride, int64_t k_head_stride, void* k_out, int64_t k_out_token_stride,
+                      int64_t k_out_head_stride, void* stream);
+
+/* A paged key-value cache: num_pages pages of page_size tokens, each with
+ * num_kv_heads heads of K and V rows of head_dim values in one activation
+ * format.  Slot s is token s % page_size of page s / page_size. */
+typedef struct hum_kv_desc {
+  int32_t fmt;           /* HUM_ACT_BF16 | HUM_ACT_FP8_TOKEN (one f32 scale per row) |
+                            HUM_ACT_MXFP8 | HUM_ACT_MXFP4 (one E8M0 scale per 32) */
+  int32_t num_kv_heads;  /* 1 .. 1024 */
+  int32_t head_dim;      /* 64 | 128 | 256 */
+  int32_t page_size;     /* 16 | 32 | 64 | 128 | 256 tokens */
+  int64_t num_pages;     /* >= 1 */
+} hum_kv_desc;
+
+/* Bytes of the cache; 0 if the description is invalid (see hum_last_error()).
+ * Layout: [num_pages][num_kv_heads] units of
+ *   K codes [page_size][row], V codes [page_size][row]
+ *     (row = head_dim bf16, head_dim E4M3 bytes or head_dim / 2 bytes of E2M1
+ *     pairs, even element in the low nibble),
+ *   K scales, V scales: f32 [page_size] each (FP8_TOKEN), or E8M0 bytes, for
+ *     K [page_size][head_dim / 32] and for V [head_dim / 32][page_size].
+ * A page is contiguous, so it moves with one copy.  The cache needs no
+ * initialisation; it is 16-byte aligned. */
+size_t hum_kv_cache_bytes(const hum_kv_desc* desc);
+
+/* Writes k, v bf16 [T][num_kv_heads][head_dim] into slots[t], quantized as
+ * hum_quant_act does (FP8_TOKEN: one scale per token and head).
+ *   slots : i64 [T]; a slot outside [0, num_pages * page_size) is skipped.
+ *           The others must differ: a slot that a call names twice holds
+ *           parts of either row afterwards.
+ *   strides in elements, head elements contiguous. */
+hum_status hum_kv_write(const hum_kv_desc* desc, void* cache, size_t cache_bytes, int64_t num_tokens,
+                        const int64_t* slots, const void* k_bf16, int64_t k_token_stride, int64_t k_head_stride,
+                        const void* v_bf16, int64_t v_token_stride, int64_t v_head_stride, void* stream);
+
+/* Reads slots[t] back: k_out, v_out bf16 [T][num_kv_heads][head_dim] =
+ * bf16(code * scale).  A slot outside [0, num_pages * page_size) reads as
+ * zeros; the same slot may be read more than once. */
+hum_status hum_kv_read(const hum_kv_desc* desc, const void* cache, size_t cache_bytes, int64_t num_tokens,
+                       const int64_t* slots, void* k_out_bf16, void* v_out_bf16, void* stream);
+
+/* Workspace bytes hum_kv_attention needs (0 on invalid arguments). */
+size_t hum_kv_attention_workspace_bytes(const hum_kv_desc* desc, int32_t num_q_heads, int64_t batch,
+                                        int64_t max_pages);
+
+/* Attention of one query row per sequence and head over the cache:
+ *   out[b][h] = sum_t softmax_t(scale * q[b][h] . K_t) V_t,
+ *   lse[b][h] = ln sum_t exp(scale * q[b][h] . K_t),
+ * over the tokens t of sequence b with max(0, n - window) <= t < n (window =
+ * 0: all t < n), n = seq_lens[b] clamped to [0, max_pages * page_size], whose
+ * page lies in [0, num_pages): the tokens of any other page id (-1 for one
+ * held elsewhere) take no part.  Where no token takes part, out is 0 and lse
+ * is -inf.  Nothing past n reaches the result, whatever the cache holds.
+ *   q           : bf16 [batch][num_q_heads][head_dim], strides in elements;
+ *                 head h reads key-value head h / (num_q_heads / num_kv_heads)
+ *   block_table : i32 [batch][max_pages], rows table_stride apart; entry
+ *                 t / page_size of a row is the page of token t
+ *   seq_lens    : i32 [batch], read by the kernel only (no device->host copy)
+ *   out         : bf16 [batch][num_q_heads][head_dim], contiguous
+ *   lse         : f32 [batch][num_q_heads] or NULL
+ *   workspace   : hum_kv_attention_workspace_bytes(...) bytes, prepared as for
+ *                 hum_linear (hum_prepare_workspace once).  Calls that may
+ *                 overlap in time need different workspaces.
+ * Products are f32 sums of bf16 values; the same call gives the same bits. */
+hum_status hum_kv_attention(const hum_kv_desc* desc, const void* cache, size_t cache_bytes, int32_t num_q_heads,
+                            int64_t batch, const void* q_bf16, int64_t q_token_stride, int64_t q_head_stride,
+                            const int32_t* block_table, int64_t table_stride, int64_t max_pages,
+                            const int32_t* seq_lens, int64_t window, float scale, void* out_bf16, float* lse,
+                            void* workspace, size_t ws_bytes, void* stream);
+
 /* ---- measurement -------------------------------------------------------- */
 
 /* Device peak probes (measurement only; the GEMM path never calls them).

@@ -21,6 +21,8 @@ __all__ = [
     "packed_weight_bytes", "prepare_weight", "dequant_weight", "quant_act",
     "select_config", "linear_workspace_bytes", "linear", "moe_workspace_bytes",
     "moe_gemm", "moe_align", "moe_reduce", "Workspace", "header_functions",
+    "KvDesc", "make_kv_desc", "rotary_inv_freq", "rotary", "kv_cache_bytes", "kv_write", "kv_read",
+    "kv_attention_workspace_bytes", "kv_attention",
 ]
 
 BF16, F32, INT4, UINT4, E2M1, E4M3, E8M0, INT8, INT3, UINT3, INT2, UINT2, INT1, UINT1, E2M3, E3M2 = range(16)
@@ -72,10 +74,29 @@ class TileConfig(ctypes.Structure):
         return "TileConfig(" + ", ".join(f"{f}={getattr(self, f)}" for f, _ in self._fields_) + ")"
 
 
+class RotaryDesc(ctypes.Structure):
+    _fields_ = [
+        ("dtype", ctypes.c_int32), ("layout", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+        ("rotary_dim", ctypes.c_int32), ("num_q_heads", ctypes.c_int32), ("num_kv_heads", ctypes.c_int32),
+        ("inverse", ctypes.c_int32), ("factor", ctypes.c_float),
+    ]
+
+
+class KvDesc(ctypes.Structure):
+    _fields_ = [
+        ("fmt", ctypes.c_int32), ("num_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+        ("page_size", ctypes.c_int32), ("num_pages", ctypes.c_int64),
+    ]
+
+    def __repr__(self):
+        return "KvDesc(" + ", ".join(f"{f}={getattr(self, f)}" for f, _ in self._fields_) + ")"
+
+
 _lib = None
 _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
 _I32 = ctypes.c_int32
+_F64 = ctypes.c_double
 _SZ = ctypes.c_size_t
 _DP = ctypes.POINTER(WeightDesc)
 _CP = ctypes.POINTER(TileConfig)
@@ -113,6 +134,15 @@ _SIGS = {
     "hum_moe_grouped_gemm_workspace_bytes": (_SZ, [_DP, _I32, _I32, _I64, _I32, _I64, _I32, _CP]),
     "hum_moe_grouped_gemm": (_I32, [_DP, _P, _I32, _I32, _I64, _I32, _P, _P, _P, _I64, _P, _I32, _P, _P, _P, _CP,
                                     _P, _SZ, _P]),
+    "hum_rotary_inv_freq": (_I32, [_I32, _F64, _I32, _F64, _F64, _F64, _F64, ctypes.POINTER(_F64),
+                                   ctypes.POINTER(ctypes.c_float)]),
+    "hum_rotary": (_I32, [_P, _I64, _P, _P, _P, _I64, _I64, _P, _I64, _I64, _P, _I64, _I64, _P, _I64, _I64, _P]),
+    "hum_kv_cache_bytes": (_SZ, [_P]),
+    "hum_kv_write": (_I32, [_P, _P, _SZ, _I64, _P, _P, _I64, _I64, _P, _I64, _I64, _P]),
+    "hum_kv_read": (_I32, [_P, _P, _SZ, _I64, _P, _P, _P, _P]),
+    "hum_kv_attention_workspace_bytes": (_SZ, [_P, _I32, _I64, _I64]),
+    "hum_kv_attention": (_I32, [_P, _P, _SZ, _I32, _I64, _P, _I64, _I64, _P, _I64, _I64, _P, _I64, ctypes.c_float,
+                                _P, _P, _P, _SZ, _P]),
 }
 
 
@@ -674,6 +704,252 @@ def moe_grouped_gemm(w: WeightDesc, packed, a, sorted_ids, offsets, block_m: int
     if keep_swiglu_f32:
         res = res + (f32,)
     return res[0] if len(res) == 1 else res
+
+
+# ---- attention side of a decode step --------------------------------------
+
+ROPE_HALF, ROPE_INTERLEAVED = range(2)
+ROPE_NONE, ROPE_LINEAR, ROPE_NTK, ROPE_YARN = range(4)
+_ROPE_LAYOUT = {"half": ROPE_HALF, "interleaved": ROPE_INTERLEAVED}
+_ROPE_SCALING = {"none": ROPE_NONE, "linear": ROPE_LINEAR, "ntk": ROPE_NTK, "yarn": ROPE_YARN}
+
+
+def _rows3(t, name, dtype, shape=None):
+    """Checks a [rows, heads, dim] tensor whose rows and heads may be strided
+    (a slice of a fused qkv product) -> (pointer, row stride, head stride)."""
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    st = t.stride()
+    if st[2] != 1 and t.shape[2] > 1:
+        raise ValueError(f"{name}'s head elements must be contiguous")
+    return t.data_ptr(), st[0], st[1]
+
+
+def _vec(t, name, dtype, n, device):
+    """Checks a contiguous 1-D tensor on `device`."""
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.dim() != 1 or t.shape[0] != n:
+        raise ValueError(f"{name} must have shape {(n,)}, got {tuple(t.shape)}")
+    if n > 1 and t.stride(0) != 1:
+        raise ValueError(f"{name} must be contiguous")
+    if t.device != device:
+        raise ValueError(f"tensors on different devices: {name} on {t.device}, not {device}")
+    return t.data_ptr()
+
+
+def _launch(device, fn, *args):
+    """fn(*args, stream) with `device` current, on its current stream."""
+    import torch
+    if torch.cuda.current_device() == device.index:
+        _check(fn(*args, torch.cuda.current_stream(device).cuda_stream))
+    else:
+        with torch.cuda.device(device):
+            _check(fn(*args, torch.cuda.current_stream(device).cuda_stream))
+
+
+def _no_overlap(out, name):
+    """An output that the caller gives must not hold two of its elements at
+    one address."""
+    if out.numel() and any(s == 0 for s, n in zip(out.stride(), out.shape) if n > 1):
+        raise ValueError(f"{name} must not be expanded (stride 0)")
+
+
+def rotary_inv_freq(rotary_dim: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
+                    original_len: float = 0.0, fast_turns: float = 32.0, slow_turns: float = 1.0, device=None):
+    """-> (inv_freq float64 [rotary_dim / 2], factor for cos and sin): what
+    rotary() takes, computed once per model."""
+    import torch
+    if scaling not in _ROPE_SCALING:
+        raise ValueError(f"scaling must be one of {sorted(_ROPE_SCALING)}")
+    buf = (ctypes.c_double * max(int(rotary_dim) // 2, 1))()
+    fac = ctypes.c_float()
+    _check(load_library().hum_rotary_inv_freq(int(rotary_dim), float(base), _ROPE_SCALING[scaling], float(factor),
+                                              float(original_len), float(fast_turns), float(slow_turns), buf,
+                                              ctypes.byref(fac)))
+    return torch.tensor(list(buf), dtype=torch.float64, device=device), fac.value
+
+
+def rotary(q, k, positions, inv_freq, layout: str = "half", factor: float = 1.0, inverse: bool = False, q_out=None,
+           k_out=None):
+    """q [T, Hq, D] and k [T, Hkv, D] (bf16 or float32; k may be None) turned
+    by positions int64 [T] * inv_freq float64 [R / 2], the first R elements of
+    each head -> (q, k), new tensors unless q_out / k_out are given (the
+    inputs themselves for a turn in place).  inverse turns back, which with
+    the same factor is the gradient."""
+    import torch
+    if q is None or q.dim() != 3 or (k is not None and k.dim() != 3):
+        raise ValueError("q and k must be 3-D tensors [T, heads, head_dim]")
+    if layout not in _ROPE_LAYOUT:
+        raise ValueError(f"layout must be one of {sorted(_ROPE_LAYOUT)}")
+    dt, dev = q.dtype, q.device
+    if dt != torch.bfloat16 and dt != torch.float32:
+        raise ValueError(f"q must be torch.bfloat16 or torch.float32, got {dt}")
+    t, hq, d = q.shape
+    hk = 0
+    qp, qts, qhs = _rows3(q, "q", dt)
+    kp = kop = None
+    kts = khs = kots = kohs = 0
+    if k is not None:
+        hk = k.shape[1]
+        kp, kts, khs = _rows3(k, "k", dt, (t, hk, d))
+    elif k_out is not None:
+        raise ValueError("k_out without k")
+    if inv_freq is None or inv_freq.dim() != 1:
+        raise ValueError("inv_freq must be a 1-D float64 tensor")
+    half = inv_freq.shape[0]
+    if q_out is not None:
+        _rows3(q_out, "q_out", dt, q.shape)
+        _no_overlap(q_out, "q_out")
+    if k_out is not None:
+        _rows3(k_out, "k_out", dt, k.shape)
+        _no_overlap(k_out, "k_out")
+    _same_device(q, k, q_out, k_out)
+    pp = _vec(positions, "positions", torch.int64, t, dev)
+    fp = _vec(inv_freq, "inv_freq", torch.float64, half, dev)
+    if dev.type != "cuda":
+        raise ValueError("q must be a device tensor")
+    if q_out is None:
+        q_out = torch.empty((t, hq, d), dtype=dt, device=dev)
+    if k is not None and k_out is None:
+        k_out = torch.empty((t, hk, d), dtype=dt, device=dev)
+    qos = q_out.stride()
+    if k is not None:
+        kop = k_out.data_ptr()
+        kots, kohs, _ = k_out.stride()
+    desc = RotaryDesc(BF16 if dt == torch.bfloat16 else F32, _ROPE_LAYOUT[layout], d, 2 * half, hq, hk, bool(inverse),
+                      factor)
+    _launch(dev, load_library().hum_rotary, ctypes.addressof(desc), t, pp, fp, qp, qts, qhs, q_out.data_ptr(), qos[0],
+            qos[1], kp, kts, khs, kop, kots, kohs)
+    return q_out, k_out
+
+
+def make_kv_desc(fmt, num_pages: int, page_size: int, num_kv_heads: int, head_dim: int) -> KvDesc:
+    """Build a KvDesc; fmt "bf16", "fp8_token", "mxfp8" or "mxfp4"."""
+    return KvDesc(_AF.get(fmt, fmt), int(num_kv_heads), int(head_dim), int(page_size), int(num_pages))
+
+
+def kv_cache_bytes(desc: KvDesc) -> int:
+    b = load_library().hum_kv_cache_bytes(ctypes.addressof(desc))
+    if b == 0:
+        raise HumError(2, load_library().hum_last_error().decode())
+    return b
+
+
+def _kv_cache(desc, cache):
+    import torch
+    if cache is None or cache.dtype != torch.uint8 or not cache.is_contiguous():
+        raise ValueError("cache must be a contiguous uint8 tensor")
+    return cache.data_ptr(), cache.numel()
+
+
+def kv_write(desc: KvDesc, cache, k, v, slots):
+    """Quantize k, v bf16 [T, Hkv, D] into slots int64 [T] of `cache` (uint8,
+    kv_cache_bytes(desc)).  Slots outside the cache (-1) are skipped; the
+    others must differ."""
+    import torch
+    cp, cb = _kv_cache(desc, cache)
+    if k is None or v is None or k.dim() != 3 or v.dim() != 3:
+        raise ValueError("k and v must be 3-D tensors [T, num_kv_heads, head_dim]")
+    t = k.shape[0]
+    shape = (t, desc.num_kv_heads, desc.head_dim)
+    kp, kts, khs = _rows3(k, "k", torch.bfloat16, shape)
+    vp, vts, vhs = _rows3(v, "v", torch.bfloat16, shape)
+    dev = cache.device
+    _same_device(cache, k, v)
+    sp = _vec(slots, "slots", torch.int64, t, dev)
+    if dev.type != "cuda":
+        raise ValueError("cache must be a device tensor")
+    _launch(dev, load_library().hum_kv_write, ctypes.addressof(desc), cp, cb, t, sp, kp, kts, khs, vp, vts, vhs)
+
+
+def kv_read(desc: KvDesc, cache, slots, k_out=None, v_out=None):
+    """slots int64 [T] of `cache` -> k, v bf16 [T, Hkv, D]; slots outside the
+    cache (-1) read as zeros."""
+    import torch
+    cp, cb = _kv_cache(desc, cache)
+    if slots is None or slots.dim() != 1:
+        raise ValueError("slots must be a 1-D int64 tensor")
+    t = slots.shape[0]
+    dev = cache.device
+    sp = _vec(slots, "slots", torch.int64, t, dev)
+    shape = (t, desc.num_kv_heads, desc.head_dim)
+    for o, nm in ((k_out, "k_out"), (v_out, "v_out")):
+        _want(o, nm, torch.bfloat16, shape)
+        if o is not None and not o.is_contiguous():
+            raise ValueError(f"{nm} must be contiguous")
+    _same_device(cache, k_out, v_out)
+    if dev.type != "cuda":
+        raise ValueError("cache must be a device tensor")
+    if k_out is None:
+        k_out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+    if v_out is None:
+        v_out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+    _launch(dev, load_library().hum_kv_read, ctypes.addressof(desc), cp, cb, t, sp, k_out.data_ptr(),
+            v_out.data_ptr())
+    return k_out, v_out
+
+
+def kv_attention_workspace_bytes(desc: KvDesc, num_q_heads: int, batch: int, max_pages: int) -> int:
+    lib = load_library()
+    b = lib.hum_kv_attention_workspace_bytes(ctypes.addressof(desc), int(num_q_heads), int(batch), int(max_pages))
+    if b == 0:
+        raise HumError(1, lib.hum_last_error().decode())
+    return b
+
+
+def kv_attention(desc: KvDesc, cache, q, block_table, seq_lens, scale: float | None = None, window: int = 0, out=None,
+                 return_lse: bool = False, workspace=None):
+    """bf16 out [B, Hq, D] (and float32 lse [B, Hq] with return_lse) of one
+    query row per sequence, q bf16 [B, Hq, D], over the first seq_lens int32
+    [B] tokens (the last `window` of them, if not 0) of the pages that
+    block_table int32 [B, max_pages] names.  scale defaults to D ** -0.5."""
+    import torch
+    cp, cb = _kv_cache(desc, cache)
+    if q is None or q.dim() != 3:
+        raise ValueError("q must be a 3-D tensor [B, num_q_heads, head_dim]")
+    b, hq, d = q.shape
+    dev = cache.device
+    qp, qts, qhs = _rows3(q, "q", torch.bfloat16, (b, hq, desc.head_dim))
+    if block_table is None or block_table.dim() != 2 or block_table.shape[0] != b:
+        raise ValueError("block_table must be a 2-D tensor [B, max_pages]")
+    mp = block_table.shape[1]
+    if block_table.dtype != torch.int32:
+        raise ValueError(f"block_table must be torch.int32, got {block_table.dtype}")
+    if mp > 1 and block_table.stride(1) != 1:
+        raise ValueError("block_table's rows must be contiguous")
+    _want(out, "out", torch.bfloat16, (b, hq, d))
+    if out is not None and not out.is_contiguous():
+        raise ValueError("out must be contiguous")
+    _same_device(cache, q, block_table, out, workspace)
+    lp = _vec(seq_lens, "seq_lens", torch.int32, b, dev)
+    if dev.type != "cuda":
+        raise ValueError("cache must be a device tensor")
+    lib = load_library()
+    need = kv_attention_workspace_bytes(desc, hq, b, mp)
+    if workspace is None:
+        if torch.cuda.is_current_stream_capturing():
+            # the graph's own, from its memory pool: two graphs captured on one
+            # stream may be replayed on two
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+            workspace[:_WS_HEADER].zero_()
+        else:
+            workspace = _workspace(dev).get(need)
+    else:
+        _want(workspace, "workspace", torch.uint8)
+        _gpu(workspace, "workspace")
+    if out is None:
+        out = torch.empty((b, hq, d), dtype=torch.bfloat16, device=dev)
+    lse = torch.empty((b, hq), dtype=torch.float32, device=dev) if return_lse else None
+    _launch(dev, lib.hum_kv_attention, ctypes.addressof(desc), cp, cb, hq, b, qp, qts, qhs, block_table.data_ptr(),
+            block_table.stride(0), mp, lp, int(window), d ** -0.5 if scale is None else scale, out.data_ptr(),
+            None if lse is None else lse.data_ptr(), workspace.data_ptr(), workspace.numel())
+    return (out, lse) if return_lse else out
+
+
+_WS_HEADER = 64 << 10   # HUM_WS_HEADER_BYTES
 
 
 (PEAK_HBM_READ, PEAK_MFMA_BF16, PEAK_MFMA_FP8, PEAK_MFMA_FP4, PEAK_MFMA_FP8_FP4, PEAK_MFMA32_BF16, PEAK_MFMA32_FP8,

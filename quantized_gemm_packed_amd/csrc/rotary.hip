@@ -1,0 +1,266 @@
+// Rotary positions: q and k of a decode step or a prompt in one launch.
+//
+// Pair i of a head turns by the angle positions[t] * inv_freq[i]:
+//   y0 = x0 c - x1 s, y1 = x0 s + x1 c,  c = a cos, s = a sin.
+// Memory bound (q and k are read and written once).  An angle in radians at
+// position 10^6 has lost 16 of f32's 24 bits, so the turn count
+// positions * inv_freq / 2 pi is formed and reduced to [-1/2, 1/2] in f64
+// (two multiplies, a round and a subtract) and only the remainder goes to
+// the f32 sine and cosine.  They are the same for every head of a token:
+// a workgroup computes them once, into LDS.
+#include <cmath>
+
+#include "dev_common.h"
+#include "hum_internal.h"
+
+namespace hum {
+
+struct RotaryParams {
+  const int64_t* positions;
+  const double* inv_freq;
+  const void* x[2];  // q, k
+  void* y[2];
+  int64_t x_ts[2], x_hs[2], y_ts[2], y_hs[2];
+  int64_t tokens;
+  int32_t heads[2];
+  int32_t half;        // rotary_dim / 2
+  int32_t rest;        // head_dim - rotary_dim elements to copy (0 when in place)
+  int32_t units;       // rotating units + copied units of a head, VEC pairs / VEC elements each
+  int32_t lane_shift;  // log2 of the lanes that share a head (all its units at once, at most 256)
+  int32_t tok_per_wg;
+  int32_t head_step;   // heads per workgroup (grid.y slices the heads)
+  float factor;
+  float sign;          // -1: inverse
+};
+
+template <typename T>
+__device__ __forceinline__ float ld1(T v) {
+  if constexpr (sizeof(T) == 2) return bf16_bits_to_f32(v);
+  else return v;
+}
+template <typename T>
+__device__ __forceinline__ T st1(float v) {
+  if constexpr (sizeof(T) == 2) return (T)f32_to_bf16_bits(v);
+  else return v;
+}
+
+template <typename T, int VEC>
+struct Pack {
+  T v[VEC];
+};
+
+// VEC elements per 16-byte access where every address allows it, else one.
+template <typename T, bool HALF, int VEC>
+__global__ __launch_bounds__(256) void rotary_kernel(const RotaryParams p) {
+  typedef Pack<T, VEC> __attribute__((aligned(sizeof(T) * VEC))) P;
+  extern __shared__ float lds[];
+  const int tid = threadIdx.x;
+  const int64_t t0 = (int64_t)blockIdx.x * p.tok_per_wg;
+  const int nt = (int)(p.tokens - t0 < p.tok_per_wg ? p.tokens - t0 : p.tok_per_wg);
+  float* cs = lds;
+  float* sn = lds + p.tok_per_wg * p.half;
+  for (int i = tid; i < nt * p.half; i += 256) {
+    const int t = i / p.half;
+    const double turns = (double)p.positions[t0 + t] * (p.inv_freq[i - t * p.half] * 0.15915494309189535);
+    const float r = (float)(turns - __builtin_rint(turns));
+    float s, c;
+    sincospif(2.0f * r, &s, &c);
+    cs[i] = c * p.factor;
+    sn[i] = s * p.factor * p.sign;
+  }
+  __syncthreads();
+  const int lanes = 1 << p.lane_shift;
+  const int u0 = tid & (lanes - 1);
+  const int rot = p.half / VEC;
+  const int hall = p.heads[0] + p.heads[1];
+  const int h0 = (int)blockIdx.y * p.head_step;
+  const int nh = hall - h0 < p.head_step ? hall - h0 : p.head_step;
+  const int step = 256 >> p.lane_shift;
+  for (int row = tid >> p.lane_shift; row < nt * nh; row += step) {
+    const int t = row / nh;
+    const int hh = h0 + row - t * nh;
+    const int which = hh >= p.heads[0];
+    const int h = hh - (which ? p.heads[0] : 0);
+    const T* x = static_cast<const T*>(p.x[which]) + (t0 + t) * p.x_ts[which] + h * p.x_hs[which];
+    T* y = static_cast<T*>(p.y[which]) + (t0 + t) * p.y_ts[which] + h * p.y_hs[which];
+    for (int u = u0; u < p.units; u += lanes) {
+      if (u < rot) {
+        const float* c = cs + t * p.half + u * VEC;
+        const float* s = sn + t * p.half + u * VEC;
+        const int at0 = HALF ? u * VEC : 2 * u * VEC;
+        const int at1 = HALF ? at0 + p.half : at0 + VEC;
+        const P a = *reinterpret_cast<const P*>(x + at0);
+        const P b = *reinterpret_cast<const P*>(x + at1);
+        P oa, ob;
+  #pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+          // interleaved: the 2 VEC elements are VEC pairs side by side
+          const float x0 = HALF ? ld1<T>(a.v[i]) : 2 * i < VEC ? ld1<T>(a.v[(2 * i) % VEC]) : ld1<T>(b.v[(2 * i) % VEC]);
+          const float x1 = HALF                ? ld1<T>(b.v[i])
+                           : 2 * i + 1 < VEC ? ld1<T>(a.v[(2 * i + 1) % VEC])
+                                             : ld1<T>(b.v[(2 * i + 1) % VEC]);
+          const T y0 = st1<T>(x0 * c[i] - x1 * s[i]);
+          const T y1 = st1<T>(x0 * s[i] + x1 * c[i]);
+          if constexpr (HALF) {
+            oa.v[i] = y0;
+            ob.v[i] = y1;
+          } else {
+            if (2 * i < VEC) oa.v[(2 * i) % VEC] = y0;
+            else ob.v[(2 * i) % VEC] = y0;
+            if (2 * i + 1 < VEC) oa.v[(2 * i + 1) % VEC] = y1;
+            else ob.v[(2 * i + 1) % VEC] = y1;
+          }
+        }
+        *reinterpret_cast<P*>(y + at0) = oa;
+        *reinterpret_cast<P*>(y + at1) = ob;
+      } else {
+        const int at = 2 * p.half + (u - rot) * VEC;
+        *reinterpret_cast<P*>(y + at) = *reinterpret_cast<const P*>(x + at);
+      }
+    }
+  }
+}
+
+template <typename T, int VEC>
+static void launch_rotary(const RotaryParams& p, bool half, dim3 grid, size_t lds, hipStream_t s) {
+  if (half) rotary_kernel<T, true, VEC><<<grid, 256, lds, s>>>(p);
+  else rotary_kernel<T, false, VEC><<<grid, 256, lds, s>>>(p);
+}
+
+}  // namespace hum
+
+using namespace hum;
+
+extern "C" {
+
+hum_status hum_rotary_inv_freq(int32_t rotary_dim, double base, int32_t scaling, double factor, double original_len,
+                               double fast_turns, double slow_turns, double* inv_freq_host, float* factor_out) {
+  clear_error();
+  if (!inv_freq_host || !factor_out) return set_error(HUM_ERR_INVALID_ARG, "NULL pointer");
+  if (rotary_dim < 2 || rotary_dim % 2 || rotary_dim > 1024)
+    return set_error(HUM_ERR_INVALID_ARG, "rotary_dim must be even, 2 .. 1024");
+  if (!(base > 1.0) || !std::isfinite(base)) return set_error(HUM_ERR_INVALID_ARG, "base must be a number above 1");
+  if (scaling < HUM_ROPE_NONE || scaling > HUM_ROPE_YARN) return set_error(HUM_ERR_INVALID_ARG, "bad scaling");
+  if (scaling != HUM_ROPE_NONE && (!(factor >= 1.0) || !std::isfinite(factor)))
+    return set_error(HUM_ERR_INVALID_ARG, "factor must be a number of at least 1");
+  const double r = rotary_dim;
+  if (scaling == HUM_ROPE_NTK) {
+    if (rotary_dim == 2) return set_error(HUM_ERR_UNSUPPORTED, "NTK scaling needs more than one pair");
+    base *= std::pow(factor, r / (r - 2.0));
+  }
+  double lo = 0, hi = 0;
+  if (scaling == HUM_ROPE_YARN) {
+    if (!(original_len >= 1.0) || !std::isfinite(original_len) || !(fast_turns > slow_turns) || !(slow_turns > 0.0) ||
+        !std::isfinite(fast_turns))
+      return set_error(HUM_ERR_INVALID_ARG, "YaRN needs original_len >= 1 and fast_turns > slow_turns > 0");
+    // the (real) pair index that turns n times over original_len positions:
+    // original_len * base^(-2i/R) = 2 pi n
+    auto pair_of = [&](double n) { return r * std::log(original_len / (n * 2.0 * M_PI)) / (2.0 * std::log(base)); };
+    lo = std::fmax(std::floor(pair_of(fast_turns)), 0.0);
+    hi = std::fmin(std::ceil(pair_of(slow_turns)), r - 1.0);
+  }
+  for (int i = 0; i < rotary_dim / 2; ++i) {
+    double f = std::pow(base, -2.0 * i / r);
+    if (scaling == HUM_ROPE_LINEAR) f /= factor;
+    if (scaling == HUM_ROPE_YARN) {
+      const double slow = std::fmin(std::fmax((i - lo) / std::fmax(hi - lo, 1e-3), 0.0), 1.0);
+      f = f * (1.0 - slow) + f / factor * slow;
+    }
+    inv_freq_host[i] = f;
+  }
+  *factor_out = scaling == HUM_ROPE_YARN ? (float)(0.1 * std::log(factor) + 1.0) : 1.0f;
+  return HUM_OK;
+}
+
+hum_status hum_rotary(const hum_rotary_desc* d, int64_t num_tokens, const int64_t* positions, const double* inv_freq,
+                      const void* q, int64_t q_ts, int64_t q_hs, void* q_out, int64_t qo_ts, int64_t qo_hs,
+                      const void* k, int64_t k_ts, int64_t k_hs, void* k_out, int64_t ko_ts, int64_t ko_hs,
+                      void* stream) {
+  clear_error();
+  if (!d) return set_error(HUM_ERR_INVALID_ARG, "desc is NULL");
+  if (d->dtype != HUM_BF16 && d->dtype != HUM_F32) return set_error(HUM_ERR_UNSUPPORTED, "dtype must be bf16 or f32");
+  if (d->layout != HUM_ROPE_HALF && d->layout != HUM_ROPE_INTERLEAVED)
+    return set_error(HUM_ERR_INVALID_ARG, "bad layout");
+  if (d->head_dim < 1 || d->head_dim > 1024) return set_error(HUM_ERR_UNSUPPORTED, "head_dim must be 1 .. 1024");
+  if (d->rotary_dim < 2 || d->rotary_dim % 2 || d->rotary_dim > d->head_dim)
+    return set_error(HUM_ERR_INVALID_ARG, "rotary_dim must be even, 2 .. head_dim");
+  if (d->num_q_heads < 0 || d->num_kv_heads < 0 || d->num_q_heads > 4096 || d->num_kv_heads > 4096)
+    return set_error(HUM_ERR_INVALID_ARG, "head counts must be 0 .. 4096");
+  if (d->inverse != 0 && d->inverse != 1) return set_error(HUM_ERR_INVALID_ARG, "inverse must be 0/1");
+  if (num_tokens < 0) return set_error(HUM_ERR_INVALID_ARG, "num_tokens must be >= 0");
+  // (a grid holds at most 2^32 - 1 threads)
+  if (num_tokens >= (int64_t)1 << 24) return set_error(HUM_ERR_UNSUPPORTED, "at most 2^24 - 1 tokens in a call");
+  const int hall = d->num_q_heads + d->num_kv_heads;
+  if (num_tokens == 0 || hall == 0) return HUM_OK;
+  if (!positions || !inv_freq || (d->num_q_heads && (!q || !q_out)) || (d->num_kv_heads && (!k || !k_out)))
+    return set_error(HUM_ERR_INVALID_ARG, "NULL pointer");
+  const int size = d->dtype == HUM_BF16 ? 2 : 4;
+  const int vec = 16 / size;
+  RotaryParams p{};
+  p.positions = positions;
+  p.inv_freq = inv_freq;
+  const void* xs[2] = {q, k};
+  void* ys[2] = {q_out, k_out};
+  const int64_t st[2][4] = {{q_ts, q_hs, qo_ts, qo_hs}, {k_ts, k_hs, ko_ts, ko_hs}};
+  const int heads[2] = {d->num_q_heads, d->num_kv_heads};
+  bool aligned = (d->rotary_dim / 2) % vec == 0 && (d->head_dim - d->rotary_dim) % vec == 0;
+  bool in_place = true;
+  for (int i = 0; i < 2; ++i) {
+    p.x[i] = xs[i];
+    p.y[i] = ys[i];
+    p.x_ts[i] = st[i][0];
+    p.x_hs[i] = st[i][1];
+    p.y_ts[i] = st[i][2];
+    p.y_hs[i] = st[i][3];
+    p.heads[i] = heads[i];
+    if (!heads[i]) continue;
+    if (reinterpret_cast<uintptr_t>(xs[i]) % size || reinterpret_cast<uintptr_t>(ys[i]) % size)
+      return set_error(HUM_ERR_INVALID_ARG, "q, k and their outputs must be aligned to their elements");
+    if (xs[i] == ys[i] && (st[i][0] != st[i][2] || st[i][1] != st[i][3]))
+      return set_error(HUM_ERR_INVALID_ARG, "in place, input and output strides must be the same");
+    if (xs[i] != ys[i]) in_place = false;
+    aligned = aligned && reinterpret_cast<uintptr_t>(xs[i]) % 16 == 0 && reinterpret_cast<uintptr_t>(ys[i]) % 16 == 0;
+    for (int j = 0; j < 4; ++j) aligned = aligned && st[i][j] % vec == 0;
+  }
+  const int v = aligned ? vec : 1;
+  p.tokens = num_tokens;
+  p.half = d->rotary_dim / 2;
+  p.rest = in_place ? 0 : d->head_dim - d->rotary_dim;
+  p.units = p.half / v + p.rest / v;
+  while (p.lane_shift < 8 && (1 << p.lane_shift) < p.units) ++p.lane_shift;
+  p.factor = d->factor;
+  p.sign = d->inverse ? -1.0f : 1.0f;
+  // Tokens per workgroup: as many as fill 256 threads with one sine and
+  // cosine each; heads are sliced over grid.y where the tokens alone would
+  // leave compute units without a workgroup.
+  int64_t tok = 256 / p.half;
+  tok = tok < 1 ? 1 : tok > 8 ? 8 : tok;
+  while (tok > 1 && (num_tokens + tok - 1) / tok < 1024) tok /= 2;
+  p.tok_per_wg = (int)tok;
+  const int64_t gx = (num_tokens + tok - 1) / tok;
+  const int rows = 256 >> p.lane_shift;  // heads a workgroup turns at once
+  int64_t gy = 1;
+  if (gx < 512) {
+    gy = (512 + gx - 1) / gx;
+    const int64_t most = (hall + rows - 1) / rows;
+    if (gy > most) gy = most;
+  }
+  p.head_step = (int)((hall + gy - 1) / gy);
+  gy = (hall + p.head_step - 1) / p.head_step;
+  const size_t lds = (size_t)tok * p.half * 2 * sizeof(float);
+  const dim3 grid((unsigned)gx, (unsigned)gy);
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  const bool hf = d->layout == HUM_ROPE_HALF;
+  if (size == 2) {
+    if (v == 8) launch_rotary<uint16_t, 8>(p, hf, grid, lds, s);
+    else launch_rotary<uint16_t, 1>(p, hf, grid, lds, s);
+  } else {
+    if (v == 4) launch_rotary<float, 4>(p, hf, grid, lds, s);
+    else launch_rotary<float, 1>(p, hf, grid, lds, s);
+  }
+  hipError_t err = hipGetLastError();
+  if (err != hipSuccess) return set_error(HUM_ERR_HIP, "rotary launch: %s", hipGetErrorString(err));
+  return HUM_OK;
+}
+
+}  // extern "C"
