@@ -40,8 +40,9 @@ def _hipcc() -> str:
 
 # Per-source flags.  The GEMM kernels keep MFMA results in ordinary VGPRs:
 # the INT path scales every K-block's MFMA result on the VALU, which reads
-# VGPRs only (AGPR results would cost one v_accvgpr_read per element).
-EXTRA = {src: ["-mllvm", "-amdgpu-mfma-vgpr-form"] for src in GEMM_SOURCES}
+# VGPRs only (AGPR results would cost one v_accvgpr_read per element).  The
+# attention kernel's scores go to the VALU the same way.
+EXTRA = {src: ["-mllvm", "-amdgpu-mfma-vgpr-form"] for src in [*GEMM_SOURCES, "kv_attention.hip"]}
 
 
 def _compile(src: str) -> str:

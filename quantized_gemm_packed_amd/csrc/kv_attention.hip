@@ -2,107 +2,577 @@
 //
 //   out = sum_t softmax_t(scale q . K_t) V_t over the sequence's tokens.
 //
-// One workgroup per (sequence, query head); its waves take every fourth
-// token, a lane D / 64 elements of the row, with the softmax's running
-// maximum and sum per wave in f32; the waves join through LDS.
+// Two thin matrix products per sequence and key-value head, with the up to 16
+// query heads that share it as columns: S^T = K Q^T (rows = tokens) and
+// O^T = V^T P^T (rows = head elements).  What bounds them is the cache's
+// bytes; the kernel is built around one pass over those.
+//
+// * A wave works alone on 32 tokens at a time (no barrier in the loop): K and
+//   V go from memory to registers, never through LDS.  The 16x16x32 MFMA
+//   wants 8 consecutive k per lane, and which token or element is "row i" or
+//   "step k" is free as long as both operands agree, so K's rows are assigned
+//   so that the scores a lane receives are those of the 8 tokens whose
+//   probabilities it has to supply to the second product: the softmax'd
+//   scores are packed to bf16 in place, with no exchange between lanes.
+// * V arrives with a token's head elements side by side in a lane, and a lane
+//   holds 8 tokens: pairs of tokens are interleaved with one byte permute per
+//   two values to form V^T's rows.
+// * Codes become bf16 exactly on the way (hardware conversions; MX scales go
+//   into them).  An FP8 row's f32 scale multiplies its score (K) or its
+//   probability (V) in f32.
+// * Scores stay in the exponent's base 2.  The reference maximum m of a head
+//   is only raised when a score exceeds it by more than 8: the probabilities
+//   stay below 2^8 times the wave's first, their f32 sums and bf16 roundings
+//   do not care, and most tiles need no exchange for a maximum and no pass
+//   over the accumulators.  Probabilities are rounded to bf16 (half a step,
+//   2^-8 of each) to feed the matrix instruction; sums, maxima and
+//   accumulators are f32.
+// * Work: the tiles of 128 tokens of all (sequence, key-value head) pairs laid
+//   end to end are cut into equal shares, one per workgroup, whatever the
+//   lengths are; every workgroup finds its share from seq_lens itself, so
+//   nothing is planned on the host.  A pair cut between workgroups is joined
+//   by whichever of them finishes last, from f32 parts, in the order of the
+//   parts (the same bits whatever finishes last).
 #include "kv_common.h"
 
 namespace hum {
 
 struct KvAttnParams {
   const uint8_t* cache;
-  int64_t unit, num_pages;
-  int32_t kv_heads, q_heads, page_shift;
+  int64_t unit;
+  int32_t num_pages, kv_heads, group, head_tiles, page_shift;  // group: query heads per key-value head
   const uint16_t* q;
   int64_t q_ts, q_hs;
+  int32_t q_vec;  // rows of q are 16-byte aligned
   const int32_t* table;
-  int64_t table_stride, max_pages;
+  int64_t table_stride;
+  int32_t max_pages, batch, window;
   const int32_t* seq_lens;
-  int64_t window;
-  float scale;
+  float scale_log2;  // scale * log2(e)
   uint16_t* out;
   float* lse;
+  uint32_t* count;  // one arrival counter per workgroup, zero between calls
+  float* part;      // two parts per workgroup
+  uint32_t part_bytes;
 };
 
-// Elements at .. at + N - 1 of a row as f32.
-template <int FMT, int D, int N>
-__device__ __forceinline__ void kv_row(const uint8_t* unit, int which, int at_token, int page_size, int at,
-                                       float (&x)[N]) {
+constexpr int kTile = 128;      // tokens of a workgroup tile, 32 per wave
+constexpr int kAttnWgs = 512;   // most workgroups: two on every CU
+constexpr int kDevScope = 16;   // sc1: through to memory, around the XCD's L2 (parts cross XCDs)
+
+// Where a lane's pieces of a row lie.
+template <int FMT, int D>
+struct AttnTile {
   using U = KvUnit<FMT, D>;
-  const uint8_t* row = unit + (int64_t)(which * page_size + at_token) * U::kRow;
-  const uint8_t* scales = unit + (int64_t)2 * page_size * U::kRow + which * page_size * U::kScale;
-  float sc = 1.0f;
-  if constexpr (FMT == HUM_ACT_FP8_TOKEN) sc = reinterpret_cast<const float*>(scales)[at_token];
-  if constexpr (U::kMx)
-    sc = e8m0_to_f32(which ? scales[(at / 32) * page_size + at_token] : scales[at_token * U::kScale + at / 32]);
+  static constexpr int kRow = U::kRow;
+  static constexpr int kKB = kRow / 4 < 16 ? kRow / 4 : 16;  // bytes of one K load
+  static constexpr int kKL = kRow / 4 / kKB;                 // K loads per row and lane
+  static constexpr int kKE = kKB * D / kRow;                 // elements of one K load
+  static constexpr int kChunks = D / 32;                     // MFMA steps of a score
+  static constexpr int kVN = D >= 128 ? D / 128 : 1;         // V loads per row and lane
+  static constexpr int kVE = D >= 128 ? 8 : 4;               // elements of one V load
+  static constexpr int kVB = kVE * kRow / D;                 // its bytes
+  static constexpr int kPart = 16 * D + 32;                  // floats of a part: O [16][D], m [16], l [16]
+};
+
+template <int B>
+__device__ __forceinline__ void load_bytes(const uint8_t* p, uint32_t* o) {
+  if constexpr (B == 16) {
+    const u32x4_t v = *reinterpret_cast<const u32x4_t*>(p);
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-    if constexpr (FMT == HUM_ACT_BF16) {
-      x[i] = bf16_bits_to_f32(reinterpret_cast<const uint16_t*>(row)[at + i]);
-    } else if constexpr (FMT == HUM_ACT_MXFP4) {
-      const uint32_t c = (row[(at + i) / 2] >> (4 * ((at + i) & 1))) & 15u;
-      x[i] = bf16_bits_to_f32(e2m1x8_to_bf16(c, 1.0f)[0] & 0xFFFF) * sc;
-    } else {
-      const u32x2_t w = {row[at + i], 0};
-      x[i] = bf16_bits_to_f32(e4m3x8_to_bf16(w, 1.0f)[0] & 0xFFFF) * sc;
-    }
+    for (int i = 0; i < 4; ++i) o[i] = v[i];
+  } else if constexpr (B == 8) {
+    const u32x2_t v = *reinterpret_cast<const u32x2_t*>(p);
+    o[0] = v[0];
+    o[1] = v[1];
+  } else if constexpr (B == 4) {
+    o[0] = *reinterpret_cast<const uint32_t*>(p);
+  } else if constexpr (B == 2) {
+    o[0] = *reinterpret_cast<const uint16_t*>(p);
   }
 }
 
+// N / 2 words of bf16 pairs from N codes.
+template <int FMT, int N>
+__device__ __forceinline__ void to_bf16(const uint32_t* w, float scale, uint32_t* o) {
+  if constexpr (FMT == HUM_ACT_BF16) {
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) o[i] = w[i];
+  } else if constexpr (FMT == HUM_ACT_MXFP4) {
+    const u32x4_t v = e2m1x8_to_bf16(w[0], scale);
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) o[i] = v[i];
+  } else {
+    const u32x2_t c = {w[0], N > 4 ? w[N > 4] : 0u};
+    const u32x4_t v = e4m3x8_to_bf16(c, scale);
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) o[i] = v[i];
+  }
+}
+
+__device__ __forceinline__ f32x4_t mfma_bf16(u32x4_t a, u32x4_t b, f32x4_t c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, b), c, 0,
+                                                 0, 0);
+}
+
+__device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// A sequence's tokens [lo, n) and its tiles.
+struct SeqSpan {
+  int32_t lo, n, first;  // first: token of the first tile
+  int32_t tiles;         // at least one (an empty row is written too)
+  __device__ __forceinline__ SeqSpan(const KvAttnParams& p, int b) {
+    n = p.seq_lens[b];
+    const int32_t most = p.max_pages << p.page_shift;
+    n = n < 0 ? 0 : n > most ? most : n;
+    lo = p.window > 0 && n > p.window ? n - p.window : 0;
+    first = lo & ~(kTile - 1);
+    tiles = (n - first + kTile - 1) / kTile;
+    tiles = tiles < 1 ? 1 : tiles;
+  }
+};
+
 template <int FMT, int D>
-__global__ __launch_bounds__(256) void kv_attention_kernel(const KvAttnParams p) {
-  constexpr int N = D / 64;
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t b = blockIdx.x;
-  const int h = blockIdx.y, hk = h / (p.q_heads / p.kv_heads);
+__global__ __launch_bounds__(256, FMT == HUM_ACT_BF16 && D == 256 ? 1 : 2) void kv_attention_kernel(
+    const KvAttnParams p) {
+  using T = AttnTile<FMT, D>;
+  using U = KvUnit<FMT, D>;
+  constexpr bool kFp8 = FMT == HUM_ACT_FP8_TOKEN;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int r = lane & 15, kq = lane >> 4;  // MFMA row / column, and which 8 of 32 steps
   const int page_size = 1 << p.page_shift;
-  int64_t n = p.seq_lens[b];
-  n = n < 0 ? 0 : n > (p.max_pages << p.page_shift) ? (p.max_pages << p.page_shift) : n;
-  const int64_t lo = p.window > 0 && n > p.window ? n - p.window : 0;
-  const uint16_t* qr = p.q + b * p.q_ts + h * p.q_hs + lane * N;
-  float q[N], acc[N] = {};
-#pragma unroll
-  for (int i = 0; i < N; ++i) q[i] = bf16_bits_to_f32(qr[i]) * p.scale;
-  float m = -__builtin_inff(), l = 0.0f;
-  for (int64_t t = lo + wave; t < n; t += 4) {
-    const int64_t page = p.table[b * p.table_stride + (t >> p.page_shift)];
-    if ((uint64_t)page >= (uint64_t)p.num_pages) continue;
-    const uint8_t* unit = p.cache + (page * p.kv_heads + hk) * p.unit;
-    float x[N];
-    kv_row<FMT, D, N>(unit, 0, (int)(t & (page_size - 1)), page_size, lane * N, x);
-    float s = 0.0f;
-#pragma unroll
-    for (int i = 0; i < N; ++i) s += q[i] * x[i];
-#pragma unroll
-    for (int w = 1; w < 64; w *= 2) s += __shfl_xor(s, w);
-    const float mn = __builtin_fmaxf(m, s);
-    const float a = m == mn ? 1.0f : __expf(m - mn), e = __expf(s - mn);
-    kv_row<FMT, D, N>(unit, 1, (int)(t & (page_size - 1)), page_size, lane * N, x);
-    l = l * a + e;
-#pragma unroll
-    for (int i = 0; i < N; ++i) acc[i] = acc[i] * a + e * x[i];
-    m = mn;
+  const float kNegInf = -__builtin_inff();
+
+  // ---- this workgroup's share ------------------------------------------------
+  // Lane i sums the tiles of a run of sequences; a scan over the lanes places
+  // the share's first tile in one run, which is then walked.
+  const int items_per_seq = p.kv_heads * p.head_tiles;
+  const int run = (p.batch + 63) / 64;
+  int64_t mine = 0;
+  for (int i = 0; i < run; ++i) {
+    const int b = lane * run + i;
+    if (b < p.batch) mine += SeqSpan(p, b).tiles;
   }
-  __shared__ float sm[4], sl[4], so[4][D];
-  if (lane == 0) {
-    sm[wave] = m;
-    sl[wave] = l;
-  }
+  int64_t upto = mine;  // inclusive scan
 #pragma unroll
-  for (int i = 0; i < N; ++i) so[wave][lane * N + i] = acc[i];
-  __syncthreads();
-  const float top = __builtin_fmaxf(__builtin_fmaxf(sm[0], sm[1]), __builtin_fmaxf(sm[2], sm[3]));
-  float total = 0.0f, w[4];
-  for (int i = 0; i < 4; ++i) {
-    w[i] = sm[i] == -__builtin_inff() ? 0.0f : __expf(sm[i] - top);
-    total += sl[i] * w[i];
+  for (int w = 1; w < 64; w *= 2) {
+    const int64_t o = __shfl_up(upto, w);
+    if (lane >= w) upto += o;
   }
-  for (int d = threadIdx.x; d < D; d += 256) {
-    float o = 0.0f;
-    for (int i = 0; i < 4; ++i) o += so[i][d] * w[i];
-    p.out[(b * p.q_heads + h) * D + d] = (uint16_t)f32_to_bf16_bits(total == 0.0f ? 0.0f : o / total);
+  const int64_t total = __shfl(upto, 63) * items_per_seq;
+  // (no more workgroups than tiles: every share that counts is non-empty)
+  const int64_t nwg = total < (int64_t)gridDim.x ? total : (int64_t)gridDim.x, wg = blockIdx.x;
+  if (wg >= nwg) return;
+  int64_t pos, end;
+  if (total < ((int64_t)1 << 22)) {  // (32-bit divisions where the products fit)
+    pos = (uint32_t)(wg * total) / (uint32_t)nwg;
+    end = (uint32_t)((wg + 1) * total) / (uint32_t)nwg;
+  } else {
+    pos = wg * total / nwg;
+    end = (wg + 1) * total / nwg;
   }
-  if (p.lse && threadIdx.x == 0) p.lse[b * p.q_heads + h] = total == 0.0f ? -__builtin_inff() : top + __logf(total);
+  pos = ((int64_t)__builtin_amdgcn_readfirstlane((int)(pos >> 32)) << 32) |
+        (uint32_t)__builtin_amdgcn_readfirstlane((int)pos);
+  end = ((int64_t)__builtin_amdgcn_readfirstlane((int)(end >> 32)) << 32) |
+        (uint32_t)__builtin_amdgcn_readfirstlane((int)end);
+  const uint64_t past = __ballot(upto * items_per_seq > pos);
+  const int run_lane = __builtin_ctzll(past);
+  int64_t seq_begin = __shfl(upto - mine, run_lane) * items_per_seq;  // first tile of sequence b
+  seq_begin = ((int64_t)__builtin_amdgcn_readfirstlane((int)(seq_begin >> 32)) << 32) |
+              (uint32_t)__builtin_amdgcn_readfirstlane((int)seq_begin);
+  int b = run_lane * run;
+  SeqSpan seq(p, b);
+  while (seq_begin + (int64_t)seq.tiles * items_per_seq <= pos) {
+    seq_begin += (int64_t)seq.tiles * items_per_seq;
+    seq = SeqSpan(p, ++b);
+  }
+  int item, tile;  // (key-value head, head tile) of the sequence, and the tile of it
+  {
+    const int64_t rel = pos - seq_begin;
+    if (rel < ((int64_t)1 << 32)) {
+      item = (int)((uint32_t)rel / (uint32_t)seq.tiles);
+      tile = (int)((uint32_t)rel % (uint32_t)seq.tiles);
+    } else {
+      item = (int)(rel / seq.tiles);
+      tile = (int)(rel % seq.tiles);
+    }
+  }
+
+  __shared__ float s_m[4][16], s_l[4][16];
+  __shared__ float s_o[4][16][D + 4];
+  __shared__ int s_last;
+
+  while (true) {
+    const int tile_end = (int)((int64_t)seq.tiles - tile < end - pos ? seq.tiles : tile + (int)(end - pos));
+    const int hk = item / p.head_tiles, ht = item - hk * p.head_tiles;
+    const int heads = p.group - ht * 16 < 16 ? p.group - ht * 16 : 16;  // live columns
+    const int q_head = hk * p.group + ht * 16;
+
+    // the query rows as MFMA B operands: column = head r, steps = the elements
+    // that a lane's K loads bring
+    u32x4_t qf[T::kChunks];
+    {
+      const uint16_t* q = p.q + b * p.q_ts + (int64_t)(q_head + (r < heads ? r : 0)) * p.q_hs;
+#pragma unroll
+      for (int c = 0; c < T::kChunks; ++c) {
+        constexpr int kPer = T::kKE / 8;
+        const int d0 = (c / kPer) * 4 * T::kKE + kq * T::kKE + (c % kPer) * 8;
+        if (p.q_vec) {
+          qf[c] = *reinterpret_cast<const u32x4_t*>(q + d0);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) qf[c][i] = (uint32_t)q[d0 + 2 * i] | ((uint32_t)q[d0 + 2 * i + 1] << 16);
+        }
+        if (r >= heads) qf[c] = u32x4_t{0, 0, 0, 0};
+      }
+    }
+
+    f32x4_t acc[T::kVN * T::kVE];
+#pragma unroll
+    for (int i = 0; i < T::kVN * T::kVE; ++i) acc[i] = f32x4_t{0, 0, 0, 0};
+    float m = kNegInf, m_safe = 0.0f, l = 0.0f;
+
+    // ---- the wave's tiles of this item ---------------------------------------
+    // (the first and the last may hold no token of the span)
+    int t = tile, t_end = tile_end;
+    const int32_t wave_first = seq.first + wave * 32;
+    if (t < t_end && wave_first + t * kTile + 32 <= seq.lo) ++t;
+    if (t < t_end && wave_first + (t_end - 1) * kTile >= seq.n) --t_end;
+
+    const int32_t* table = p.table + b * p.table_stride;
+    const uint32_t page_stride = (uint32_t)p.kv_heads * (uint32_t)p.unit;
+    const uint8_t* head_base = p.cache + (int64_t)hk * p.unit;
+    auto page_of = [&](int32_t tok) -> int32_t {
+      int32_t i = tok >> p.page_shift;
+      i = i < p.max_pages ? i : p.max_pages - 1;
+      return table[i];
+    };
+    // a page outside the cache: read page 0 instead, its tokens are masked
+    auto unit_of = [&](int32_t page) -> const uint8_t* {
+      const uint32_t pg = (uint32_t)page < (uint32_t)p.num_pages ? (uint32_t)page : 0u;
+      return head_base + (uint64_t)pg * page_stride;
+    };
+
+    uint32_t kw[2][T::kKL][T::kKB / 4];
+    uint32_t ks[2][2];  // MX: scale bytes of the two K rows
+    uint32_t vw[8][T::kVN][T::kVB < 4 ? 1 : T::kVB / 4];
+    uint32_t vs[T::kVN][2];    // MX: scale bytes of the 8 tokens
+    float kf[8], vf[8];        // FP8: row scales of the 8 tokens
+    const int kg = (lane >> 2) & 3;  // the granule of 8 tokens this lane's K rows lie in
+
+    auto load_k = [&](int32_t t0, const uint8_t* unit) {
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        const int at = (t0 + kg * 8 + s * 4 + (lane & 3)) & (page_size - 1);
+        const uint8_t* row = unit + at * T::kRow + kq * T::kKB;
+#pragma unroll
+        for (int j = 0; j < T::kKL; ++j) load_bytes<T::kKB>(row + j * 4 * T::kKB, kw[s][j]);
+        if constexpr (U::kMx) load_bytes<U::kScale>(unit + 2 * page_size * T::kRow + at * U::kScale, ks[s]);
+      }
+    };
+    auto load_v = [&](int32_t t0, const uint8_t* unit) {
+      const int at = (t0 + kq * 8) & (page_size - 1);
+      const uint8_t* row = unit + (page_size + at) * T::kRow + r * T::kVB;
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int j = 0; j < T::kVN; ++j) load_bytes<T::kVB>(row + i * T::kRow + j * 16 * T::kVB, vw[i][j]);
+      const uint8_t* scales = unit + 2 * page_size * T::kRow;
+      if constexpr (kFp8) {
+        load_bytes<16>(scales + at * 4, reinterpret_cast<uint32_t*>(kf));
+        load_bytes<16>(scales + at * 4 + 16, reinterpret_cast<uint32_t*>(kf + 4));
+        load_bytes<16>(scales + (page_size + at) * 4, reinterpret_cast<uint32_t*>(vf));
+        load_bytes<16>(scales + (page_size + at) * 4 + 16, reinterpret_cast<uint32_t*>(vf + 4));
+      }
+      if constexpr (U::kMx) {
+#pragma unroll
+        for (int j = 0; j < T::kVN; ++j) {
+          const int g = j * 4 + (r * T::kVE) / 32;
+          load_bytes<8>(scales + (U::kScale + g) * page_size + at, vs[j]);
+        }
+      }
+    };
+
+    int32_t page_v = 0, page_k = 0;          // of the tile in flight
+    int32_t next_v = 0, next_k = 0;          // of the one after
+    if (t < t_end) {
+      const int32_t t0 = wave_first + t * kTile;
+      page_v = page_of(t0 + kq * 8);
+      page_k = page_of(t0 + kg * 8);
+      load_k(t0, unit_of(page_k));
+      load_v(t0, unit_of(page_v));
+      if (t + 1 < t_end) {
+        next_v = page_of(t0 + kTile + kq * 8);
+        next_k = page_of(t0 + kTile + kg * 8);
+      }
+    }
+    for (; t < t_end; ++t) {
+      const int32_t t0 = wave_first + t * kTile;
+      const bool more = t + 1 < t_end;
+      // scores: rows 4 kq + j of sub-tile s are tokens 8 kq + 4 s + j
+      float x[8];
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        f32x4_t c4 = {0, 0, 0, 0};
+#pragma unroll
+        for (int c = 0; c < T::kChunks; ++c) {
+          constexpr int kPer = T::kKE / 8;
+          constexpr int kW = T::kKB / 4 / kPer;  // code words of a chunk
+          float sc = 1.0f;
+          if constexpr (U::kMx) {
+            // (the word is known at compile time, the byte goes by the lane)
+            const int g0 = (c / kPer) * 4 * T::kKE / 32;
+            sc = e8m0_to_f32((ks[s][g0 / 4] >> (8 * ((g0 & 3) + kq * T::kKE / 32))) & 0xFFu);
+          }
+          u32x4_t a;
+          uint32_t o[4];
+          to_bf16<FMT, 8>(&kw[s][c / kPer][(c % kPer) * kW], sc, o);
+          a = u32x4_t{o[0], o[1], o[2], o[3]};
+          c4 = mfma_bf16(a, qf[c], c4);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          x[s * 4 + j] = c4[j] * p.scale_log2;
+          if constexpr (kFp8) x[s * 4 + j] *= kf[s * 4 + j];
+        }
+      }
+      // tokens outside the span or on a page outside the cache
+      const bool page_ok = (uint32_t)page_v < (uint32_t)p.num_pages;
+      const bool whole = t0 >= seq.lo && t0 + 32 <= seq.n && __ballot(!page_ok) == 0;
+      if (!whole) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int32_t tok = t0 + kq * 8 + i;
+          if (!(page_ok && tok >= seq.lo && tok < seq.n)) {
+            x[i] = kNegInf;
+            // whatever the cache holds there: 0 * NaN is NaN
+            vf[i] = 0.0f;
+#pragma unroll
+            for (int j = 0; j < T::kVN; ++j) {
+#pragma unroll
+              for (int w = 0; w < (T::kVB < 4 ? 1 : T::kVB / 4); ++w) vw[i][j][w] = 0;
+              if constexpr (U::kMx) vs[j][i >> 2] &= ~(0xFFu << (8 * (i & 3)));
+            }
+          }
+        }
+      }
+      if (more) {
+        page_k = next_k;
+        load_k(t0 + kTile, unit_of(next_k));
+      }
+      __builtin_amdgcn_sched_barrier(0);
+      float top = x[0];
+#pragma unroll
+      for (int i = 1; i < 8; ++i) top = __builtin_fmaxf(top, x[i]);
+      if (__ballot(top > m + 8.0f)) {
+        top = __builtin_fmaxf(top, __shfl_xor(top, 16));
+        top = __builtin_fmaxf(top, __shfl_xor(top, 32));
+        const float mn = __builtin_fmaxf(m, top);
+        const float a = m == mn ? 1.0f : exp2_fast(m - mn);
+        m = mn;
+        m_safe = mn == kNegInf ? 0.0f : mn;
+        l *= a;
+#pragma unroll
+        for (int i = 0; i < T::kVN * T::kVE; ++i) acc[i] *= a;
+      }
+      float pr[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        pr[i] = exp2_fast(x[i] - m_safe);
+        l += pr[i];
+        if constexpr (kFp8) pr[i] *= vf[i];
+      }
+      u32x4_t pb;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) pb[i] = f32x2_to_bf16x2_bits(pr[2 * i], pr[2 * i + 1]);
+#pragma unroll
+      for (int j = 0; j < T::kVN; ++j) {
+        uint32_t w[8][T::kVE / 2];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          float sc = 1.0f;
+          if constexpr (U::kMx) sc = e8m0_to_f32((vs[j][i >> 2] >> (8 * (i & 3))) & 0xFFu);
+          to_bf16<FMT, T::kVE>(vw[i][j], sc, w[i]);
+        }
+#pragma unroll
+        for (int e = 0; e < T::kVE; ++e) {
+          // element e of tokens 2 i, 2 i + 1: their low or high halves
+          const uint32_t sel = e & 1 ? 0x07060302u : 0x05040100u;
+          u32x4_t a;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) a[i] = __builtin_amdgcn_perm(w[2 * i + 1][e / 2], w[2 * i][e / 2], sel);
+          acc[j * T::kVE + e] = mfma_bf16(a, pb, acc[j * T::kVE + e]);
+        }
+      }
+      if (more) {
+        page_v = next_v;
+        load_v(t0 + kTile, unit_of(next_v));
+        if (t + 2 < t_end) {
+          next_v = page_of(t0 + 2 * kTile + kq * 8);
+          next_k = page_of(t0 + 2 * kTile + kg * 8);
+        }
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+
+    // ---- join the four waves -------------------------------------------------
+    l += __shfl_xor(l, 16);
+    l += __shfl_xor(l, 32);
+    if (kq == 0) {
+      s_m[wave][r] = m;
+      s_l[wave][r] = l;
+    }
+    __syncthreads();
+    {
+      const float top = __builtin_fmaxf(__builtin_fmaxf(s_m[0][r], s_m[1][r]), __builtin_fmaxf(s_m[2][r], s_m[3][r]));
+      const float a = m == kNegInf ? 0.0f : m == top ? 1.0f : exp2_fast(m - top);
+      if (r < heads) {
+        // accumulator (j, e), register i: element j * 128 + (4 kq + i) * kVE + e
+#pragma unroll
+        for (int j = 0; j < T::kVN; ++j)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int e = 0; e < T::kVE; e += 4) {
+              float4 v;
+              v.x = acc[j * T::kVE + e][i] * a;
+              v.y = acc[j * T::kVE + e + 1][i] * a;
+              v.z = acc[j * T::kVE + e + 2][i] * a;
+              v.w = acc[j * T::kVE + e + 3][i] * a;
+              *reinterpret_cast<float4*>(&s_o[wave][r][j * 128 + (4 * kq + i) * T::kVE + e]) = v;
+            }
+      }
+    }
+    __syncthreads();
+    auto waves_m = [&](int h) {
+      return __builtin_fmaxf(__builtin_fmaxf(s_m[0][h], s_m[1][h]), __builtin_fmaxf(s_m[2][h], s_m[3][h]));
+    };
+    auto waves_l = [&](int h, float top) {
+      float sum = 0.0f;
+#pragma unroll
+      for (int w = 0; w < 4; ++w)
+        sum += s_m[w][h] == kNegInf ? 0.0f : s_l[w][h] * (s_m[w][h] == top ? 1.0f : exp2_fast(s_m[w][h] - top));
+      return sum;
+    };
+    auto waves_o = [&](int h, int d) {
+      f32x4_t o = {0, 0, 0, 0};
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        const float4 v = *reinterpret_cast<const float4*>(&s_o[w][h][d]);
+        o += f32x4_t{v.x, v.y, v.z, v.w};
+      }
+      return o;
+    };
+    auto store = [&](int h, int d, f32x4_t o, float sum) {
+      const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+      u32x2_t w = {f32x2_to_bf16x2_bits(o[0] * inv, o[1] * inv), f32x2_to_bf16x2_bits(o[2] * inv, o[3] * inv)};
+      if (sum == 0.0f) w = u32x2_t{0, 0};
+      *reinterpret_cast<u32x2_t*>(p.out + ((int64_t)b * p.kv_heads * p.group + q_head + h) * D + d) = w;
+    };
+    auto store_lse = [&](int h, float top, float sum) {
+      if (p.lse)
+        p.lse[(int64_t)b * p.kv_heads * p.group + q_head + h] =
+            sum == 0.0f ? kNegInf : (top + __log2f(sum)) * 0.6931471805599453f;
+    };
+    const int64_t item_begin = seq_begin + (int64_t)item * seq.tiles, item_end = item_begin + seq.tiles;
+    if (tile == 0 && tile_end == seq.tiles) {
+      for (int i = threadIdx.x * 4; i < heads * D; i += 1024) {
+        const int h = i / D, d = i - h * D;
+        const float top = waves_m(h), sum = waves_l(h, top);
+        store(h, d, waves_o(h, d), sum);
+        if (d == 0) store_lse(h, top, sum);
+      }
+    } else {
+      // the workgroups first .. last share this item
+      int64_t first, last;
+      if (total < ((int64_t)1 << 22)) {
+        first = ((uint32_t)((item_begin + 1) * nwg) - 1u) / (uint32_t)total;
+        last = ((uint32_t)(item_end * nwg) - 1u) / (uint32_t)total;
+      } else {
+        first = ((item_begin + 1) * nwg - 1) / total;
+        last = (item_end * nwg - 1) / total;
+      }
+      const int nseg = (int)(last - first) + 1;
+      const __amdgpu_buffer_rsrc_t rp =
+          __builtin_amdgcn_make_buffer_rsrc(p.part, (short)0, (int)p.part_bytes, 0x00020000);
+      // slot 2 g: the part that g's share begins inside; 2 g + 1: the part that it begins
+      auto slot = [&](int64_t g) { return (uint32_t)((2 * g + (g == first ? 1 : 0)) * T::kPart * 4); };
+      const uint32_t my = slot(wg);
+      for (int i = threadIdx.x * 4; i < heads * D; i += 1024) {
+        const int h = i / D, d = i - h * D;
+        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, waves_o(h, d)), rp, my + i * 4, 0, kDevScope);
+        if (d == 0) {
+          const float top = waves_m(h), sum = waves_l(h, top);
+          __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(top), rp, my + (16 * D + h) * 4, 0, kDevScope);
+          __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(sum), rp, my + (16 * D + 16 + h) * 4, 0, kDevScope);
+        }
+      }
+      // the part is complete in memory before the count goes up
+      __builtin_amdgcn_s_waitcnt(0);
+      __syncthreads();
+      if (threadIdx.x == 0) {
+        const uint32_t old = __hip_atomic_fetch_add(p.count + first, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        const int is_last = old + 1 == (uint32_t)nseg;
+        if (is_last) __hip_atomic_store(p.count + first, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        s_last = is_last;
+      }
+      __syncthreads();
+      if (s_last) {
+        for (int i = threadIdx.x * 4; i < heads * D; i += 1024) {
+          const int h = i / D, d = i - h * D;
+          float top = kNegInf, sum = 0.0f;
+          f32x4_t o = {0, 0, 0, 0};
+#pragma unroll 4
+          for (int64_t g = first; g <= last; ++g) {
+            const uint32_t at = slot(g);
+            const float gm = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rp, at + (16 * D + h) * 4, 0, kDevScope));
+            const float gl =
+                __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rp, at + (16 * D + 16 + h) * 4, 0, kDevScope));
+            const f32x4_t go =
+                __builtin_bit_cast(f32x4_t, __builtin_amdgcn_raw_buffer_load_b128(rp, at + i * 4, 0, kDevScope));
+            const float mn = __builtin_fmaxf(top, gm);
+            const float ao = top == kNegInf ? 0.0f : top == mn ? 1.0f : exp2_fast(top - mn);
+            const float ag = gm == kNegInf ? 0.0f : gm == mn ? 1.0f : exp2_fast(gm - mn);
+            sum = sum * ao + gl * ag;
+            o = o * ao + go * ag;
+            top = mn;
+          }
+          store(h, d, o, sum);
+          if (d == 0) store_lse(h, top, sum);
+        }
+      }
+    }
+    // ---- next item -------------------------------------------------------------
+    pos += tile_end - tile;
+    if (pos >= end) return;
+    tile = 0;
+    if (++item == items_per_seq) {
+      item = 0;
+      seq_begin += (int64_t)seq.tiles * items_per_seq;
+      seq = SeqSpan(p, ++b);
+    }
+    __syncthreads();  // the LDS rows are read before the next item writes them
+  }
+}
+
+// Workgroups of a call: never more than there can be tiles.
+static int attn_wgs(const hum_kv_desc* d, int32_t num_q_heads, int64_t batch, int64_t max_pages) {
+  const int64_t group = num_q_heads / d->num_kv_heads;
+  const int64_t tiles = max_pages * d->page_size / kTile + 1;
+  const int64_t all = batch * d->num_kv_heads * ((group + 15) / 16);
+  if (all >= kAttnWgs || all * tiles >= kAttnWgs) return kAttnWgs;
+  return (int)(all * tiles < 1 ? 1 : all * tiles);
+}
+
+static hum_status check_attn(const hum_kv_desc* d, int32_t num_q_heads, int64_t batch, int64_t max_pages, KvLayout* l) {
+  hum_status st = kv_layout(d, l);
+  if (st != HUM_OK) return st;
+  if (num_q_heads < 1 || num_q_heads % d->num_kv_heads || num_q_heads / d->num_kv_heads > 1024)
+    return set_error(HUM_ERR_INVALID_ARG, "num_q_heads must be 1 .. 1024 times num_kv_heads");
+  if (batch < 0 || batch > 0xFFFF) return set_error(HUM_ERR_INVALID_ARG, "batch must be 0 .. 65535");
+  if (max_pages < 0 || max_pages > ((int64_t)1 << 30) / d->page_size)
+    return set_error(HUM_ERR_INVALID_ARG, "max_pages must be >= 0, sequences at most 2^30 tokens");
+  return HUM_OK;
 }
 
 }  // namespace hum
@@ -115,12 +585,9 @@ size_t hum_kv_attention_workspace_bytes(const hum_kv_desc* desc, int32_t num_q_h
                                         int64_t max_pages) {
   clear_error();
   KvLayout l;
-  if (kv_layout(desc, &l) != HUM_OK) return 0;
-  if (num_q_heads < 1 || num_q_heads % desc->num_kv_heads || batch < 0 || max_pages < 0) {
-    set_error(HUM_ERR_INVALID_ARG, "num_q_heads must be a multiple of num_kv_heads, batch and max_pages >= 0");
-    return 0;
-  }
-  return HUM_WS_HEADER_BYTES;
+  if (check_attn(desc, num_q_heads, batch, max_pages, &l) != HUM_OK) return 0;
+  // the counters, then two parts per workgroup
+  return HUM_WS_HEADER_BYTES + (size_t)attn_wgs(desc, num_q_heads, batch, max_pages) * 2 * (16 * desc->head_dim + 32) * 4;
 }
 
 hum_status hum_kv_attention(const hum_kv_desc* desc, const void* cache, size_t cache_bytes, int32_t num_q_heads,
@@ -129,47 +596,50 @@ hum_status hum_kv_attention(const hum_kv_desc* desc, const void* cache, size_t c
                             float scale, void* out_bf16, float* lse, void* workspace, size_t ws_bytes, void* stream) {
   clear_error();
   KvLayout l;
-  hum_status st = kv_layout(desc, &l);
+  hum_status st = check_attn(desc, num_q_heads, batch, max_pages, &l);
   if (st != HUM_OK) return st;
-  if (num_q_heads < 1 || num_q_heads % desc->num_kv_heads || num_q_heads / desc->num_kv_heads > 1024)
-    return set_error(HUM_ERR_INVALID_ARG, "num_q_heads must be a multiple of num_kv_heads (at most 1024 times)");
-  if (batch < 0 || batch > 0xFFFF) return set_error(HUM_ERR_INVALID_ARG, "batch must be 0 .. 65535");
-  if (max_pages < 0 || max_pages > (int64_t)0x7FFFFFFF / desc->page_size)
-    return set_error(HUM_ERR_INVALID_ARG, "max_pages must be >= 0, sequences below 2^31 tokens");
   if (window < 0) return set_error(HUM_ERR_INVALID_ARG, "window must be >= 0");
   if (!(scale - scale == 0.0f)) return set_error(HUM_ERR_INVALID_ARG, "scale must be finite");
   if (batch == 0) return HUM_OK;
   if (!cache || !q_bf16 || (max_pages && !block_table) || !seq_lens || !out_bf16 || !workspace)
     return set_error(HUM_ERR_INVALID_ARG, "NULL pointer");
   if (reinterpret_cast<uintptr_t>(cache) % 16) return set_error(HUM_ERR_INVALID_ARG, "the cache must be 16-byte aligned");
+  if (reinterpret_cast<uintptr_t>(workspace) % 16)
+    return set_error(HUM_ERR_INVALID_ARG, "the workspace must be 16-byte aligned");
   if (reinterpret_cast<uintptr_t>(q_bf16) % 2 || reinterpret_cast<uintptr_t>(out_bf16) % 16)
     return set_error(HUM_ERR_INVALID_ARG, "q must be aligned to its elements, out to 16 bytes");
   if (cache_bytes < (size_t)l.bytes)
     return set_error(HUM_ERR_WORKSPACE, "cache of %zu bytes, the description takes %lld", cache_bytes, (long long)l.bytes);
   const size_t need = hum_kv_attention_workspace_bytes(desc, num_q_heads, batch, max_pages);
   if (ws_bytes < need) return set_error(HUM_ERR_WORKSPACE, "workspace of %zu bytes, %zu needed", ws_bytes, need);
+  const int wgs = attn_wgs(desc, num_q_heads, batch, max_pages);
   KvAttnParams p{};
   p.cache = static_cast<const uint8_t*>(cache);
   p.unit = l.unit;
-  p.num_pages = desc->num_pages;
+  p.num_pages = (int32_t)desc->num_pages;
   p.kv_heads = desc->num_kv_heads;
-  p.q_heads = num_q_heads;
+  p.group = num_q_heads / desc->num_kv_heads;
+  p.head_tiles = (p.group + 15) / 16;
   p.page_shift = __builtin_ctz((unsigned)desc->page_size);
   p.q = static_cast<const uint16_t*>(q_bf16);
   p.q_ts = q_ts;
   p.q_hs = q_hs;
+  p.q_vec = reinterpret_cast<uintptr_t>(q_bf16) % 16 == 0 && (q_ts | q_hs) % 8 == 0;
   p.table = block_table;
   p.table_stride = table_stride;
-  p.max_pages = max_pages;
+  p.max_pages = (int32_t)max_pages;
+  p.batch = (int32_t)batch;
+  p.window = (int32_t)(window < ((int64_t)1 << 30) ? window : (int64_t)1 << 30);
   p.seq_lens = seq_lens;
-  p.window = window;
-  p.scale = scale;
+  p.scale_log2 = (float)((double)scale * 1.4426950408889634);
   p.out = static_cast<uint16_t*>(out_bf16);
   p.lse = lse;
+  p.count = static_cast<uint32_t*>(workspace);
+  p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + HUM_WS_HEADER_BYTES);
+  p.part_bytes = (uint32_t)((size_t)wgs * 2 * (16 * desc->head_dim + 32) * 4);
   hipStream_t s = static_cast<hipStream_t>(stream);
-  const dim3 grid((unsigned)batch, (unsigned)num_q_heads);
   kv_dispatch(desc, [&](auto fmt, auto dim) {
-    kv_attention_kernel<decltype(fmt)::value, decltype(dim)::value><<<grid, 256, 0, s>>>(p);
+    kv_attention_kernel<decltype(fmt)::value, decltype(dim)::value><<<wgs, 256, 0, s>>>(p);
   });
   hipError_t err = hipGetLastError();
   if (err != hipSuccess) return set_error(HUM_ERR_HIP, "kv_attention launch: %s", hipGetErrorString(err));
