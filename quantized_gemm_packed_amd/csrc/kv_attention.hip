@@ -24,9 +24,12 @@
 //   is only raised when a score exceeds it by more than 8: the probabilities
 //   stay below 2^8 times the wave's first, their f32 sums and bf16 roundings
 //   do not care, and most tiles need no exchange for a maximum and no pass
-//   over the accumulators.  Probabilities are rounded to bf16 (half a step,
-//   2^-8 of each) to feed the matrix instruction; sums, maxima and
-//   accumulators are f32.
+//   over the accumulators.  Sums, maxima and accumulators are f32.
+// * A probability goes into the second product as the sum of two bf16, its
+//   rounding and what that left (2^-16 of it in all): with one alone the
+//   result's error against float64 is 1.4 times that of its own rounding to
+//   bf16.  The matrix units are idle most of the time (the twice as many
+//   products cost 0 to 3 %).
 // * Work: the tiles of 128 tokens of all (sequence, key-value head) pairs laid
 //   end to end are cut into equal shares, one per workgroup, whatever the
 //   lengths are; every workgroup finds its share from seq_lens itself, so
@@ -51,13 +54,16 @@ struct KvAttnParams {
   float scale_log2;  // scale * log2(e)
   uint16_t* out;
   float* lse;
-  uint32_t* count;  // one arrival counter per workgroup, zero between calls
-  float* part;      // two parts per workgroup
+  uint32_t* count;  // arrival counters (3 kAttnWgs, in the workspace's header), zero between calls
+  float* part;      // kSlots slots per workgroup
   uint32_t part_bytes;
+  int32_t part_heads;  // heads of a slot: m, l and O rows
 };
 
 constexpr int kTile = 128;      // tokens of a workgroup tile, 32 per wave
-constexpr int kAttnWgs = 512;   // most workgroups: two on every CU
+constexpr int kAttnWgs = 512;  // most workgroups: two on every CU
+constexpr int kSlots = 4;       // of a workgroup: its two parts, and the joins of a group of parts that it leads
+constexpr int kJoin = 8;        // parts read at once when a cut pair is joined
 constexpr int kDevScope = 16;   // sc1: through to memory, around the XCD's L2 (parts cross XCDs)
 
 // Where a lane's pieces of a row lie.
@@ -72,7 +78,7 @@ struct AttnTile {
   static constexpr int kVN = D >= 128 ? D / 128 : 1;         // V loads per row and lane
   static constexpr int kVE = D >= 128 ? 8 : 4;               // elements of one V load
   static constexpr int kVB = kVE * kRow / D;                 // its bytes
-  static constexpr int kPart = 16 * D + 32;                  // floats of a part: O [16][D], m [16], l [16]
+  static constexpr int kVW = kVB < 4 ? 1 : kVB / 4;          // words of a V load
 };
 
 template <int B>
@@ -121,16 +127,42 @@ __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_ex
 struct SeqSpan {
   int32_t lo, n, first;  // first: token of the first tile
   int32_t tiles;         // at least one (an empty row is written too)
-  __device__ __forceinline__ SeqSpan(const KvAttnParams& p, int b) {
-    n = p.seq_lens[b];
+  __device__ __forceinline__ SeqSpan(const KvAttnParams& p, int32_t len) {
     const int32_t most = p.max_pages << p.page_shift;
-    n = n < 0 ? 0 : n > most ? most : n;
+    n = len < 0 ? 0 : len > most ? most : len;
     lo = p.window > 0 && n > p.window ? n - p.window : 0;
     first = lo & ~(kTile - 1);
     tiles = (n - first + kTile - 1) / kTile;
     tiles = tiles < 1 ? 1 : tiles;
   }
 };
+
+// The tiles [tile, tile_end) of one (sequence, key-value head, 16 query
+// heads) that a workgroup takes, and those [t, t_end) of them in which its
+// wave has tokens.
+struct AttnItem {
+  int32_t b, hk, ht, tile, tile_end, t, t_end, wave_first;
+  SeqSpan seq;
+  const int32_t* table;
+  const uint8_t* base;  // the head's unit of page 0
+  __device__ __forceinline__ AttnItem(const KvAttnParams& p, int32_t b_, int32_t hk_, int32_t ht_, SeqSpan s, int32_t tile_,
+                                      int64_t left, int wave)
+      : b(b_), hk(hk_), ht(ht_), tile(tile_), seq(s) {
+    tile_end = seq.tiles - tile < left ? seq.tiles : tile + (int32_t)left;
+    t = tile;
+    t_end = tile_end;
+    wave_first = seq.first + wave * 32;
+    if (t < t_end && wave_first + t * kTile + 32 <= seq.lo) ++t;
+    if (t < t_end && wave_first + (t_end - 1) * kTile >= seq.n) --t_end;
+    table = p.table + b * p.table_stride;
+    base = p.cache + (int64_t)hk * p.unit;
+  }
+};
+
+__device__ __forceinline__ int64_t uniform64(int64_t v) {
+  return ((int64_t)__builtin_amdgcn_readfirstlane((int)(v >> 32)) << 32) |
+         (uint32_t)__builtin_amdgcn_readfirstlane((int)v);
+}
 
 template <int FMT, int D>
 __global__ __launch_bounds__(256, FMT == HUM_ACT_BF16 && D == 256 ? 1 : 2) void kv_attention_kernel(
@@ -151,7 +183,7 @@ __global__ __launch_bounds__(256, FMT == HUM_ACT_BF16 && D == 256 ? 1 : 2) void 
   int64_t mine = 0;
   for (int i = 0; i < run; ++i) {
     const int b = lane * run + i;
-    if (b < p.batch) mine += SeqSpan(p, b).tiles;
+    if (b < p.batch) mine += SeqSpan(p, p.seq_lens[b]).tiles;
   }
   int64_t upto = mine;  // inclusive scan
 #pragma unroll
@@ -159,157 +191,175 @@ __global__ __launch_bounds__(256, FMT == HUM_ACT_BF16 && D == 256 ? 1 : 2) void 
     const int64_t o = __shfl_up(upto, w);
     if (lane >= w) upto += o;
   }
-  const int64_t total = __shfl(upto, 63) * items_per_seq;
+  const int64_t total = uniform64(__shfl(upto, 63)) * items_per_seq;
   // (no more workgroups than tiles: every share that counts is non-empty)
   const int64_t nwg = total < (int64_t)gridDim.x ? total : (int64_t)gridDim.x, wg = blockIdx.x;
   if (wg >= nwg) return;
+  const bool small = total < ((int64_t)1 << 22);  // 32-bit divisions where the products fit
   int64_t pos, end;
-  if (total < ((int64_t)1 << 22)) {  // (32-bit divisions where the products fit)
+  if (small) {
     pos = (uint32_t)(wg * total) / (uint32_t)nwg;
     end = (uint32_t)((wg + 1) * total) / (uint32_t)nwg;
   } else {
     pos = wg * total / nwg;
     end = (wg + 1) * total / nwg;
   }
-  pos = ((int64_t)__builtin_amdgcn_readfirstlane((int)(pos >> 32)) << 32) |
-        (uint32_t)__builtin_amdgcn_readfirstlane((int)pos);
-  end = ((int64_t)__builtin_amdgcn_readfirstlane((int)(end >> 32)) << 32) |
-        (uint32_t)__builtin_amdgcn_readfirstlane((int)end);
-  const uint64_t past = __ballot(upto * items_per_seq > pos);
-  const int run_lane = __builtin_ctzll(past);
-  int64_t seq_begin = __shfl(upto - mine, run_lane) * items_per_seq;  // first tile of sequence b
-  seq_begin = ((int64_t)__builtin_amdgcn_readfirstlane((int)(seq_begin >> 32)) << 32) |
-              (uint32_t)__builtin_amdgcn_readfirstlane((int)seq_begin);
-  int b = run_lane * run;
-  SeqSpan seq(p, b);
-  while (seq_begin + (int64_t)seq.tiles * items_per_seq <= pos) {
-    seq_begin += (int64_t)seq.tiles * items_per_seq;
-    seq = SeqSpan(p, ++b);
-  }
-  int item, tile;  // (key-value head, head tile) of the sequence, and the tile of it
-  {
-    const int64_t rel = pos - seq_begin;
-    if (rel < ((int64_t)1 << 32)) {
-      item = (int)((uint32_t)rel / (uint32_t)seq.tiles);
-      tile = (int)((uint32_t)rel % (uint32_t)seq.tiles);
-    } else {
-      item = (int)(rel / seq.tiles);
-      tile = (int)(rel % seq.tiles);
+  pos = uniform64(pos);
+  end = uniform64(end);
+  auto first_item = [&]() {
+    const uint64_t past = __ballot(upto * items_per_seq > pos);
+    const int run_lane = __builtin_ctzll(past);
+    int64_t begin = uniform64(__shfl(upto - mine, run_lane)) * items_per_seq;  // first tile of sequence b
+    int b = run_lane * run;
+    SeqSpan seq(p, p.seq_lens[b]);
+    while (begin + (int64_t)seq.tiles * items_per_seq <= pos) {
+      begin += (int64_t)seq.tiles * items_per_seq;
+      seq = SeqSpan(p, p.seq_lens[++b]);
     }
-  }
+    const int64_t rel = pos - begin;
+    const int item = rel < ((int64_t)1 << 32) ? (int)((uint32_t)rel / (uint32_t)seq.tiles) : (int)(rel / seq.tiles);
+    const int tile = (int)(rel - (int64_t)item * seq.tiles);
+    const int hk = (int)((uint32_t)item / (uint32_t)p.head_tiles);
+    return AttnItem(p, b, hk, item - hk * p.head_tiles, seq, tile, end - pos, wave);
+  };
+  AttnItem cur = first_item();
+  int32_t len_after = p.seq_lens[cur.b + 1 < p.batch ? cur.b + 1 : cur.b];  // of the next sequence, loaded ahead
 
   __shared__ float s_m[4][16], s_l[4][16];
   __shared__ float s_o[4][16][D + 4];
   __shared__ int s_last;
 
-  while (true) {
-    const int tile_end = (int)((int64_t)seq.tiles - tile < end - pos ? seq.tiles : tile + (int)(end - pos));
-    const int hk = item / p.head_tiles, ht = item - hk * p.head_tiles;
-    const int heads = p.group - ht * 16 < 16 ? p.group - ht * 16 : 16;  // live columns
-    const int q_head = hk * p.group + ht * 16;
+  const uint32_t page_stride = (uint32_t)p.kv_heads * (uint32_t)p.unit;
+  const int kg = (lane >> 2) & 3;  // the granule of 8 tokens this lane's K rows lie in
+  auto page_of = [&](const AttnItem& w, int32_t tok) -> int32_t {
+    int32_t i = tok >> p.page_shift;
+    i = i < p.max_pages ? i : p.max_pages - 1;
+    return w.table[i];
+  };
+  // a page outside the cache: read page 0 instead, its tokens are masked
+  auto unit_of = [&](const uint8_t* base, int32_t page) -> const uint8_t* {
+    const uint32_t pg = (uint32_t)page < (uint32_t)p.num_pages ? (uint32_t)page : 0u;
+    return base + (uint64_t)pg * page_stride;
+  };
 
-    // the query rows as MFMA B operands: column = head r, steps = the elements
-    // that a lane's K loads bring
-    u32x4_t qf[T::kChunks];
-    {
-      const uint16_t* q = p.q + b * p.q_ts + (int64_t)(q_head + (r < heads ? r : 0)) * p.q_hs;
+  u32x4_t qf[T::kChunks];
+  uint32_t kw[2][T::kKL][T::kKB / 4];
+  uint32_t ks[2][2];  // MX: scale bytes of the two K rows
+  uint32_t vw[8][T::kVN][T::kVW];
+  uint32_t vs[T::kVN][2];  // MX: scale bytes of the 8 tokens
+  float kf[8], vf[8];      // FP8: row scales of the 8 tokens
+
+  // The query rows as MFMA B operands: column = head r, steps = the elements
+  // that a lane's K loads bring.
+  auto load_q = [&](const AttnItem& w) {
+    const int live = p.group - w.ht * 16;
+    const uint16_t* q = p.q + w.b * p.q_ts + (int64_t)(w.hk * p.group + w.ht * 16 + (r < live ? r : 0)) * p.q_hs;
 #pragma unroll
-      for (int c = 0; c < T::kChunks; ++c) {
-        constexpr int kPer = T::kKE / 8;
-        const int d0 = (c / kPer) * 4 * T::kKE + kq * T::kKE + (c % kPer) * 8;
-        if (p.q_vec) {
-          qf[c] = *reinterpret_cast<const u32x4_t*>(q + d0);
-        } else {
+    for (int c = 0; c < T::kChunks; ++c) {
+      constexpr int kPer = T::kKE / 8;
+      const int d0 = (c / kPer) * 4 * T::kKE + kq * T::kKE + (c % kPer) * 8;
+      if (p.q_vec) {
+        qf[c] = *reinterpret_cast<const u32x4_t*>(q + d0);
+      } else {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) qf[c][i] = (uint32_t)q[d0 + 2 * i] | ((uint32_t)q[d0 + 2 * i + 1] << 16);
-        }
-        if (r >= heads) qf[c] = u32x4_t{0, 0, 0, 0};
+        for (int i = 0; i < 4; ++i) qf[c][i] = (uint32_t)q[d0 + 2 * i] | ((uint32_t)q[d0 + 2 * i + 1] << 16);
       }
     }
+  };
+  auto load_k = [&](int32_t t0, const uint8_t* unit) {
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      const int at = (t0 + kg * 8 + s * 4 + (lane & 3)) & (page_size - 1);
+      const uint8_t* row = unit + at * T::kRow + kq * T::kKB;
+#pragma unroll
+      for (int j = 0; j < T::kKL; ++j) load_bytes<T::kKB>(row + j * 4 * T::kKB, kw[s][j]);
+      if constexpr (U::kMx) load_bytes<U::kScale>(unit + 2 * page_size * T::kRow + at * U::kScale, ks[s]);
+    }
+  };
+  auto load_v = [&](int32_t t0, const uint8_t* unit) {
+    const int at = (t0 + kq * 8) & (page_size - 1);
+    const uint8_t* row = unit + (page_size + at) * T::kRow + r * T::kVB;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+#pragma unroll
+      for (int j = 0; j < T::kVN; ++j) load_bytes<T::kVB>(row + i * T::kRow + j * 16 * T::kVB, vw[i][j]);
+    const uint8_t* scales = unit + 2 * page_size * T::kRow;
+    if constexpr (kFp8) {
+      load_bytes<16>(scales + at * 4, reinterpret_cast<uint32_t*>(kf));
+      load_bytes<16>(scales + at * 4 + 16, reinterpret_cast<uint32_t*>(kf + 4));
+      load_bytes<16>(scales + (page_size + at) * 4, reinterpret_cast<uint32_t*>(vf));
+      load_bytes<16>(scales + (page_size + at) * 4 + 16, reinterpret_cast<uint32_t*>(vf + 4));
+    }
+    if constexpr (U::kMx) {
+#pragma unroll
+      for (int j = 0; j < T::kVN; ++j) {
+        const int g = j * 4 + (r * T::kVE) / 32;
+        load_bytes<8>(scales + (U::kScale + g) * page_size + at, vs[j]);
+      }
+    }
+  };
+
+  // Pages of the tile in flight (V's lanes, K's lanes) and of the one after.
+  int32_t page_v = 0, page_k = 0, page2_v = 0, page2_k = 0;
+  auto first_pages = [&](const AttnItem& w, int32_t& v, int32_t& k, int32_t& v2, int32_t& k2) {
+    if (w.t < w.t_end) {
+      const int32_t t0 = w.wave_first + w.t * kTile;
+      v = page_of(w, t0 + kq * 8);
+      k = page_of(w, t0 + kg * 8);
+      if (w.t + 1 < w.t_end) {
+        v2 = page_of(w, t0 + kTile + kq * 8);
+        k2 = page_of(w, t0 + kTile + kg * 8);
+      }
+    }
+  };
+  auto load_first = [&](const AttnItem& w, int32_t v, int32_t k) {
+    load_q(w);
+    if (w.t < w.t_end) {
+      const int32_t t0 = w.wave_first + w.t * kTile;
+      load_k(t0, unit_of(w.base, k));
+      load_v(t0, unit_of(w.base, v));
+    }
+  };
+  first_pages(cur, page_v, page_k, page2_v, page2_k);
+  load_first(cur, page_v, page_k);
+
+  while (true) {
+    const int heads = p.group - cur.ht * 16 < 16 ? p.group - cur.ht * 16 : 16;  // live columns
+    const int q_head = cur.hk * p.group + cur.ht * 16;
+
+    // The next item's query, pages and first tile are fetched while this one
+    // ends: short sequences would otherwise wait for memory at every item.
+    const int64_t left = end - pos - (cur.tile_end - cur.tile);
+    AttnItem nxt = cur;
+    int32_t nv = 0, nk = 0, nv2 = 0, nk2 = 0;
+    if (left > 0) {
+      int32_t b = cur.b, hk = cur.hk, ht = cur.ht + 1;
+      SeqSpan seq = cur.seq;
+      if (ht == p.head_tiles) {
+        ht = 0;
+        if (++hk == p.kv_heads) {
+          hk = 0;
+          ++b;
+          seq = SeqSpan(p, len_after);
+          len_after = p.seq_lens[b + 1 < p.batch ? b + 1 : b];
+        }
+      }
+      nxt = AttnItem(p, b, hk, ht, seq, 0, left, wave);
+      first_pages(nxt, nv, nk, nv2, nk2);
+    }
+    const bool nxt_tiles = left > 0 && nxt.t < nxt.t_end;
 
     f32x4_t acc[T::kVN * T::kVE];
 #pragma unroll
     for (int i = 0; i < T::kVN * T::kVE; ++i) acc[i] = f32x4_t{0, 0, 0, 0};
     float m = kNegInf, m_safe = 0.0f, l = 0.0f;
 
-    // ---- the wave's tiles of this item ---------------------------------------
-    // (the first and the last may hold no token of the span)
-    int t = tile, t_end = tile_end;
-    const int32_t wave_first = seq.first + wave * 32;
-    if (t < t_end && wave_first + t * kTile + 32 <= seq.lo) ++t;
-    if (t < t_end && wave_first + (t_end - 1) * kTile >= seq.n) --t_end;
-
-    const int32_t* table = p.table + b * p.table_stride;
-    const uint32_t page_stride = (uint32_t)p.kv_heads * (uint32_t)p.unit;
-    const uint8_t* head_base = p.cache + (int64_t)hk * p.unit;
-    auto page_of = [&](int32_t tok) -> int32_t {
-      int32_t i = tok >> p.page_shift;
-      i = i < p.max_pages ? i : p.max_pages - 1;
-      return table[i];
-    };
-    // a page outside the cache: read page 0 instead, its tokens are masked
-    auto unit_of = [&](int32_t page) -> const uint8_t* {
-      const uint32_t pg = (uint32_t)page < (uint32_t)p.num_pages ? (uint32_t)page : 0u;
-      return head_base + (uint64_t)pg * page_stride;
-    };
-
-    uint32_t kw[2][T::kKL][T::kKB / 4];
-    uint32_t ks[2][2];  // MX: scale bytes of the two K rows
-    uint32_t vw[8][T::kVN][T::kVB < 4 ? 1 : T::kVB / 4];
-    uint32_t vs[T::kVN][2];    // MX: scale bytes of the 8 tokens
-    float kf[8], vf[8];        // FP8: row scales of the 8 tokens
-    const int kg = (lane >> 2) & 3;  // the granule of 8 tokens this lane's K rows lie in
-
-    auto load_k = [&](int32_t t0, const uint8_t* unit) {
-#pragma unroll
-      for (int s = 0; s < 2; ++s) {
-        const int at = (t0 + kg * 8 + s * 4 + (lane & 3)) & (page_size - 1);
-        const uint8_t* row = unit + at * T::kRow + kq * T::kKB;
-#pragma unroll
-        for (int j = 0; j < T::kKL; ++j) load_bytes<T::kKB>(row + j * 4 * T::kKB, kw[s][j]);
-        if constexpr (U::kMx) load_bytes<U::kScale>(unit + 2 * page_size * T::kRow + at * U::kScale, ks[s]);
-      }
-    };
-    auto load_v = [&](int32_t t0, const uint8_t* unit) {
-      const int at = (t0 + kq * 8) & (page_size - 1);
-      const uint8_t* row = unit + (page_size + at) * T::kRow + r * T::kVB;
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-#pragma unroll
-        for (int j = 0; j < T::kVN; ++j) load_bytes<T::kVB>(row + i * T::kRow + j * 16 * T::kVB, vw[i][j]);
-      const uint8_t* scales = unit + 2 * page_size * T::kRow;
-      if constexpr (kFp8) {
-        load_bytes<16>(scales + at * 4, reinterpret_cast<uint32_t*>(kf));
-        load_bytes<16>(scales + at * 4 + 16, reinterpret_cast<uint32_t*>(kf + 4));
-        load_bytes<16>(scales + (page_size + at) * 4, reinterpret_cast<uint32_t*>(vf));
-        load_bytes<16>(scales + (page_size + at) * 4 + 16, reinterpret_cast<uint32_t*>(vf + 4));
-      }
-      if constexpr (U::kMx) {
-#pragma unroll
-        for (int j = 0; j < T::kVN; ++j) {
-          const int g = j * 4 + (r * T::kVE) / 32;
-          load_bytes<8>(scales + (U::kScale + g) * page_size + at, vs[j]);
-        }
-      }
-    };
-
-    int32_t page_v = 0, page_k = 0;          // of the tile in flight
-    int32_t next_v = 0, next_k = 0;          // of the one after
-    if (t < t_end) {
-      const int32_t t0 = wave_first + t * kTile;
-      page_v = page_of(t0 + kq * 8);
-      page_k = page_of(t0 + kg * 8);
-      load_k(t0, unit_of(page_k));
-      load_v(t0, unit_of(page_v));
-      if (t + 1 < t_end) {
-        next_v = page_of(t0 + kTile + kq * 8);
-        next_k = page_of(t0 + kTile + kg * 8);
-      }
-    }
-    for (; t < t_end; ++t) {
-      const int32_t t0 = wave_first + t * kTile;
-      const bool more = t + 1 < t_end;
-      // scores: rows 4 kq + j of sub-tile s are tokens 8 kq + 4 s + j
+    if (cur.t >= cur.t_end && left > 0) load_first(nxt, nv, nk);
+    for (int t = cur.t; t < cur.t_end; ++t) {
+      const int32_t t0 = cur.wave_first + t * kTile;
+      const bool more = t + 1 < cur.t_end;
+      // scores: rows 4 kq + j of sub-tile s are tokens 8 kq + 4 s + j (a dead
+      // column repeats the first head's row and is never stored)
       float x[8];
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
@@ -338,28 +388,30 @@ __global__ __launch_bounds__(256, FMT == HUM_ACT_BF16 && D == 256 ? 1 : 2) void 
       }
       // tokens outside the span or on a page outside the cache
       const bool page_ok = (uint32_t)page_v < (uint32_t)p.num_pages;
-      const bool whole = t0 >= seq.lo && t0 + 32 <= seq.n && __ballot(!page_ok) == 0;
+      const bool whole = t0 >= cur.seq.lo && t0 + 32 <= cur.seq.n && __ballot(!page_ok) == 0;
       if (!whole) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const int32_t tok = t0 + kq * 8 + i;
-          if (!(page_ok && tok >= seq.lo && tok < seq.n)) {
+          if (!(page_ok && tok >= cur.seq.lo && tok < cur.seq.n)) {
             x[i] = kNegInf;
             // whatever the cache holds there: 0 * NaN is NaN
             vf[i] = 0.0f;
 #pragma unroll
             for (int j = 0; j < T::kVN; ++j) {
 #pragma unroll
-              for (int w = 0; w < (T::kVB < 4 ? 1 : T::kVB / 4); ++w) vw[i][j][w] = 0;
+              for (int w = 0; w < T::kVW; ++w) vw[i][j][w] = 0;
               if constexpr (U::kMx) vs[j][i >> 2] &= ~(0xFFu << (8 * (i & 3)));
             }
           }
         }
       }
-      if (more) {
-        page_k = next_k;
-        load_k(t0 + kTile, unit_of(next_k));
-      }
+      // the tile after this one: of this item or of the next
+      const bool ahead = more || nxt_tiles;
+      const int32_t t0_ahead = more ? t0 + kTile : nxt.wave_first + nxt.t * kTile;
+      const uint8_t* base_ahead = more ? cur.base : nxt.base;
+      if (ahead) load_k(t0_ahead, unit_of(base_ahead, more ? page2_k : nk));
+      if (!more && left > 0) load_q(nxt);
       __builtin_amdgcn_sched_barrier(0);
       float top = x[0];
 #pragma unroll
@@ -382,9 +434,14 @@ __global__ __launch_bounds__(256, FMT == HUM_ACT_BF16 && D == 256 ? 1 : 2) void 
         l += pr[i];
         if constexpr (kFp8) pr[i] *= vf[i];
       }
-      u32x4_t pb;
+      // probabilities as the sum of two bf16 (16 significant bits)
+      u32x4_t pb, pl;
 #pragma unroll
       for (int i = 0; i < 4; ++i) pb[i] = f32x2_to_bf16x2_bits(pr[2 * i], pr[2 * i + 1]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        pl[i] = f32x2_to_bf16x2_bits(pr[2 * i] - bf16_bits_to_f32(pb[i] & 0xFFFF),
+                                     pr[2 * i + 1] - __uint_as_float(pb[i] & 0xFFFF0000u));
 #pragma unroll
       for (int j = 0; j < T::kVN; ++j) {
         uint32_t w[8][T::kVE / 2];
@@ -402,14 +459,15 @@ __global__ __launch_bounds__(256, FMT == HUM_ACT_BF16 && D == 256 ? 1 : 2) void 
 #pragma unroll
           for (int i = 0; i < 4; ++i) a[i] = __builtin_amdgcn_perm(w[2 * i + 1][e / 2], w[2 * i][e / 2], sel);
           acc[j * T::kVE + e] = mfma_bf16(a, pb, acc[j * T::kVE + e]);
+          acc[j * T::kVE + e] = mfma_bf16(a, pl, acc[j * T::kVE + e]);
         }
       }
+      if (ahead) load_v(t0_ahead, unit_of(base_ahead, more ? page2_v : nv));
       if (more) {
-        page_v = next_v;
-        load_v(t0 + kTile, unit_of(next_v));
-        if (t + 2 < t_end) {
-          next_v = page_of(t0 + 2 * kTile + kq * 8);
-          next_k = page_of(t0 + 2 * kTile + kg * 8);
+        page_v = page2_v;
+        if (t + 2 < cur.t_end) {
+          page2_v = page_of(cur, t0 + 2 * kTile + kq * 8);
+          page2_k = page_of(cur, t0 + 2 * kTile + kg * 8);
         }
       }
       __builtin_amdgcn_sched_barrier(0);
@@ -463,94 +521,163 @@ __global__ __launch_bounds__(256, FMT == HUM_ACT_BF16 && D == 256 ? 1 : 2) void 
       }
       return o;
     };
-    auto store = [&](int h, int d, f32x4_t o, float sum) {
-      const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+    // the finished row of head h, elements d .. d + 3
+    auto store_out = [&](int h, int d, f32x4_t o, float top, float sum) {
+      const int64_t row = (int64_t)cur.b * p.kv_heads * p.group + q_head + h;
+      const float inv = 1.0f / sum;
       u32x2_t w = {f32x2_to_bf16x2_bits(o[0] * inv, o[1] * inv), f32x2_to_bf16x2_bits(o[2] * inv, o[3] * inv)};
       if (sum == 0.0f) w = u32x2_t{0, 0};
-      *reinterpret_cast<u32x2_t*>(p.out + ((int64_t)b * p.kv_heads * p.group + q_head + h) * D + d) = w;
+      *reinterpret_cast<u32x2_t*>(p.out + row * D + d) = w;
+      if (d == 0 && p.lse) p.lse[row] = sum == 0.0f ? kNegInf : (top + __log2f(sum)) * 0.6931471805599453f;
     };
-    auto store_lse = [&](int h, float top, float sum) {
-      if (p.lse)
-        p.lse[(int64_t)b * p.kv_heads * p.group + q_head + h] =
-            sum == 0.0f ? kNegInf : (top + __log2f(sum)) * 0.6931471805599453f;
-    };
-    const int64_t item_begin = seq_begin + (int64_t)item * seq.tiles, item_end = item_begin + seq.tiles;
-    if (tile == 0 && tile_end == seq.tiles) {
+    if (cur.tile == 0 && cur.tile_end == cur.seq.tiles) {
       for (int i = threadIdx.x * 4; i < heads * D; i += 1024) {
         const int h = i / D, d = i - h * D;
         const float top = waves_m(h), sum = waves_l(h, top);
-        store(h, d, waves_o(h, d), sum);
-        if (d == 0) store_lse(h, top, sum);
+        store_out(h, d, waves_o(h, d), top, sum);
       }
     } else {
-      // the workgroups first .. last share this item
+      // The workgroups first .. last hold a part of this item each.  Up to
+      // kJoin parts are joined by whichever arrives last; more of them first
+      // in groups, whose joins are then joined, so that no workgroup reads
+      // many parts one after the other.
+      const int64_t begin = pos - cur.tile;
       int64_t first, last;
-      if (total < ((int64_t)1 << 22)) {
-        first = ((uint32_t)((item_begin + 1) * nwg) - 1u) / (uint32_t)total;
-        last = ((uint32_t)(item_end * nwg) - 1u) / (uint32_t)total;
+      if (small) {
+        first = ((uint32_t)((begin + 1) * nwg) - 1u) / (uint32_t)total;
+        last = ((uint32_t)((begin + cur.seq.tiles) * nwg) - 1u) / (uint32_t)total;
       } else {
-        first = ((item_begin + 1) * nwg - 1) / total;
-        last = (item_end * nwg - 1) / total;
+        first = ((begin + 1) * nwg - 1) / total;
+        last = ((begin + cur.seq.tiles) * nwg - 1) / total;
       }
-      const int nseg = (int)(last - first) + 1;
+      const int w0 = (int)uniform64(first), nseg = (int)uniform64(last) - w0 + 1, seg = (int)wg - w0;
       const __amdgpu_buffer_rsrc_t rp =
           __builtin_amdgcn_make_buffer_rsrc(p.part, (short)0, (int)p.part_bytes, 0x00020000);
-      // slot 2 g: the part that g's share begins inside; 2 g + 1: the part that it begins
-      auto slot = [&](int64_t g) { return (uint32_t)((2 * g + (g == first ? 1 : 0)) * T::kPart * 4); };
-      const uint32_t my = slot(wg);
-      for (int i = threadIdx.x * 4; i < heads * D; i += 1024) {
-        const int h = i / D, d = i - h * D;
-        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, waves_o(h, d)), rp, my + i * 4, 0, kDevScope);
+      const uint32_t part_floats = (uint32_t)p.part_heads * (D + 2);
+      // Of a workgroup's slots, 0 is the part of an item that its share begins
+      // inside, 1 of one that it begins; 2 and 3 the joins of the groups of
+      // parts that those lead.
+      auto slot = [&](int sg, bool joined) {
+        return (uint32_t)((w0 + sg) * kSlots + (sg == 0 ? 1 : 0) + (joined ? 2 : 0)) * part_floats * 4;
+      };
+      auto put = [&](uint32_t at, int h, int d, f32x4_t o, float top, float sum) {
+        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, o), rp, at + (h * D + d) * 4, 0, kDevScope);
         if (d == 0) {
-          const float top = waves_m(h), sum = waves_l(h, top);
-          __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(top), rp, my + (16 * D + h) * 4, 0, kDevScope);
-          __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(sum), rp, my + (16 * D + 16 + h) * 4, 0, kDevScope);
+          const u32x2_t ml = {__float_as_uint(top), __float_as_uint(sum)};
+          __builtin_amdgcn_raw_buffer_store_b64(ml, rp, at + (p.part_heads * D + 2 * h) * 4, 0, kDevScope);
         }
-      }
-      // the part is complete in memory before the count goes up
-      __builtin_amdgcn_s_waitcnt(0);
-      __syncthreads();
-      if (threadIdx.x == 0) {
-        const uint32_t old = __hip_atomic_fetch_add(p.count + first, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        const int is_last = old + 1 == (uint32_t)nseg;
-        if (is_last) __hip_atomic_store(p.count + first, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        s_last = is_last;
-      }
-      __syncthreads();
-      if (s_last) {
-        for (int i = threadIdx.x * 4; i < heads * D; i += 1024) {
-          const int h = i / D, d = i - h * D;
+      };
+      // whether this workgroup is the last of n to arrive at a counter, which
+      // is left at zero; what each stored before is in memory by then
+      auto arrive = [&](int counter, int n) -> bool {
+        __builtin_amdgcn_s_waitcnt(0);
+        __syncthreads();
+        if (threadIdx.x == 0) {
+          const uint32_t old = __hip_atomic_fetch_add(p.count + counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+          const int is_last = old + 1 == (uint32_t)n;
+          if (is_last) __hip_atomic_store(p.count + counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+          s_last = is_last;
+        }
+        __syncthreads();
+        return s_last != 0;
+      };
+      // joins the slots of segments sg, sg + step, ... (n of them), four
+      // elements per thread; threads to spare take every groups-th of them
+      auto join = [&](int sg, int step, int n, bool joined, auto&& sink) {
+        const int units = heads * (D / 4);
+        const int groups = units >= 256 ? 1 : 256 / units;
+        float* s_j = &s_o[0][0][0];  // [256][6]: the groups' top, sum, o
+        for (int i0 = 0; i0 < units; i0 += 256) {
+          const int grp = groups == 1 ? 0 : (int)threadIdx.x / units;
+          const int i = i0 + (int)threadIdx.x - grp * units;
+          const bool live = grp < groups && i < units;
+          const int h = i / (D / 4), d = (i - h * (D / 4)) * 4;
           float top = kNegInf, sum = 0.0f;
           f32x4_t o = {0, 0, 0, 0};
-#pragma unroll 4
-          for (int64_t g = first; g <= last; ++g) {
-            const uint32_t at = slot(g);
-            const float gm = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rp, at + (16 * D + h) * 4, 0, kDevScope));
-            const float gl =
-                __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rp, at + (16 * D + 16 + h) * 4, 0, kDevScope));
-            const f32x4_t go =
-                __builtin_bit_cast(f32x4_t, __builtin_amdgcn_raw_buffer_load_b128(rp, at + i * 4, 0, kDevScope));
-            const float mn = __builtin_fmaxf(top, gm);
-            const float ao = top == kNegInf ? 0.0f : top == mn ? 1.0f : exp2_fast(top - mn);
-            const float ag = gm == kNegInf ? 0.0f : gm == mn ? 1.0f : exp2_fast(gm - mn);
-            sum = sum * ao + gl * ag;
-            o = o * ao + go * ag;
-            top = mn;
+          if (live) {
+            for (int g = grp; g < n; g += groups * kJoin) {
+              u32x2_t ml[kJoin];
+              f32x4_t go[kJoin];
+#pragma unroll
+              for (int k = 0; k < kJoin; ++k) {
+                const int gk = g + k * groups;
+                if (gk < n) {
+                  const uint32_t at = slot(sg + gk * step, joined);
+                  ml[k] = __builtin_amdgcn_raw_buffer_load_b64(rp, at + (p.part_heads * D + 2 * h) * 4, 0, kDevScope);
+                  go[k] = __builtin_bit_cast(
+                      f32x4_t, __builtin_amdgcn_raw_buffer_load_b128(rp, at + (h * D + d) * 4, 0, kDevScope));
+                } else {
+                  ml[k] = u32x2_t{__float_as_uint(kNegInf), 0u};
+                  go[k] = f32x4_t{0, 0, 0, 0};
+                }
+              }
+              float mn = top;
+#pragma unroll
+              for (int k = 0; k < kJoin; ++k) mn = __builtin_fmaxf(mn, __uint_as_float(ml[k][0]));
+              const float ao = top == kNegInf ? 0.0f : top == mn ? 1.0f : exp2_fast(top - mn);
+              sum *= ao;
+              o *= ao;
+#pragma unroll
+              for (int k = 0; k < kJoin; ++k) {
+                const float gm = __uint_as_float(ml[k][0]);
+                const float ag = gm == kNegInf ? 0.0f : gm == mn ? 1.0f : exp2_fast(gm - mn);
+                sum += __uint_as_float(ml[k][1]) * ag;
+                o += go[k] * ag;
+              }
+              top = mn;
+            }
           }
-          store(h, d, o, sum);
-          if (d == 0) store_lse(h, top, sum);
+          if (groups > 1) {
+            float* j = s_j + threadIdx.x * 6;
+            j[0] = top;
+            j[1] = sum;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) j[2 + k] = o[k];
+            __syncthreads();
+            if (grp == 0) {
+              for (int k = 1; k < groups; ++k) {
+                const float* v = s_j + (threadIdx.x + k * units) * 6;
+                const float mn = __builtin_fmaxf(top, v[0]);
+                const float ao = top == kNegInf ? 0.0f : top == mn ? 1.0f : exp2_fast(top - mn);
+                const float ag = v[0] == kNegInf ? 0.0f : v[0] == mn ? 1.0f : exp2_fast(v[0] - mn);
+                sum = sum * ao + v[1] * ag;
+                o = o * ao + f32x4_t{v[2], v[3], v[4], v[5]} * ag;
+                top = mn;
+              }
+            }
+          }
+          if (live && grp == 0) sink(h, d, o, top, sum);
+        }
+      };
+      for (int i = threadIdx.x * 4; i < heads * D; i += 1024) {
+        const int h = i / D, d = i - h * D;
+        const float top = waves_m(h), sum = waves_l(h, top);
+        put(slot(seg, false), h, d, waves_o(h, d), top, sum);
+      }
+      // counters: of an item at its first workgroup; of a group at the slot
+      // of the part that leads it, after those
+      if (nseg <= kJoin) {
+        if (arrive(w0, nseg)) join(0, 1, nseg, false, store_out);
+      } else {
+        const int size = nseg <= 64 ? 8 : nseg <= 256 ? 16 : 32;
+        const int lead = seg & ~(size - 1);
+        const int members = nseg - lead < size ? nseg - lead : size;
+        if (arrive(kAttnWgs + 2 * (w0 + lead) + (lead == 0 ? 1 : 0), members)) {
+          join(lead, 1, members, false, [&](int h, int d, f32x4_t o, float top, float sum) {
+            put(slot(lead, true), h, d, o, top, sum);
+          });
+          const int ngroups = (nseg + size - 1) / size;
+          if (arrive(w0, ngroups)) join(0, size, ngroups, true, store_out);
         }
       }
     }
     // ---- next item -------------------------------------------------------------
-    pos += tile_end - tile;
-    if (pos >= end) return;
-    tile = 0;
-    if (++item == items_per_seq) {
-      item = 0;
-      seq_begin += (int64_t)seq.tiles * items_per_seq;
-      seq = SeqSpan(p, ++b);
-    }
+    if (left <= 0) return;
+    pos = end - left;
+    cur = nxt;
+    page_v = nv;
+    page2_v = nv2;
+    page2_k = nk2;
     __syncthreads();  // the LDS rows are read before the next item writes them
   }
 }
@@ -562,6 +689,16 @@ static int attn_wgs(const hum_kv_desc* d, int32_t num_q_heads, int64_t batch, in
   const int64_t all = batch * d->num_kv_heads * ((group + 15) / 16);
   if (all >= kAttnWgs || all * tiles >= kAttnWgs) return kAttnWgs;
   return (int)(all * tiles < 1 ? 1 : all * tiles);
+}
+
+// Heads of a slot (even: slots stay 16-byte aligned), and the slots' bytes.
+static int attn_part_heads(const hum_kv_desc* d, int32_t num_q_heads) {
+  const int group = num_q_heads / d->num_kv_heads;
+  return group >= 16 ? 16 : (group + 1) & ~1;
+}
+static size_t attn_part_bytes(const hum_kv_desc* d, int32_t num_q_heads, int64_t batch, int64_t max_pages) {
+  return (size_t)attn_wgs(d, num_q_heads, batch, max_pages) * kSlots * attn_part_heads(d, num_q_heads) *
+         (d->head_dim + 2) * 4;
 }
 
 static hum_status check_attn(const hum_kv_desc* d, int32_t num_q_heads, int64_t batch, int64_t max_pages, KvLayout* l) {
@@ -586,8 +723,7 @@ size_t hum_kv_attention_workspace_bytes(const hum_kv_desc* desc, int32_t num_q_h
   clear_error();
   KvLayout l;
   if (check_attn(desc, num_q_heads, batch, max_pages, &l) != HUM_OK) return 0;
-  // the counters, then two parts per workgroup
-  return HUM_WS_HEADER_BYTES + (size_t)attn_wgs(desc, num_q_heads, batch, max_pages) * 2 * (16 * desc->head_dim + 32) * 4;
+  return HUM_WS_HEADER_BYTES + attn_part_bytes(desc, num_q_heads, batch, max_pages);
 }
 
 hum_status hum_kv_attention(const hum_kv_desc* desc, const void* cache, size_t cache_bytes, int32_t num_q_heads,
@@ -636,7 +772,8 @@ hum_status hum_kv_attention(const hum_kv_desc* desc, const void* cache, size_t c
   p.lse = lse;
   p.count = static_cast<uint32_t*>(workspace);
   p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + HUM_WS_HEADER_BYTES);
-  p.part_bytes = (uint32_t)((size_t)wgs * 2 * (16 * desc->head_dim + 32) * 4);
+  p.part_bytes = (uint32_t)attn_part_bytes(desc, num_q_heads, batch, max_pages);
+  p.part_heads = attn_part_heads(desc, num_q_heads);
   hipStream_t s = static_cast<hipStream_t>(stream);
   kv_dispatch(desc, [&](auto fmt, auto dim) {
     kv_attention_kernel<decltype(fmt)::value, decltype(dim)::value><<<wgs, 256, 0, s>>>(p);

@@ -193,11 +193,24 @@ def test_attention_large_scores_and_scale(fmt):
         c.check(c.run(return_lse=True, scale=s), scale=s, what=f"scale {s}")
 
 
-@pytest.mark.parametrize("fmt,d", [("fp8_token", 128), ("bf16", 64)])
-def test_attention_long_sequence(fmt, d):
-    c = Case(14, fmt, [20011, 3], 8, 1, d, 64)
+@pytest.mark.parametrize("fmt,d,n", [("fp8_token", 128, 20011), ("bf16", 64, 20011), ("mxfp4", 64, 60001)])
+def test_attention_long_sequence(fmt, d, n):
+    """One key-value head: its tiles are cut into as many parts as there are
+    workgroups (joined in groups, then the groups)."""
+    c = Case(14, fmt, [n, 3], 8, 1, d, 64)
     c.check(c.run(return_lse=True), what="long")
     c.check(c.run(return_lse=True, window=12345), window=12345, what="long window")
+
+
+def test_attention_batches_of_many_lengths():
+    """Sequences more than lanes, workgroups that end inside a head, between
+    heads and between sequences; also the head tiles of more than 16 query
+    heads per key-value head, one of them ragged."""
+    g = np.random.default_rng(16)
+    for lens, hq, hk in ((list(g.integers(0, 400, 150)), 6, 3), (list(g.integers(0, 300, 70)), 36, 1)):
+        c = Case(17, "bf16", [int(n) for n in lens], hq, hk, 64, 16)
+        c.check(c.run(return_lse=True), what=f"{len(lens)} sequences")
+        c.check(c.run(return_lse=True, window=100), window=100, what=f"{len(lens)} sequences, window")
 
 
 def test_attention_no_sequences_and_no_pages():
