@@ -708,11 +708,15 @@ def moe_grouped_gemm(w: WeightDesc, packed, a, sorted_ids, offsets, block_m: int
 
 # ---- attention side of a decode step --------------------------------------
 
+_WS_HEADER = 64 << 10   # HUM_WS_HEADER_BYTES
 ROPE_HALF, ROPE_INTERLEAVED = range(2)
 ROPE_NONE, ROPE_LINEAR, ROPE_NTK, ROPE_YARN = range(4)
 _ROPE_LAYOUT = {"half": ROPE_HALF, "interleaved": ROPE_INTERLEAVED}
 _ROPE_SCALING = {"none": ROPE_NONE, "linear": ROPE_LINEAR, "ntk": ROPE_NTK, "yarn": ROPE_YARN}
 
+
+# These calls run once or more per layer and token, so their host side is kept
+# short: every check is an attribute or an integer comparison.
 
 def _rows3(t, name, dtype, shape=None):
     """Checks a [rows, heads, dim] tensor whose rows and heads may be strided
@@ -727,27 +731,55 @@ def _rows3(t, name, dtype, shape=None):
     return t.data_ptr(), st[0], st[1]
 
 
-def _vec(t, name, dtype, n, device):
-    """Checks a contiguous 1-D tensor on `device`."""
+def _vec(t, name, dtype, n, dev):
+    """Checks a contiguous 1-D tensor on device number `dev` (-1: the CPU)."""
     if t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
     if t.dim() != 1 or t.shape[0] != n:
         raise ValueError(f"{name} must have shape {(n,)}, got {tuple(t.shape)}")
     if n > 1 and t.stride(0) != 1:
         raise ValueError(f"{name} must be contiguous")
-    if t.device != device:
-        raise ValueError(f"tensors on different devices: {name} on {t.device}, not {device}")
+    if t.get_device() != dev:
+        raise ValueError(f"tensors on different devices: {name} on {t.device}")
     return t.data_ptr()
 
 
-def _launch(device, fn, *args):
-    """fn(*args, stream) with `device` current, on its current stream."""
+def _device_of(t, name, *others):
+    """The number of the GPU that `t` and every other tensor (or None) is on."""
+    dev = t.get_device()
+    for o in others:
+        if o is not None and o.get_device() != dev:
+            raise ValueError(f"tensors on different devices: {t.device} and {o.device}")
+    if dev < 0:
+        raise ValueError(f"{name} must be a device tensor")
+    return dev
+
+
+def _launch(dev, fn, *args):
+    """fn(*args, stream) with GPU `dev` current, on its current stream."""
     import torch
-    if torch.cuda.current_device() == device.index:
-        _check(fn(*args, torch.cuda.current_stream(device).cuda_stream))
+    if torch.cuda.current_device() == dev:
+        status = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
     else:
-        with torch.cuda.device(device):
-            _check(fn(*args, torch.cuda.current_stream(device).cuda_stream))
+        with torch.cuda.device(dev):
+            status = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
+    if status:
+        _check(status)
+
+
+def _call_workspace(dev, need):
+    """Scratch of one call on GPU `dev`'s current stream: the stream's own, or,
+    while it is captured, the graph's own from its memory pool (two graphs
+    captured on one stream may be replayed on two)."""
+    import torch
+    if torch.cuda.is_current_stream_capturing():
+        ws = torch.empty(need, dtype=torch.uint8, device=torch.device("cuda", dev))
+        ws[:_WS_HEADER].zero_()
+        return ws
+    ws = _WS.get((dev, torch._C._cuda_getCurrentRawStream(dev)))
+    if ws is not None and ws.buf is not None and ws.buf.numel() >= need:
+        return ws.buf
+    return _workspace(torch.device("cuda", dev)).get(need)
 
 
 def _no_overlap(out, name):
@@ -784,7 +816,7 @@ def rotary(q, k, positions, inv_freq, layout: str = "half", factor: float = 1.0,
         raise ValueError("q and k must be 3-D tensors [T, heads, head_dim]")
     if layout not in _ROPE_LAYOUT:
         raise ValueError(f"layout must be one of {sorted(_ROPE_LAYOUT)}")
-    dt, dev = q.dtype, q.device
+    dt = q.dtype
     if dt != torch.bfloat16 and dt != torch.float32:
         raise ValueError(f"q must be torch.bfloat16 or torch.float32, got {dt}")
     t, hq, d = q.shape
@@ -806,23 +838,22 @@ def rotary(q, k, positions, inv_freq, layout: str = "half", factor: float = 1.0,
     if k_out is not None:
         _rows3(k_out, "k_out", dt, k.shape)
         _no_overlap(k_out, "k_out")
-    _same_device(q, k, q_out, k_out)
+    dev = q.get_device()
     pp = _vec(positions, "positions", torch.int64, t, dev)
     fp = _vec(inv_freq, "inv_freq", torch.float64, half, dev)
-    if dev.type != "cuda":
-        raise ValueError("q must be a device tensor")
+    _device_of(q, "q", k, q_out, k_out)
     if q_out is None:
-        q_out = torch.empty((t, hq, d), dtype=dt, device=dev)
-    if k is not None and k_out is None:
-        k_out = torch.empty((t, hk, d), dtype=dt, device=dev)
-    qos = q_out.stride()
+        q_out = torch.empty_like(q)
+    qots, qohs, _ = q_out.stride()
     if k is not None:
+        if k_out is None:
+            k_out = torch.empty_like(k)
         kop = k_out.data_ptr()
         kots, kohs, _ = k_out.stride()
     desc = RotaryDesc(BF16 if dt == torch.bfloat16 else F32, _ROPE_LAYOUT[layout], d, 2 * half, hq, hk, bool(inverse),
                       factor)
-    _launch(dev, load_library().hum_rotary, ctypes.addressof(desc), t, pp, fp, qp, qts, qhs, q_out.data_ptr(), qos[0],
-            qos[1], kp, kts, khs, kop, kots, kohs)
+    _launch(dev, load_library().hum_rotary, ctypes.addressof(desc), t, pp, fp, qp, qts, qhs, q_out.data_ptr(), qots,
+            qohs, kp, kts, khs, kop, kots, kohs)
     return q_out, k_out
 
 
@@ -857,11 +888,8 @@ def kv_write(desc: KvDesc, cache, k, v, slots):
     shape = (t, desc.num_kv_heads, desc.head_dim)
     kp, kts, khs = _rows3(k, "k", torch.bfloat16, shape)
     vp, vts, vhs = _rows3(v, "v", torch.bfloat16, shape)
-    dev = cache.device
-    _same_device(cache, k, v)
-    sp = _vec(slots, "slots", torch.int64, t, dev)
-    if dev.type != "cuda":
-        raise ValueError("cache must be a device tensor")
+    sp = _vec(slots, "slots", torch.int64, t, cache.get_device())
+    dev = _device_of(cache, "cache", k, v)
     _launch(dev, load_library().hum_kv_write, ctypes.addressof(desc), cp, cb, t, sp, kp, kts, khs, vp, vts, vhs)
 
 
@@ -873,20 +901,17 @@ def kv_read(desc: KvDesc, cache, slots, k_out=None, v_out=None):
     if slots is None or slots.dim() != 1:
         raise ValueError("slots must be a 1-D int64 tensor")
     t = slots.shape[0]
-    dev = cache.device
-    sp = _vec(slots, "slots", torch.int64, t, dev)
+    sp = _vec(slots, "slots", torch.int64, t, cache.get_device())
     shape = (t, desc.num_kv_heads, desc.head_dim)
     for o, nm in ((k_out, "k_out"), (v_out, "v_out")):
         _want(o, nm, torch.bfloat16, shape)
         if o is not None and not o.is_contiguous():
             raise ValueError(f"{nm} must be contiguous")
-    _same_device(cache, k_out, v_out)
-    if dev.type != "cuda":
-        raise ValueError("cache must be a device tensor")
+    dev = _device_of(cache, "cache", k_out, v_out)
     if k_out is None:
-        k_out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+        k_out = cache.new_empty(shape, dtype=torch.bfloat16)
     if v_out is None:
-        v_out = torch.empty(shape, dtype=torch.bfloat16, device=dev)
+        v_out = cache.new_empty(shape, dtype=torch.bfloat16)
     _launch(dev, load_library().hum_kv_read, ctypes.addressof(desc), cp, cb, t, sp, k_out.data_ptr(),
             v_out.data_ptr())
     return k_out, v_out
@@ -911,7 +936,6 @@ def kv_attention(desc: KvDesc, cache, q, block_table, seq_lens, scale: float | N
     if q is None or q.dim() != 3:
         raise ValueError("q must be a 3-D tensor [B, num_q_heads, head_dim]")
     b, hq, d = q.shape
-    dev = cache.device
     qp, qts, qhs = _rows3(q, "q", torch.bfloat16, (b, hq, desc.head_dim))
     if block_table is None or block_table.dim() != 2 or block_table.shape[0] != b:
         raise ValueError("block_table must be a 2-D tensor [B, max_pages]")
@@ -923,33 +947,22 @@ def kv_attention(desc: KvDesc, cache, q, block_table, seq_lens, scale: float | N
     _want(out, "out", torch.bfloat16, (b, hq, d))
     if out is not None and not out.is_contiguous():
         raise ValueError("out must be contiguous")
-    _same_device(cache, q, block_table, out, workspace)
-    lp = _vec(seq_lens, "seq_lens", torch.int32, b, dev)
-    if dev.type != "cuda":
-        raise ValueError("cache must be a device tensor")
+    lp = _vec(seq_lens, "seq_lens", torch.int32, b, cache.get_device())
+    dev = _device_of(cache, "cache", q, block_table, out, workspace)
     lib = load_library()
     need = kv_attention_workspace_bytes(desc, hq, b, mp)
     if workspace is None:
-        if torch.cuda.is_current_stream_capturing():
-            # the graph's own, from its memory pool: two graphs captured on one
-            # stream may be replayed on two
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-            workspace[:_WS_HEADER].zero_()
-        else:
-            workspace = _workspace(dev).get(need)
+        workspace = _call_workspace(dev, need)
     else:
         _want(workspace, "workspace", torch.uint8)
         _gpu(workspace, "workspace")
     if out is None:
-        out = torch.empty((b, hq, d), dtype=torch.bfloat16, device=dev)
-    lse = torch.empty((b, hq), dtype=torch.float32, device=dev) if return_lse else None
+        out = q.new_empty((b, hq, d))
+    lse = q.new_empty((b, hq), dtype=torch.float32) if return_lse else None
     _launch(dev, lib.hum_kv_attention, ctypes.addressof(desc), cp, cb, hq, b, qp, qts, qhs, block_table.data_ptr(),
             block_table.stride(0), mp, lp, int(window), d ** -0.5 if scale is None else scale, out.data_ptr(),
             None if lse is None else lse.data_ptr(), workspace.data_ptr(), workspace.numel())
     return (out, lse) if return_lse else out
-
-
-_WS_HEADER = 64 << 10   # HUM_WS_HEADER_BYTES
 
 
 (PEAK_HBM_READ, PEAK_MFMA_BF16, PEAK_MFMA_FP8, PEAK_MFMA_FP4, PEAK_MFMA_FP8_FP4, PEAK_MFMA32_BF16, PEAK_MFMA32_FP8,

@@ -17,29 +17,39 @@ struct KvMoveParams {
   int64_t slots_all;  // num_pages * page_size
   int32_t heads, page_shift;
   int64_t tokens;
+  int32_t tok_per_wg;  // tokens of a workgroup
+  int32_t head_step;   // rows (K's heads, then V's) of a token that a workgroup takes (grid.y slices them)
   const int64_t* slots;
   const uint16_t* x[2];  // write: k, v
   int64_t ts[2], hs[2];
   uint16_t* out[2];  // read: k, v, contiguous
 };
 
-// A lane's place: which row (token, K or V, head) and which 8 of its values.
+constexpr int kMoveRows = 4;  // rows whose loads a thread has in flight at once
+
+// A workgroup's rows, and a lane's place in one: which token, K or V, head.
 template <int D>
-struct KvPlace {
-  int64_t token;
-  int32_t which, head, lane;
-  bool valid;
-  __device__ __forceinline__ KvPlace(const KvMoveParams& p) {
-    constexpr int kLanes = D / 8;
-    const int64_t rows = p.tokens * 2 * p.heads;
-    const int64_t row = (int64_t)blockIdx.x * (256 / kLanes) + threadIdx.x / kLanes;
+struct KvRows {
+  static constexpr int kLanes = D / 8;
+  static constexpr int kStep = 256 / kLanes;  // rows at once
+  int64_t t0;
+  int32_t r0, nr, rows, lane;
+  float inv_nr;
+  __device__ __forceinline__ KvRows(const KvMoveParams& p) {
+    t0 = (int64_t)blockIdx.x * p.tok_per_wg;
+    const int nt = (int)(p.tokens - t0 < p.tok_per_wg ? p.tokens - t0 : p.tok_per_wg);
+    r0 = (int)blockIdx.y * p.head_step;
+    nr = 2 * p.heads - r0 < p.head_step ? 2 * p.heads - r0 : p.head_step;
+    rows = nt * nr;
+    inv_nr = 1.0f / (float)nr;  // rows below 2^17: (row + 1/2) inv_nr is never a whole step off
     lane = threadIdx.x % kLanes;
-    valid = row < rows;
-    const int64_t r = valid ? row : 0;
-    token = r / (2 * p.heads);
-    const int32_t rest = (int32_t)(r - token * 2 * p.heads);
-    which = rest >= p.heads;
-    head = rest - which * p.heads;
+  }
+  __device__ __forceinline__ void place(const KvMoveParams& p, int row, int64_t* token, int* which, int* head) const {
+    const int t = (int)(((float)row + 0.5f) * inv_nr);
+    const int r = r0 + row - t * nr;
+    *token = t0 + t;
+    *which = r >= p.heads;
+    *head = r - *which * p.heads;
   }
 };
 
@@ -66,96 +76,143 @@ struct KvOffsets {
 template <int FMT, int D, bool VEC>
 __global__ __launch_bounds__(256) void kv_write_kernel(const KvMoveParams p) {
   using U = KvUnit<FMT, D>;
-  constexpr int kLanes = D / 8;
-  const KvPlace<D> me(p);
-  const int64_t slot = me.valid ? p.slots[me.token] : -1;
-  // (unsigned: negative slots are past the end too; a row's lanes agree)
-  const bool live = (uint64_t)slot < (uint64_t)p.slots_all;
-  u32x4_t v = {0, 0, 0, 0};
-  if (live) {
-    const uint16_t* x = p.x[me.which] + me.token * p.ts[me.which] + me.head * p.hs[me.which] + me.lane * 8;
-    if constexpr (VEC) {
-      v = *reinterpret_cast<const u32x4_t*>(x);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] = (uint32_t)x[2 * i] | ((uint32_t)x[2 * i + 1] << 16);
-    }
-  }
-  const int64_t page = slot >> p.page_shift;
+  const KvRows<D> me(p);
   const int page_size = 1 << p.page_shift;
-  const KvOffsets<FMT, D> off(me.which, (int)(slot & (page_size - 1)), page_size);
-  uint8_t* unit = p.cache + (live ? page * p.heads + me.head : 0) * p.unit;
-  if constexpr (FMT == HUM_ACT_BF16) {
-    if (live) *reinterpret_cast<u32x4_t*>(unit + off.code + me.lane * 16) = v;
-  } else {
-    float f[8];
+  // (the same number of passes for every thread: a row's lanes agree)
+  for (int row0 = threadIdx.x / me.kLanes; row0 < me.rows; row0 += me.kStep * kMoveRows) {
+    u32x4_t v[kMoveRows];
+    int64_t slot[kMoveRows];
+    int which[kMoveRows], head[kMoveRows];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      f[2 * i] = bf16_bits_to_f32(v[i] & 0xFFFF);
-      f[2 * i + 1] = bf16_bits_to_f32(v[i] >> 16);
-    }
-    float amax = 0.0f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) amax = __builtin_fmaxf(amax, __builtin_fabsf(f[i]));
-    if constexpr (FMT == HUM_ACT_FP8_TOKEN) {
-#pragma unroll
-      for (int m = 1; m < kLanes; m *= 2) amax = __builtin_fmaxf(amax, __shfl_xor(amax, m));
-      const float sc = amax > 0.0f ? amax / 448.0f : 1.0f;  // IEEE f32 division
-      if (!live) return;
-      u32x2_t o;
-      o[0] = f32x2_to_e4m3x2(f[0] / sc, f[1] / sc) | (f32x2_to_e4m3x2(f[2] / sc, f[3] / sc) << 16);
-      o[1] = f32x2_to_e4m3x2(f[4] / sc, f[5] / sc) | (f32x2_to_e4m3x2(f[6] / sc, f[7] / sc) << 16);
-      *reinterpret_cast<u32x2_t*>(unit + off.code + me.lane * 8) = o;
-      if (me.lane == 0) *reinterpret_cast<float*>(unit + off.scale) = sc;
-    } else {
-      amax = quad_max(amax);  // four lanes hold one block of 32
-      const int e = mx_scale_code_emax(amax, FMT == HUM_ACT_MXFP8 ? 8 : 2);
-      const float inv = mx_inv_scale(e);
-      if (!live) return;
-      if constexpr (FMT == HUM_ACT_MXFP8) {
-        u32x2_t o;
-        o[0] = f32x2_to_e4m3x2(f[0] * inv, f[1] * inv) | (f32x2_to_e4m3x2(f[2] * inv, f[3] * inv) << 16);
-        o[1] = f32x2_to_e4m3x2(f[4] * inv, f[5] * inv) | (f32x2_to_e4m3x2(f[6] * inv, f[7] * inv) << 16);
-        *reinterpret_cast<u32x2_t*>(unit + off.code + me.lane * 8) = o;
+    for (int k = 0; k < kMoveRows; ++k) {
+      const int row = row0 + k * me.kStep;
+      v[k] = u32x4_t{0, 0, 0, 0};
+      slot[k] = -1;
+      which[k] = head[k] = 0;
+      if (row >= me.rows) continue;
+      int64_t token;
+      me.place(p, row, &token, &which[k], &head[k]);
+      slot[k] = p.slots[token];
+      const uint16_t* x = which[k] ? p.x[1] + token * p.ts[1] + head[k] * p.hs[1] : p.x[0] + token * p.ts[0] + head[k] * p.hs[0];
+      x += me.lane * 8;
+      if constexpr (VEC) {
+        v[k] = *reinterpret_cast<const u32x4_t*>(x);
       } else {
-        uint32_t o = 0;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) o |= f32_to_e2m1(f[i] * inv) << (4 * i);
-        *reinterpret_cast<uint32_t*>(unit + off.code + me.lane * 4) = o;
+        for (int i = 0; i < 4; ++i) v[k][i] = (uint32_t)x[2 * i] | ((uint32_t)x[2 * i + 1] << 16);
       }
-      if ((me.lane & 3) == 0) unit[off.scale + (me.lane >> 2) * off.scale_step] = (uint8_t)e;
+    }
+#pragma unroll
+    for (int k = 0; k < kMoveRows; ++k) {
+      // (unsigned: negative slots are past the end too)
+      const bool live = (uint64_t)slot[k] < (uint64_t)p.slots_all;
+      const int64_t page = live ? slot[k] >> p.page_shift : 0;
+      const KvOffsets<FMT, D> off(which[k], (int)slot[k] & (page_size - 1), page_size);
+      uint8_t* unit = p.cache + (page * p.heads + head[k]) * p.unit;
+      if constexpr (FMT == HUM_ACT_BF16) {
+        if (live) *reinterpret_cast<u32x4_t*>(unit + off.code + me.lane * 16) = v[k];
+      } else {
+        float f[8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          f[2 * i] = bf16_bits_to_f32(v[k][i] & 0xFFFF);
+          f[2 * i + 1] = bf16_bits_to_f32(v[k][i] >> 16);
+        }
+        float amax = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) amax = __builtin_fmaxf(amax, __builtin_fabsf(f[i]));
+        if constexpr (FMT == HUM_ACT_FP8_TOKEN) {
+#pragma unroll
+          for (int m = 1; m < me.kLanes; m *= 2) amax = __builtin_fmaxf(amax, __shfl_xor(amax, m));
+          const float sc = amax > 0.0f ? amax / 448.0f : 1.0f;  // IEEE f32 division
+          u32x2_t o;
+          o[0] = f32x2_to_e4m3x2(f[0] / sc, f[1] / sc) | (f32x2_to_e4m3x2(f[2] / sc, f[3] / sc) << 16);
+          o[1] = f32x2_to_e4m3x2(f[4] / sc, f[5] / sc) | (f32x2_to_e4m3x2(f[6] / sc, f[7] / sc) << 16);
+          if (live) {
+            *reinterpret_cast<u32x2_t*>(unit + off.code + me.lane * 8) = o;
+            if (me.lane == 0) *reinterpret_cast<float*>(unit + off.scale) = sc;
+          }
+        } else {
+          amax = quad_max(amax);  // four lanes hold one block of 32
+          const int e = mx_scale_code_emax(amax, FMT == HUM_ACT_MXFP8 ? 8 : 2);
+          const float inv = mx_inv_scale(e);
+          if (live) {
+            if constexpr (FMT == HUM_ACT_MXFP8) {
+              u32x2_t o;
+              o[0] = f32x2_to_e4m3x2(f[0] * inv, f[1] * inv) | (f32x2_to_e4m3x2(f[2] * inv, f[3] * inv) << 16);
+              o[1] = f32x2_to_e4m3x2(f[4] * inv, f[5] * inv) | (f32x2_to_e4m3x2(f[6] * inv, f[7] * inv) << 16);
+              *reinterpret_cast<u32x2_t*>(unit + off.code + me.lane * 8) = o;
+            } else {
+              uint32_t o = 0;
+#pragma unroll
+              for (int i = 0; i < 8; ++i) o |= f32_to_e2m1(f[i] * inv) << (4 * i);
+              *reinterpret_cast<uint32_t*>(unit + off.code + me.lane * 4) = o;
+            }
+            if ((me.lane & 3) == 0) unit[off.scale + (me.lane >> 2) * off.scale_step] = (uint8_t)e;
+          }
+        }
+      }
     }
   }
 }
 
 template <int FMT, int D>
 __global__ __launch_bounds__(256) void kv_read_kernel(const KvMoveParams p) {
-  const KvPlace<D> me(p);
-  if (!me.valid) return;
-  const int64_t slot = p.slots[me.token];
-  u32x4_t o = {0, 0, 0, 0};
-  if ((uint64_t)slot < (uint64_t)p.slots_all) {
-    const int64_t page = slot >> p.page_shift;
-    const int page_size = 1 << p.page_shift;
-    const KvOffsets<FMT, D> off(me.which, (int)(slot & (page_size - 1)), page_size);
-    const uint8_t* unit = p.cache + (page * p.heads + me.head) * p.unit;
-    if constexpr (FMT == HUM_ACT_BF16) {
-      o = *reinterpret_cast<const u32x4_t*>(unit + off.code + me.lane * 16);
-    } else {
-      // codes as exact bf16, then one f32 product with the scale, rounded once
-      float sc;
-      if constexpr (FMT == HUM_ACT_FP8_TOKEN) sc = *reinterpret_cast<const float*>(unit + off.scale);
-      else sc = e8m0_to_f32(unit[off.scale + (me.lane >> 2) * off.scale_step]);
-      if constexpr (FMT == HUM_ACT_MXFP4)
-        o = e2m1x8_to_bf16(*reinterpret_cast<const uint32_t*>(unit + off.code + me.lane * 4), 1.0f);
-      else
-        o = e4m3x8_to_bf16(*reinterpret_cast<const u32x2_t*>(unit + off.code + me.lane * 8), 1.0f);
+  using U = KvUnit<FMT, D>;
+  const KvRows<D> me(p);
+  const int page_size = 1 << p.page_shift;
+  for (int row0 = threadIdx.x / me.kLanes; row0 < me.rows; row0 += me.kStep * kMoveRows) {
+    constexpr int kB = 8 * U::kRow / D;  // code bytes of a lane
+    uint32_t w[kMoveRows][kB / 4];
+    float sc[kMoveRows];
+    int64_t slot[kMoveRows], token[kMoveRows];
+    int which[kMoveRows], head[kMoveRows];
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        o[i] = f32x2_to_bf16x2_bits(bf16_bits_to_f32(o[i] & 0xFFFF) * sc, bf16_bits_to_f32(o[i] >> 16) * sc);
+    for (int k = 0; k < kMoveRows; ++k) {
+      const int row = row0 + k * me.kStep < me.rows ? row0 + k * me.kStep : row0;
+      me.place(p, row, &token[k], &which[k], &head[k]);
+      slot[k] = p.slots[token[k]];
+    }
+#pragma unroll
+    for (int k = 0; k < kMoveRows; ++k) {
+      // (a slot outside the cache: read slot 0, write zeros)
+      const int64_t s = (uint64_t)slot[k] < (uint64_t)p.slots_all ? slot[k] : 0;
+      const KvOffsets<FMT, D> off(which[k], (int)s & (page_size - 1), page_size);
+      const uint8_t* unit = p.cache + ((s >> p.page_shift) * p.heads + head[k]) * p.unit;
+      const uint8_t* code = unit + off.code + me.lane * kB;
+      if constexpr (kB == 16) {
+        const u32x4_t c = *reinterpret_cast<const u32x4_t*>(code);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[k][i] = c[i];
+      } else if constexpr (kB == 8) {
+        const u32x2_t c = *reinterpret_cast<const u32x2_t*>(code);
+        w[k][0] = c[0];
+        w[k][1] = c[1];
+      } else {
+        w[k][0] = *reinterpret_cast<const uint32_t*>(code);
+      }
+      if constexpr (FMT == HUM_ACT_FP8_TOKEN) sc[k] = *reinterpret_cast<const float*>(unit + off.scale);
+      if constexpr (U::kMx) sc[k] = __uint_as_float(unit[off.scale + (me.lane >> 2) * off.scale_step]);
+    }
+#pragma unroll
+    for (int k = 0; k < kMoveRows; ++k) {
+      if (row0 + k * me.kStep >= me.rows) continue;
+      u32x4_t o;
+      if constexpr (FMT == HUM_ACT_BF16) {
+        o = u32x4_t{w[k][0], w[k][1], w[k][2], w[k][3]};
+      } else {
+        // codes as exact bf16, then one f32 product with the scale, rounded once
+        if constexpr (FMT == HUM_ACT_MXFP4) o = e2m1x8_to_bf16(w[k][0], 1.0f);
+        else o = e4m3x8_to_bf16(u32x2_t{w[k][0], w[k][1]}, 1.0f);
+        const float s = U::kMx ? e8m0_to_f32(__float_as_uint(sc[k])) : sc[k];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          o[i] = f32x2_to_bf16x2_bits(bf16_bits_to_f32(o[i] & 0xFFFF) * s, bf16_bits_to_f32(o[i] >> 16) * s);
+      }
+      if ((uint64_t)slot[k] >= (uint64_t)p.slots_all) o = u32x4_t{0, 0, 0, 0};
+      *reinterpret_cast<u32x4_t*>((which[k] ? p.out[1] : p.out[0]) + (token[k] * p.heads + head[k]) * D + me.lane * 8) = o;
     }
   }
-  *reinterpret_cast<u32x4_t*>(p.out[me.which] + (me.token * p.heads + me.head) * D + me.lane * 8) = o;
 }
 
 hum_status kv_layout(const hum_kv_desc* d, KvLayout* l) {
@@ -189,9 +246,8 @@ static hum_status kv_move_params(const hum_kv_desc* d, const void* cache, size_t
   if (reinterpret_cast<uintptr_t>(cache) % 16) return set_error(HUM_ERR_INVALID_ARG, "the cache must be 16-byte aligned");
   if (cache_bytes < (size_t)l.bytes)
     return set_error(HUM_ERR_WORKSPACE, "cache of %zu bytes, the description takes %lld", cache_bytes, (long long)l.bytes);
-  // (a grid holds at most 2^32 - 1 threads, D / 8 of them a row)
-  if (num_tokens > ((int64_t)1 << 32) / (2 * d->num_kv_heads * (d->head_dim / 8)) - 256)
-    return set_error(HUM_ERR_UNSUPPORTED, "too many tokens for one call");
+  // (a grid holds at most 2^32 - 1 threads)
+  if (num_tokens >= (int64_t)1 << 24) return set_error(HUM_ERR_UNSUPPORTED, "at most 2^24 - 1 tokens in a call");
   p->cache = static_cast<uint8_t*>(const_cast<void*>(cache));
   p->unit = l.unit;
   p->slots_all = d->num_pages * d->page_size;
@@ -202,9 +258,17 @@ static hum_status kv_move_params(const hum_kv_desc* d, const void* cache, size_t
   return HUM_OK;
 }
 
-static unsigned kv_move_grid(const hum_kv_desc* d, int64_t num_tokens) {
-  const int64_t rows = num_tokens * 2 * d->num_kv_heads, per = 256 / (d->head_dim / 8);
-  return (unsigned)((rows + per - 1) / per);
+// Workgroups: kMoveRows passes of rows each, fewer where the rows would
+// otherwise leave compute units without one (a token's rows are cut over
+// grid.y if need be).
+static dim3 kv_move_grid(const hum_kv_desc* d, KvMoveParams* p) {
+  const int64_t per_tok = 2 * d->num_kv_heads, step = 256 / (d->head_dim / 8);
+  int64_t rows = step * kMoveRows;
+  while (rows > step && p->tokens * per_tok / rows < 1024) rows /= 2;
+  p->tok_per_wg = (int32_t)(rows >= per_tok ? rows / per_tok : 1);
+  p->head_step = (int32_t)(rows >= per_tok ? per_tok : rows);
+  return dim3((unsigned)((p->tokens + p->tok_per_wg - 1) / p->tok_per_wg),
+              (unsigned)((per_tok + p->head_step - 1) / p->head_step));
 }
 
 }  // namespace hum
@@ -236,7 +300,7 @@ hum_status hum_kv_write(const hum_kv_desc* desc, void* cache, size_t cache_bytes
   p.hs[0] = k_hs;
   p.hs[1] = v_hs;
   const bool vec = at % 16 == 0 && (k_ts | k_hs | v_ts | v_hs) % 8 == 0;
-  const unsigned grid = kv_move_grid(desc, num_tokens);
+  const dim3 grid = kv_move_grid(desc, &p);
   hipStream_t s = static_cast<hipStream_t>(stream);
   kv_dispatch(desc, [&](auto fmt, auto dim) {
     constexpr int F = decltype(fmt)::value, D = decltype(dim)::value;
@@ -259,7 +323,7 @@ hum_status hum_kv_read(const hum_kv_desc* desc, const void* cache, size_t cache_
     return set_error(HUM_ERR_INVALID_ARG, "k_out and v_out must be 16-byte aligned");
   p.out[0] = static_cast<uint16_t*>(k_out);
   p.out[1] = static_cast<uint16_t*>(v_out);
-  const unsigned grid = kv_move_grid(desc, num_tokens);
+  const dim3 grid = kv_move_grid(desc, &p);
   hipStream_t s = static_cast<hipStream_t>(stream);
   kv_dispatch(desc, [&](auto fmt, auto dim) {
     kv_read_kernel<decltype(fmt)::value, decltype(dim)::value><<<grid, 256, 0, s>>>(p);

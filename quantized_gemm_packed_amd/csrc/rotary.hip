@@ -25,7 +25,7 @@ struct RotaryParams {
   int32_t heads[2];
   int32_t half;        // rotary_dim / 2
   int32_t rest;        // head_dim - rotary_dim elements to copy (0 when in place)
-  int32_t units;       // rotating units + copied units of a head, VEC pairs / VEC elements each
+  int32_t units;       // rotating units (VEC pairs) and copied ones (2 VEC elements) of a head
   int32_t lane_shift;  // log2 of the lanes that share a head (all its units at once, at most 256)
   int32_t tok_per_wg;
   int32_t head_step;   // heads per workgroup (grid.y slices the heads)
@@ -50,9 +50,14 @@ struct Pack {
 };
 
 // VEC elements per 16-byte access where every address allows it, else one.
+// A lane's unit is two pieces of VEC elements of one head: the two halves of
+// VEC pairs (or VEC adjacent pairs), or two pieces to copy.  Each thread has
+// the loads of kRows heads in flight before it computes the first: with one
+// the loop waits for memory at every head.
 template <typename T, bool HALF, int VEC>
 __global__ __launch_bounds__(256) void rotary_kernel(const RotaryParams p) {
   typedef Pack<T, VEC> __attribute__((aligned(sizeof(T) * VEC))) P;
+  constexpr int kRows = 4;
   extern __shared__ float lds[];
   const int tid = threadIdx.x;
   const int64_t t0 = (int64_t)blockIdx.x * p.tok_per_wg;
@@ -70,52 +75,71 @@ __global__ __launch_bounds__(256) void rotary_kernel(const RotaryParams p) {
   }
   __syncthreads();
   const int lanes = 1 << p.lane_shift;
-  const int u0 = tid & (lanes - 1);
   const int rot = p.half / VEC;
   const int hall = p.heads[0] + p.heads[1];
   const int h0 = (int)blockIdx.y * p.head_step;
   const int nh = hall - h0 < p.head_step ? hall - h0 : p.head_step;
+  const float inv_nh = 1.0f / (float)nh;  // rows below 2^17: (row + 1/2) inv_nh is never a whole step off
   const int step = 256 >> p.lane_shift;
-  for (int row = tid >> p.lane_shift; row < nt * nh; row += step) {
-    const int t = row / nh;
-    const int hh = h0 + row - t * nh;
-    const int which = hh >= p.heads[0];
-    const int h = hh - (which ? p.heads[0] : 0);
-    const T* x = static_cast<const T*>(p.x[which]) + (t0 + t) * p.x_ts[which] + h * p.x_hs[which];
-    T* y = static_cast<T*>(p.y[which]) + (t0 + t) * p.y_ts[which] + h * p.y_hs[which];
-    for (int u = u0; u < p.units; u += lanes) {
-      if (u < rot) {
-        const float* c = cs + t * p.half + u * VEC;
-        const float* s = sn + t * p.half + u * VEC;
-        const int at0 = HALF ? u * VEC : 2 * u * VEC;
-        const int at1 = HALF ? at0 + p.half : at0 + VEC;
-        const P a = *reinterpret_cast<const P*>(x + at0);
-        const P b = *reinterpret_cast<const P*>(x + at1);
-        P oa, ob;
-  #pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-          // interleaved: the 2 VEC elements are VEC pairs side by side
-          const float x0 = HALF ? ld1<T>(a.v[i]) : 2 * i < VEC ? ld1<T>(a.v[(2 * i) % VEC]) : ld1<T>(b.v[(2 * i) % VEC]);
-          const float x1 = HALF                ? ld1<T>(b.v[i])
-                           : 2 * i + 1 < VEC ? ld1<T>(a.v[(2 * i + 1) % VEC])
-                                             : ld1<T>(b.v[(2 * i + 1) % VEC]);
-          const T y0 = st1<T>(x0 * c[i] - x1 * s[i]);
-          const T y1 = st1<T>(x0 * s[i] + x1 * c[i]);
-          if constexpr (HALF) {
-            oa.v[i] = y0;
-            ob.v[i] = y1;
-          } else {
-            if (2 * i < VEC) oa.v[(2 * i) % VEC] = y0;
-            else ob.v[(2 * i) % VEC] = y0;
-            if (2 * i + 1 < VEC) oa.v[(2 * i + 1) % VEC] = y1;
-            else ob.v[(2 * i + 1) % VEC] = y1;
+  const int rows = nt * nh;
+  for (int row0 = tid >> p.lane_shift; row0 < rows; row0 += step * kRows) {
+    const T* x[kRows];
+    T* y[kRows];
+    int tok[kRows];
+#pragma unroll
+    for (int k = 0; k < kRows; ++k) {
+      const int row = row0 + k * step < rows ? row0 + k * step : row0;
+      tok[k] = (int)(((float)row + 0.5f) * inv_nh);
+      const int hh = h0 + row - tok[k] * nh;
+      const int which = hh >= p.heads[0];
+      const int h = hh - (which ? p.heads[0] : 0);
+      x[k] = static_cast<const T*>(which ? p.x[1] : p.x[0]) + (t0 + tok[k]) * (which ? p.x_ts[1] : p.x_ts[0]) +
+             h * (which ? p.x_hs[1] : p.x_hs[0]);
+      y[k] = static_cast<T*>(which ? p.y[1] : p.y[0]) + (t0 + tok[k]) * (which ? p.y_ts[1] : p.y_ts[0]) +
+             h * (which ? p.y_hs[1] : p.y_hs[0]);
+    }
+    for (int u = tid & (lanes - 1); u < p.units; u += lanes) {
+      const bool turn = u < rot;
+      const int at0 = turn ? (HALF ? u * VEC : 2 * u * VEC) : 2 * p.half + 2 * (u - rot) * VEC;
+      const int at1 = turn && HALF ? at0 + p.half : at0 + VEC;
+      const bool two = turn || at1 + VEC <= 2 * p.half + p.rest;
+      P a[kRows], b[kRows];
+#pragma unroll
+      for (int k = 0; k < kRows; ++k) {
+        if (row0 + k * step >= rows) continue;
+        a[k] = *reinterpret_cast<const P*>(x[k] + at0);
+        if (two) b[k] = *reinterpret_cast<const P*>(x[k] + at1);
+      }
+      if (turn) {
+#pragma unroll
+        for (int k = 0; k < kRows; ++k) {
+          const float* c = cs + tok[k] * p.half + u * VEC;
+          const float* s = sn + tok[k] * p.half + u * VEC;
+          T e[2 * VEC];  // the unit's elements, pairs at (i, i + VEC) or (2 i, 2 i + 1)
+#pragma unroll
+          for (int i = 0; i < VEC; ++i) {
+            e[i] = a[k].v[i];
+            e[VEC + i] = b[k].v[i];
+          }
+#pragma unroll
+          for (int i = 0; i < VEC; ++i) {
+            const int i0 = HALF ? i : 2 * i, i1 = HALF ? VEC + i : 2 * i + 1;
+            const float x0 = ld1<T>(e[i0]), x1 = ld1<T>(e[i1]);
+            e[i0] = st1<T>(x0 * c[i] - x1 * s[i]);
+            e[i1] = st1<T>(x0 * s[i] + x1 * c[i]);
+          }
+#pragma unroll
+          for (int i = 0; i < VEC; ++i) {
+            a[k].v[i] = e[i];
+            b[k].v[i] = e[VEC + i];
           }
         }
-        *reinterpret_cast<P*>(y + at0) = oa;
-        *reinterpret_cast<P*>(y + at1) = ob;
-      } else {
-        const int at = 2 * p.half + (u - rot) * VEC;
-        *reinterpret_cast<P*>(y + at) = *reinterpret_cast<const P*>(x + at);
+      }
+#pragma unroll
+      for (int k = 0; k < kRows; ++k) {
+        if (row0 + k * step >= rows) continue;
+        *reinterpret_cast<P*>(y[k] + at0) = a[k];
+        if (two) *reinterpret_cast<P*>(y[k] + at1) = b[k];
       }
     }
   }
@@ -226,7 +250,7 @@ hum_status hum_rotary(const hum_rotary_desc* d, int64_t num_tokens, const int64_
   p.tokens = num_tokens;
   p.half = d->rotary_dim / 2;
   p.rest = in_place ? 0 : d->head_dim - d->rotary_dim;
-  p.units = p.half / v + p.rest / v;
+  p.units = p.half / v + (p.rest / v + 1) / 2;
   while (p.lane_shift < 8 && (1 << p.lane_shift) < p.units) ++p.lane_shift;
   p.factor = d->factor;
   p.sign = d->inverse ? -1.0f : 1.0f;
