@@ -13,43 +13,43 @@ namespace hum {
 
 struct KvMoveParams {
   uint8_t* cache;
-  int64_t unit;       // bytes of a (page, head) unit
-  int64_t slots_all;  // num_pages * page_size
+  uint32_t unit;         // bytes of a (page, head) unit
+  uint32_t page_stride;  // bytes of a page
+  int64_t slots_all;     // num_pages * page_size
   int32_t heads, page_shift;
   int64_t tokens;
-  int32_t tok_per_wg;  // tokens of a workgroup
-  int32_t head_step;   // rows (K's heads, then V's) of a token that a workgroup takes (grid.y slices them)
+  int32_t rows_wg;   // rows (K's heads, then V's) of a token that a workgroup takes; grid.y slices them
+  int32_t tok_pass;  // tokens whose rows a workgroup moves at once
+  int32_t passes;    // and how often it does
   const int64_t* slots;
   const uint16_t* x[2];  // write: k, v
   int64_t ts[2], hs[2];
   uint16_t* out[2];  // read: k, v, contiguous
 };
 
-constexpr int kMoveRows = 4;  // rows whose loads a thread has in flight at once
+constexpr int kMoveRows = 4;  // tokens whose rows a thread has in flight at once
 
-// A workgroup's rows, and a lane's place in one: which token, K or V, head.
+// A thread's place: the same head of K or V, and the same 8 of its values,
+// for every token it moves (what would otherwise be an index calculation per
+// row bounds these kernels: they have one to four bytes to move per
+// instruction).
 template <int D>
-struct KvRows {
+struct KvPlace {
   static constexpr int kLanes = D / 8;
-  static constexpr int kStep = 256 / kLanes;  // rows at once
-  int64_t t0;
-  int32_t r0, nr, rows, lane;
-  float inv_nr;
-  __device__ __forceinline__ KvRows(const KvMoveParams& p) {
-    t0 = (int64_t)blockIdx.x * p.tok_per_wg;
-    const int nt = (int)(p.tokens - t0 < p.tok_per_wg ? p.tokens - t0 : p.tok_per_wg);
-    r0 = (int)blockIdx.y * p.head_step;
-    nr = 2 * p.heads - r0 < p.head_step ? 2 * p.heads - r0 : p.head_step;
-    rows = nt * nr;
-    inv_nr = 1.0f / (float)nr;  // rows below 2^17: (row + 1/2) inv_nr is never a whole step off
+  int64_t t0;      // its first token
+  int32_t tokens;  // how many, tok_pass apart (none for a thread without a row)
+  int32_t which, head, lane;
+  __device__ __forceinline__ KvPlace(const KvMoveParams& p) {
+    const int row = threadIdx.x / kLanes;
     lane = threadIdx.x % kLanes;
-  }
-  __device__ __forceinline__ void place(const KvMoveParams& p, int row, int64_t* token, int* which, int* head) const {
-    const int t = (int)(((float)row + 0.5f) * inv_nr);
-    const int r = r0 + row - t * nr;
-    *token = t0 + t;
-    *which = r >= p.heads;
-    *head = r - *which * p.heads;
+    const int tt = (int)((uint32_t)row / (uint32_t)p.rows_wg);
+    const int r = (int)blockIdx.y * p.rows_wg + row - tt * p.rows_wg;
+    which = r >= p.heads;
+    head = r - which * p.heads;
+    t0 = (int64_t)blockIdx.x * (p.tok_pass * p.passes) + tt;
+    const int64_t left = p.tokens - t0;  // of them, every tok_pass-th
+    const int mine = left <= 0 ? 0 : left >= (int64_t)p.tok_pass * p.passes ? p.passes : (int)((uint32_t)(left + p.tok_pass - 1) / (uint32_t)p.tok_pass);
+    tokens = tt < p.tok_pass && r < 2 * p.heads ? mine : 0;
   }
 };
 
@@ -76,41 +76,46 @@ struct KvOffsets {
 template <int FMT, int D, bool VEC>
 __global__ __launch_bounds__(256) void kv_write_kernel(const KvMoveParams p) {
   using U = KvUnit<FMT, D>;
-  const KvRows<D> me(p);
+  constexpr int kB = 8 * U::kRow / D;  // code bytes of a lane
+  const KvPlace<D> me(p);
   const int page_size = 1 << p.page_shift;
-  // (the same number of passes for every thread: a row's lanes agree)
-  for (int row0 = threadIdx.x / me.kLanes; row0 < me.rows; row0 += me.kStep * kMoveRows) {
+  const KvOffsets<FMT, D> off0(me.which, 0, page_size);
+  uint8_t* const base = p.cache + (uint64_t)me.head * p.unit;
+  const int64_t* slots = p.slots + me.t0;
+  const int64_t ts = (me.which ? p.ts[1] : p.ts[0]) * p.tok_pass;
+  const uint16_t* x = (me.which ? p.x[1] + me.t0 * p.ts[1] + me.head * p.hs[1] : p.x[0] + me.t0 * p.ts[0] + me.head * p.hs[0]) + me.lane * 8;
+  // (every thread makes every pass: the lanes of a row exchange their maxima)
+  for (int n = 0; n < p.passes; n += kMoveRows) {
     u32x4_t v[kMoveRows];
     int64_t slot[kMoveRows];
-    int which[kMoveRows], head[kMoveRows];
 #pragma unroll
     for (int k = 0; k < kMoveRows; ++k) {
-      const int row = row0 + k * me.kStep;
       v[k] = u32x4_t{0, 0, 0, 0};
       slot[k] = -1;
-      which[k] = head[k] = 0;
-      if (row >= me.rows) continue;
-      int64_t token;
-      me.place(p, row, &token, &which[k], &head[k]);
-      slot[k] = p.slots[token];
-      const uint16_t* x = which[k] ? p.x[1] + token * p.ts[1] + head[k] * p.hs[1] : p.x[0] + token * p.ts[0] + head[k] * p.hs[0];
-      x += me.lane * 8;
-      if constexpr (VEC) {
-        v[k] = *reinterpret_cast<const u32x4_t*>(x);
-      } else {
+      if (n + k < me.tokens) {
+        slot[k] = slots[k * p.tok_pass];
+        const uint16_t* xr = x + k * ts;
+        if constexpr (VEC) {
+          v[k] = *reinterpret_cast<const u32x4_t*>(xr);
+        } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[k][i] = (uint32_t)x[2 * i] | ((uint32_t)x[2 * i + 1] << 16);
+          for (int i = 0; i < 4; ++i) v[k][i] = (uint32_t)xr[2 * i] | ((uint32_t)xr[2 * i + 1] << 16);
+        }
       }
     }
+    slots += kMoveRows * p.tok_pass;
+    x += kMoveRows * ts;
 #pragma unroll
     for (int k = 0; k < kMoveRows; ++k) {
       // (unsigned: negative slots are past the end too)
       const bool live = (uint64_t)slot[k] < (uint64_t)p.slots_all;
-      const int64_t page = live ? slot[k] >> p.page_shift : 0;
-      const KvOffsets<FMT, D> off(which[k], (int)slot[k] & (page_size - 1), page_size);
-      uint8_t* unit = p.cache + (page * p.heads + head[k]) * p.unit;
+      const uint32_t page = (uint32_t)(slot[k] >> p.page_shift);
+      const uint32_t at = (uint32_t)slot[k] & (uint32_t)(page_size - 1);
+      uint8_t* unit = base + (uint64_t)page * p.page_stride;
+      uint8_t* code = unit + (uint32_t)(off0.code + at * U::kRow + me.lane * kB);
+      uint8_t* scale = unit + (uint32_t)(off0.scale + at * (U::kMx && me.which ? 1 : U::kScale));
       if constexpr (FMT == HUM_ACT_BF16) {
-        if (live) *reinterpret_cast<u32x4_t*>(unit + off.code + me.lane * 16) = v[k];
+        if (live) *reinterpret_cast<u32x4_t*>(code) = v[k];
       } else {
         float f[8];
 #pragma unroll
@@ -129,26 +134,37 @@ __global__ __launch_bounds__(256) void kv_write_kernel(const KvMoveParams p) {
           o[0] = f32x2_to_e4m3x2(f[0] / sc, f[1] / sc) | (f32x2_to_e4m3x2(f[2] / sc, f[3] / sc) << 16);
           o[1] = f32x2_to_e4m3x2(f[4] / sc, f[5] / sc) | (f32x2_to_e4m3x2(f[6] / sc, f[7] / sc) << 16);
           if (live) {
-            *reinterpret_cast<u32x2_t*>(unit + off.code + me.lane * 8) = o;
-            if (me.lane == 0) *reinterpret_cast<float*>(unit + off.scale) = sc;
+            *reinterpret_cast<u32x2_t*>(code) = o;
+            if (me.lane == 0) *reinterpret_cast<float*>(scale) = sc;
           }
         } else {
           amax = quad_max(amax);  // four lanes hold one block of 32
           const int e = mx_scale_code_emax(amax, FMT == HUM_ACT_MXFP8 ? 8 : 2);
-          const float inv = mx_inv_scale(e);
+          // The hardware conversions, two floats over a power of two to two
+          // codes, nearest even.  E2M1 saturates by itself; E4M3 becomes NaN
+          // past 448, so what the rule saturates is clamped first.
+          const float sc = e8m0_to_f32((uint32_t)e);
           if (live) {
             if constexpr (FMT == HUM_ACT_MXFP8) {
-              u32x2_t o;
-              o[0] = f32x2_to_e4m3x2(f[0] * inv, f[1] * inv) | (f32x2_to_e4m3x2(f[2] * inv, f[3] * inv) << 16);
-              o[1] = f32x2_to_e4m3x2(f[4] * inv, f[5] * inv) | (f32x2_to_e4m3x2(f[6] * inv, f[7] * inv) << 16);
-              *reinterpret_cast<u32x2_t*>(unit + off.code + me.lane * 8) = o;
+              const float top = 448.0f * sc;
+              typedef short s16x2_v __attribute__((ext_vector_type(2)));
+              s16x2_v o[2] = {{0, 0}, {0, 0}};
+#pragma unroll
+              for (int i = 0; i < 8; ++i) f[i] = __builtin_fminf(__builtin_fmaxf(f[i], -top), top);
+              o[0] = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(o[0], f[0], f[1], sc, false);
+              o[0] = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(o[0], f[2], f[3], sc, true);
+              o[1] = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(o[1], f[4], f[5], sc, false);
+              o[1] = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(o[1], f[6], f[7], sc, true);
+              *reinterpret_cast<u32x2_t*>(code) = u32x2_t{__builtin_bit_cast(uint32_t, o[0]), __builtin_bit_cast(uint32_t, o[1])};
             } else {
               uint32_t o = 0;
-#pragma unroll
-              for (int i = 0; i < 8; ++i) o |= f32_to_e2m1(f[i] * inv) << (4 * i);
-              *reinterpret_cast<uint32_t*>(unit + off.code + me.lane * 4) = o;
+              o = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(o, f[0], f[1], sc, 0);
+              o = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(o, f[2], f[3], sc, 1);
+              o = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(o, f[4], f[5], sc, 2);
+              o = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(o, f[6], f[7], sc, 3);
+              *reinterpret_cast<uint32_t*>(code) = o;
             }
-            if ((me.lane & 3) == 0) unit[off.scale + (me.lane >> 2) * off.scale_step] = (uint8_t)e;
+            if ((me.lane & 3) == 0) scale[(me.lane >> 2) * off0.scale_step] = (uint8_t)e;
           }
         }
       }
@@ -159,27 +175,28 @@ __global__ __launch_bounds__(256) void kv_write_kernel(const KvMoveParams p) {
 template <int FMT, int D>
 __global__ __launch_bounds__(256) void kv_read_kernel(const KvMoveParams p) {
   using U = KvUnit<FMT, D>;
-  const KvRows<D> me(p);
+  constexpr int kB = 8 * U::kRow / D;  // code bytes of a lane
+  const KvPlace<D> me(p);
   const int page_size = 1 << p.page_shift;
-  for (int row0 = threadIdx.x / me.kLanes; row0 < me.rows; row0 += me.kStep * kMoveRows) {
-    constexpr int kB = 8 * U::kRow / D;  // code bytes of a lane
+  const KvOffsets<FMT, D> off0(me.which, 0, page_size);
+  const uint8_t* const base = p.cache + (uint64_t)me.head * p.unit;
+  const int64_t* slots = p.slots + me.t0;
+  const int64_t os = (int64_t)p.tok_pass * p.heads * D;
+  uint16_t* out = (me.which ? p.out[1] : p.out[0]) + (me.t0 * p.heads + me.head) * D + me.lane * 8;
+  for (int n = 0; n < me.tokens; n += kMoveRows) {
     uint32_t w[kMoveRows][kB / 4];
-    float sc[kMoveRows];
-    int64_t slot[kMoveRows], token[kMoveRows];
-    int which[kMoveRows], head[kMoveRows];
+    uint32_t sc[kMoveRows];
+    bool live[kMoveRows];
 #pragma unroll
     for (int k = 0; k < kMoveRows; ++k) {
-      const int row = row0 + k * me.kStep < me.rows ? row0 + k * me.kStep : row0;
-      me.place(p, row, &token[k], &which[k], &head[k]);
-      slot[k] = p.slots[token[k]];
-    }
-#pragma unroll
-    for (int k = 0; k < kMoveRows; ++k) {
+      const int64_t slot = slots[n + k < me.tokens ? k * p.tok_pass : 0];
+      live[k] = (uint64_t)slot < (uint64_t)p.slots_all;
       // (a slot outside the cache: read slot 0, write zeros)
-      const int64_t s = (uint64_t)slot[k] < (uint64_t)p.slots_all ? slot[k] : 0;
-      const KvOffsets<FMT, D> off(which[k], (int)s & (page_size - 1), page_size);
-      const uint8_t* unit = p.cache + ((s >> p.page_shift) * p.heads + head[k]) * p.unit;
-      const uint8_t* code = unit + off.code + me.lane * kB;
+      const uint32_t page = live[k] ? (uint32_t)(slot >> p.page_shift) : 0u;
+      const uint32_t at = live[k] ? (uint32_t)slot & (uint32_t)(page_size - 1) : 0u;
+      const uint8_t* unit = base + (uint64_t)page * p.page_stride;
+      const uint8_t* code = unit + (uint32_t)(off0.code + at * U::kRow + me.lane * kB);
+      const uint8_t* scale = unit + (uint32_t)(off0.scale + at * (U::kMx && me.which ? 1 : U::kScale));
       if constexpr (kB == 16) {
         const u32x4_t c = *reinterpret_cast<const u32x4_t*>(code);
 #pragma unroll
@@ -191,12 +208,12 @@ __global__ __launch_bounds__(256) void kv_read_kernel(const KvMoveParams p) {
       } else {
         w[k][0] = *reinterpret_cast<const uint32_t*>(code);
       }
-      if constexpr (FMT == HUM_ACT_FP8_TOKEN) sc[k] = *reinterpret_cast<const float*>(unit + off.scale);
-      if constexpr (U::kMx) sc[k] = __uint_as_float(unit[off.scale + (me.lane >> 2) * off.scale_step]);
+      if constexpr (FMT == HUM_ACT_FP8_TOKEN) sc[k] = *reinterpret_cast<const uint32_t*>(scale);
+      if constexpr (U::kMx) sc[k] = scale[(me.lane >> 2) * off0.scale_step];
     }
 #pragma unroll
     for (int k = 0; k < kMoveRows; ++k) {
-      if (row0 + k * me.kStep >= me.rows) continue;
+      if (n + k >= me.tokens) break;
       u32x4_t o;
       if constexpr (FMT == HUM_ACT_BF16) {
         o = u32x4_t{w[k][0], w[k][1], w[k][2], w[k][3]};
@@ -204,14 +221,16 @@ __global__ __launch_bounds__(256) void kv_read_kernel(const KvMoveParams p) {
         // codes as exact bf16, then one f32 product with the scale, rounded once
         if constexpr (FMT == HUM_ACT_MXFP4) o = e2m1x8_to_bf16(w[k][0], 1.0f);
         else o = e4m3x8_to_bf16(u32x2_t{w[k][0], w[k][1]}, 1.0f);
-        const float s = U::kMx ? e8m0_to_f32(__float_as_uint(sc[k])) : sc[k];
+        const float s = U::kMx ? e8m0_to_f32(sc[k]) : __uint_as_float(sc[k]);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
           o[i] = f32x2_to_bf16x2_bits(bf16_bits_to_f32(o[i] & 0xFFFF) * s, bf16_bits_to_f32(o[i] >> 16) * s);
       }
-      if ((uint64_t)slot[k] >= (uint64_t)p.slots_all) o = u32x4_t{0, 0, 0, 0};
-      *reinterpret_cast<u32x4_t*>((which[k] ? p.out[1] : p.out[0]) + (token[k] * p.heads + head[k]) * D + me.lane * 8) = o;
+      if (!live[k]) o = u32x4_t{0, 0, 0, 0};
+      *reinterpret_cast<u32x4_t*>(out + k * os) = o;
     }
+    slots += kMoveRows * p.tok_pass;
+    out += kMoveRows * os;
   }
 }
 
@@ -249,7 +268,8 @@ static hum_status kv_move_params(const hum_kv_desc* d, const void* cache, size_t
   // (a grid holds at most 2^32 - 1 threads)
   if (num_tokens >= (int64_t)1 << 24) return set_error(HUM_ERR_UNSUPPORTED, "at most 2^24 - 1 tokens in a call");
   p->cache = static_cast<uint8_t*>(const_cast<void*>(cache));
-  p->unit = l.unit;
+  p->unit = (uint32_t)l.unit;
+  p->page_stride = (uint32_t)(l.unit * d->num_kv_heads);
   p->slots_all = d->num_pages * d->page_size;
   p->heads = d->num_kv_heads;
   p->page_shift = __builtin_ctz((unsigned)d->page_size);
@@ -258,17 +278,29 @@ static hum_status kv_move_params(const hum_kv_desc* d, const void* cache, size_t
   return HUM_OK;
 }
 
-// Workgroups: kMoveRows passes of rows each, fewer where the rows would
-// otherwise leave compute units without one (a token's rows are cut over
-// grid.y if need be).
+// Workgroups: the rows of a token are sliced so that as few threads as
+// possible are left without one; kMoveRows passes each, fewer where the
+// tokens would otherwise leave compute units without a workgroup.
 static dim3 kv_move_grid(const hum_kv_desc* d, KvMoveParams* p) {
-  const int64_t per_tok = 2 * d->num_kv_heads, step = 256 / (d->head_dim / 8);
-  int64_t rows = step * kMoveRows;
-  while (rows > step && p->tokens * per_tok / rows < 1024) rows /= 2;
-  p->tok_per_wg = (int32_t)(rows >= per_tok ? rows / per_tok : 1);
-  p->head_step = (int32_t)(rows >= per_tok ? per_tok : rows);
-  return dim3((unsigned)((p->tokens + p->tok_per_wg - 1) / p->tok_per_wg),
-              (unsigned)((per_tok + p->head_step - 1) / p->head_step));
+  const int all = 2 * d->num_kv_heads, step = 256 / (d->head_dim / 8);
+  int best = 0;
+  double best_use = 0.0;
+  for (int y = (all + step - 1) / step; y <= all; ++y) {
+    const int rows = (all + y - 1) / y, slices = (all + rows - 1) / rows;
+    const double use = (double)(step / rows) * all / ((double)step * slices);
+    if (use > best_use + 1e-9) {
+      best_use = use;
+      best = rows;
+    }
+    if (use > 0.9) break;
+  }
+  p->rows_wg = best;
+  p->tok_pass = step / best;
+  const int64_t slices = (all + best - 1) / best;
+  p->passes = kMoveRows;
+  while (p->passes > 1 && p->tokens * slices / (p->tok_pass * p->passes) < 1024) p->passes /= 2;
+  const int64_t tok = (int64_t)p->tok_pass * p->passes;
+  return dim3((unsigned)((p->tokens + tok - 1) / tok), (unsigned)slices);
 }
 
 }  // namespace hum
