@@ -50,6 +50,7 @@ struct KvAttnParams {
   const int32_t* table;
   int64_t table_stride;
   int32_t max_pages, batch, window;
+  int32_t small;  // the call's tiles times its workgroups fit in 32 bits, whatever the lengths
   const int32_t* seq_lens;
   float scale_log2;  // scale * log2(e)
   uint16_t* out;
@@ -159,6 +160,22 @@ struct AttnItem {
   }
 };
 
+// Inclusive sum over the wave's lanes: inside each row of 16, then row 0's
+// and row 2's totals into the next row, then the lower half's into the upper.
+__device__ __forceinline__ uint32_t wave_scan_add(uint32_t v) {
+  auto add = [&](auto ctrl, auto rows) {
+    v += (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, decltype(ctrl)::value, decltype(rows)::value, 0xF, false);
+  };
+  using std::integral_constant;
+  add(integral_constant<int, 0x111>{}, integral_constant<int, 0xF>{});  // row_shr:1
+  add(integral_constant<int, 0x112>{}, integral_constant<int, 0xF>{});
+  add(integral_constant<int, 0x114>{}, integral_constant<int, 0xF>{});
+  add(integral_constant<int, 0x118>{}, integral_constant<int, 0xF>{});
+  add(integral_constant<int, 0x142>{}, integral_constant<int, 0xA>{});  // row_bcast:15
+  add(integral_constant<int, 0x143>{}, integral_constant<int, 0xC>{});  // row_bcast:31
+  return v;
+}
+
 __device__ __forceinline__ int64_t uniform64(int64_t v) {
   return ((int64_t)__builtin_amdgcn_readfirstlane((int)(v >> 32)) << 32) |
          (uint32_t)__builtin_amdgcn_readfirstlane((int)v);
@@ -177,27 +194,40 @@ __global__ __launch_bounds__(256, FMT == HUM_ACT_BF16 && D == 256 ? 1 : 2) void 
 
   // ---- this workgroup's share ------------------------------------------------
   // Lane i sums the tiles of a run of sequences; a scan over the lanes places
-  // the share's first tile in one run, which is then walked.
+  // the share's first tile in one run, which is then walked.  (What this
+  // costs is latency before the first load: the lengths are read once, the
+  // scan stays in registers, 32-bit arithmetic wherever the call's sizes allow
+  // it.)
   const int items_per_seq = p.kv_heads * p.head_tiles;
   const int run = (p.batch + 63) / 64;
+  int32_t len = 0;  // of the lane's last sequence: the only one in batches of up to 64
   int64_t mine = 0;
   for (int i = 0; i < run; ++i) {
     const int b = lane * run + i;
-    if (b < p.batch) mine += SeqSpan(p, p.seq_lens[b]).tiles;
+    if (b < p.batch) {
+      len = p.seq_lens[b];
+      mine += SeqSpan(p, len).tiles;
+    }
   }
-  int64_t upto = mine;  // inclusive scan
+  int64_t upto, total;  // inclusive scan
+  if (p.small) {
+    const uint32_t u = wave_scan_add((uint32_t)mine);
+    upto = u;
+    total = (uint32_t)__builtin_amdgcn_readlane((int)u, 63) * (uint32_t)items_per_seq;
+  } else {
+    upto = mine;
 #pragma unroll
-  for (int w = 1; w < 64; w *= 2) {
-    const int64_t o = __shfl_up(upto, w);
-    if (lane >= w) upto += o;
+    for (int w = 1; w < 64; w *= 2) {
+      const int64_t o = __shfl_up(upto, w);
+      if (lane >= w) upto += o;
+    }
+    total = uniform64(__shfl(upto, 63)) * items_per_seq;
   }
-  const int64_t total = uniform64(__shfl(upto, 63)) * items_per_seq;
   // (no more workgroups than tiles: every share that counts is non-empty)
   const int64_t nwg = total < (int64_t)gridDim.x ? total : (int64_t)gridDim.x, wg = blockIdx.x;
   if (wg >= nwg) return;
-  const bool small = total < ((int64_t)1 << 22);  // 32-bit divisions where the products fit
   int64_t pos, end;
-  if (small) {
+  if (p.small) {
     pos = (uint32_t)(wg * total) / (uint32_t)nwg;
     end = (uint32_t)((wg + 1) * total) / (uint32_t)nwg;
   } else {
@@ -206,24 +236,30 @@ __global__ __launch_bounds__(256, FMT == HUM_ACT_BF16 && D == 256 ? 1 : 2) void 
   }
   pos = uniform64(pos);
   end = uniform64(end);
+  auto length_of = [&](int b) -> int32_t {
+    return run == 1 ? __builtin_amdgcn_readlane(len, b & 63) : p.seq_lens[b];
+  };
   auto first_item = [&]() {
-    const uint64_t past = __ballot(upto * items_per_seq > pos);
+    const uint64_t past = p.small ? __ballot((uint32_t)upto * (uint32_t)items_per_seq > (uint32_t)pos)
+                                  : __ballot(upto * items_per_seq > pos);
     const int run_lane = __builtin_ctzll(past);
-    int64_t begin = uniform64(__shfl(upto - mine, run_lane)) * items_per_seq;  // first tile of sequence b
+    int64_t begin;  // first tile of sequence b
+    if (p.small) begin = (uint32_t)__builtin_amdgcn_readlane((int)(upto - mine), run_lane) * (uint32_t)items_per_seq;
+    else begin = uniform64(__shfl(upto - mine, run_lane)) * items_per_seq;
     int b = run_lane * run;
-    SeqSpan seq(p, p.seq_lens[b]);
+    SeqSpan seq(p, length_of(b));
     while (begin + (int64_t)seq.tiles * items_per_seq <= pos) {
       begin += (int64_t)seq.tiles * items_per_seq;
-      seq = SeqSpan(p, p.seq_lens[++b]);
+      seq = SeqSpan(p, length_of(++b));
     }
     const int64_t rel = pos - begin;
     const int item = rel < ((int64_t)1 << 32) ? (int)((uint32_t)rel / (uint32_t)seq.tiles) : (int)(rel / seq.tiles);
     const int tile = (int)(rel - (int64_t)item * seq.tiles);
-    const int hk = (int)((uint32_t)item / (uint32_t)p.head_tiles);
+    const int hk = p.head_tiles == 1 ? item : (int)((uint32_t)item / (uint32_t)p.head_tiles);
     return AttnItem(p, b, hk, item - hk * p.head_tiles, seq, tile, end - pos, wave);
   };
   AttnItem cur = first_item();
-  int32_t len_after = p.seq_lens[cur.b + 1 < p.batch ? cur.b + 1 : cur.b];  // of the next sequence, loaded ahead
+  int32_t len_after = length_of(cur.b + 1 < p.batch ? cur.b + 1 : cur.b);  // of the next sequence, loaded ahead
 
   __shared__ float s_m[4][16], s_l[4][16];
   __shared__ float s_o[4][16][D + 4];
@@ -341,7 +377,7 @@ __global__ __launch_bounds__(256, FMT == HUM_ACT_BF16 && D == 256 ? 1 : 2) void 
           hk = 0;
           ++b;
           seq = SeqSpan(p, len_after);
-          len_after = p.seq_lens[b + 1 < p.batch ? b + 1 : b];
+          len_after = length_of(b + 1 < p.batch ? b + 1 : b);
         }
       }
       nxt = AttnItem(p, b, hk, ht, seq, 0, left, wave);
@@ -543,7 +579,7 @@ __global__ __launch_bounds__(256, FMT == HUM_ACT_BF16 && D == 256 ? 1 : 2) void 
       // many parts one after the other.
       const int64_t begin = pos - cur.tile;
       int64_t first, last;
-      if (small) {
+      if (p.small) {
         first = ((uint32_t)((begin + 1) * nwg) - 1u) / (uint32_t)total;
         last = ((uint32_t)((begin + cur.seq.tiles) * nwg) - 1u) / (uint32_t)total;
       } else {
@@ -767,6 +803,10 @@ hum_status hum_kv_attention(const hum_kv_desc* desc, const void* cache, size_t c
   p.batch = (int32_t)batch;
   p.window = (int32_t)(window < ((int64_t)1 << 30) ? window : (int64_t)1 << 30);
   p.seq_lens = seq_lens;
+  {
+    const int64_t all = batch * p.kv_heads * p.head_tiles, tiles = max_pages * desc->page_size / kTile + 1;
+    p.small = all < ((int64_t)1 << 31) / (tiles * kAttnWgs);
+  }
   p.scale_log2 = (float)((double)scale * 1.4426950408889634);
   p.out = static_cast<uint16_t*>(out_bf16);
   p.lse = lse;
