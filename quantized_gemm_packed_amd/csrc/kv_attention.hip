@@ -46,7 +46,6 @@ struct KvAttnParams {
   int32_t num_pages, kv_heads, group, head_tiles, page_shift;  // group: query heads per key-value head
   const uint16_t* q;
   int64_t q_ts, q_hs;
-  int32_t q_vec;  // rows of q are 16-byte aligned
   const int32_t* table;
   int64_t table_stride;
   int32_t max_pages, batch, window;
@@ -138,26 +137,19 @@ struct SeqSpan {
   }
 };
 
-// The tiles [tile, tile_end) of one (sequence, key-value head, 16 query
-// heads) that a workgroup takes, and those [t, t_end) of them in which its
-// wave has tokens.
+// One (sequence, key-value head, 16 query heads).
 struct AttnItem {
-  int32_t b, hk, ht, tile, tile_end, t, t_end, wave_first;
+  int32_t b, hk, ht;
   SeqSpan seq;
-  const int32_t* table;
-  const uint8_t* base;  // the head's unit of page 0
-  __device__ __forceinline__ AttnItem(const KvAttnParams& p, int32_t b_, int32_t hk_, int32_t ht_, SeqSpan s, int32_t tile_,
-                                      int64_t left, int wave)
-      : b(b_), hk(hk_), ht(ht_), tile(tile_), seq(s) {
-    tile_end = seq.tiles - tile < left ? seq.tiles : tile + (int32_t)left;
-    t = tile;
-    t_end = tile_end;
-    wave_first = seq.first + wave * 32;
-    if (t < t_end && wave_first + t * kTile + 32 <= seq.lo) ++t;
-    if (t < t_end && wave_first + (t_end - 1) * kTile >= seq.n) --t_end;
-    table = p.table + b * p.table_stride;
-    base = p.cache + (int64_t)hk * p.unit;
-  }
+};
+
+// Scalar loads: the lengths and the block table do not change under the call.
+typedef const __attribute__((address_space(4))) int32_t* scalar_i32_t;
+__device__ __forceinline__ scalar_i32_t scalar_ptr(const int32_t* p) { return (scalar_i32_t)(uintptr_t)p; }
+
+// 16 bytes at any 2-byte boundary.
+struct __attribute__((packed, aligned(2))) Bytes16 {
+  uint32_t w[4];
 };
 
 // Inclusive sum over the wave's lanes: inside each row of 16, then row 0's
@@ -237,8 +229,9 @@ __global__ __launch_bounds__(256, FMT == HUM_ACT_BF16 && D == 256 ? 1 : 2) void 
   pos = uniform64(pos);
   end = uniform64(end);
   auto length_of = [&](int b) -> int32_t {
-    return run == 1 ? __builtin_amdgcn_readlane(len, b & 63) : p.seq_lens[b];
+    return run == 1 ? __builtin_amdgcn_readlane(len, b & 63) : scalar_ptr(p.seq_lens)[b];
   };
+  int tile;  // of the first item
   auto first_item = [&]() {
     const uint64_t past = p.small ? __ballot((uint32_t)upto * (uint32_t)items_per_seq > (uint32_t)pos)
                                   : __ballot(upto * items_per_seq > pos);
@@ -254,148 +247,194 @@ __global__ __launch_bounds__(256, FMT == HUM_ACT_BF16 && D == 256 ? 1 : 2) void 
     }
     const int64_t rel = pos - begin;
     const int item = rel < ((int64_t)1 << 32) ? (int)((uint32_t)rel / (uint32_t)seq.tiles) : (int)(rel / seq.tiles);
-    const int tile = (int)(rel - (int64_t)item * seq.tiles);
+    tile = (int)(rel - (int64_t)item * seq.tiles);
     const int hk = p.head_tiles == 1 ? item : (int)((uint32_t)item / (uint32_t)p.head_tiles);
-    return AttnItem(p, b, hk, item - hk * p.head_tiles, seq, tile, end - pos, wave);
+    return AttnItem{b, hk, item - hk * p.head_tiles, seq};
+  };
+  auto next_item = [&](AttnItem& i) {
+    if (++i.ht == p.head_tiles) {
+      i.ht = 0;
+      if (++i.hk == p.kv_heads) {
+        i.hk = 0;
+        ++i.b;
+        i.seq = SeqSpan(p, length_of(i.b));
+      }
+    }
   };
   AttnItem cur = first_item();
-  int32_t len_after = length_of(cur.b + 1 < p.batch ? cur.b + 1 : cur.b);  // of the next sequence, loaded ahead
 
-  __shared__ float s_m[4][16], s_l[4][16];
+  __shared__ float s_m[2][4][16], s_l[2][4][16];
   __shared__ float s_o[4][16][D + 4];
+  __shared__ __attribute__((aligned(16))) uint16_t s_q[16][D + 8];
   __shared__ int s_last;
 
+  // ---- loads ---------------------------------------------------------------
+  // Every wave has one tile in registers and the next in flight.  The number
+  // of loads between two points of the loop is fixed (a tile with nothing in
+  // it reads page 0, which stays in the L2; page numbers are scalar), so that
+  // the wait for K leaves V in flight, and the wait for V the next K.
   const uint32_t page_stride = (uint32_t)p.kv_heads * (uint32_t)p.unit;
   const int kg = (lane >> 2) & 3;  // the granule of 8 tokens this lane's K rows lie in
-  auto page_of = [&](const AttnItem& w, int32_t tok) -> int32_t {
-    int32_t i = tok >> p.page_shift;
-    i = i < p.max_pages ? i : p.max_pages - 1;
-    return w.table[i];
-  };
-  // a page outside the cache: read page 0 instead, its tokens are masked
-  auto unit_of = [&](const uint8_t* base, int32_t page) -> const uint8_t* {
-    const uint32_t pg = (uint32_t)page < (uint32_t)p.num_pages ? (uint32_t)page : 0u;
-    return base + (uint64_t)pg * page_stride;
-  };
+  const uint32_t in_k = (uint32_t)(kg * 8 + (lane & 3)) & (uint32_t)(page_size - 1);
+  const uint32_t in_v = (uint32_t)(kq * 8) & (uint32_t)(page_size - 1);
+  const uint32_t off_k = in_k * T::kRow + kq * T::kKB;
+  const uint32_t off_v = ((uint32_t)page_size + in_v) * T::kRow + r * T::kVB;
+  const uint32_t scales = 2u * (uint32_t)page_size * T::kRow;
 
-  u32x4_t qf[T::kChunks];
   uint32_t kw[2][T::kKL][T::kKB / 4];
   uint32_t ks[2][2];  // MX: scale bytes of the two K rows
   uint32_t vw[8][T::kVN][T::kVW];
   uint32_t vs[T::kVN][2];  // MX: scale bytes of the 8 tokens
   float kf[8], vf[8];      // FP8: row scales of the 8 tokens
 
-  // The query rows as MFMA B operands: column = head r, steps = the elements
-  // that a lane's K loads bring.
-  auto load_q = [&](const AttnItem& w) {
-    const int live = p.group - w.ht * 16;
-    const uint16_t* q = p.q + w.b * p.q_ts + (int64_t)(w.hk * p.group + w.ht * 16 + (r < live ? r : 0)) * p.q_hs;
-#pragma unroll
-    for (int c = 0; c < T::kChunks; ++c) {
-      constexpr int kPer = T::kKE / 8;
-      const int d0 = (c / kPer) * 4 * T::kKE + kq * T::kKE + (c % kPer) * 8;
-      if (p.q_vec) {
-        qf[c] = *reinterpret_cast<const u32x4_t*>(q + d0);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) qf[c][i] = (uint32_t)q[d0 + 2 * i] | ((uint32_t)q[d0 + 2 * i + 1] << 16);
-      }
-    }
+  // A tile on its way: the units its two halves of 16 tokens lie in.
+  struct Fetch {
+    int32_t t0;
+    const uint8_t *u0, *u1;
+    bool ok0, ok1;
   };
-  auto load_k = [&](int32_t t0, const uint8_t* unit) {
+  auto load_k = [&](const Fetch& f) {
+    const uint8_t* u = kg >= 2 ? f.u1 : f.u0;
+    const uint32_t in = (uint32_t)f.t0 & (uint32_t)(page_size - 1);
+    const uint8_t* row = u + (in * T::kRow + off_k);
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
-      const int at = (t0 + kg * 8 + s * 4 + (lane & 3)) & (page_size - 1);
-      const uint8_t* row = unit + at * T::kRow + kq * T::kKB;
 #pragma unroll
-      for (int j = 0; j < T::kKL; ++j) load_bytes<T::kKB>(row + j * 4 * T::kKB, kw[s][j]);
-      if constexpr (U::kMx) load_bytes<U::kScale>(unit + 2 * page_size * T::kRow + at * U::kScale, ks[s]);
+      for (int j = 0; j < T::kKL; ++j) load_bytes<T::kKB>(row + s * 4 * T::kRow + j * 4 * T::kKB, kw[s][j]);
+      if constexpr (U::kMx) load_bytes<U::kScale>(u + (scales + (in + in_k + s * 4) * U::kScale), ks[s]);
+    }
+    if constexpr (kFp8) {  // (of the tokens whose scores the lane receives)
+      const uint8_t* sc = (kq >= 2 ? f.u1 : f.u0) + (scales + (in + in_v) * 4);
+      load_bytes<16>(sc, reinterpret_cast<uint32_t*>(kf));
+      load_bytes<16>(sc + 16, reinterpret_cast<uint32_t*>(kf + 4));
     }
   };
-  auto load_v = [&](int32_t t0, const uint8_t* unit) {
-    const int at = (t0 + kq * 8) & (page_size - 1);
-    const uint8_t* row = unit + (page_size + at) * T::kRow + r * T::kVB;
+  auto load_v = [&](const Fetch& f) {
+    const uint8_t* u = kq >= 2 ? f.u1 : f.u0;
+    const uint32_t in = (uint32_t)f.t0 & (uint32_t)(page_size - 1);
+    const uint8_t* row = u + (in * T::kRow + off_v);
 #pragma unroll
     for (int i = 0; i < 8; ++i)
 #pragma unroll
       for (int j = 0; j < T::kVN; ++j) load_bytes<T::kVB>(row + i * T::kRow + j * 16 * T::kVB, vw[i][j]);
-    const uint8_t* scales = unit + 2 * page_size * T::kRow;
     if constexpr (kFp8) {
-      load_bytes<16>(scales + at * 4, reinterpret_cast<uint32_t*>(kf));
-      load_bytes<16>(scales + at * 4 + 16, reinterpret_cast<uint32_t*>(kf + 4));
-      load_bytes<16>(scales + (page_size + at) * 4, reinterpret_cast<uint32_t*>(vf));
-      load_bytes<16>(scales + (page_size + at) * 4 + 16, reinterpret_cast<uint32_t*>(vf + 4));
+      const uint8_t* sc = u + (scales + (page_size + in + in_v) * 4);
+      load_bytes<16>(sc, reinterpret_cast<uint32_t*>(vf));
+      load_bytes<16>(sc + 16, reinterpret_cast<uint32_t*>(vf + 4));
     }
     if constexpr (U::kMx) {
+      const uint8_t* sc = u + (scales + (U::kScale + (r * T::kVE) / 32) * page_size + in + in_v);
 #pragma unroll
-      for (int j = 0; j < T::kVN; ++j) {
-        const int g = j * 4 + (r * T::kVE) / 32;
-        load_bytes<8>(scales + (U::kScale + g) * page_size + at, vs[j]);
-      }
+      for (int j = 0; j < T::kVN; ++j) load_bytes<8>(sc + j * 4 * page_size, vs[j]);
     }
   };
 
-  // Pages of the tile in flight (V's lanes, K's lanes) and of the one after.
-  int32_t page_v = 0, page_k = 0, page2_v = 0, page2_k = 0;
-  auto first_pages = [&](const AttnItem& w, int32_t& v, int32_t& k, int32_t& v2, int32_t& k2) {
-    if (w.t < w.t_end) {
-      const int32_t t0 = w.wave_first + w.t * kTile;
-      v = page_of(w, t0 + kq * 8);
-      k = page_of(w, t0 + kg * 8);
-      if (w.t + 1 < w.t_end) {
-        v2 = page_of(w, t0 + kTile + kq * 8);
-        k2 = page_of(w, t0 + kTile + kg * 8);
+  // The fetch runs two tiles ahead of the arithmetic, through the items:
+  // page numbers of one tile, then its K and V.
+  AttnItem ft = cur;
+  int ft_tile = tile;
+  int64_t ft_left = end - pos;
+  struct Pages {
+    int32_t t0, lo, p0, p1;
+    const uint8_t* base;
+  };
+  auto fetch_pages = [&]() -> Pages {
+    Pages g;
+    g.t0 = ft.seq.first + wave * 32 + ft_tile * kTile;
+    g.lo = ft.seq.lo;
+    g.base = p.cache + (int64_t)ft.hk * p.unit;
+    g.p0 = g.p1 = -1;
+    if (ft_left > 0) {
+      const scalar_i32_t table = scalar_ptr(p.table + ft.b * p.table_stride);
+      if (g.t0 < ft.seq.n) g.p0 = table[g.t0 >> p.page_shift];
+      if (g.t0 + 16 < ft.seq.n) g.p1 = table[(g.t0 + 16) >> p.page_shift];
+      --ft_left;
+      if (++ft_tile == ft.seq.tiles && ft_left > 0) {
+        ft_tile = 0;
+        next_item(ft);
       }
     }
+    return g;
   };
-  auto load_first = [&](const AttnItem& w, int32_t v, int32_t k) {
-    load_q(w);
-    if (w.t < w.t_end) {
-      const int32_t t0 = w.wave_first + w.t * kTile;
-      load_k(t0, unit_of(w.base, k));
-      load_v(t0, unit_of(w.base, v));
+  // a page outside the cache, or none: read page 0 instead, masked
+  auto resolve = [&](const Pages& g) -> Fetch {
+    Fetch f;
+    f.t0 = g.t0;
+    f.ok0 = (uint32_t)g.p0 < (uint32_t)p.num_pages && g.t0 + 16 > g.lo;
+    f.ok1 = (uint32_t)g.p1 < (uint32_t)p.num_pages && g.t0 + 32 > g.lo;
+    f.u0 = g.base + (uint64_t)(f.ok0 ? (uint32_t)g.p0 : 0u) * page_stride;
+    f.u1 = g.base + (uint64_t)(f.ok1 ? (uint32_t)g.p1 : 0u) * page_stride;
+    return f;
+  };
+
+  // The query rows go through LDS: the next item's are loaded while this one
+  // runs and stored when it ends.
+  constexpr int kQN = D == 256 ? 2 : 1;  // 16-byte pieces of a thread
+  u32x4_t qn[kQN];
+  auto load_q = [&](const AttnItem& w) {
+    const int live = p.group - w.ht * 16 < 16 ? p.group - w.ht * 16 : 16;
+    const uint16_t* q = p.q + w.b * p.q_ts + (int64_t)(w.hk * p.group + w.ht * 16) * p.q_hs;
+#pragma unroll
+    for (int i = 0; i < kQN; ++i) {
+      int h = (threadIdx.x + i * 256) / (D / 8);
+      h = h < live ? h : live - 1;  // (dead columns repeat a live row and are never stored)
+      const Bytes16 v = *reinterpret_cast<const Bytes16*>(q + h * p.q_hs + (threadIdx.x % (D / 8)) * 8);
+      qn[i] = u32x4_t{v.w[0], v.w[1], v.w[2], v.w[3]};
     }
   };
-  first_pages(cur, page_v, page_k, page2_v, page2_k);
-  load_first(cur, page_v, page_k);
+  auto stage_q = [&]() {
+#pragma unroll
+    for (int i = 0; i < kQN; ++i) {
+      const int h = (threadIdx.x + i * 256) / (D / 8);
+      if (h < 16) *reinterpret_cast<u32x4_t*>(&s_q[h][(threadIdx.x % (D / 8)) * 8]) = qn[i];
+    }
+  };
+  // MFMA B operand of step c: column = head r, steps = the elements that a
+  // lane's K loads bring
+  auto q_frag = [&](int c) -> u32x4_t {
+    constexpr int kPer = T::kKE / 8;
+    const int d0 = (c / kPer) * 4 * T::kKE + kq * T::kKE + (c % kPer) * 8;
+    return *reinterpret_cast<const u32x4_t*>(&s_q[r][d0]);
+  };
+
+  load_q(cur);
+  Pages pages = fetch_pages();
+  Fetch ahead = resolve(pages);
+  pages = fetch_pages();
+  stage_q();
+  load_k(ahead);
+  load_v(ahead);
+  int buf = 0;
+  __syncthreads();
 
   while (true) {
     const int heads = p.group - cur.ht * 16 < 16 ? p.group - cur.ht * 16 : 16;  // live columns
     const int q_head = cur.hk * p.group + cur.ht * 16;
-
-    // The next item's query, pages and first tile are fetched while this one
-    // ends: short sequences would otherwise wait for memory at every item.
-    const int64_t left = end - pos - (cur.tile_end - cur.tile);
+    const int64_t share = end - pos;
+    const int tile_end = cur.seq.tiles - tile < share ? cur.seq.tiles : tile + (int)share;
+    const int64_t left = share - (tile_end - tile);
     AttnItem nxt = cur;
-    int32_t nv = 0, nk = 0, nv2 = 0, nk2 = 0;
-    if (left > 0) {
-      int32_t b = cur.b, hk = cur.hk, ht = cur.ht + 1;
-      SeqSpan seq = cur.seq;
-      if (ht == p.head_tiles) {
-        ht = 0;
-        if (++hk == p.kv_heads) {
-          hk = 0;
-          ++b;
-          seq = SeqSpan(p, len_after);
-          len_after = length_of(b + 1 < p.batch ? b + 1 : b);
-        }
-      }
-      nxt = AttnItem(p, b, hk, ht, seq, 0, left, wave);
-      first_pages(nxt, nv, nk, nv2, nk2);
+    if (left > 0) next_item(nxt);
+
+    u32x4_t qf[D == 256 ? 1 : T::kChunks];
+    if constexpr (D < 256) {
+#pragma unroll
+      for (int c = 0; c < T::kChunks; ++c) qf[c] = q_frag(c);
     }
-    const bool nxt_tiles = left > 0 && nxt.t < nxt.t_end;
+    load_q(nxt);
 
     f32x4_t acc[T::kVN * T::kVE];
 #pragma unroll
     for (int i = 0; i < T::kVN * T::kVE; ++i) acc[i] = f32x4_t{0, 0, 0, 0};
     float m = kNegInf, m_safe = 0.0f, l = 0.0f;
 
-    if (cur.t >= cur.t_end && left > 0) load_first(nxt, nv, nk);
-    for (int t = cur.t; t < cur.t_end; ++t) {
-      const int32_t t0 = cur.wave_first + t * kTile;
-      const bool more = t + 1 < cur.t_end;
-      // scores: rows 4 kq + j of sub-tile s are tokens 8 kq + 4 s + j (a dead
-      // column repeats the first head's row and is never stored)
+    int t = tile;
+    do {
+      const int32_t t0 = ahead.t0;
+      const bool ok0 = ahead.ok0, ok1 = ahead.ok1;
+      ahead = resolve(pages);
+      pages = fetch_pages();
+      // scores: rows 4 kq + j of sub-tile s are tokens 8 kq + 4 s + j
       float x[8];
 #pragma unroll
       for (int s = 0; s < 2; ++s) {
@@ -410,11 +449,12 @@ __global__ __launch_bounds__(256, FMT == HUM_ACT_BF16 && D == 256 ? 1 : 2) void 
             const int g0 = (c / kPer) * 4 * T::kKE / 32;
             sc = e8m0_to_f32((ks[s][g0 / 4] >> (8 * ((g0 & 3) + kq * T::kKE / 32))) & 0xFFu);
           }
-          u32x4_t a;
           uint32_t o[4];
           to_bf16<FMT, 8>(&kw[s][c / kPer][(c % kPer) * kW], sc, o);
-          a = u32x4_t{o[0], o[1], o[2], o[3]};
-          c4 = mfma_bf16(a, qf[c], c4);
+          u32x4_t q;
+          if constexpr (D == 256) q = q_frag(c);
+          else q = qf[c];
+          c4 = mfma_bf16(u32x4_t{o[0], o[1], o[2], o[3]}, q, c4);
         }
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -423,9 +463,8 @@ __global__ __launch_bounds__(256, FMT == HUM_ACT_BF16 && D == 256 ? 1 : 2) void 
         }
       }
       // tokens outside the span or on a page outside the cache
-      const bool page_ok = (uint32_t)page_v < (uint32_t)p.num_pages;
-      const bool whole = t0 >= cur.seq.lo && t0 + 32 <= cur.seq.n && __ballot(!page_ok) == 0;
-      if (!whole) {
+      if (!(ok0 && ok1 && t0 >= cur.seq.lo && t0 + 32 <= cur.seq.n)) {
+        const bool page_ok = kq >= 2 ? ok1 : ok0;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const int32_t tok = t0 + kq * 8 + i;
@@ -442,12 +481,7 @@ __global__ __launch_bounds__(256, FMT == HUM_ACT_BF16 && D == 256 ? 1 : 2) void 
           }
         }
       }
-      // the tile after this one: of this item or of the next
-      const bool ahead = more || nxt_tiles;
-      const int32_t t0_ahead = more ? t0 + kTile : nxt.wave_first + nxt.t * kTile;
-      const uint8_t* base_ahead = more ? cur.base : nxt.base;
-      if (ahead) load_k(t0_ahead, unit_of(base_ahead, more ? page2_k : nk));
-      if (!more && left > 0) load_q(nxt);
+      load_k(ahead);
       __builtin_amdgcn_sched_barrier(0);
       float top = x[0];
 #pragma unroll
@@ -498,27 +532,25 @@ __global__ __launch_bounds__(256, FMT == HUM_ACT_BF16 && D == 256 ? 1 : 2) void 
           acc[j * T::kVE + e] = mfma_bf16(a, pl, acc[j * T::kVE + e]);
         }
       }
-      if (ahead) load_v(t0_ahead, unit_of(base_ahead, more ? page2_v : nv));
-      if (more) {
-        page_v = page2_v;
-        if (t + 2 < cur.t_end) {
-          page2_v = page_of(cur, t0 + 2 * kTile + kq * 8);
-          page2_k = page_of(cur, t0 + 2 * kTile + kg * 8);
-        }
-      }
+      load_v(ahead);
       __builtin_amdgcn_sched_barrier(0);
-    }
+    } while (++t < tile_end);
 
     // ---- join the four waves -------------------------------------------------
+    // (s_m and s_l alternate between two buffers, s_o is written only after
+    // every wave has read it: no barrier is needed after the rows are out)
+    auto waves_m = [&](int h) {
+      return __builtin_fmaxf(__builtin_fmaxf(s_m[buf][0][h], s_m[buf][1][h]), __builtin_fmaxf(s_m[buf][2][h], s_m[buf][3][h]));
+    };
     l += __shfl_xor(l, 16);
     l += __shfl_xor(l, 32);
     if (kq == 0) {
-      s_m[wave][r] = m;
-      s_l[wave][r] = l;
+      s_m[buf][wave][r] = m;
+      s_l[buf][wave][r] = l;
     }
     __syncthreads();
     {
-      const float top = __builtin_fmaxf(__builtin_fmaxf(s_m[0][r], s_m[1][r]), __builtin_fmaxf(s_m[2][r], s_m[3][r]));
+      const float top = waves_m(r);
       const float a = m == kNegInf ? 0.0f : m == top ? 1.0f : exp2_fast(m - top);
       if (r < heads) {
         // accumulator (j, e), register i: element j * 128 + (4 kq + i) * kVE + e
@@ -537,15 +569,13 @@ __global__ __launch_bounds__(256, FMT == HUM_ACT_BF16 && D == 256 ? 1 : 2) void 
             }
       }
     }
+    stage_q();  // (every wave is past its last read of the rows)
     __syncthreads();
-    auto waves_m = [&](int h) {
-      return __builtin_fmaxf(__builtin_fmaxf(s_m[0][h], s_m[1][h]), __builtin_fmaxf(s_m[2][h], s_m[3][h]));
-    };
     auto waves_l = [&](int h, float top) {
       float sum = 0.0f;
 #pragma unroll
       for (int w = 0; w < 4; ++w)
-        sum += s_m[w][h] == kNegInf ? 0.0f : s_l[w][h] * (s_m[w][h] == top ? 1.0f : exp2_fast(s_m[w][h] - top));
+        sum += s_m[buf][w][h] == kNegInf ? 0.0f : s_l[buf][w][h] * (s_m[buf][w][h] == top ? 1.0f : exp2_fast(s_m[buf][w][h] - top));
       return sum;
     };
     auto waves_o = [&](int h, int d) {
@@ -566,7 +596,7 @@ __global__ __launch_bounds__(256, FMT == HUM_ACT_BF16 && D == 256 ? 1 : 2) void 
       *reinterpret_cast<u32x2_t*>(p.out + row * D + d) = w;
       if (d == 0 && p.lse) p.lse[row] = sum == 0.0f ? kNegInf : (top + __log2f(sum)) * 0.6931471805599453f;
     };
-    if (cur.tile == 0 && cur.tile_end == cur.seq.tiles) {
+    if (tile == 0 && tile_end == cur.seq.tiles) {
       for (int i = threadIdx.x * 4; i < heads * D; i += 1024) {
         const int h = i / D, d = i - h * D;
         const float top = waves_m(h), sum = waves_l(h, top);
@@ -577,7 +607,7 @@ __global__ __launch_bounds__(256, FMT == HUM_ACT_BF16 && D == 256 ? 1 : 2) void 
       // kJoin parts are joined by whichever arrives last; more of them first
       // in groups, whose joins are then joined, so that no workgroup reads
       // many parts one after the other.
-      const int64_t begin = pos - cur.tile;
+      const int64_t begin = pos - tile;
       int64_t first, last;
       if (p.small) {
         first = ((uint32_t)((begin + 1) * nwg) - 1u) / (uint32_t)total;
@@ -710,11 +740,9 @@ __global__ __launch_bounds__(256, FMT == HUM_ACT_BF16 && D == 256 ? 1 : 2) void 
     // ---- next item -------------------------------------------------------------
     if (left <= 0) return;
     pos = end - left;
+    tile = 0;
     cur = nxt;
-    page_v = nv;
-    page2_v = nv2;
-    page2_k = nk2;
-    __syncthreads();  // the LDS rows are read before the next item writes them
+    buf ^= 1;
   }
 }
 
@@ -796,7 +824,6 @@ hum_status hum_kv_attention(const hum_kv_desc* desc, const void* cache, size_t c
   p.q = static_cast<const uint16_t*>(q_bf16);
   p.q_ts = q_ts;
   p.q_hs = q_hs;
-  p.q_vec = reinterpret_cast<uintptr_t>(q_bf16) % 16 == 0 && (q_ts | q_hs) % 8 == 0;
   p.table = block_table;
   p.table_stride = table_stride;
   p.max_pages = (int32_t)max_pages;
