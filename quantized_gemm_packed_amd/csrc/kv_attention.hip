@@ -603,10 +603,12 @@ __global__ __launch_bounds__(256, FMT == HUM_ACT_BF16 && D == 256 ? 1 : 2) void 
         store_out(h, d, waves_o(h, d), top, sum);
       }
     } else {
-      // The workgroups first .. last hold a part of this item each.  Up to
-      // kJoin parts are joined by whichever arrives last; more of them first
-      // in groups, whose joins are then joined, so that no workgroup reads
-      // many parts one after the other.
+      // The workgroups first .. last hold a part of this item each, joined by
+      // whichever arrives last.  It reads kJoin parts per thread at once, and
+      // has threads for `lanes` parts of every element; more than two such
+      // rounds of parts are joined in groups first, whose joins are then
+      // joined (a round of reads costs about half of a level: storing, the
+      // arrival and reading again).
       const int64_t begin = pos - tile;
       int64_t first, last;
       if (p.small) {
@@ -722,10 +724,13 @@ __global__ __launch_bounds__(256, FMT == HUM_ACT_BF16 && D == 256 ? 1 : 2) void 
       }
       // counters: of an item at its first workgroup; of a group at the slot
       // of the part that leads it, after those
-      if (nseg <= kJoin) {
+      const int lanes = heads * (D / 4) >= 256 ? 1 : 256 / (heads * (D / 4));
+      const int round = kJoin * lanes;
+      if (nseg <= 2 * round) {
         if (arrive(w0, nseg)) join(0, 1, nseg, false, store_out);
       } else {
-        const int size = nseg <= 64 ? 8 : nseg <= 256 ? 16 : 32;
+        int size = 8;
+        while (size < round || size * 2 * round < nseg) size *= 2;
         const int lead = seg & ~(size - 1);
         const int members = nseg - lead < size ? nseg - lead : size;
         if (arrive(kAttnWgs + 2 * (w0 + lead) + (lead == 0 ? 1 : 0), members)) {
@@ -746,13 +751,20 @@ __global__ __launch_bounds__(256, FMT == HUM_ACT_BF16 && D == 256 ? 1 : 2) void 
   }
 }
 
-// Workgroups of a call: never more than there can be tiles.
+// Workgroups of a call: never more than there can be tiles.  One on every CU
+// where there are fewer heads (of all sequences) than kAttnWgs: fewer parts
+// to join, and a CU's four waves keep as many bytes in flight (one sequence
+// of 131072 FP8 tokens, 8 heads: 57.3 us with 512, 54.1 with 256; 48 bf16
+// sequences, 384 heads: 405 and 401).  Two with more heads, where a second
+// workgroup works while the first ends one head and begins the next (64
+// ragged sequences, 512 heads: 110 us with 512, 118 with 256; 256 short
+// ones, 4096 heads: 63 and 82).
 static int attn_wgs(const hum_kv_desc* d, int32_t num_q_heads, int64_t batch, int64_t max_pages) {
   const int64_t group = num_q_heads / d->num_kv_heads;
   const int64_t tiles = max_pages * d->page_size / kTile + 1;
   const int64_t all = batch * d->num_kv_heads * ((group + 15) / 16);
-  if (all >= kAttnWgs || all * tiles >= kAttnWgs) return kAttnWgs;
-  return (int)(all * tiles < 1 ? 1 : all * tiles);
+  if (all >= kAttnWgs) return kAttnWgs;
+  return (int)(all * tiles >= kAttnWgs / 2 ? kAttnWgs / 2 : all * tiles < 1 ? 1 : all * tiles);
 }
 
 // Heads of a slot (even: slots stay 16-byte aligned), and the slots' bytes.
