@@ -752,19 +752,24 @@ __global__ __launch_bounds__(256, FMT == HUM_ACT_BF16 && D == 256 ? 1 : 2) void 
 }
 
 // Workgroups of a call: never more than there can be tiles.  One on every CU
-// where there are fewer heads (of all sequences) than kAttnWgs: fewer parts
-// to join, and a CU's four waves keep as many bytes in flight (one sequence
-// of 131072 FP8 tokens, 8 heads: 57.3 us with 512, 54.1 with 256; 48 bf16
-// sequences, 384 heads: 405 and 401).  Two with more heads, where a second
-// workgroup works while the first ends one head and begins the next (64
-// ragged sequences, 512 heads: 110 us with 512, 118 with 256; 256 short
-// ones, 4096 heads: 63 and 82).
+// where there are fewer heads (of all sequences) than kAttnWgs and a wave's
+// tile is large enough to keep the memory busy (rows of 128 bytes and more;
+// E2M1 codes take too many instructions a byte for one wave per SIMD): fewer
+// parts to join (one sequence of 131072 FP8 tokens, 8 heads of 128: 57.3 us
+// with 512, 54.1 with 256; 48 bf16 sequences, 384 heads: 405 and 401), and
+// the bf16 kernel of 256-wide heads fits a CU once.  Two with more heads,
+// where a second workgroup works while the first ends one head and begins
+// the next (64 ragged sequences, 512 heads: 110 us with 512, 118 with 256;
+// 256 short ones, 4096 heads: 63 and 82), and with small rows (32 sequences
+// in MXFP4 of 128-wide heads, 512 MiB: 5.3 TB/s with 512, 4.0 with 256).
 static int attn_wgs(const hum_kv_desc* d, int32_t num_q_heads, int64_t batch, int64_t max_pages) {
   const int64_t group = num_q_heads / d->num_kv_heads;
   const int64_t tiles = max_pages * d->page_size / kTile + 1;
   const int64_t all = batch * d->num_kv_heads * ((group + 15) / 16);
-  if (all >= kAttnWgs) return kAttnWgs;
-  return (int)(all * tiles >= kAttnWgs / 2 ? kAttnWgs / 2 : all * tiles < 1 ? 1 : all * tiles);
+  const bool once = d->fmt == HUM_ACT_BF16 && d->head_dim == 256;
+  const bool wide = d->fmt != HUM_ACT_MXFP4 && d->head_dim * (d->fmt == HUM_ACT_BF16 ? 2 : 1) >= 128;
+  const int64_t most = once || (wide && all < kAttnWgs) ? kAttnWgs / 2 : kAttnWgs;
+  return (int)(all * tiles >= most ? most : all * tiles < 1 ? 1 : all * tiles);
 }
 
 // Heads of a slot (even: slots stay 16-byte aligned), and the slots' bytes.
