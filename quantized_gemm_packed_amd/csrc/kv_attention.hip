@@ -202,7 +202,7 @@ __global__ __launch_bounds__(256, FMT == HUM_ACT_BF16 && D == 256 ? 1 : 2) void 
     }
   }
   int64_t upto, total;  // inclusive scan
-  if (p.small) {
+  if (__builtin_expect(p.small, 1)) {
     const uint32_t u = wave_scan_add((uint32_t)mine);
     upto = u;
     total = (uint32_t)__builtin_amdgcn_readlane((int)u, 63) * (uint32_t)items_per_seq;
@@ -219,7 +219,7 @@ __global__ __launch_bounds__(256, FMT == HUM_ACT_BF16 && D == 256 ? 1 : 2) void 
   const int64_t nwg = total < (int64_t)gridDim.x ? total : (int64_t)gridDim.x, wg = blockIdx.x;
   if (wg >= nwg) return;
   int64_t pos, end;
-  if (p.small) {
+  if (__builtin_expect(p.small, 1)) {
     pos = (uint32_t)(wg * total) / (uint32_t)nwg;
     end = (uint32_t)((wg + 1) * total) / (uint32_t)nwg;
   } else {
@@ -237,7 +237,7 @@ __global__ __launch_bounds__(256, FMT == HUM_ACT_BF16 && D == 256 ? 1 : 2) void 
                                   : __ballot(upto * items_per_seq > pos);
     const int run_lane = __builtin_ctzll(past);
     int64_t begin;  // first tile of sequence b
-    if (p.small) begin = (uint32_t)__builtin_amdgcn_readlane((int)(upto - mine), run_lane) * (uint32_t)items_per_seq;
+    if (__builtin_expect(p.small, 1)) begin = (uint32_t)__builtin_amdgcn_readlane((int)(upto - mine), run_lane) * (uint32_t)items_per_seq;
     else begin = uniform64(__shfl(upto - mine, run_lane)) * items_per_seq;
     int b = run_lane * run;
     SeqSpan seq(p, length_of(b));
@@ -246,7 +246,7 @@ __global__ __launch_bounds__(256, FMT == HUM_ACT_BF16 && D == 256 ? 1 : 2) void 
       seq = SeqSpan(p, length_of(++b));
     }
     const int64_t rel = pos - begin;
-    const int item = rel < ((int64_t)1 << 32) ? (int)((uint32_t)rel / (uint32_t)seq.tiles) : (int)(rel / seq.tiles);
+    const int item = __builtin_expect(rel < ((int64_t)1 << 32), 1) ? (int)((uint32_t)rel / (uint32_t)seq.tiles) : (int)(rel / seq.tiles);
     tile = (int)(rel - (int64_t)item * seq.tiles);
     const int hk = p.head_tiles == 1 ? item : (int)((uint32_t)item / (uint32_t)p.head_tiles);
     return AttnItem{b, hk, item - hk * p.head_tiles, seq};
@@ -400,10 +400,10 @@ __global__ __launch_bounds__(256, FMT == HUM_ACT_BF16 && D == 256 ? 1 : 2) void 
   load_q(cur);
   Pages pages = fetch_pages();
   Fetch ahead = resolve(pages);
-  pages = fetch_pages();
-  stage_q();
   load_k(ahead);
   load_v(ahead);
+  pages = fetch_pages();
+  stage_q();
   int buf = 0;
   __syncthreads();
 
@@ -463,7 +463,7 @@ __global__ __launch_bounds__(256, FMT == HUM_ACT_BF16 && D == 256 ? 1 : 2) void 
         }
       }
       // tokens outside the span or on a page outside the cache
-      if (!(ok0 && ok1 && t0 >= cur.seq.lo && t0 + 32 <= cur.seq.n)) {
+      if (__builtin_expect(!(ok0 && ok1 && t0 >= cur.seq.lo && t0 + 32 <= cur.seq.n), 0)) {
         const bool page_ok = kq >= 2 ? ok1 : ok0;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
@@ -611,7 +611,7 @@ __global__ __launch_bounds__(256, FMT == HUM_ACT_BF16 && D == 256 ? 1 : 2) void 
       // arrival and reading again).
       const int64_t begin = pos - tile;
       int64_t first, last;
-      if (p.small) {
+      if (__builtin_expect(p.small, 1)) {
         first = ((uint32_t)((begin + 1) * nwg) - 1u) / (uint32_t)total;
         last = ((uint32_t)((begin + cur.seq.tiles) * nwg) - 1u) / (uint32_t)total;
       } else {
@@ -726,20 +726,28 @@ __global__ __launch_bounds__(256, FMT == HUM_ACT_BF16 && D == 256 ? 1 : 2) void 
       // of the part that leads it, after those
       const int lanes = heads * (D / 4) >= 256 ? 1 : 256 / (heads * (D / 4));
       const int round = kJoin * lanes;
-      if (nseg <= 2 * round) {
-        if (arrive(w0, nseg)) join(0, 1, nseg, false, store_out);
-      } else {
-        int size = 8;
+      int counter = w0, sg = 0, step = 1, n = nseg, size = 0;
+      bool joined = false;  // whether the parts are joins of groups
+      if (nseg > 2 * round) {
+        size = 8;
         while (size < round || size * 2 * round < nseg) size *= 2;
-        const int lead = seg & ~(size - 1);
-        const int members = nseg - lead < size ? nseg - lead : size;
-        if (arrive(kAttnWgs + 2 * (w0 + lead) + (lead == 0 ? 1 : 0), members)) {
-          join(lead, 1, members, false, [&](int h, int d, f32x4_t o, float top, float sum) {
-            put(slot(lead, true), h, d, o, top, sum);
-          });
-          const int ngroups = (nseg + size - 1) / size;
-          if (arrive(w0, ngroups)) join(0, size, ngroups, true, store_out);
-        }
+        sg = seg & ~(size - 1);
+        n = nseg - sg < size ? nseg - sg : size;
+        counter = kAttnWgs + 2 * (w0 + sg) + (sg == 0 ? 1 : 0);
+      }
+      while (arrive(counter, n)) {
+        const bool final = size == 0 || joined;
+        const uint32_t to = slot(sg, true);
+        join(sg, step, n, joined, [&](int h, int d, f32x4_t o, float top, float sum) {
+          if (final) store_out(h, d, o, top, sum);
+          else put(to, h, d, o, top, sum);
+        });
+        if (final) break;
+        joined = true;
+        counter = w0;
+        sg = 0;
+        step = size;
+        n = (nseg + size - 1) / size;
       }
     }
     // ---- next item -------------------------------------------------------------
