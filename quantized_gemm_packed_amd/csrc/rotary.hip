@@ -52,8 +52,8 @@ struct Pack {
 // VEC elements per 16-byte access where every address allows it, else one.
 // A lane's unit is two pieces of VEC elements of one head: the two halves of
 // VEC pairs (or VEC adjacent pairs), or two pieces to copy.  Each thread has
-// the loads of kRows heads in flight before it computes the first: with one
-// the loop waits for memory at every head.
+// the loads of kRows heads in flight at once (with one the loop waits for
+// memory at every head), the first of them while the angles are computed.
 template <typename T, bool HALF, int VEC>
 __global__ __launch_bounds__(256) void rotary_kernel(const RotaryParams p) {
   typedef Pack<T, VEC> __attribute__((aligned(sizeof(T) * VEC))) P;
@@ -64,6 +64,47 @@ __global__ __launch_bounds__(256) void rotary_kernel(const RotaryParams p) {
   const int nt = (int)(p.tokens - t0 < p.tok_per_wg ? p.tokens - t0 : p.tok_per_wg);
   float* cs = lds;
   float* sn = lds + p.tok_per_wg * p.half;
+
+  const int lanes = 1 << p.lane_shift;
+  const int rot = p.half / VEC;
+  const int hall = p.heads[0] + p.heads[1];
+  const int h0 = (int)blockIdx.y * p.head_step;
+  const int nh = hall - h0 < p.head_step ? hall - h0 : p.head_step;
+  const float inv_nh = 1.0f / (float)nh;  // rows below 2^17: (row + 1/2) inv_nh is never a whole step off
+  const int step = 256 >> p.lane_shift;
+  const int rows = nt * nh;
+
+  // the rows row0, row0 + step, ... and the unit u of each
+  int row0 = tid >> p.lane_shift, u = tid & (lanes - 1);
+  bool live = u < p.units && row0 < rows;
+  T* y[kRows];
+  int tok[kRows];
+  int at0 = 0, at1 = 0;
+  bool turn = false, two = false;
+  P a[kRows], b[kRows];
+  auto load = [&]() {
+    turn = u < rot;
+    at0 = turn ? (HALF ? u * VEC : 2 * u * VEC) : 2 * p.half + 2 * (u - rot) * VEC;
+    at1 = turn && HALF ? at0 + p.half : at0 + VEC;
+    two = turn || at1 + VEC <= 2 * p.half + p.rest;
+#pragma unroll
+    for (int k = 0; k < kRows; ++k) {
+      const int row = row0 + k * step < rows ? row0 + k * step : row0;
+      tok[k] = (int)(((float)row + 0.5f) * inv_nh);
+      const int hh = h0 + row - tok[k] * nh;
+      const int which = hh >= p.heads[0];
+      const int h = hh - (which ? p.heads[0] : 0);
+      const T* x = static_cast<const T*>(which ? p.x[1] : p.x[0]) + (t0 + tok[k]) * (which ? p.x_ts[1] : p.x_ts[0]) +
+                   h * (which ? p.x_hs[1] : p.x_hs[0]);
+      y[k] = static_cast<T*>(which ? p.y[1] : p.y[0]) + (t0 + tok[k]) * (which ? p.y_ts[1] : p.y_ts[0]) +
+             h * (which ? p.y_hs[1] : p.y_hs[0]);
+      // (a row past the last: the first again, which is not stored)
+      a[k] = *reinterpret_cast<const P*>(x + at0);
+      if (two) b[k] = *reinterpret_cast<const P*>(x + at1);
+    }
+  };
+  if (live) load();
+
   for (int i = tid; i < nt * p.half; i += 256) {
     const int t = i / p.half;
     const double turns = (double)p.positions[t0 + t] * (p.inv_freq[i - t * p.half] * 0.15915494309189535);
@@ -74,74 +115,46 @@ __global__ __launch_bounds__(256) void rotary_kernel(const RotaryParams p) {
     sn[i] = s * p.factor * p.sign;
   }
   __syncthreads();
-  const int lanes = 1 << p.lane_shift;
-  const int rot = p.half / VEC;
-  const int hall = p.heads[0] + p.heads[1];
-  const int h0 = (int)blockIdx.y * p.head_step;
-  const int nh = hall - h0 < p.head_step ? hall - h0 : p.head_step;
-  const float inv_nh = 1.0f / (float)nh;  // rows below 2^17: (row + 1/2) inv_nh is never a whole step off
-  const int step = 256 >> p.lane_shift;
-  const int rows = nt * nh;
-  for (int row0 = tid >> p.lane_shift; row0 < rows; row0 += step * kRows) {
-    const T* x[kRows];
-    T* y[kRows];
-    int tok[kRows];
-#pragma unroll
-    for (int k = 0; k < kRows; ++k) {
-      const int row = row0 + k * step < rows ? row0 + k * step : row0;
-      tok[k] = (int)(((float)row + 0.5f) * inv_nh);
-      const int hh = h0 + row - tok[k] * nh;
-      const int which = hh >= p.heads[0];
-      const int h = hh - (which ? p.heads[0] : 0);
-      x[k] = static_cast<const T*>(which ? p.x[1] : p.x[0]) + (t0 + tok[k]) * (which ? p.x_ts[1] : p.x_ts[0]) +
-             h * (which ? p.x_hs[1] : p.x_hs[0]);
-      y[k] = static_cast<T*>(which ? p.y[1] : p.y[0]) + (t0 + tok[k]) * (which ? p.y_ts[1] : p.y_ts[0]) +
-             h * (which ? p.y_hs[1] : p.y_hs[0]);
-    }
-    for (int u = tid & (lanes - 1); u < p.units; u += lanes) {
-      const bool turn = u < rot;
-      const int at0 = turn ? (HALF ? u * VEC : 2 * u * VEC) : 2 * p.half + 2 * (u - rot) * VEC;
-      const int at1 = turn && HALF ? at0 + p.half : at0 + VEC;
-      const bool two = turn || at1 + VEC <= 2 * p.half + p.rest;
-      P a[kRows], b[kRows];
+
+  while (live) {
+    if (turn) {
 #pragma unroll
       for (int k = 0; k < kRows; ++k) {
-        if (row0 + k * step >= rows) continue;
-        a[k] = *reinterpret_cast<const P*>(x[k] + at0);
-        if (two) b[k] = *reinterpret_cast<const P*>(x[k] + at1);
-      }
-      if (turn) {
+        const float* c = cs + tok[k] * p.half + u * VEC;
+        const float* s = sn + tok[k] * p.half + u * VEC;
+        T e[2 * VEC];  // the unit's elements, pairs at (i, i + VEC) or (2 i, 2 i + 1)
 #pragma unroll
-        for (int k = 0; k < kRows; ++k) {
-          const float* c = cs + tok[k] * p.half + u * VEC;
-          const float* s = sn + tok[k] * p.half + u * VEC;
-          T e[2 * VEC];  // the unit's elements, pairs at (i, i + VEC) or (2 i, 2 i + 1)
+        for (int i = 0; i < VEC; ++i) {
+          e[i] = a[k].v[i];
+          e[VEC + i] = b[k].v[i];
+        }
 #pragma unroll
-          for (int i = 0; i < VEC; ++i) {
-            e[i] = a[k].v[i];
-            e[VEC + i] = b[k].v[i];
-          }
+        for (int i = 0; i < VEC; ++i) {
+          const int i0 = HALF ? i : 2 * i, i1 = HALF ? VEC + i : 2 * i + 1;
+          const float x0 = ld1<T>(e[i0]), x1 = ld1<T>(e[i1]);
+          e[i0] = st1<T>(x0 * c[i] - x1 * s[i]);
+          e[i1] = st1<T>(x0 * s[i] + x1 * c[i]);
+        }
 #pragma unroll
-          for (int i = 0; i < VEC; ++i) {
-            const int i0 = HALF ? i : 2 * i, i1 = HALF ? VEC + i : 2 * i + 1;
-            const float x0 = ld1<T>(e[i0]), x1 = ld1<T>(e[i1]);
-            e[i0] = st1<T>(x0 * c[i] - x1 * s[i]);
-            e[i1] = st1<T>(x0 * s[i] + x1 * c[i]);
-          }
-#pragma unroll
-          for (int i = 0; i < VEC; ++i) {
-            a[k].v[i] = e[i];
-            b[k].v[i] = e[VEC + i];
-          }
+        for (int i = 0; i < VEC; ++i) {
+          a[k].v[i] = e[i];
+          b[k].v[i] = e[VEC + i];
         }
       }
-#pragma unroll
-      for (int k = 0; k < kRows; ++k) {
-        if (row0 + k * step >= rows) continue;
-        *reinterpret_cast<P*>(y[k] + at0) = a[k];
-        if (two) *reinterpret_cast<P*>(y[k] + at1) = b[k];
-      }
     }
+#pragma unroll
+    for (int k = 0; k < kRows; ++k) {
+      if (row0 + k * step >= rows) continue;
+      *reinterpret_cast<P*>(y[k] + at0) = a[k];
+      if (two) *reinterpret_cast<P*>(y[k] + at1) = b[k];
+    }
+    u += lanes;
+    if (u >= p.units) {
+      u = tid & (lanes - 1);
+      row0 += step * kRows;
+    }
+    live = row0 < rows;
+    if (live) load();
   }
 }
 
