@@ -512,7 +512,8 @@ hum_status hum_rotary_inv_freq(int32_t rotary_dim, double base, int32_t scaling,
  * positions[t] * inv_freq[i], both in one launch:
  *   y0 = x0 cos - x1 sin, y1 = x0 sin + x1 cos, in f32, rounded once.
  * The angle is reduced in float64, so far positions keep their precision.
- *   positions : i64 [T]; inv_freq : f64 [rotary_dim / 2] (device)
+ *   positions : i64 [T], |position| < 2^53 (negative ones turn back);
+ *               inv_freq : f64 [rotary_dim / 2] (device)
  *   strides   : elements from token to token and from head to head (head
  *               elements are contiguous); any, as long as the rows of an
  *               output do not overlap
@@ -560,7 +561,8 @@ hum_status hum_kv_write(const hum_kv_desc* desc, void* cache, size_t cache_bytes
 
 /* Reads slots[t] back: k_out, v_out bf16 [T][num_kv_heads][head_dim] =
  * bf16(code * scale).  A slot outside [0, num_pages * page_size) reads as
- * zeros; the same slot may be read more than once. */
+ * zeros; the same slot may be read more than once.  k_out and v_out must not
+ * overlap. */
 hum_status hum_kv_read(const hum_kv_desc* desc, const void* cache, size_t cache_bytes, int64_t num_tokens,
                        const int64_t* slots, void* k_out_bf16, void* v_out_bf16, void* stream);
 
@@ -575,7 +577,9 @@ size_t hum_kv_attention_workspace_bytes(const hum_kv_desc* desc, int32_t num_q_h
  * 0: all t < n), n = seq_lens[b] clamped to [0, max_pages * page_size], whose
  * page lies in [0, num_pages): the tokens of any other page id (-1 for one
  * held elsewhere) take no part.  Where no token takes part, out is 0 and lse
- * is -inf.  Nothing past n reaches the result, whatever the cache holds.
+ * is -inf.  Nothing past n or before the window reaches the result, whatever
+ * the cache holds there; the values that do take part have to be finite (an
+ * infinity or NaN among them makes what it reaches NaN).
  *   q           : bf16 [batch][num_q_heads][head_dim], strides in elements;
  *                 head h reads key-value head h / (num_q_heads / num_kv_heads)
  *   block_table : i32 [batch][max_pages], rows table_stride apart; entry

@@ -758,7 +758,7 @@ def _device_of(t, name, *others):
 def _launch(dev, fn, *args):
     """fn(*args, stream) with GPU `dev` current, on its current stream."""
     import torch
-    if torch.cuda.current_device() == dev:
+    if torch._C._cuda_getDevice() == dev:
         status = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
     else:
         with torch.cuda.device(dev):
@@ -911,7 +911,9 @@ def kv_read(desc: KvDesc, cache, slots, k_out=None, v_out=None):
     if k_out is None:
         k_out = cache.new_empty(shape, dtype=torch.bfloat16)
     if v_out is None:
-        v_out = cache.new_empty(shape, dtype=torch.bfloat16)
+        v_out = torch.empty_like(k_out)
+    elif v_out is k_out:
+        raise ValueError("k_out and v_out must be two tensors")
     _launch(dev, load_library().hum_kv_read, ctypes.addressof(desc), cp, cb, t, sp, k_out.data_ptr(),
             v_out.data_ptr())
     return k_out, v_out
@@ -944,22 +946,28 @@ def kv_attention(desc: KvDesc, cache, q, block_table, seq_lens, scale: float | N
         raise ValueError(f"block_table must be torch.int32, got {block_table.dtype}")
     if mp > 1 and block_table.stride(1) != 1:
         raise ValueError("block_table's rows must be contiguous")
-    _want(out, "out", torch.bfloat16, (b, hq, d))
-    if out is not None and not out.is_contiguous():
-        raise ValueError("out must be contiguous")
+    if out is not None:
+        _want(out, "out", torch.bfloat16, (b, hq, d))
+        if not out.is_contiguous():
+            raise ValueError("out must be contiguous")
     lp = _vec(seq_lens, "seq_lens", torch.int32, b, cache.get_device())
     dev = _device_of(cache, "cache", q, block_table, out, workspace)
     lib = load_library()
-    need = kv_attention_workspace_bytes(desc, hq, b, mp)
+    ad = ctypes.addressof(desc)
+    need = lib.hum_kv_attention_workspace_bytes(ad, hq, b, mp)
+    if need == 0:
+        raise HumError(1, lib.hum_last_error().decode())
     if workspace is None:
         workspace = _call_workspace(dev, need)
     else:
         _want(workspace, "workspace", torch.uint8)
         _gpu(workspace, "workspace")
     if out is None:
-        out = q.new_empty((b, hq, d))
+        out = torch.empty_like(q)
+        if not out.is_contiguous():    # (q's heads outermost)
+            out = q.new_empty((b, hq, d))
     lse = q.new_empty((b, hq), dtype=torch.float32) if return_lse else None
-    _launch(dev, lib.hum_kv_attention, ctypes.addressof(desc), cp, cb, hq, b, qp, qts, qhs, block_table.data_ptr(),
+    _launch(dev, lib.hum_kv_attention, ad, cp, cb, hq, b, qp, qts, qhs, block_table.data_ptr(),
             block_table.stride(0), mp, lp, int(window), d ** -0.5 if scale is None else scale, out.data_ptr(),
             None if lse is None else lse.data_ptr(), workspace.data_ptr(), workspace.numel())
     return (out, lse) if return_lse else out

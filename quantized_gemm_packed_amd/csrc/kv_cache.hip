@@ -351,6 +351,7 @@ hum_status hum_kv_read(const hum_kv_desc* desc, const void* cache, size_t cache_
   hum_status st = kv_move_params(desc, cache, cache_bytes, num_tokens, slots, &p);
   if (st != HUM_OK || num_tokens == 0) return st;
   if (!k_out || !v_out) return set_error(HUM_ERR_INVALID_ARG, "NULL pointer");
+  if (k_out == v_out) return set_error(HUM_ERR_INVALID_ARG, "k_out and v_out must be two buffers");
   if ((reinterpret_cast<uintptr_t>(k_out) | reinterpret_cast<uintptr_t>(v_out)) % 16)
     return set_error(HUM_ERR_INVALID_ARG, "k_out and v_out must be 16-byte aligned");
   p.out[0] = static_cast<uint16_t*>(k_out);

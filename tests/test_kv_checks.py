@@ -120,8 +120,8 @@ def test_cache_abi_refusals(lib):
                                      k.get("k", P(64)), 128, 64, P(64), 128, 64, None)
     assert w(c=None) == 1 and w(c=P(72)) == 1 and w(nb=nb - 1) == 3 and w(t=-1) == 1 and w(s=None) == 1
     assert w(k=None) == 1 and w(k=P(65)) == 1 and w(t=1 << 40) == 2 and w(t=0) == 0
-    r = lambda ko=P(64), vo=P(64): lib.hum_kv_read(a, P(64), nb, 3, P(8), ko, vo, None)  # noqa: E731
-    assert r(ko=None) == 1 and r(vo=P(72)) == 1
+    r = lambda ko=P(64), vo=P(128): lib.hum_kv_read(a, P(64), nb, 3, P(8), ko, vo, None)  # noqa: E731
+    assert r(ko=None) == 1 and r(vo=P(72)) == 1 and r(vo=P(64)) == 1
 
 
 def test_attention_binding_refusals(lib):
