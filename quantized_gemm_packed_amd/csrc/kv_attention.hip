@@ -61,7 +61,7 @@ struct KvAttnParams {
 };
 
 constexpr int kTile = 128;      // tokens of a workgroup tile, 32 per wave
-constexpr int kAttnWgs = 512;  // most workgroups: two on every CU
+constexpr int kAttnWgs = 512;   // most workgroups: two on every CU
 constexpr int kSlots = 4;       // of a workgroup: its two parts, and the joins of a group of parts that it leads
 constexpr int kJoin = 8;        // parts read at once when a cut pair is joined
 constexpr int kDevScope = 16;   // sc1: through to memory, around the XCD's L2 (parts cross XCDs)
@@ -122,6 +122,13 @@ __device__ __forceinline__ f32x4_t mfma_bf16(u32x4_t a, u32x4_t b, f32x4_t c) {
 }
 
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// What turns sums with reference maximum m into sums with the larger one.
+// Where m is -inf nothing has been added (the sums are zero), or only NaN,
+// which has to stay.
+__device__ __forceinline__ float rescale(float m, float larger) {
+  return m == larger || m == -__builtin_inff() ? 1.0f : exp2_fast(m - larger);
+}
 
 // A sequence's tokens [lo, n) and its tiles.
 struct SeqSpan {
@@ -490,7 +497,7 @@ __global__ __launch_bounds__(256, FMT == HUM_ACT_BF16 && D == 256 ? 1 : 2) void 
         top = __builtin_fmaxf(top, __shfl_xor(top, 16));
         top = __builtin_fmaxf(top, __shfl_xor(top, 32));
         const float mn = __builtin_fmaxf(m, top);
-        const float a = m == mn ? 1.0f : exp2_fast(m - mn);
+        const float a = rescale(m, mn);
         m = mn;
         m_safe = mn == kNegInf ? 0.0f : mn;
         l *= a;
@@ -551,7 +558,7 @@ __global__ __launch_bounds__(256, FMT == HUM_ACT_BF16 && D == 256 ? 1 : 2) void 
     __syncthreads();
     {
       const float top = waves_m(r);
-      const float a = m == kNegInf ? 0.0f : m == top ? 1.0f : exp2_fast(m - top);
+      const float a = rescale(m, top);
       if (r < heads) {
         // accumulator (j, e), register i: element j * 128 + (4 kq + i) * kVE + e
 #pragma unroll
@@ -575,7 +582,7 @@ __global__ __launch_bounds__(256, FMT == HUM_ACT_BF16 && D == 256 ? 1 : 2) void 
       float sum = 0.0f;
 #pragma unroll
       for (int w = 0; w < 4; ++w)
-        sum += s_m[buf][w][h] == kNegInf ? 0.0f : s_l[buf][w][h] * (s_m[buf][w][h] == top ? 1.0f : exp2_fast(s_m[buf][w][h] - top));
+        sum += s_l[buf][w][h] * rescale(s_m[buf][w][h], top);
       return sum;
     };
     auto waves_o = [&](int h, int d) {
@@ -682,13 +689,12 @@ __global__ __launch_bounds__(256, FMT == HUM_ACT_BF16 && D == 256 ? 1 : 2) void 
               float mn = top;
 #pragma unroll
               for (int k = 0; k < kJoin; ++k) mn = __builtin_fmaxf(mn, __uint_as_float(ml[k][0]));
-              const float ao = top == kNegInf ? 0.0f : top == mn ? 1.0f : exp2_fast(top - mn);
+              const float ao = rescale(top, mn);
               sum *= ao;
               o *= ao;
 #pragma unroll
               for (int k = 0; k < kJoin; ++k) {
-                const float gm = __uint_as_float(ml[k][0]);
-                const float ag = gm == kNegInf ? 0.0f : gm == mn ? 1.0f : exp2_fast(gm - mn);
+                const float ag = rescale(__uint_as_float(ml[k][0]), mn);
                 sum += __uint_as_float(ml[k][1]) * ag;
                 o += go[k] * ag;
               }
@@ -706,8 +712,7 @@ __global__ __launch_bounds__(256, FMT == HUM_ACT_BF16 && D == 256 ? 1 : 2) void 
               for (int k = 1; k < groups; ++k) {
                 const float* v = s_j + (threadIdx.x + k * units) * 6;
                 const float mn = __builtin_fmaxf(top, v[0]);
-                const float ao = top == kNegInf ? 0.0f : top == mn ? 1.0f : exp2_fast(top - mn);
-                const float ag = v[0] == kNegInf ? 0.0f : v[0] == mn ? 1.0f : exp2_fast(v[0] - mn);
+                const float ao = rescale(top, mn), ag = rescale(v[0], mn);
                 sum = sum * ao + v[1] * ag;
                 o = o * ao + f32x4_t{v[2], v[3], v[4], v[5]} * ag;
                 top = mn;

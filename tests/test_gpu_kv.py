@@ -213,6 +213,35 @@ def test_attention_batches_of_many_lengths():
         c.check(c.run(return_lse=True, window=100), window=100, what=f"{len(lens)} sequences, window")
 
 
+@pytest.mark.parametrize("lens", [[40, 700], [5000, 300]])
+def test_attention_nan_reaches_what_it_takes_part_in(lens):
+    """A NaN among the values that take part: in a V element, that element of
+    the heads that share it; in a K element or a query, their whole rows.
+    Everything else keeps its bits."""
+    c = Case(18, "bf16", lens, 4, 2, 64, 16)
+    want, wl = c.run(return_lse=True)
+
+    def poisoned(which, elem):
+        buf = c.dev["cache"].clone().view(c.pages, 2, -1).view(torch.bfloat16)
+        page, at = int(c.table[0, 1]), 3                       # token 19 of sequence 0, key-value head 1
+        buf[page, 1, (which * 16 + at) * 64 + elem] = float("nan")
+        return c.run(return_lse=True, cache=buf.view(torch.uint8).view(-1))
+
+    out, lse = poisoned(1, 7)
+    exp = want.clone()
+    exp[0, 2:, 7] = float("nan")
+    assert torch.equal(torch.isnan(out), torch.isnan(exp)) and torch.equal(out.nan_to_num(), exp.nan_to_num())
+    assert torch.equal(lse, wl)
+    out, lse = poisoned(0, 7)
+    assert torch.isnan(out[0, 2:]).all() and torch.isnan(lse[0, 2:]).all()
+    assert torch.equal(out[0, :2], want[0, :2]) and torch.equal(out[1], want[1])
+    q = c.dev["q"].clone()
+    q[1, 3] = float("nan")
+    out, lse = c.run(return_lse=True, q=q)
+    assert torch.isnan(out[1, 3]).all() and torch.isnan(lse[1, 3])
+    assert torch.equal(out[0], want[0]) and torch.equal(out[1, :3], want[1, :3])
+
+
 def test_attention_no_sequences_and_no_pages():
     c = Case(15, "bf16", [20], 4, 2, 64, 16)
     e = c.run(return_lse=True, q=c.dev["q"][:0], block_table=c.dev["block_table"][:0], seq_lens=c.dev["seq_lens"][:0])
