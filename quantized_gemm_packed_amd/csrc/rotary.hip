@@ -49,7 +49,8 @@ struct Pack {
   T v[VEC];
 };
 
-// VEC elements per 16-byte access where every address allows it, else one.
+// VEC: elements per access, as many as every address and the sizes allow (16
+// bytes, then halves of it down to one element).
 // A lane's unit is two pieces of VEC elements of one head: the two halves of
 // VEC pairs (or VEC adjacent pairs), or two pieces to copy.  Each thread has
 // the loads of kRows heads in flight at once (with one the loop waits for
@@ -232,7 +233,6 @@ hum_status hum_rotary(const hum_rotary_desc* d, int64_t num_tokens, const int64_
   if (!positions || !inv_freq || (d->num_q_heads && (!q || !q_out)) || (d->num_kv_heads && (!k || !k_out)))
     return set_error(HUM_ERR_INVALID_ARG, "NULL pointer");
   const int size = d->dtype == HUM_BF16 ? 2 : 4;
-  const int vec = 16 / size;
   RotaryParams p{};
   p.positions = positions;
   p.inv_freq = inv_freq;
@@ -240,7 +240,9 @@ hum_status hum_rotary(const hum_rotary_desc* d, int64_t num_tokens, const int64_
   void* ys[2] = {q_out, k_out};
   const int64_t st[2][4] = {{q_ts, q_hs, qo_ts, qo_hs}, {k_ts, k_hs, ko_ts, ko_hs}};
   const int heads[2] = {d->num_q_heads, d->num_kv_heads};
-  bool aligned = (d->rotary_dim / 2) % vec == 0 && (d->head_dim - d->rotary_dim) % vec == 0;
+  // whatever an access has to divide, in elements: the two halves, the rest of
+  // a head, the strides and the addresses
+  int64_t all = (d->rotary_dim / 2) | (d->head_dim - d->rotary_dim);
   bool in_place = true;
   for (int i = 0; i < 2; ++i) {
     p.x[i] = xs[i];
@@ -256,10 +258,11 @@ hum_status hum_rotary(const hum_rotary_desc* d, int64_t num_tokens, const int64_
     if (xs[i] == ys[i] && (st[i][0] != st[i][2] || st[i][1] != st[i][3]))
       return set_error(HUM_ERR_INVALID_ARG, "in place, input and output strides must be the same");
     if (xs[i] != ys[i]) in_place = false;
-    aligned = aligned && reinterpret_cast<uintptr_t>(xs[i]) % 16 == 0 && reinterpret_cast<uintptr_t>(ys[i]) % 16 == 0;
-    for (int j = 0; j < 4; ++j) aligned = aligned && st[i][j] % vec == 0;
+    all |= (int64_t)(reinterpret_cast<uintptr_t>(xs[i]) | reinterpret_cast<uintptr_t>(ys[i])) / size;
+    for (int j = 0; j < 4; ++j) all |= st[i][j];
   }
-  const int v = aligned ? vec : 1;
+  int v = 16 / size;
+  while (all % v) v /= 2;
   p.tokens = num_tokens;
   p.half = d->rotary_dim / 2;
   p.rest = in_place ? 0 : d->head_dim - d->rotary_dim;
@@ -290,9 +293,12 @@ hum_status hum_rotary(const hum_rotary_desc* d, int64_t num_tokens, const int64_
   const bool hf = d->layout == HUM_ROPE_HALF;
   if (size == 2) {
     if (v == 8) launch_rotary<uint16_t, 8>(p, hf, grid, lds, s);
+    else if (v == 4) launch_rotary<uint16_t, 4>(p, hf, grid, lds, s);
+    else if (v == 2) launch_rotary<uint16_t, 2>(p, hf, grid, lds, s);
     else launch_rotary<uint16_t, 1>(p, hf, grid, lds, s);
   } else {
     if (v == 4) launch_rotary<float, 4>(p, hf, grid, lds, s);
+    else if (v == 2) launch_rotary<float, 2>(p, hf, grid, lds, s);
     else launch_rotary<float, 1>(p, hf, grid, lds, s);
   }
   hipError_t err = hipGetLastError();

@@ -35,7 +35,7 @@ def _check(y, x, pos, f, layout, factor, inverse, what):
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("layout", ["half", "interleaved"])
 @pytest.mark.parametrize("t,hq,hk,d,r", [(1, 1, 1, 128, 128), (7, 32, 8, 128, 64), (300, 5, 1, 80, 40),
-                                         (33, 3, 2, 64, 6), (2, 4, 4, 2, 2), (1500, 2, 1, 96, 96), (5, 2, 1, 1024, 1022),
+                                         (33, 3, 2, 64, 6), (2, 4, 4, 2, 2), (70, 4, 1, 80, 20), (70, 4, 1, 72, 24), (1500, 2, 1, 96, 96), (5, 2, 1, 1024, 1022),
                                          (3, 1, 1, 1023, 2)])
 def test_rotary(dtype, layout, t, hq, hk, d, r):
     print(f"case rotary {dtype} {layout} {t} {hq} {hk} {d} {r}", flush=True)
