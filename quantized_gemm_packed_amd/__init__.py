@@ -3,7 +3,9 @@
 Argument marshalling only: every step of the computation runs in the HIP
 kernels of ``libhum.so``; PyTorch provides device memory and the current
 stream.  The names mirror the C ABI in ``include/hum.h``.  If the library is
-not built, every entry point raises -- there is no CPU fallback.
+not built, every entry point raises -- there is no CPU fallback.  The
+decode-step calls (rotary, kv_write, kv_read, kv_attention) are marshalled by
+``_binding.so``, host code built beside it.
 """
 from __future__ import annotations
 
@@ -715,56 +717,25 @@ _ROPE_LAYOUT = {"half": ROPE_HALF, "interleaved": ROPE_INTERLEAVED}
 _ROPE_SCALING = {"none": ROPE_NONE, "linear": ROPE_LINEAR, "ntk": ROPE_NTK, "yarn": ROPE_YARN}
 
 
-# These calls run once or more per layer and token, so their host side is kept
-# short: every check is an attribute or an integer comparison.
-
-def _rows3(t, name, dtype, shape=None):
-    """Checks a [rows, heads, dim] tensor whose rows and heads may be strided
-    (a slice of a fused qkv product) -> (pointer, row stride, head stride)."""
-    if t.dtype != dtype:
-        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if shape is not None and t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    st = t.stride()
-    if st[2] != 1 and t.shape[2] > 1:
-        raise ValueError(f"{name}'s head elements must be contiguous")
-    return t.data_ptr(), st[0], st[1]
+_nat = None
 
 
-def _vec(t, name, dtype, n, dev):
-    """Checks a contiguous 1-D tensor on device number `dev` (-1: the CPU)."""
-    if t.dtype != dtype:
-        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.dim() != 1 or t.shape[0] != n:
-        raise ValueError(f"{name} must have shape {(n,)}, got {tuple(t.shape)}")
-    if n > 1 and t.stride(0) != 1:
-        raise ValueError(f"{name} must be contiguous")
-    if t.get_device() != dev:
-        raise ValueError(f"tensors on different devices: {name} on {t.device}")
-    return t.data_ptr()
-
-
-def _device_of(t, name, *others):
-    """The number of the GPU that `t` and every other tensor (or None) is on."""
-    dev = t.get_device()
-    for o in others:
-        if o is not None and o.get_device() != dev:
-            raise ValueError(f"tensors on different devices: {t.device} and {o.device}")
-    if dev < 0:
-        raise ValueError(f"{name} must be a device tensor")
-    return dev
-
-
-def _launch(dev, fn, *args):
-    """fn(*args, stream) with GPU `dev` current, on its current stream."""
-    import torch
-    if torch._C._cuda_getDevice() == dev:
-        status = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
-    else:
-        with torch.cuda.device(dev):
-            status = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
-    if status:
-        _check(status)
+def _native():
+    """The native marshalling of the calls below (``csrc/binding.cpp``: their
+    checks, outputs and launch in one call; they run once or more per layer
+    and token, where marshalling in Python costs more than a small launch)."""
+    global _nat
+    if _nat is None:
+        import torch
+        load_library()
+        try:
+            from . import _binding
+        except ImportError as e:
+            raise RuntimeError(f"{_HERE}/_binding.so is not built or does not load ({e}); run "
+                               "__graft_entry__.build()") from e
+        _binding.setup(HumError, torch._C._cuda_getCurrentRawStream, _call_workspace, _WS)
+        _nat = _binding
+    return _nat
 
 
 def _call_workspace(dev, need):
@@ -772,21 +743,12 @@ def _call_workspace(dev, need):
     while it is captured, the graph's own from its memory pool (two graphs
     captured on one stream may be replayed on two)."""
     import torch
+    device = torch.device("cuda", dev)
     if torch.cuda.is_current_stream_capturing():
-        ws = torch.empty(need, dtype=torch.uint8, device=torch.device("cuda", dev))
+        ws = torch.empty(need, dtype=torch.uint8, device=device)
         ws[:_WS_HEADER].zero_()
         return ws
-    ws = _WS.get((dev, torch._C._cuda_getCurrentRawStream(dev)))
-    if ws is not None and ws.buf is not None and ws.buf.numel() >= need:
-        return ws.buf
-    return _workspace(torch.device("cuda", dev)).get(need)
-
-
-def _no_overlap(out, name):
-    """An output that the caller gives must not hold two of its elements at
-    one address."""
-    if out.numel() and any(s == 0 for s, n in zip(out.stride(), out.shape) if n > 1):
-        raise ValueError(f"{name} must not be expanded (stride 0)")
+    return _workspace(device).get(need)
 
 
 def rotary_inv_freq(rotary_dim: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
@@ -811,50 +773,9 @@ def rotary(q, k, positions, inv_freq, layout: str = "half", factor: float = 1.0,
     each head -> (q, k), new tensors unless q_out / k_out are given (the
     inputs themselves for a turn in place).  inverse turns back, which with
     the same factor is the gradient."""
-    import torch
-    if q is None or q.dim() != 3 or (k is not None and k.dim() != 3):
-        raise ValueError("q and k must be 3-D tensors [T, heads, head_dim]")
     if layout not in _ROPE_LAYOUT:
         raise ValueError(f"layout must be one of {sorted(_ROPE_LAYOUT)}")
-    dt = q.dtype
-    if dt != torch.bfloat16 and dt != torch.float32:
-        raise ValueError(f"q must be torch.bfloat16 or torch.float32, got {dt}")
-    t, hq, d = q.shape
-    hk = 0
-    qp, qts, qhs = _rows3(q, "q", dt)
-    kp = kop = None
-    kts = khs = kots = kohs = 0
-    if k is not None:
-        hk = k.shape[1]
-        kp, kts, khs = _rows3(k, "k", dt, (t, hk, d))
-    elif k_out is not None:
-        raise ValueError("k_out without k")
-    if inv_freq is None or inv_freq.dim() != 1:
-        raise ValueError("inv_freq must be a 1-D float64 tensor")
-    half = inv_freq.shape[0]
-    if q_out is not None:
-        _rows3(q_out, "q_out", dt, q.shape)
-        _no_overlap(q_out, "q_out")
-    if k_out is not None:
-        _rows3(k_out, "k_out", dt, k.shape)
-        _no_overlap(k_out, "k_out")
-    dev = q.get_device()
-    pp = _vec(positions, "positions", torch.int64, t, dev)
-    fp = _vec(inv_freq, "inv_freq", torch.float64, half, dev)
-    _device_of(q, "q", k, q_out, k_out)
-    if q_out is None:
-        q_out = torch.empty_like(q)
-    qots, qohs, _ = q_out.stride()
-    if k is not None:
-        if k_out is None:
-            k_out = torch.empty_like(k)
-        kop = k_out.data_ptr()
-        kots, kohs, _ = k_out.stride()
-    desc = RotaryDesc(BF16 if dt == torch.bfloat16 else F32, _ROPE_LAYOUT[layout], d, 2 * half, hq, hk, bool(inverse),
-                      factor)
-    _launch(dev, load_library().hum_rotary, ctypes.addressof(desc), t, pp, fp, qp, qts, qhs, q_out.data_ptr(), qots,
-            qohs, kp, kts, khs, kop, kots, kohs)
-    return q_out, k_out
+    return (_nat or _native()).rotary(q, k, positions, inv_freq, _ROPE_LAYOUT[layout], factor, inverse, q_out, k_out)
 
 
 def make_kv_desc(fmt, num_pages: int, page_size: int, num_kv_heads: int, head_dim: int) -> KvDesc:
@@ -869,54 +790,17 @@ def kv_cache_bytes(desc: KvDesc) -> int:
     return b
 
 
-def _kv_cache(desc, cache):
-    import torch
-    if cache is None or cache.dtype != torch.uint8 or not cache.is_contiguous():
-        raise ValueError("cache must be a contiguous uint8 tensor")
-    return cache.data_ptr(), cache.numel()
-
-
 def kv_write(desc: KvDesc, cache, k, v, slots):
     """Quantize k, v bf16 [T, Hkv, D] into slots int64 [T] of `cache` (uint8,
     kv_cache_bytes(desc)).  Slots outside the cache (-1) are skipped; the
     others must differ."""
-    import torch
-    cp, cb = _kv_cache(desc, cache)
-    if k is None or v is None or k.dim() != 3 or v.dim() != 3:
-        raise ValueError("k and v must be 3-D tensors [T, num_kv_heads, head_dim]")
-    t = k.shape[0]
-    shape = (t, desc.num_kv_heads, desc.head_dim)
-    kp, kts, khs = _rows3(k, "k", torch.bfloat16, shape)
-    vp, vts, vhs = _rows3(v, "v", torch.bfloat16, shape)
-    sp = _vec(slots, "slots", torch.int64, t, cache.get_device())
-    dev = _device_of(cache, "cache", k, v)
-    _launch(dev, load_library().hum_kv_write, ctypes.addressof(desc), cp, cb, t, sp, kp, kts, khs, vp, vts, vhs)
+    (_nat or _native()).kv_write(desc, cache, k, v, slots)
 
 
 def kv_read(desc: KvDesc, cache, slots, k_out=None, v_out=None):
     """slots int64 [T] of `cache` -> k, v bf16 [T, Hkv, D]; slots outside the
     cache (-1) read as zeros."""
-    import torch
-    cp, cb = _kv_cache(desc, cache)
-    if slots is None or slots.dim() != 1:
-        raise ValueError("slots must be a 1-D int64 tensor")
-    t = slots.shape[0]
-    sp = _vec(slots, "slots", torch.int64, t, cache.get_device())
-    shape = (t, desc.num_kv_heads, desc.head_dim)
-    for o, nm in ((k_out, "k_out"), (v_out, "v_out")):
-        _want(o, nm, torch.bfloat16, shape)
-        if o is not None and not o.is_contiguous():
-            raise ValueError(f"{nm} must be contiguous")
-    dev = _device_of(cache, "cache", k_out, v_out)
-    if k_out is None:
-        k_out = cache.new_empty(shape, dtype=torch.bfloat16)
-    if v_out is None:
-        v_out = torch.empty_like(k_out)
-    elif v_out is k_out:
-        raise ValueError("k_out and v_out must be two tensors")
-    _launch(dev, load_library().hum_kv_read, ctypes.addressof(desc), cp, cb, t, sp, k_out.data_ptr(),
-            v_out.data_ptr())
-    return k_out, v_out
+    return (_nat or _native()).kv_read(desc, cache, slots, k_out, v_out)
 
 
 def kv_attention_workspace_bytes(desc: KvDesc, num_q_heads: int, batch: int, max_pages: int) -> int:
@@ -933,44 +817,8 @@ def kv_attention(desc: KvDesc, cache, q, block_table, seq_lens, scale: float | N
     query row per sequence, q bf16 [B, Hq, D], over the first seq_lens int32
     [B] tokens (the last `window` of them, if not 0) of the pages that
     block_table int32 [B, max_pages] names.  scale defaults to D ** -0.5."""
-    import torch
-    cp, cb = _kv_cache(desc, cache)
-    if q is None or q.dim() != 3:
-        raise ValueError("q must be a 3-D tensor [B, num_q_heads, head_dim]")
-    b, hq, d = q.shape
-    qp, qts, qhs = _rows3(q, "q", torch.bfloat16, (b, hq, desc.head_dim))
-    if block_table is None or block_table.dim() != 2 or block_table.shape[0] != b:
-        raise ValueError("block_table must be a 2-D tensor [B, max_pages]")
-    mp = block_table.shape[1]
-    if block_table.dtype != torch.int32:
-        raise ValueError(f"block_table must be torch.int32, got {block_table.dtype}")
-    if mp > 1 and block_table.stride(1) != 1:
-        raise ValueError("block_table's rows must be contiguous")
-    if out is not None:
-        _want(out, "out", torch.bfloat16, (b, hq, d))
-        if not out.is_contiguous():
-            raise ValueError("out must be contiguous")
-    lp = _vec(seq_lens, "seq_lens", torch.int32, b, cache.get_device())
-    dev = _device_of(cache, "cache", q, block_table, out, workspace)
-    lib = load_library()
-    ad = ctypes.addressof(desc)
-    need = lib.hum_kv_attention_workspace_bytes(ad, hq, b, mp)
-    if need == 0:
-        raise HumError(1, lib.hum_last_error().decode())
-    if workspace is None:
-        workspace = _call_workspace(dev, need)
-    else:
-        _want(workspace, "workspace", torch.uint8)
-        _gpu(workspace, "workspace")
-    if out is None:
-        out = torch.empty_like(q)
-        if not out.is_contiguous():    # (q's heads outermost)
-            out = q.new_empty((b, hq, d))
-    lse = q.new_empty((b, hq), dtype=torch.float32) if return_lse else None
-    _launch(dev, lib.hum_kv_attention, ad, cp, cb, hq, b, qp, qts, qhs, block_table.data_ptr(),
-            block_table.stride(0), mp, lp, int(window), d ** -0.5 if scale is None else scale, out.data_ptr(),
-            None if lse is None else lse.data_ptr(), workspace.data_ptr(), workspace.numel())
-    return (out, lse) if return_lse else out
+    return (_nat or _native()).kv_attention(desc, cache, q, block_table, seq_lens, scale, window, out, return_lse,
+                                            workspace)
 
 
 (PEAK_HBM_READ, PEAK_MFMA_BF16, PEAK_MFMA_FP8, PEAK_MFMA_FP4, PEAK_MFMA_FP8_FP4, PEAK_MFMA32_BF16, PEAK_MFMA32_FP8,

@@ -1,4 +1,5 @@
-"""Builds libhum.so (all HIP kernels + the C ABI) for gfx950 with hipcc.
+"""Builds libhum.so (all HIP kernels + the C ABI) for gfx950 with hipcc, and
+_binding.so (host code: native marshalling of the decode-step calls).
 
 The library is built in-tree, next to this file, so it travels with the
 source tree.  Every translation unit is compiled with packed-FP32 code
@@ -54,8 +55,30 @@ def _compile(src: str) -> str:
     return obj
 
 
+def _build_binding() -> None:
+    """_binding.so: the native marshalling of the decode-step calls (host code
+    against torch's headers; its HIP and hum symbols come with libhum.so)."""
+    import sysconfig
+
+    import torch
+    base = os.path.dirname(torch.__file__)
+    out = os.path.join(HERE, "_binding.so")
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-D__HIP_PLATFORM_AMD__",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-I", os.path.join(ROOT, "include"), "-isystem", os.path.join(base, "include"),
+           "-isystem", os.path.join(base, "include", "torch", "csrc", "api", "include"),
+           "-isystem", "/opt/rocm/include", "-I", sysconfig.get_paths()["include"],
+           os.path.join(CSRC, "binding.cpp"), "-o", out + ".tmp", "-L", HERE, "-l:libhum.so", "-Wl,-rpath,$ORIGIN",
+           "-L", os.path.join(base, "lib"), "-lc10", "-ltorch_cpu", "-ltorch_python"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for binding.cpp:\n{r.stderr[-6000:]}")
+    os.replace(out + ".tmp", out)
+
+
 def build_library(verbose: bool = True) -> str:
-    """Compile every source and link libhum.so; returns the library path."""
+    """Compile every source and link libhum.so and the native binding; returns
+    the library path."""
     os.makedirs(BUILD_DIR, exist_ok=True)
     jobs = min(len(SOURCES), max(1, int(os.environ.get("MAX_JOBS", "8"))))
     with ThreadPoolExecutor(jobs) as ex:
@@ -72,6 +95,7 @@ def build_library(verbose: bool = True) -> str:
     if nm.returncode != 0 or missing:
         raise RuntimeError(f"{tmp}: undefined library symbols: {missing[:5]}")
     os.replace(tmp, LIB)
+    _build_binding()
     if verbose:
         print(f"built {LIB}", file=sys.stderr)
     return LIB

@@ -158,3 +158,31 @@ def test_attention_abi_refusals(lib):
         kw.update(bad)
         with pytest.raises(hum.HumError):
             hum.kv_attention_workspace_bytes(d, **kw)
+
+
+def test_binding_refuses_what_is_no_tensor_or_description(lib):
+    d = hum.make_kv_desc("bf16", 4, 16, 2, 64)
+    cache = torch.zeros(hum.kv_cache_bytes(d), dtype=torch.uint8)
+    k, s = _bf(3, 2, 64), torch.zeros(3, dtype=torch.int64)
+    for bad in (None, [1, 2], np.zeros(4)):
+        with pytest.raises(ValueError, match="slots must be a"):
+            hum.kv_write(d, cache, k, k, bad)
+        with pytest.raises(ValueError, match="k must be a"):
+            hum.kv_write(d, cache, bad, k, s)
+        with pytest.raises(ValueError, match="cache must be a"):
+            hum.kv_read(d, bad, s)
+        with pytest.raises(ValueError, match="positions must be a"):
+            hum.rotary(k, None, bad, torch.zeros(32, dtype=torch.float64))
+    with pytest.raises(ValueError, match="KvDesc"):
+        hum.kv_write(hum.TileConfig(), cache, k, k, s)
+    with pytest.raises(TypeError):
+        hum.kv_write(None, cache, k, k, s)
+    q, tab, n = _bf(3, 4, 64), torch.zeros((3, 2), dtype=torch.int32), torch.zeros(3, dtype=torch.int32)
+    with pytest.raises(ValueError, match="workspace"):
+        hum.kv_attention(d, cache, q, tab, n, workspace=torch.zeros(8))
+    with pytest.raises(ValueError, match="seq_lens must have shape"):
+        hum.kv_attention(d, cache, q, tab, n.view(3, 1))
+    with pytest.raises(ValueError, match="rows must be contiguous"):
+        hum.kv_attention(d, cache, q, torch.zeros((3, 4), dtype=torch.int32)[:, ::2], n)
+    with pytest.raises(ValueError, match="layout"):
+        hum.rotary(k, None, s, torch.zeros(32, dtype=torch.float64), layout=0)
