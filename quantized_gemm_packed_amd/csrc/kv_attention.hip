@@ -60,7 +60,9 @@ struct KvAttnParams {
   int32_t part_heads;  // heads of a slot: m, l and O rows
 };
 
-constexpr int kTile = 128;      // tokens of a workgroup tile, 32 per wave
+constexpr int kWaves = 4;                  // of a workgroup
+constexpr int kThreads = 64 * kWaves;
+constexpr int kTile = 32 * kWaves;         // tokens of a workgroup tile
 constexpr int kAttnWgs = 512;   // most workgroups: two on every CU
 constexpr int kSlots = 4;       // of a workgroup: its two parts, and the joins of a group of parts that it leads
 constexpr int kJoin = 8;        // parts read at once when a cut pair is joined
@@ -181,7 +183,7 @@ __device__ __forceinline__ int64_t uniform64(int64_t v) {
 }
 
 template <int FMT, int D>
-__global__ __launch_bounds__(256, FMT == HUM_ACT_BF16 && D == 256 ? 1 : 2) void kv_attention_kernel(
+__global__ __launch_bounds__(kThreads, FMT == HUM_ACT_BF16 && D == 256 ? 1 : 2) void kv_attention_kernel(
     const KvAttnParams p) {
   using T = AttnTile<FMT, D>;
   using U = KvUnit<FMT, D>;
@@ -222,8 +224,12 @@ __global__ __launch_bounds__(256, FMT == HUM_ACT_BF16 && D == 256 ? 1 : 2) void 
     }
     total = uniform64(__shfl(upto, 63)) * items_per_seq;
   }
-  // (no more workgroups than tiles: every share that counts is non-empty)
-  const int64_t nwg = total < (int64_t)gridDim.x ? total : (int64_t)gridDim.x, wg = blockIdx.x;
+  // No more workgroups than tiles (every share that counts is non-empty), and
+  // where a head has up to three tiles on average, none than heads: two more
+  // tiles in a row cost about as much as joining parts (16 sequences of 333
+  // FP8 tokens: 9.8 us cut, 8.2 whole; one of 200: 8.3 and 6.9).
+  const int64_t items = (int64_t)p.batch * items_per_seq, most = total <= 3 * items ? items : total;
+  const int64_t nwg = most < (int64_t)gridDim.x ? most : (int64_t)gridDim.x, wg = blockIdx.x;
   if (wg >= nwg) return;
   int64_t pos, end;
   if (__builtin_expect(p.small, 1)) {
@@ -270,8 +276,8 @@ __global__ __launch_bounds__(256, FMT == HUM_ACT_BF16 && D == 256 ? 1 : 2) void 
   };
   AttnItem cur = first_item();
 
-  __shared__ float s_m[2][4][16], s_l[2][4][16];
-  __shared__ float s_o[4][16][D + 4];
+  __shared__ float s_m[2][kWaves][16], s_l[2][kWaves][16];
+  __shared__ float s_o[kWaves][16][D + 4];
   __shared__ __attribute__((aligned(16))) uint16_t s_q[16][D + 8];
   __shared__ int s_last;
 
@@ -376,14 +382,14 @@ __global__ __launch_bounds__(256, FMT == HUM_ACT_BF16 && D == 256 ? 1 : 2) void 
 
   // The query rows go through LDS: the next item's are loaded while this one
   // runs and stored when it ends.
-  constexpr int kQN = D == 256 ? 2 : 1;  // 16-byte pieces of a thread
+  constexpr int kQN = 16 * (D / 8) > kThreads ? 16 * (D / 8) / kThreads : 1;  // 16-byte pieces of a thread
   u32x4_t qn[kQN];
   auto load_q = [&](const AttnItem& w) {
     const int live = p.group - w.ht * 16 < 16 ? p.group - w.ht * 16 : 16;
     const uint16_t* q = p.q + w.b * p.q_ts + (int64_t)(w.hk * p.group + w.ht * 16) * p.q_hs;
 #pragma unroll
     for (int i = 0; i < kQN; ++i) {
-      int h = (threadIdx.x + i * 256) / (D / 8);
+      int h = (threadIdx.x + i * kThreads) / (D / 8);
       h = h < live ? h : live - 1;  // (dead columns repeat a live row and are never stored)
       const Bytes16 v = *reinterpret_cast<const Bytes16*>(q + h * p.q_hs + (threadIdx.x % (D / 8)) * 8);
       qn[i] = u32x4_t{v.w[0], v.w[1], v.w[2], v.w[3]};
@@ -392,7 +398,7 @@ __global__ __launch_bounds__(256, FMT == HUM_ACT_BF16 && D == 256 ? 1 : 2) void 
   auto stage_q = [&]() {
 #pragma unroll
     for (int i = 0; i < kQN; ++i) {
-      const int h = (threadIdx.x + i * 256) / (D / 8);
+      const int h = (threadIdx.x + i * kThreads) / (D / 8);
       if (h < 16) *reinterpret_cast<u32x4_t*>(&s_q[h][(threadIdx.x % (D / 8)) * 8]) = qn[i];
     }
   };
@@ -543,11 +549,14 @@ __global__ __launch_bounds__(256, FMT == HUM_ACT_BF16 && D == 256 ? 1 : 2) void 
       __builtin_amdgcn_sched_barrier(0);
     } while (++t < tile_end);
 
-    // ---- join the four waves -------------------------------------------------
+    // ---- join the waves ----------------------------------------------------
     // (s_m and s_l alternate between two buffers, s_o is written only after
     // every wave has read it: no barrier is needed after the rows are out)
     auto waves_m = [&](int h) {
-      return __builtin_fmaxf(__builtin_fmaxf(s_m[buf][0][h], s_m[buf][1][h]), __builtin_fmaxf(s_m[buf][2][h], s_m[buf][3][h]));
+      float top = s_m[buf][0][h];
+#pragma unroll
+      for (int w = 1; w < kWaves; ++w) top = __builtin_fmaxf(top, s_m[buf][w][h]);
+      return top;
     };
     l += __shfl_xor(l, 16);
     l += __shfl_xor(l, 32);
@@ -581,14 +590,14 @@ __global__ __launch_bounds__(256, FMT == HUM_ACT_BF16 && D == 256 ? 1 : 2) void 
     auto waves_l = [&](int h, float top) {
       float sum = 0.0f;
 #pragma unroll
-      for (int w = 0; w < 4; ++w)
+      for (int w = 0; w < kWaves; ++w)
         sum += s_l[buf][w][h] * rescale(s_m[buf][w][h], top);
       return sum;
     };
     auto waves_o = [&](int h, int d) {
       f32x4_t o = {0, 0, 0, 0};
 #pragma unroll
-      for (int w = 0; w < 4; ++w) {
+      for (int w = 0; w < kWaves; ++w) {
         const float4 v = *reinterpret_cast<const float4*>(&s_o[w][h][d]);
         o += f32x4_t{v.x, v.y, v.z, v.w};
       }
@@ -604,7 +613,7 @@ __global__ __launch_bounds__(256, FMT == HUM_ACT_BF16 && D == 256 ? 1 : 2) void 
       if (d == 0 && p.lse) p.lse[row] = sum == 0.0f ? kNegInf : (top + __log2f(sum)) * 0.6931471805599453f;
     };
     if (tile == 0 && tile_end == cur.seq.tiles) {
-      for (int i = threadIdx.x * 4; i < heads * D; i += 1024) {
+      for (int i = threadIdx.x * 4; i < heads * D; i += 4 * kThreads) {
         const int h = i / D, d = i - h * D;
         const float top = waves_m(h), sum = waves_l(h, top);
         store_out(h, d, waves_o(h, d), top, sum);
@@ -660,9 +669,9 @@ __global__ __launch_bounds__(256, FMT == HUM_ACT_BF16 && D == 256 ? 1 : 2) void 
       // elements per thread; threads to spare take every groups-th of them
       auto join = [&](int sg, int step, int n, bool joined, auto&& sink) {
         const int units = heads * (D / 4);
-        const int groups = units >= 256 ? 1 : 256 / units;
-        float* s_j = &s_o[0][0][0];  // [256][6]: the groups' top, sum, o
-        for (int i0 = 0; i0 < units; i0 += 256) {
+        const int groups = units >= kThreads ? 1 : kThreads / units;
+        float* s_j = &s_o[0][0][0];  // [kThreads][6]: the groups' top, sum, o
+        for (int i0 = 0; i0 < units; i0 += kThreads) {
           const int grp = groups == 1 ? 0 : (int)threadIdx.x / units;
           const int i = i0 + (int)threadIdx.x - grp * units;
           const bool live = grp < groups && i < units;
@@ -722,14 +731,14 @@ __global__ __launch_bounds__(256, FMT == HUM_ACT_BF16 && D == 256 ? 1 : 2) void 
           if (live && grp == 0) sink(h, d, o, top, sum);
         }
       };
-      for (int i = threadIdx.x * 4; i < heads * D; i += 1024) {
+      for (int i = threadIdx.x * 4; i < heads * D; i += 4 * kThreads) {
         const int h = i / D, d = i - h * D;
         const float top = waves_m(h), sum = waves_l(h, top);
         put(slot(seg, false), h, d, waves_o(h, d), top, sum);
       }
       // counters: of an item at its first workgroup; of a group at the slot
       // of the part that leads it, after those
-      const int lanes = heads * (D / 4) >= 256 ? 1 : 256 / (heads * (D / 4));
+      const int lanes = heads * (D / 4) >= kThreads ? 1 : kThreads / (heads * (D / 4));
       const int round = kJoin * lanes;
       int counter = w0, sg = 0, step = 1, n = nseg, size = 0;
       bool joined = false;  // whether the parts are joins of groups
@@ -873,7 +882,7 @@ hum_status hum_kv_attention(const hum_kv_desc* desc, const void* cache, size_t c
   p.part_heads = attn_part_heads(desc, num_q_heads);
   hipStream_t s = static_cast<hipStream_t>(stream);
   kv_dispatch(desc, [&](auto fmt, auto dim) {
-    kv_attention_kernel<decltype(fmt)::value, decltype(dim)::value><<<wgs, 256, 0, s>>>(p);
+    kv_attention_kernel<decltype(fmt)::value, decltype(dim)::value><<<wgs, kThreads, 0, s>>>(p);
   });
   hipError_t err = hipGetLastError();
   if (err != hipSuccess) return set_error(HUM_ERR_HIP, "kv_attention launch: %s", hipGetErrorString(err));
