@@ -118,6 +118,13 @@ __device__ __forceinline__ void to_bf16(const uint32_t* w, float scale, uint32_t
   }
 }
 
+// Byte i of w, an E8M0 code, as the scale operand of the conversions.  They
+// read its exponent field only, so that also code 0 (2^-127, an f32 zero) is
+// exact: checked for every code of E4M3 and E2M1 and every scale.
+__device__ __forceinline__ float mx_scale_bits(uint32_t w, int i) {
+  return __uint_as_float((i < 3 ? w << (23 - 8 * i) : w >> 1) & 0x7F800000u);
+}
+
 __device__ __forceinline__ f32x4_t mfma_bf16(u32x4_t a, u32x4_t b, f32x4_t c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, b), c, 0,
                                                  0, 0);
@@ -460,7 +467,7 @@ __global__ __launch_bounds__(kThreads, FMT == HUM_ACT_BF16 && D == 256 ? 1 : 2) 
           if constexpr (U::kMx) {
             // (the word is known at compile time, the byte goes by the lane)
             const int g0 = (c / kPer) * 4 * T::kKE / 32;
-            sc = e8m0_to_f32((ks[s][g0 / 4] >> (8 * ((g0 & 3) + kq * T::kKE / 32))) & 0xFFu);
+            sc = __uint_as_float(((ks[s][g0 / 4] >> (8 * ((g0 & 3) + kq * T::kKE / 32))) & 0xFFu) << 23);
           }
           uint32_t o[4];
           to_bf16<FMT, 8>(&kw[s][c / kPer][(c % kPer) * kW], sc, o);
@@ -531,7 +538,7 @@ __global__ __launch_bounds__(kThreads, FMT == HUM_ACT_BF16 && D == 256 ? 1 : 2) 
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           float sc = 1.0f;
-          if constexpr (U::kMx) sc = e8m0_to_f32((vs[j][i >> 2] >> (8 * (i & 3))) & 0xFFu);
+          if constexpr (U::kMx) sc = mx_scale_bits(vs[j][i >> 2], i & 3);
           to_bf16<FMT, T::kVE>(vw[i][j], sc, w[i]);
         }
 #pragma unroll

@@ -193,6 +193,24 @@ def test_attention_large_scores_and_scale(fmt):
         c.check(c.run(return_lse=True, scale=s), scale=s, what=f"scale {s}")
 
 
+@pytest.mark.parametrize("fmt", ["mxfp8", "mxfp4"])
+def test_attention_mx_scales_at_their_ends(fmt):
+    """Values whose E8M0 scales are near and at the smallest code, and large ones."""
+    c = Case(19, fmt, [64, 33], 4, 2, 128, 16)
+    g = np.random.default_rng(20)
+    for b, n in enumerate((64, 33)):
+        t = np.arange(n)
+        slots = c.table[b][t // 16].astype(np.int64) * 16 + t % 16
+        e = g.integers(-126, -100, (n, 2, 4)).repeat(32, -1)
+        k = synth.bf16_bits(np.ldexp(g.standard_normal((n, 2, 128)), np.where(e < -120, e, 0)).astype(np.float32))
+        v = synth.bf16_bits(np.ldexp(g.standard_normal((n, 2, 128)), np.where(e % 2 == 0, 100, 90)).astype(np.float32))
+        c.cache.write(slots, k, v)
+    scales = c.cache.buf[:, :, 2 * 16 * c.cache.row:2 * 16 * c.cache.row + 16 * 4]
+    assert (scales == 0).any()
+    c.dev["cache"] = torch.from_numpy(c.cache.buf.reshape(-1)).cuda()
+    c.check(c.run(return_lse=True), what="scales")
+
+
 @pytest.mark.parametrize("fmt,d,n", [("fp8_token", 128, 20011), ("bf16", 64, 20011), ("mxfp4", 64, 60001)])
 def test_attention_long_sequence(fmt, d, n):
     """One key-value head: its tiles are cut into as many parts as there are
