@@ -7,6 +7,10 @@
 // 16 bytes of bf16 each; the maximum is a shuffle inside them (a DPP quad
 // for an MX block), so nothing goes through LDS.  Memory bound: each row is
 // read once and its codes written once.
+//
+// Measured on MI355X, 16384 tokens of 8 heads of 128 in MXFP8: written in
+// 21.8 us (4.7 TB/s read + written; a large copy reaches 4.85), read back in
+// 19.9 us (5.1 TB/s); 256 tokens in FP8: 3.6 and 3.0 us, a launch's own time.
 #include "kv_common.h"
 
 namespace hum {
