@@ -518,7 +518,7 @@ hum_status hum_rotary_inv_freq(int32_t rotary_dim, double base, int32_t scaling,
  *               elements are contiguous); any, as long as the rows of an
  *               output do not overlap
  *   out       : may be the input itself (same pointer and strides), but may
- *               not overlap it otherwise
+ *               not overlap it otherwise, nor the other input and output
  * q (with q_out) or k (with k_out) may be NULL where its head count is 0. */
 hum_status hum_rotary(const hum_rotary_desc* desc, int64_t num_tokens, const int64_t* positions,
                       const double* inv_freq, const void* q, int64_t q_token_stride, int64_t q_head_stride,
@@ -586,7 +586,8 @@ size_t hum_kv_attention_workspace_bytes(const hum_kv_desc* desc, int32_t num_q_h
  *                 t / page_size of a row is the page of token t
  *   seq_lens    : i32 [batch], read by the kernel only (no device->host copy)
  *   out         : bf16 [batch][num_q_heads][head_dim], contiguous
- *   lse         : f32 [batch][num_q_heads] or NULL
+ *   lse         : f32 [batch][num_q_heads] or NULL; out and lse must not
+ *                 overlap the inputs
  *   workspace   : hum_kv_attention_workspace_bytes(...) bytes, prepared as for
  *                 hum_linear (hum_prepare_workspace once).  Calls that may
  *                 overlap in time need different workspaces.

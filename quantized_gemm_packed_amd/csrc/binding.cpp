@@ -59,6 +59,7 @@ const at::Tensor& tensor(PyObject* o, const char* name, int dims, const char* wh
 
 void want_dtype(const at::Tensor& t, const char* name, at::ScalarType dt) {
   if (t.scalar_type() != dt) fail("%s must be %s, got %s", name, dtype_name(dt), dtype_name(t.scalar_type()));
+  if (t.is_neg()) fail("%s must hold its values (a negated view does not: resolve_neg())", name);
 }
 
 // A [rows, heads, dim] tensor of the given shape and type; rows and heads may

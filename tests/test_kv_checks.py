@@ -92,6 +92,7 @@ def test_rotary_abi_refusals(lib):
     assert call(d=0) == 2 and call(d=1025) == 2 and call(r=63) == 1 and call(r=66) == 1 and call(r=0) == 1
     assert call(hq=-1) == 1 and call(inv=2) == 1 and call(x=None) == 1 and call(x=P(65)) == 1
     assert call(x=P(64), y=P(64), same_strides=False) == 1
+    assert call(y=P(256)) == 1 and call(y=P(512)) == 1 and call(x=P(512), y=P(64)) == 1   # k, k's output, q = k's output
     assert call(t=0) == 0 and lib.hum_rotary(None, 0, *[None] * 2, None, 0, 0, None, 0, 0, None, 0, 0, None, 0, 0,
                                              None) == 1
 
@@ -186,3 +187,7 @@ def test_binding_refuses_what_is_no_tensor_or_description(lib):
         hum.kv_attention(d, cache, q, torch.zeros((3, 4), dtype=torch.int32)[:, ::2], n)
     with pytest.raises(ValueError, match="layout"):
         hum.rotary(k, None, s, torch.zeros(32, dtype=torch.float64), layout=0)
+    with pytest.raises(ValueError, match="negated"):
+        hum.rotary(torch._neg_view(k.float()), None, s, torch.zeros(32, dtype=torch.float64))
+    with pytest.raises((ValueError, TypeError)):
+        hum.kv_attention(d, cache, q, tab, n, window=1.5)
