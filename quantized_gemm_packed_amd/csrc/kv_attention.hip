@@ -54,7 +54,6 @@ struct KvAttnParams {
   const int32_t* table;
   int64_t table_stride;
   int32_t max_pages, batch, window;
-  int32_t small;  // the call's tiles times its workgroups fit in 32 bits, whatever the lengths
   const int32_t* seq_lens;
   float scale_log2;  // scale * log2(e)
   uint16_t* out;
@@ -189,11 +188,6 @@ __device__ __forceinline__ uint32_t wave_scan_add(uint32_t v) {
   return v;
 }
 
-__device__ __forceinline__ int64_t uniform64(int64_t v) {
-  return ((int64_t)__builtin_amdgcn_readfirstlane((int)(v >> 32)) << 32) |
-         (uint32_t)__builtin_amdgcn_readfirstlane((int)v);
-}
-
 template <int FMT, int D>
 __global__ __launch_bounds__(kThreads, FMT == HUM_ACT_BF16 && D == 256 ? 1 : 2) void kv_attention_kernel(
     const KvAttnParams p) {
@@ -209,12 +203,12 @@ __global__ __launch_bounds__(kThreads, FMT == HUM_ACT_BF16 && D == 256 ? 1 : 2) 
   // Lane i sums the tiles of a run of sequences; a scan over the lanes places
   // the share's first tile in one run, which is then walked.  (What this
   // costs is latency before the first load: the lengths are read once, the
-  // scan stays in registers, 32-bit arithmetic wherever the call's sizes allow
-  // it.)
+  // scan stays in registers, and tiles are counted in 32 bits, which the host
+  // checks.)
   const int items_per_seq = p.kv_heads * p.head_tiles;
   const int run = (p.batch + 63) / 64;
   int32_t len = 0;  // of the lane's last sequence: the only one in batches of up to 64
-  int64_t mine = 0;
+  int32_t mine = 0;
   for (int i = 0; i < run; ++i) {
     const int b = lane * run + i;
     if (b < p.batch) {
@@ -222,57 +216,44 @@ __global__ __launch_bounds__(kThreads, FMT == HUM_ACT_BF16 && D == 256 ? 1 : 2) 
       mine += SeqSpan(p, len).tiles;
     }
   }
-  int64_t upto, total;  // inclusive scan
-  if (__builtin_expect(p.small, 1)) {
-    const uint32_t u = wave_scan_add((uint32_t)mine);
-    upto = u;
-    total = (uint32_t)__builtin_amdgcn_readlane((int)u, 63) * (uint32_t)items_per_seq;
-  } else {
-    upto = mine;
-#pragma unroll
-    for (int w = 1; w < 64; w *= 2) {
-      const int64_t o = __shfl_up(upto, w);
-      if (lane >= w) upto += o;
-    }
-    total = uniform64(__shfl(upto, 63)) * items_per_seq;
-  }
+  const int32_t upto = (int32_t)wave_scan_add((uint32_t)mine);
+  const int32_t total = __builtin_amdgcn_readlane(upto, 63) * items_per_seq;
   // No more workgroups than tiles (every share that counts is non-empty), and
   // where a head has up to three tiles on average, none than heads: two more
   // tiles in a row cost about as much as joining parts (16 sequences of 333
   // FP8 tokens: 9.8 us cut, 8.2 whole; one of 200: 8.3 and 6.9).
-  const int64_t items = (int64_t)p.batch * items_per_seq, most = total <= 3 * items ? items : total;
-  const int64_t nwg = most < (int64_t)gridDim.x ? most : (int64_t)gridDim.x, wg = blockIdx.x;
+  const int32_t items = p.batch * items_per_seq, most = total <= 3 * (int64_t)items ? items : total;
+  const int32_t nwg = most < (int32_t)gridDim.x ? most : (int32_t)gridDim.x, wg = blockIdx.x;
   if (wg >= nwg) return;
-  int64_t pos, end;
-  if (__builtin_expect(p.small, 1)) {
-    pos = (uint32_t)(wg * total) / (uint32_t)nwg;
-    end = (uint32_t)((wg + 1) * total) / (uint32_t)nwg;
-  } else {
-    pos = wg * total / nwg;
-    end = (wg + 1) * total / nwg;
-  }
-  pos = uniform64(pos);
-  end = uniform64(end);
+  // shares of `each` tiles, the first `longer` of them one more
+  const int32_t each = nwg == total ? 1 : (int32_t)((uint32_t)total / (uint32_t)nwg), longer = total - each * nwg;
+  int32_t pos = wg * each + (wg < longer ? wg : longer);
+  const int32_t end = pos + each + (wg < longer ? 1 : 0);
+  // the workgroup whose share holds tile t
+  auto owner = [&](int32_t t) -> int32_t {
+    const int32_t border = longer * (each + 1);
+    return t < border ? (int32_t)((uint32_t)t / (uint32_t)(each + 1))
+                      : longer + (int32_t)((uint32_t)(t - border) / (uint32_t)each);
+  };
   auto length_of = [&](int b) -> int32_t {
     return run == 1 ? __builtin_amdgcn_readlane(len, b & 63) : scalar_ptr(p.seq_lens)[b];
   };
   int tile;  // of the first item
   auto first_item = [&]() {
-    const uint64_t past = p.small ? __ballot((uint32_t)upto * (uint32_t)items_per_seq > (uint32_t)pos)
-                                  : __ballot(upto * items_per_seq > pos);
-    const int run_lane = __builtin_ctzll(past);
-    int64_t begin;  // first tile of sequence b
-    if (__builtin_expect(p.small, 1)) begin = (uint32_t)__builtin_amdgcn_readlane((int)(upto - mine), run_lane) * (uint32_t)items_per_seq;
-    else begin = uniform64(__shfl(upto - mine, run_lane)) * items_per_seq;
+    const int run_lane = __builtin_ctzll(__ballot(upto * items_per_seq > pos));
+    int32_t begin = __builtin_amdgcn_readlane(upto - mine, run_lane) * items_per_seq;  // first tile of sequence b
     int b = run_lane * run;
     SeqSpan seq(p, length_of(b));
-    while (begin + (int64_t)seq.tiles * items_per_seq <= pos) {
-      begin += (int64_t)seq.tiles * items_per_seq;
+    while (begin + seq.tiles * items_per_seq <= pos) {
+      begin += seq.tiles * items_per_seq;
       seq = SeqSpan(p, length_of(++b));
     }
-    const int64_t rel = pos - begin;
-    const int item = __builtin_expect(rel < ((int64_t)1 << 32), 1) ? (int)((uint32_t)rel / (uint32_t)seq.tiles) : (int)(rel / seq.tiles);
-    tile = (int)(rel - (int64_t)item * seq.tiles);
+    tile = pos - begin;
+    int item = 0;
+    if (tile >= seq.tiles) {
+      item = (int)((uint32_t)tile / (uint32_t)seq.tiles);
+      tile -= item * seq.tiles;
+    }
     const int hk = p.head_tiles == 1 ? item : (int)((uint32_t)item / (uint32_t)p.head_tiles);
     return AttnItem{b, hk, item - hk * p.head_tiles, seq};
   };
@@ -358,7 +339,7 @@ __global__ __launch_bounds__(kThreads, FMT == HUM_ACT_BF16 && D == 256 ? 1 : 2) 
   // page numbers of one tile, then its K and V.
   AttnItem ft = cur;
   int ft_tile = tile;
-  int64_t ft_left = end - pos;
+  int32_t ft_left = end - pos;
   struct Pages {
     int32_t t0, lo, p0, p1;
     const uint8_t* base;
@@ -435,9 +416,9 @@ __global__ __launch_bounds__(kThreads, FMT == HUM_ACT_BF16 && D == 256 ? 1 : 2) 
   while (true) {
     const int heads = p.group - cur.ht * 16 < 16 ? p.group - cur.ht * 16 : 16;  // live columns
     const int q_head = cur.hk * p.group + cur.ht * 16;
-    const int64_t share = end - pos;
-    const int tile_end = cur.seq.tiles - tile < share ? cur.seq.tiles : tile + (int)share;
-    const int64_t left = share - (tile_end - tile);
+    const int32_t share = end - pos;
+    const int tile_end = cur.seq.tiles - tile < share ? cur.seq.tiles : tile + share;
+    const int32_t left = share - (tile_end - tile);
     AttnItem nxt = cur;
     if (left > 0) next_item(nxt);
 
@@ -637,16 +618,9 @@ __global__ __launch_bounds__(kThreads, FMT == HUM_ACT_BF16 && D == 256 ? 1 : 2) 
       // rounds of parts are joined in groups first, whose joins are then
       // joined (a round of reads costs about half of a level: storing, the
       // arrival and reading again).
-      const int64_t begin = pos - tile;
-      int64_t first, last;
-      if (__builtin_expect(p.small, 1)) {
-        first = ((uint32_t)((begin + 1) * nwg) - 1u) / (uint32_t)total;
-        last = ((uint32_t)((begin + cur.seq.tiles) * nwg) - 1u) / (uint32_t)total;
-      } else {
-        first = ((begin + 1) * nwg - 1) / total;
-        last = ((begin + cur.seq.tiles) * nwg - 1) / total;
-      }
-      const int w0 = (int)uniform64(first), nseg = (int)uniform64(last) - w0 + 1, seg = (int)wg - w0;
+      const int32_t begin = pos - tile;
+      const int w0 = __builtin_amdgcn_readfirstlane(owner(begin));
+      const int nseg = __builtin_amdgcn_readfirstlane(owner(begin + cur.seq.tiles - 1)) - w0 + 1, seg = wg - w0;
       const __amdgpu_buffer_rsrc_t rp =
           __builtin_amdgcn_make_buffer_rsrc(p.part, (short)0, (int)p.part_bytes, 0x00020000);
       const uint32_t part_floats = (uint32_t)p.part_heads * (D + 2);
@@ -785,6 +759,11 @@ __global__ __launch_bounds__(kThreads, FMT == HUM_ACT_BF16 && D == 256 ? 1 : 2) 
   }
 }
 
+// (sequence, key-value head, 16 query heads) of a call.
+static int64_t attn_items(const hum_kv_desc* d, int32_t num_q_heads, int64_t batch) {
+  return batch * d->num_kv_heads * ((num_q_heads / d->num_kv_heads + 15) / 16);
+}
+
 // Workgroups of a call: never more than there can be tiles.  One on every CU
 // where there are fewer heads (of all sequences) than kAttnWgs and a wave's
 // tile is large enough to keep the memory busy (rows of 128 bytes and more;
@@ -797,9 +776,8 @@ __global__ __launch_bounds__(kThreads, FMT == HUM_ACT_BF16 && D == 256 ? 1 : 2) 
 // 256 short ones, 4096 heads: 63 and 82), and with small rows (32 sequences
 // in MXFP4 of 128-wide heads, 512 MiB: 5.3 TB/s with 512, 4.0 with 256).
 static int attn_wgs(const hum_kv_desc* d, int32_t num_q_heads, int64_t batch, int64_t max_pages) {
-  const int64_t group = num_q_heads / d->num_kv_heads;
   const int64_t tiles = max_pages * d->page_size / kTile + 1;
-  const int64_t all = batch * d->num_kv_heads * ((group + 15) / 16);
+  const int64_t all = attn_items(d, num_q_heads, batch);
   const bool once = d->fmt == HUM_ACT_BF16 && d->head_dim == 256;
   const bool wide = d->fmt != HUM_ACT_MXFP4 && d->head_dim * (d->fmt == HUM_ACT_BF16 ? 2 : 1) >= 128;
   const int64_t most = once || (wide && all < kAttnWgs) ? kAttnWgs / 2 : kAttnWgs;
@@ -824,6 +802,8 @@ static hum_status check_attn(const hum_kv_desc* d, int32_t num_q_heads, int64_t 
   if (batch < 0 || batch > 0xFFFF) return set_error(HUM_ERR_INVALID_ARG, "batch must be 0 .. 65535");
   if (max_pages < 0 || max_pages > ((int64_t)1 << 30) / d->page_size)
     return set_error(HUM_ERR_INVALID_ARG, "max_pages must be >= 0, sequences at most 2^30 tokens");
+  if (attn_items(d, num_q_heads, batch) * (max_pages * d->page_size / kTile + 1) >= (int64_t)1 << 31)
+    return set_error(HUM_ERR_UNSUPPORTED, "batch x heads x max_pages x page_size must stay below 2^38");
   return HUM_OK;
 }
 
@@ -881,10 +861,6 @@ hum_status hum_kv_attention(const hum_kv_desc* desc, const void* cache, size_t c
   p.batch = (int32_t)batch;
   p.window = (int32_t)(window < ((int64_t)1 << 30) ? window : (int64_t)1 << 30);
   p.seq_lens = seq_lens;
-  {
-    const int64_t all = batch * p.kv_heads * p.head_tiles, tiles = max_pages * desc->page_size / kTile + 1;
-    p.small = all < ((int64_t)1 << 31) / (tiles * kAttnWgs);
-  }
   p.scale_log2 = (float)((double)scale * 1.4426950408889634);
   p.out = static_cast<uint16_t*>(out_bf16);
   p.lse = lse;

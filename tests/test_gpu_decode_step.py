@@ -174,9 +174,9 @@ def test_side_streams_and_shared_workspaces():
     assert not ws[:64 << 10].any()
 
 
-def test_attention_table_wide_enough_for_64_bit_tiles():
-    """A block table whose width alone (not the lengths) passes 32-bit tile
-    arithmetic: the same bits as with a narrow one."""
+def test_attention_table_of_millions_of_pages():
+    """A block table as wide as the longest sequences a call may have, its
+    entries past the lengths never read as pages."""
     c = Case(70, "bf16", [3000, 0, 129], 4, 2, 64, 16)
     mp = 6_000_000
     wide = torch.full((3, mp), -1, dtype=torch.int32, device="cuda")

@@ -153,6 +153,7 @@ def test_attention_abi_refusals(lib):
     assert call(q=None) == 1 and call(q=P(65)) == 1 and call(tab=None) == 1 and call(lens=None) == 1
     assert call(out=None) == 1 and call(out=P(72)) == 1 and call(c=P(72)) == 1 and call(mp=-1) == 1
     assert call(mp=1 << 30) == 1 and call(win=-1) == 1 and call(scale=float("nan")) == 1
+    assert call(b=65535, mp=1 << 24) == 2 and call(b=65536) == 1      # tiles past 32 bits, too many sequences
     assert call(scale=float("inf")) == 1 and call(ws=None) == 1 and call(wsb=need - 1) == 3 and call(b=0) == 0
     for bad in (dict(num_q_heads=3), dict(batch=-1), dict(max_pages=-1)):
         kw = dict(num_q_heads=4, batch=3, max_pages=2)
