@@ -57,6 +57,42 @@ struct KvPlace {
   }
 };
 
+// Max over the N lanes (8, 16 or 32) that hold one row.
+template <int N>
+__device__ __forceinline__ float row_max(float v) {
+  v = quad_max(v);
+  auto with = [&](auto ctrl) {
+    v = __builtin_fmaxf(v, __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), decltype(ctrl)::value, 0xF, 0xF, false)));
+  };
+  with(std::integral_constant<int, 0x141>{});                         // row_half_mirror: the other quad of eight
+  if constexpr (N >= 16) with(std::integral_constant<int, 0x140>{});  // row_mirror: the other eight of sixteen
+  if constexpr (N >= 32) v = __builtin_fmaxf(v, __shfl_xor(v, 16));
+  return v;
+}
+
+// f[i] / s as an IEEE f32 division gives it (the FP8 rule's quotient: a code
+// can hang on its last bit), for eight values: with y = RN(1 / s), q = RN(f y)
+// and the exact remainder r = f - q s, RN(q + r y) is the rounded quotient
+// (Markstein, "Computation of elementary functions on the IBM RISC
+// System/6000 processor", 1990), four instructions a value where the
+// division takes eleven.  That holds while nothing over- or underflows: s
+// within [2^-80, 2^120] (values below 2^-10 s, whose remainder may underflow,
+// become zero codes either way); other scales divide.  The sign is set from
+// f: q + r y loses that of -0.
+__device__ __forceinline__ void divide8(float (&f)[8], float s) {
+  if (s >= 0x1p-80f && s <= 0x1p120f) {
+    const float y = 1.0f / s;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float q = f[i] * y;
+      f[i] = __builtin_copysignf(__builtin_fmaf(__builtin_fmaf(-q, s, f[i]), y, q), f[i]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = f[i] / s;
+  }
+}
+
 // Byte offsets of token `at` of a page inside its (page, head) unit: its code
 // row, and its scale (or the first of them) with the step to the next.
 template <int FMT, int D>
@@ -131,12 +167,12 @@ __global__ __launch_bounds__(256) void kv_write_kernel(const KvMoveParams p) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) amax = __builtin_fmaxf(amax, __builtin_fabsf(f[i]));
         if constexpr (FMT == HUM_ACT_FP8_TOKEN) {
-#pragma unroll
-          for (int m = 1; m < me.kLanes; m *= 2) amax = __builtin_fmaxf(amax, __shfl_xor(amax, m));
+          amax = row_max<D / 8>(amax);
           const float sc = amax > 0.0f ? amax / 448.0f : 1.0f;  // IEEE f32 division
+          divide8(f, sc);
           u32x2_t o;
-          o[0] = f32x2_to_e4m3x2(f[0] / sc, f[1] / sc) | (f32x2_to_e4m3x2(f[2] / sc, f[3] / sc) << 16);
-          o[1] = f32x2_to_e4m3x2(f[4] / sc, f[5] / sc) | (f32x2_to_e4m3x2(f[6] / sc, f[7] / sc) << 16);
+          o[0] = f32x2_to_e4m3x2(f[0], f[1]) | (f32x2_to_e4m3x2(f[2], f[3]) << 16);
+          o[1] = f32x2_to_e4m3x2(f[4], f[5]) | (f32x2_to_e4m3x2(f[6], f[7]) << 16);
           if (live) {
             *reinterpret_cast<u32x2_t*>(code) = o;
             if (me.lane == 0) *reinterpret_cast<float*>(scale) = sc;

@@ -76,6 +76,37 @@ def test_cache_bytes_and_round_trip(fmt, t, h, d, ps):
     assert torch.equal(cache, cache2)
 
 
+@pytest.mark.parametrize("exponent", [0, -69, -71, -126, 120, 127])
+def test_fp8_rows_of_every_quotient(exponent):
+    """Every bf16 mantissa over every scale's: rows whose maximum has each of
+    the 128 mantissas and whose other values are all bf16 down to 2^-13 of it,
+    both signs, so that no quotient near a rounding border is missed; exponents
+    on both sides of where the division changes its form."""
+    vals = ((np.arange(13 * 128, dtype=np.int64)) + ((exponent + 127 - 12) << 7))
+    vals = vals[vals >= 0]
+    rows = []
+    for m in range(128):
+        top = ((exponent + 127) << 7) + m
+        low = vals[vals <= top]
+        low = np.concatenate([low, low + 0x8000, [0x8000, 0]])
+        pad = -len(low) % 127
+        low = np.concatenate([low, np.zeros(pad, np.int64)]).reshape(-1, 127)
+        rows.append(np.concatenate([np.full((len(low), 1), top), low], 1))
+    x = np.concatenate(rows).astype(np.uint16)
+    t = len(x)
+    desc = hum.make_kv_desc("fp8_token", -(-t // 16), 16, 1, 128)
+    ref, _ = A.quantize_rows(x, "fp8_token")
+    cache = torch.zeros(hum.kv_cache_bytes(desc), dtype=torch.uint8, device="cuda")
+    xb = _bf(x).view(t, 1, 128)
+    hum.kv_write(desc, cache, xb, xb, torch.arange(t, device="cuda"))
+    unit = cache.view(-1, 2 * 16 * 132).cpu().numpy()
+    for which in (0, 1):
+        got = unit[:, which * 16 * 128:(which + 1) * 16 * 128].reshape(-1, 128)[:t]
+        assert np.array_equal(got, ref), np.argwhere(got != ref)[:5]
+    scales = unit[:, 2 * 16 * 128:2 * 16 * 128 + 64].copy().view(np.float32).reshape(-1)[:t]
+    assert np.array_equal(scales, A.quantize_rows(x, "fp8_token")[1].view(np.float32).reshape(-1))
+
+
 def test_cache_empty_call_and_repeated_reads():
     desc = hum.make_kv_desc("fp8_token", 2, 16, 1, 64)
     cache = torch.zeros(hum.kv_cache_bytes(desc), dtype=torch.uint8, device="cuda")
