@@ -519,7 +519,8 @@ hum_status hum_rotary_inv_freq(int32_t rotary_dim, double base, int32_t scaling,
  *               output do not overlap
  *   out       : may be the input itself (same pointer and strides), but may
  *               not overlap it otherwise, nor the other input and output
- * q (with q_out) or k (with k_out) may be NULL where its head count is 0. */
+ * q (with q_out) or k (with k_out) may be NULL where its head count is 0.
+ * At most 2^24 - 1 tokens in a call. */
 hum_status hum_rotary(const hum_rotary_desc* desc, int64_t num_tokens, const int64_t* positions,
                       const double* inv_freq, const void* q, int64_t q_token_stride, int64_t q_head_stride,
                       void* q_out, int64_t q_out_token_stride, int64_t q_out_head_stride, const void* k,
@@ -554,7 +555,10 @@ size_t hum_kv_cache_bytes(const hum_kv_desc* desc);
  *   slots : i64 [T]; a slot outside [0, num_pages * page_size) is skipped.
  *           The others must differ: a slot that a call names twice holds
  *           parts of either row afterwards.
- *   strides in elements, head elements contiguous. */
+ *   strides in elements, head elements contiguous.
+ * An infinity or NaN is kept in bf16; in the other formats the row that it is
+ * in (its block of 32, MX) holds no meaningful codes afterwards.
+ * At most 2^24 - 1 tokens in a call (hum_kv_read too). */
 hum_status hum_kv_write(const hum_kv_desc* desc, void* cache, size_t cache_bytes, int64_t num_tokens,
                         const int64_t* slots, const void* k_bf16, int64_t k_token_stride, int64_t k_head_stride,
                         const void* v_bf16, int64_t v_token_stride, int64_t v_head_stride, void* stream);
@@ -580,6 +584,9 @@ size_t hum_kv_attention_workspace_bytes(const hum_kv_desc* desc, int32_t num_q_h
  * is -inf.  Nothing past n or before the window reaches the result, whatever
  * the cache holds there; the values that do take part have to be finite (an
  * infinity or NaN among them makes what it reaches NaN).
+ * batch is at most 65535, max_pages * page_size at most 2^30, and
+ * batch * num_kv_heads * ceil(query heads per key-value head / 16) *
+ * (max_pages * page_size + 128) stays below 2^38.
  *   q           : bf16 [batch][num_q_heads][head_dim], strides in elements;
  *                 head h reads key-value head h / (num_q_heads / num_kv_heads)
  *   block_table : i32 [batch][max_pages], rows table_stride apart; entry

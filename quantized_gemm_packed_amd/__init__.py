@@ -816,7 +816,10 @@ def kv_attention(desc: KvDesc, cache, q, block_table, seq_lens, scale: float | N
     """bf16 out [B, Hq, D] (and float32 lse [B, Hq] with return_lse) of one
     query row per sequence, q bf16 [B, Hq, D], over the first seq_lens int32
     [B] tokens (the last `window` of them, if not 0) of the pages that
-    block_table int32 [B, max_pages] names.  scale defaults to D ** -0.5."""
+    block_table int32 [B, max_pages] names.  scale defaults to D ** -0.5.
+    workspace: uint8 of kv_attention_workspace_bytes(...), zeroed before its
+    first call and not shared by calls that may overlap in time; by default
+    the current stream's own, or a captured graph's own."""
     return (_nat or _native()).kv_attention(desc, cache, q, block_table, seq_lens, scale, window, out, return_lse,
                                             workspace)
 

@@ -283,6 +283,7 @@ PyObject* kv_read(PyObject*, PyObject* const* a, Py_ssize_t n) {
     want_contiguous(*out[i], names[i]);
   }
   const int dev = device_of("cache", {cache, &slots, out[0], out[1]});
+  if (!hum_kv_cache_bytes(desc.d)) raise_status(HUM_ERR_UNSUPPORTED);
   at::Tensor fresh[2];
   for (int i = 0; i < 2; ++i) {
     if (out[i]) continue;

@@ -830,7 +830,8 @@ hum_status hum_kv_attention(const hum_kv_desc* desc, const void* cache, size_t c
   hum_status st = check_attn(desc, num_q_heads, batch, max_pages, &l);
   if (st != HUM_OK) return st;
   if (window < 0) return set_error(HUM_ERR_INVALID_ARG, "window must be >= 0");
-  if (!(scale - scale == 0.0f)) return set_error(HUM_ERR_INVALID_ARG, "scale must be finite");
+  const float scale_log2 = (float)((double)scale * 1.4426950408889634);
+  if (!(scale_log2 - scale_log2 == 0.0f)) return set_error(HUM_ERR_INVALID_ARG, "scale must be finite (times log2 e too)");
   if (batch == 0) return HUM_OK;
   if (!cache || !q_bf16 || (max_pages && !block_table) || !seq_lens || !out_bf16 || !workspace)
     return set_error(HUM_ERR_INVALID_ARG, "NULL pointer");
@@ -839,6 +840,9 @@ hum_status hum_kv_attention(const hum_kv_desc* desc, const void* cache, size_t c
     return set_error(HUM_ERR_INVALID_ARG, "the workspace must be 16-byte aligned");
   if (reinterpret_cast<uintptr_t>(q_bf16) % 2 || reinterpret_cast<uintptr_t>(out_bf16) % 16)
     return set_error(HUM_ERR_INVALID_ARG, "q must be aligned to its elements, out to 16 bytes");
+  // (scalar loads drop an address's low bits)
+  if ((reinterpret_cast<uintptr_t>(block_table) | reinterpret_cast<uintptr_t>(seq_lens) | reinterpret_cast<uintptr_t>(lse)) % 4)
+    return set_error(HUM_ERR_INVALID_ARG, "block_table, seq_lens and lse must be aligned to their elements");
   if (cache_bytes < (size_t)l.bytes)
     return set_error(HUM_ERR_WORKSPACE, "cache of %zu bytes, the description takes %lld", cache_bytes, (long long)l.bytes);
   const size_t need = hum_kv_attention_workspace_bytes(desc, num_q_heads, batch, max_pages);
@@ -861,7 +865,7 @@ hum_status hum_kv_attention(const hum_kv_desc* desc, const void* cache, size_t c
   p.batch = (int32_t)batch;
   p.window = (int32_t)(window < ((int64_t)1 << 30) ? window : (int64_t)1 << 30);
   p.seq_lens = seq_lens;
-  p.scale_log2 = (float)((double)scale * 1.4426950408889634);
+  p.scale_log2 = scale_log2;
   p.out = static_cast<uint16_t*>(out_bf16);
   p.lse = lse;
   p.count = static_cast<uint32_t*>(workspace);

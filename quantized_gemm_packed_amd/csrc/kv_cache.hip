@@ -303,6 +303,7 @@ static hum_status kv_move_params(const hum_kv_desc* d, const void* cache, size_t
   if (num_tokens == 0) return HUM_OK;
   if (!cache || !slots) return set_error(HUM_ERR_INVALID_ARG, "NULL pointer");
   if (reinterpret_cast<uintptr_t>(cache) % 16) return set_error(HUM_ERR_INVALID_ARG, "the cache must be 16-byte aligned");
+  if (reinterpret_cast<uintptr_t>(slots) % 8) return set_error(HUM_ERR_INVALID_ARG, "slots must be aligned to its elements");
   if (cache_bytes < (size_t)l.bytes)
     return set_error(HUM_ERR_WORKSPACE, "cache of %zu bytes, the description takes %lld", cache_bytes, (long long)l.bytes);
   // (a grid holds at most 2^32 - 1 threads)
@@ -391,8 +392,10 @@ hum_status hum_kv_read(const hum_kv_desc* desc, const void* cache, size_t cache_
   hum_status st = kv_move_params(desc, cache, cache_bytes, num_tokens, slots, &p);
   if (st != HUM_OK || num_tokens == 0) return st;
   if (!k_out || !v_out) return set_error(HUM_ERR_INVALID_ARG, "NULL pointer");
-  if (k_out == v_out) return set_error(HUM_ERR_INVALID_ARG, "k_out and v_out must be two buffers");
-  if ((reinterpret_cast<uintptr_t>(k_out) | reinterpret_cast<uintptr_t>(v_out)) % 16)
+  const uintptr_t ka = reinterpret_cast<uintptr_t>(k_out), va = reinterpret_cast<uintptr_t>(v_out);
+  if ((ka < va ? va - ka : ka - va) < (uintptr_t)num_tokens * desc->num_kv_heads * desc->head_dim * 2)
+    return set_error(HUM_ERR_INVALID_ARG, "k_out and v_out must not overlap");
+  if ((ka | va) % 16)
     return set_error(HUM_ERR_INVALID_ARG, "k_out and v_out must be 16-byte aligned");
   p.out[0] = static_cast<uint16_t*>(k_out);
   p.out[1] = static_cast<uint16_t*>(v_out);

@@ -236,6 +236,8 @@ hum_status hum_rotary(const hum_rotary_desc* d, int64_t num_tokens, const int64_
   if (num_tokens == 0 || hall == 0) return HUM_OK;
   if (!positions || !inv_freq || (d->num_q_heads && (!q || !q_out)) || (d->num_kv_heads && (!k || !k_out)))
     return set_error(HUM_ERR_INVALID_ARG, "NULL pointer");
+  if ((reinterpret_cast<uintptr_t>(positions) | reinterpret_cast<uintptr_t>(inv_freq)) % 8)
+    return set_error(HUM_ERR_INVALID_ARG, "positions and inv_freq must be aligned to their elements");
   if (d->num_q_heads && d->num_kv_heads && (q_out == k_out || q_out == k || k_out == q))
     return set_error(HUM_ERR_INVALID_ARG, "q's output must be another buffer than k and its output, k's another than q");
   const int size = d->dtype == HUM_BF16 ? 2 : 4;

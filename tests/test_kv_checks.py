@@ -192,3 +192,23 @@ def test_binding_refuses_what_is_no_tensor_or_description(lib):
         hum.rotary(torch._neg_view(k.float()), None, s, torch.zeros(32, dtype=torch.float64))
     with pytest.raises((ValueError, TypeError)):
         hum.kv_attention(d, cache, q, tab, n, window=1.5)
+
+
+def test_addresses_that_a_kernel_cannot_read_are_refused(lib):
+    d = hum.make_kv_desc("bf16", 4, 16, 2, 64)
+    a, nb, need = ctypes.addressof(d), hum.kv_cache_bytes(d), hum.kv_attention_workspace_bytes(d, 4, 3, 2)
+
+    def attn(tab=P(64), lens=P(64), lse=None, scale=1.0):
+        return lib.hum_kv_attention(a, P(64), nb, 4, 3, P(64), 256, 64, tab, 2, 2, lens, 0, scale, P(64), lse, P(256),
+                                    need, None)
+    assert attn(tab=P(66)) == 1 and attn(lens=P(65)) == 1 and attn(lse=P(66)) == 1
+    assert attn(scale=3e38) == 1                                     # infinite in base 2
+    assert lib.hum_kv_write(a, P(64), nb, 3, P(12), P(64), 128, 64, P(64), 128, 64, None) == 1
+    # outputs of 3 x 2 x 64 bf16 = 768 bytes that share their last or first 16
+    assert lib.hum_kv_read(a, P(64), nb, 3, P(8), P(1024), P(1024 + 752), None) == 1
+    assert lib.hum_kv_read(a, P(64), nb, 3, P(8), P(1024 + 752), P(1024), None) == 1
+    assert lib.hum_kv_read(a, P(64), nb, 3, P(12), P(1024), P(4096), None) == 1
+    r = hum.RotaryDesc(hum.BF16, 0, 64, 64, 2, 0, 0, 1.0)
+    for pos, freq in ((P(20), P(16)), (P(16), P(20))):
+        assert lib.hum_rotary(ctypes.addressof(r), 4, pos, freq, P(64), 128, 64, P(4096), 128, 64, None, 0, 0, None, 0, 0,
+                              None) == 1
