@@ -585,8 +585,7 @@ size_t hum_kv_attention_workspace_bytes(const hum_kv_desc* desc, int32_t num_q_h
  * the cache holds there; the values that do take part have to be finite (an
  * infinity or NaN among them makes what it reaches NaN).
  * batch is at most 65535, max_pages * page_size at most 2^30, and
- * batch * num_kv_heads * ceil(query heads per key-value head / 16) *
- * (max_pages * page_size + 128) stays below 2^38.
+ * batch * num_kv_heads * (max_pages * page_size + 128) stays below 2^38.
  *   q           : bf16 [batch][num_q_heads][head_dim], strides in elements;
  *                 head h reads key-value head h / (num_q_heads / num_kv_heads)
  *   block_table : i32 [batch][max_pages], rows table_stride apart; entry

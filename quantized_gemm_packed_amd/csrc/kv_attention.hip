@@ -62,6 +62,7 @@ struct KvAttnParams {
   float* part;      // kSlots slots per workgroup
   uint32_t part_bytes;
   int32_t part_heads;  // heads of a slot: m, l and O rows
+  int32_t wgs;         // workgroups of one head tile
 };
 
 constexpr int kWaves = 4;                  // of a workgroup
@@ -157,9 +158,9 @@ struct SeqSpan {
   }
 };
 
-// One (sequence, key-value head, 16 query heads).
+// One (sequence, key-value head), for a workgroup's 16 query heads of it.
 struct AttnItem {
-  int32_t b, hk, ht;
+  int32_t b, hk;
   SeqSpan seq;
 };
 
@@ -205,7 +206,17 @@ __global__ __launch_bounds__(kThreads, FMT == HUM_ACT_BF16 && D == 256 ? 1 : 2) 
   // costs is latency before the first load: the lengths are read once, the
   // scan stays in registers, and tiles are counted in 32 bits, which the host
   // checks.)
-  const int items_per_seq = p.kv_heads * p.head_tiles;
+  // Where more than 16 query heads share a key-value head, as many
+  // workgroups as that takes have the same share of the cache, on one XCD
+  // (workgroups go to the eight in turn): they read it at about the same
+  // time, so that all but one find it in the XCD's L2.
+  const int turn = (int)blockIdx.x >> 3;
+  const int wg8 = p.head_tiles == 1 ? turn : (int)((uint32_t)turn / (uint32_t)p.head_tiles);
+  const int wg = wg8 * 8 + ((int)blockIdx.x & 7);   // among those of its 16 query heads
+  const int ht = turn - wg8 * p.head_tiles;         // which 16
+  const int wg_base = ht * p.wgs;                   // of its slots and counters
+  const int heads = p.group - ht * 16 < 16 ? p.group - ht * 16 : 16;  // live columns
+  const int items_per_seq = p.kv_heads;
   const int run = (p.batch + 63) / 64;
   int32_t len = 0;  // of the lane's last sequence: the only one in batches of up to 64
   int32_t mine = 0;
@@ -223,7 +234,7 @@ __global__ __launch_bounds__(kThreads, FMT == HUM_ACT_BF16 && D == 256 ? 1 : 2) 
   // tiles in a row cost about as much as joining parts (16 sequences of 333
   // FP8 tokens: 9.8 us cut, 8.2 whole; one of 200: 8.3 and 6.9).
   const int32_t items = p.batch * items_per_seq, most = total <= 3 * (int64_t)items ? items : total;
-  const int32_t nwg = most < (int32_t)gridDim.x ? most : (int32_t)gridDim.x, wg = blockIdx.x;
+  const int32_t nwg = most < p.wgs ? most : p.wgs;
   if (wg >= nwg) return;
   // shares of `each` tiles, the first `longer` of them one more
   const int32_t each = nwg == total ? 1 : (int32_t)((uint32_t)total / (uint32_t)nwg), longer = total - each * nwg;
@@ -254,17 +265,13 @@ __global__ __launch_bounds__(kThreads, FMT == HUM_ACT_BF16 && D == 256 ? 1 : 2) 
       item = (int)((uint32_t)tile / (uint32_t)seq.tiles);
       tile -= item * seq.tiles;
     }
-    const int hk = p.head_tiles == 1 ? item : (int)((uint32_t)item / (uint32_t)p.head_tiles);
-    return AttnItem{b, hk, item - hk * p.head_tiles, seq};
+    return AttnItem{b, item, seq};
   };
   auto next_item = [&](AttnItem& i) {
-    if (++i.ht == p.head_tiles) {
-      i.ht = 0;
-      if (++i.hk == p.kv_heads) {
-        i.hk = 0;
-        ++i.b;
-        i.seq = SeqSpan(p, length_of(i.b));
-      }
+    if (++i.hk == p.kv_heads) {
+      i.hk = 0;
+      ++i.b;
+      i.seq = SeqSpan(p, length_of(i.b));
     }
   };
   AttnItem cur = first_item();
@@ -378,12 +385,11 @@ __global__ __launch_bounds__(kThreads, FMT == HUM_ACT_BF16 && D == 256 ? 1 : 2) 
   constexpr int kQN = 16 * (D / 8) > kThreads ? 16 * (D / 8) / kThreads : 1;  // 16-byte pieces of a thread
   u32x4_t qn[kQN];
   auto load_q = [&](const AttnItem& w) {
-    const int live = p.group - w.ht * 16 < 16 ? p.group - w.ht * 16 : 16;
-    const uint16_t* q = p.q + w.b * p.q_ts + (int64_t)(w.hk * p.group + w.ht * 16) * p.q_hs;
+    const uint16_t* q = p.q + w.b * p.q_ts + (int64_t)(w.hk * p.group + ht * 16) * p.q_hs;
 #pragma unroll
     for (int i = 0; i < kQN; ++i) {
       int h = (threadIdx.x + i * kThreads) / (D / 8);
-      h = h < live ? h : live - 1;  // (dead columns repeat a live row and are never stored)
+      h = h < heads ? h : heads - 1;  // (dead columns repeat a live row and are never stored)
       const Bytes16 v = *reinterpret_cast<const Bytes16*>(q + h * p.q_hs + (threadIdx.x % (D / 8)) * 8);
       qn[i] = u32x4_t{v.w[0], v.w[1], v.w[2], v.w[3]};
     }
@@ -414,8 +420,7 @@ __global__ __launch_bounds__(kThreads, FMT == HUM_ACT_BF16 && D == 256 ? 1 : 2) 
   __syncthreads();
 
   while (true) {
-    const int heads = p.group - cur.ht * 16 < 16 ? p.group - cur.ht * 16 : 16;  // live columns
-    const int q_head = cur.hk * p.group + cur.ht * 16;
+    const int q_head = cur.hk * p.group + ht * 16;
     const int32_t share = end - pos;
     const int tile_end = cur.seq.tiles - tile < share ? cur.seq.tiles : tile + share;
     const int32_t left = share - (tile_end - tile);
@@ -628,7 +633,7 @@ __global__ __launch_bounds__(kThreads, FMT == HUM_ACT_BF16 && D == 256 ? 1 : 2) 
       // inside, 1 of one that it begins; 2 and 3 the joins of the groups of
       // parts that those lead.
       auto slot = [&](int sg, bool joined) {
-        return (uint32_t)((w0 + sg) * kSlots + (sg == 0 ? 1 : 0) + (joined ? 2 : 0)) * part_floats * 4;
+        return (uint32_t)((wg_base + w0 + sg) * kSlots + (sg == 0 ? 1 : 0) + (joined ? 2 : 0)) * part_floats * 4;
       };
       auto put = [&](uint32_t at, int h, int d, f32x4_t o, float top, float sum) {
         __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, o), rp, at + (h * D + d) * 4, 0, kDevScope);
@@ -726,14 +731,14 @@ __global__ __launch_bounds__(kThreads, FMT == HUM_ACT_BF16 && D == 256 ? 1 : 2) 
       // of the part that leads it, after those
       const int lanes = heads * (D / 4) >= kThreads ? 1 : kThreads / (heads * (D / 4));
       const int round = kJoin * lanes;
-      int counter = w0, sg = 0, step = 1, n = nseg, size = 0;
+      int counter = wg_base + w0, sg = 0, step = 1, n = nseg, size = 0;
       bool joined = false;  // whether the parts are joins of groups
       if (nseg > 2 * round) {
         size = 8;
         while (size < round || size * 2 * round < nseg) size *= 2;
         sg = seg & ~(size - 1);
         n = nseg - sg < size ? nseg - sg : size;
-        counter = kAttnWgs + 2 * (w0 + sg) + (sg == 0 ? 1 : 0);
+        counter = kAttnWgs + 2 * (wg_base + w0 + sg) + (sg == 0 ? 1 : 0);
       }
       while (arrive(counter, n)) {
         const bool final = size == 0 || joined;
@@ -744,7 +749,7 @@ __global__ __launch_bounds__(kThreads, FMT == HUM_ACT_BF16 && D == 256 ? 1 : 2) 
         });
         if (final) break;
         joined = true;
-        counter = w0;
+        counter = wg_base + w0;
         sg = 0;
         step = size;
         n = (nseg + size - 1) / size;
@@ -759,12 +764,12 @@ __global__ __launch_bounds__(kThreads, FMT == HUM_ACT_BF16 && D == 256 ? 1 : 2) 
   }
 }
 
-// (sequence, key-value head, 16 query heads) of a call.
-static int64_t attn_items(const hum_kv_desc* d, int32_t num_q_heads, int64_t batch) {
-  return batch * d->num_kv_heads * ((num_q_heads / d->num_kv_heads + 15) / 16);
+// Blocks of 16 query heads that share a key-value head.
+static int attn_head_tiles(const hum_kv_desc* d, int32_t num_q_heads) {
+  return (num_q_heads / d->num_kv_heads + 15) / 16;
 }
 
-// Workgroups of a call: never more than there can be tiles.  One on every CU
+// Workgroups of a call, per block of 16 query heads: never more than there can be tiles.  One on every CU
 // where there are fewer heads (of all sequences) than kAttnWgs and a wave's
 // tile is large enough to keep the memory busy (rows of 128 bytes and more;
 // E2M1 codes take too many instructions a byte for one wave per SIMD): fewer
@@ -776,12 +781,13 @@ static int64_t attn_items(const hum_kv_desc* d, int32_t num_q_heads, int64_t bat
 // 256 short ones, 4096 heads: 63 and 82), and with small rows (32 sequences
 // in MXFP4 of 128-wide heads, 512 MiB: 5.3 TB/s with 512, 4.0 with 256).
 static int attn_wgs(const hum_kv_desc* d, int32_t num_q_heads, int64_t batch, int64_t max_pages) {
-  const int64_t tiles = max_pages * d->page_size / kTile + 1;
-  const int64_t all = attn_items(d, num_q_heads, batch);
+  const int64_t tiles = max_pages * d->page_size / kTile + 1, items = batch * d->num_kv_heads;
+  const int head_tiles = attn_head_tiles(d, num_q_heads);
   const bool once = d->fmt == HUM_ACT_BF16 && d->head_dim == 256;
   const bool wide = d->fmt != HUM_ACT_MXFP4 && d->head_dim * (d->fmt == HUM_ACT_BF16 ? 2 : 1) >= 128;
-  const int64_t most = once || (wide && all < kAttnWgs) ? kAttnWgs / 2 : kAttnWgs;
-  return (int)(all * tiles >= most ? most : all * tiles < 1 ? 1 : all * tiles);
+  int64_t most = (once || (wide && items * head_tiles < kAttnWgs) ? kAttnWgs / 2 : kAttnWgs) / head_tiles;
+  if (most > 8) most &= ~7;  // the grid is made of eights
+  return (int)(items * tiles >= most ? most : items * tiles < 1 ? 1 : items * tiles);
 }
 
 // Heads of a slot (even: slots stay 16-byte aligned), and the slots' bytes.
@@ -790,7 +796,7 @@ static int attn_part_heads(const hum_kv_desc* d, int32_t num_q_heads) {
   return group >= 16 ? 16 : (group + 1) & ~1;
 }
 static size_t attn_part_bytes(const hum_kv_desc* d, int32_t num_q_heads, int64_t batch, int64_t max_pages) {
-  return (size_t)attn_wgs(d, num_q_heads, batch, max_pages) * kSlots * attn_part_heads(d, num_q_heads) *
+  return (size_t)attn_wgs(d, num_q_heads, batch, max_pages) * attn_head_tiles(d, num_q_heads) * kSlots * attn_part_heads(d, num_q_heads) *
          (d->head_dim + 2) * 4;
 }
 
@@ -802,8 +808,8 @@ static hum_status check_attn(const hum_kv_desc* d, int32_t num_q_heads, int64_t 
   if (batch < 0 || batch > 0xFFFF) return set_error(HUM_ERR_INVALID_ARG, "batch must be 0 .. 65535");
   if (max_pages < 0 || max_pages > ((int64_t)1 << 30) / d->page_size)
     return set_error(HUM_ERR_INVALID_ARG, "max_pages must be >= 0, sequences at most 2^30 tokens");
-  if (attn_items(d, num_q_heads, batch) * (max_pages * d->page_size / kTile + 1) >= (int64_t)1 << 31)
-    return set_error(HUM_ERR_UNSUPPORTED, "batch x heads x max_pages x page_size must stay below 2^38");
+  if (batch * d->num_kv_heads * (max_pages * d->page_size / kTile + 1) >= (int64_t)1 << 31)
+    return set_error(HUM_ERR_UNSUPPORTED, "batch x num_kv_heads x max_pages x page_size must stay below 2^38");
   return HUM_OK;
 }
 
@@ -847,14 +853,14 @@ hum_status hum_kv_attention(const hum_kv_desc* desc, const void* cache, size_t c
     return set_error(HUM_ERR_WORKSPACE, "cache of %zu bytes, the description takes %lld", cache_bytes, (long long)l.bytes);
   const size_t need = hum_kv_attention_workspace_bytes(desc, num_q_heads, batch, max_pages);
   if (ws_bytes < need) return set_error(HUM_ERR_WORKSPACE, "workspace of %zu bytes, %zu needed", ws_bytes, need);
-  const int wgs = attn_wgs(desc, num_q_heads, batch, max_pages);
   KvAttnParams p{};
   p.cache = static_cast<const uint8_t*>(cache);
   p.unit = l.unit;
   p.num_pages = (int32_t)desc->num_pages;
   p.kv_heads = desc->num_kv_heads;
   p.group = num_q_heads / desc->num_kv_heads;
-  p.head_tiles = (p.group + 15) / 16;
+  p.head_tiles = attn_head_tiles(desc, num_q_heads);
+  p.wgs = attn_wgs(desc, num_q_heads, batch, max_pages);
   p.page_shift = __builtin_ctz((unsigned)desc->page_size);
   p.q = static_cast<const uint16_t*>(q_bf16);
   p.q_ts = q_ts;
@@ -874,7 +880,7 @@ hum_status hum_kv_attention(const hum_kv_desc* desc, const void* cache, size_t c
   p.part_heads = attn_part_heads(desc, num_q_heads);
   hipStream_t s = static_cast<hipStream_t>(stream);
   kv_dispatch(desc, [&](auto fmt, auto dim) {
-    kv_attention_kernel<decltype(fmt)::value, decltype(dim)::value><<<wgs, kThreads, 0, s>>>(p);
+    kv_attention_kernel<decltype(fmt)::value, decltype(dim)::value><<<(p.wgs + 7) / 8 * 8 * p.head_tiles, kThreads, 0, s>>>(p);
   });
   hipError_t err = hipGetLastError();
   if (err != hipSuccess) return set_error(HUM_ERR_HIP, "kv_attention launch: %s", hipGetErrorString(err));
