@@ -251,6 +251,20 @@ def test_attention_long_sequence(fmt, d, n):
     c.check(c.run(return_lse=True, window=12345), window=12345, what="long window")
 
 
+@pytest.mark.parametrize("fmt,lens,hq,hk,d", [("fp8_token", [20011, 3], 40, 1, 128), ("bf16", [900, 0, 65], 1024, 1, 64),
+                                              ("mxfp4", [1, 2500], 66, 2, 256), ("mxfp8", [3000] * 3, 200, 1, 128)])
+def test_attention_many_query_heads_per_kv_head(fmt, lens, hq, hk, d):
+    """Blocks of 16 query heads that read the same share of the cache, cut
+    into parts and joined separately, the last block ragged."""
+    print(f"case heads {fmt} {lens} {hq} {hk} {d}", flush=True)
+    c = Case(21, fmt, lens, hq, hk, d, 32)
+    got = c.run(return_lse=True)
+    c.check(got, what="heads")
+    c.check(c.run(return_lse=True, window=700), window=700, what="heads, window")
+    again = c.run(return_lse=True)
+    assert torch.equal(got[0], again[0]) and torch.equal(got[1], again[1])
+
+
 def test_attention_batches_of_many_lengths():
     """Sequences more than lanes, workgroups that end inside a head, between
     heads and between sequences; also the head tiles of more than 16 query
