@@ -30,7 +30,7 @@ struct RotaryParams {
   int32_t half;        // rotary_dim / 2
   int32_t rest;        // head_dim - rotary_dim elements to copy (0 when in place)
   int32_t units;       // rotating units (VEC pairs) and copied ones (2 VEC elements) of a head
-  int32_t lane_shift;  // log2 of the lanes that share a head (all its units at once, at most 256)
+  int32_t lanes;       // that share a head (all its units at once, at most 256)
   int32_t tok_per_wg;
   int32_t head_step;   // heads per workgroup (grid.y slices the heads)
   float factor;
@@ -70,18 +70,19 @@ __global__ __launch_bounds__(256) void rotary_kernel(const RotaryParams p) {
   float* cs = lds;
   float* sn = lds + p.tok_per_wg * p.half;
 
-  const int lanes = 1 << p.lane_shift;
+  const int lanes = p.lanes;
   const int rot = p.half / VEC;
   const int hall = p.heads[0] + p.heads[1];
   const int h0 = (int)blockIdx.y * p.head_step;
   const int nh = hall - h0 < p.head_step ? hall - h0 : p.head_step;
   const float inv_nh = 1.0f / (float)nh;  // rows below 2^17: (row + 1/2) inv_nh is never a whole step off
-  const int step = 256 >> p.lane_shift;
+  const int step = (int)(256u / (uint32_t)lanes);
   const int rows = nt * nh;
 
   // the rows row0, row0 + step, ... and the unit u of each
-  int row0 = tid >> p.lane_shift, u = tid & (lanes - 1);
-  bool live = u < p.units && row0 < rows;
+  const int first_row = (int)(((float)tid + 0.5f) / (float)lanes), first_u = tid - first_row * lanes;
+  int row0 = first_row, u = first_u;
+  bool live = row0 < step && row0 < rows;
   T* y[kRows];
   int tok[kRows];
   int at0 = 0, at1 = 0;
@@ -155,7 +156,7 @@ __global__ __launch_bounds__(256) void rotary_kernel(const RotaryParams p) {
     }
     u += lanes;
     if (u >= p.units) {
-      u = tid & (lanes - 1);
+      u = first_u;
       row0 += step * kRows;
     }
     live = row0 < rows;
@@ -275,7 +276,7 @@ hum_status hum_rotary(const hum_rotary_desc* d, int64_t num_tokens, const int64_
   p.half = d->rotary_dim / 2;
   p.rest = in_place ? 0 : d->head_dim - d->rotary_dim;
   p.units = p.half / v + (p.rest / v + 1) / 2;
-  while (p.lane_shift < 8 && (1 << p.lane_shift) < p.units) ++p.lane_shift;
+  p.lanes = p.units < 256 ? p.units : 256;
   p.factor = d->factor;
   p.sign = d->inverse ? -1.0f : 1.0f;
   // Tokens per workgroup: as many as fill 256 threads with one sine and
@@ -286,7 +287,7 @@ hum_status hum_rotary(const hum_rotary_desc* d, int64_t num_tokens, const int64_
   while (tok > 1 && (num_tokens + tok - 1) / tok < 1024) tok /= 2;
   p.tok_per_wg = (int)tok;
   const int64_t gx = (num_tokens + tok - 1) / tok;
-  const int rows = 256 >> p.lane_shift;  // heads a workgroup turns at once
+  const int rows = 256 / p.lanes;  // heads a workgroup turns at once
   int64_t gy = 1;
   if (gx < 512) {
     gy = (512 + gx - 1) / gx;
