@@ -72,20 +72,20 @@ __device__ __forceinline__ float row_max(float v) {
 
 // f[i] / s as an IEEE f32 division gives it (the FP8 rule's quotient: a code
 // can hang on its last bit), for eight values: with y = RN(1 / s), q = RN(f y)
-// and the exact remainder r = f - q s, RN(q + r y) is the rounded quotient
+// and the exact remainder r = q s - f, RN(q - r y) is the rounded quotient
 // (Markstein, "Computation of elementary functions on the IBM RISC
-// System/6000 processor", 1990), four instructions a value where the
+// System/6000 processor", 1990), three instructions a value where the
 // division takes eleven.  That holds while nothing over- or underflows: s
 // within [2^-80, 2^120] (values below 2^-10 s, whose remainder may underflow,
-// become zero codes either way); other scales divide.  The sign is set from
-// f: q + r y loses that of -0.
+// become zero codes either way); other scales divide.  A zero keeps its sign:
+// r is then +0, and q - 0 is q.
 __device__ __forceinline__ void divide8(float (&f)[8], float s) {
   if (s >= 0x1p-80f && s <= 0x1p120f) {
     const float y = 1.0f / s;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const float q = f[i] * y;
-      f[i] = __builtin_copysignf(__builtin_fmaf(__builtin_fmaf(-q, s, f[i]), y, q), f[i]);
+      f[i] = __builtin_fmaf(-__builtin_fmaf(q, s, -f[i]), y, q);
     }
   } else {
 #pragma unroll
