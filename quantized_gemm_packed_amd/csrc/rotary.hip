@@ -111,9 +111,11 @@ __global__ __launch_bounds__(256) void rotary_kernel(const RotaryParams p) {
                    h * (which ? p.x_hs[1] : p.x_hs[0]);
       y[k] = static_cast<T*>(which ? p.y[1] : p.y[0]) + (t0 + tok[k]) * (which ? p.y_ts[1] : p.y_ts[0]) +
              h * (which ? p.y_hs[1] : p.y_hs[0]);
-      // (a row past the last: the first again, which is not stored)
-      a[k] = *reinterpret_cast<const P*>(x + at0);
-      if (two) b[k] = *reinterpret_cast<const P*>(x + at1);
+      // (of a row past the last nothing is read or stored)
+      if (row0 + k * step < rows) {
+        a[k] = *reinterpret_cast<const P*>(x + at0);
+        if (two) b[k] = *reinterpret_cast<const P*>(x + at1);
+      }
     }
   };
   if (live) load();
