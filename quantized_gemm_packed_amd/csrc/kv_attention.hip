@@ -38,9 +38,9 @@
 //   parts (the same bits whatever finishes last).
 //
 // Measured on MI355X: 48 sequences of 8192 to 16384 bf16 tokens (8 heads of
-// 128, 32 query heads, 2.4 GB) 399 us, 6.1 TB/s; 64 sequences of 1 to 8191 in
-// MXFP8 110 us (5.2 TB/s); one of 131072 in FP8 53 us (5.2 TB/s); 256 of 0 to
-// 515 in bf16 with 16 heads of 64 63 us (4.3 TB/s); one of 333 tokens 8.2 us.
+// 128, 32 query heads, 2.4 GB) 400 us, 6.0 TB/s; 64 sequences of 1 to 8191 in
+// MXFP8 109 us (5.3 TB/s); one of 131072 in FP8 53 us (5.2 TB/s); 256 of 0 to
+// 515 in bf16 with 16 heads of 64 59 us (4.6 TB/s); one of 333 tokens 8.2 us.
 #include "kv_common.h"
 
 namespace hum {
@@ -209,7 +209,10 @@ __global__ __launch_bounds__(kThreads, FMT == HUM_ACT_BF16 && D == 256 ? 1 : 2) 
   // Where more than 16 query heads share a key-value head, as many
   // workgroups as that takes have the same share of the cache, on one XCD
   // (workgroups go to the eight in turn): they read it at about the same
-  // time, so that all but one find it in the XCD's L2.
+  // time, so that all but one find it in the XCD's L2 (32 sequences of 8192
+  // bf16 tokens, 2 heads of 128 with 32 query heads each: 48.8 us; one
+  // workgroup after another in a share of its own, which reads the cache
+  // from memory twice: 79.8).
   const int turn = (int)blockIdx.x >> 3;
   const int wg8 = p.head_tiles == 1 ? turn : (int)((uint32_t)turn / (uint32_t)p.head_tiles);
   const int wg = wg8 * 8 + ((int)blockIdx.x & 7);   // among those of its 16 query heads
@@ -778,7 +781,7 @@ static int attn_head_tiles(const hum_kv_desc* d, int32_t num_q_heads) {
 // the bf16 kernel of 256-wide heads fits a CU once.  Two with more heads,
 // where a second workgroup works while the first ends one head and begins
 // the next (64 ragged sequences, 512 heads: 110 us with 512, 118 with 256;
-// 256 short ones, 4096 heads: 63 and 82), and with small rows (32 sequences
+// 256 short ones, 4096 heads: 59 and 82), and with small rows (32 sequences
 // in MXFP4 of 128-wide heads, 512 MiB: 5.3 TB/s with 512, 4.0 with 256).
 static int attn_wgs(const hum_kv_desc* d, int32_t num_q_heads, int64_t batch, int64_t max_pages) {
   const int64_t tiles = max_pages * d->page_size / kTile + 1, items = batch * d->num_kv_heads;

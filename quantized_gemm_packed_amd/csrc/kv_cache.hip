@@ -8,9 +8,12 @@
 // for an MX block), so nothing goes through LDS.  Memory bound: each row is
 // read once and its codes written once.
 //
-// Measured on MI355X, 16384 tokens of 8 heads of 128 in MXFP8: written in
-// 21.8 us (4.7 TB/s read + written; a large copy reaches 4.85), read back in
-// 19.9 us (5.1 TB/s); 256 tokens in FP8: 3.6 and 3.0 us, a launch's own time.
+// Measured on MI355X, 16384 tokens of 8 heads of 128 in MXFP8, inputs that
+// change from call to call: written in 21.6 us (4.7 TB/s read + written; a
+// large copy reaches 4.85), read back in 19.9 us (5.1 TB/s).  The same inputs
+// again, partly from the last-level cache: 17.8 and 17.6 us; in FP8, which
+// has the most arithmetic, 18.8 and 17.6.  256 tokens in FP8: 3.3 and 3.1 us,
+// a launch's own time.
 #include "kv_common.h"
 
 namespace hum {

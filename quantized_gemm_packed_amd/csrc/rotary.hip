@@ -10,8 +10,8 @@
 // a workgroup computes them once, into LDS.
 //
 // Measured on MI355X: 16384 tokens of 32 + 8 bf16 heads of 128, 64 elements
-// turned in adjacent pairs: 73 us, 4.6 TB/s read + written (a large copy
-// reaches 4.85); a decode step of 64 tokens: 3.3 us, a launch's own time.
+// turned in adjacent pairs, inputs that change from call to call: 73 us,
+// 4.6 TB/s read + written (a large copy reaches 4.85); a decode step of 64 tokens: 3.3 us, a launch's own time.
 #include <cmath>
 
 #include "dev_common.h"
