@@ -5,9 +5,12 @@
 // Memory bound (q and k are read and written once).  An angle in radians at
 // position 10^6 has lost 16 of f32's 24 bits, so the turn count
 // positions * inv_freq / 2 pi is formed and reduced to [-1/2, 1/2] in f64
-// (two multiplies, a round and a subtract) and only the remainder goes to
-// the f32 sine and cosine.  They are the same for every head of a token:
-// a workgroup computes them once, into LDS.
+// (two multiplies, a round and a subtract).  The remainder goes to the f32
+// sine and cosine as an f32 and the rest of it, to first order: without the
+// rest the angle is off by up to 2 pi 2^-26, more than the functions' own
+// error, and sines next to half a turn by thousands of their ulps.  They are
+// the same for every head of a token: a workgroup computes them once, into
+// LDS.
 //
 // Measured on MI355X: 16384 tokens of 32 + 8 bf16 heads of 128, 64 elements
 // turned in adjacent pairs, inputs that change from call to call: 73 us,
@@ -123,11 +126,12 @@ __global__ __launch_bounds__(256) void rotary_kernel(const RotaryParams p) {
   for (int i = tid; i < nt * p.half; i += 256) {
     const int t = i / p.half;
     const double turns = (double)p.positions[t0 + t] * (p.inv_freq[i - t * p.half] * 0.15915494309189535);
-    const float r = (float)(turns - __builtin_rint(turns));
+    const double rem = turns - __builtin_rint(turns);
+    const float r = (float)rem, lo = (float)(rem - r) * 6.28318531f;
     float s, c;
     sincospif(2.0f * r, &s, &c);
-    cs[i] = c * p.factor;
-    sn[i] = s * p.factor * p.sign;
+    cs[i] = __builtin_fmaf(-s, lo, c) * p.factor;
+    sn[i] = __builtin_fmaf(c, lo, s) * p.factor * p.sign;
   }
   __syncthreads();
 
