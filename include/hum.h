@@ -582,8 +582,12 @@ size_t hum_kv_attention_workspace_bytes(const hum_kv_desc* desc, int32_t num_q_h
  * page lies in [0, num_pages): the tokens of any other page id (-1 for one
  * held elsewhere) take no part.  Where no token takes part, out is 0 and lse
  * is -inf.  Nothing past n or before the window reaches the result, whatever
- * the cache holds there; the values that do take part have to be finite (an
- * infinity or NaN among them makes what it reaches NaN).
+ * the cache holds there.  The values that do take part have to be finite, and
+ * so have the scores, in f32 and times log2(e): an infinity or NaN among them
+ * makes what it reaches infinite or NaN, a score of -inf leaves its token out.
+ * V may be any finite value (no sum passes the largest of them); magnitudes
+ * below 2^-90 times the tokens that may take part, at most max_pages *
+ * page_size (FP8_TOKEN: rows whose largest is), may lose bits, down to zero.
  * batch is at most 65535, max_pages * page_size at most 2^30, and
  * batch * num_kv_heads * (max_pages * page_size + 128) stays below 2^38.
  *   q           : bf16 [batch][num_q_heads][head_dim], strides in elements;

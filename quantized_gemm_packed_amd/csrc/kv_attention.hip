@@ -21,10 +21,12 @@
 //   into them).  An FP8 row's f32 scale multiplies its score (K) or its
 //   probability (V) in f32.
 // * Scores stay in the exponent's base 2.  The reference maximum m of a head
-//   is only raised when a score exceeds it by more than 8: the probabilities
-//   stay below 2^8 times the wave's first, their f32 sums and bf16 roundings
-//   do not care, and most tiles need no exchange for a maximum and no pass
-//   over the accumulators.  Sums, maxima and accumulators are f32.
+//   is only raised (to the next whole number) when a score exceeds it by more
+//   than 8: most tiles need no exchange for a maximum and no pass over the
+//   accumulators.  Probabilities are formed against m + lift, lift = 8 + log2
+//   of the tokens that may take part (known on the host): none passes 1 over
+//   their number, so no sum of finite V passes the largest of them; f32 sums
+//   and bf16 roundings do not care.  Sums, maxima and accumulators are f32.
 // * A probability goes into the second product as the sum of two bf16, its
 //   rounding and what that left (2^-16 of it in all): with one alone the
 //   result's error against float64 is 1.4 times that of its own rounding to
@@ -56,6 +58,7 @@ struct KvAttnParams {
   int32_t max_pages, batch, window;
   const int32_t* seq_lens;
   float scale_log2;  // scale * log2(e)
+  float lift;        // probabilities are 2^(score - m - lift)
   uint16_t* out;
   float* lse;
   uint32_t* count;  // arrival counters (3 kAttnWgs, in the workspace's header), zero between calls
@@ -503,10 +506,10 @@ __global__ __launch_bounds__(kThreads, FMT == HUM_ACT_BF16 && D == 256 ? 1 : 2) 
       if (__ballot(top > m + 8.0f)) {
         top = __builtin_fmaxf(top, __shfl_xor(top, 16));
         top = __builtin_fmaxf(top, __shfl_xor(top, 32));
-        const float mn = __builtin_fmaxf(m, top);
+        const float mn = __builtin_fmaxf(m, __builtin_ceilf(top));
         const float a = rescale(m, mn);
         m = mn;
-        m_safe = mn == kNegInf ? 0.0f : mn;
+        m_safe = mn == kNegInf ? 0.0f : mn + p.lift;
         l *= a;
 #pragma unroll
         for (int i = 0; i < T::kVN * T::kVE; ++i) acc[i] *= a;
@@ -611,7 +614,7 @@ __global__ __launch_bounds__(kThreads, FMT == HUM_ACT_BF16 && D == 256 ? 1 : 2) 
       u32x2_t w = {f32x2_to_bf16x2_bits(o[0] * inv, o[1] * inv), f32x2_to_bf16x2_bits(o[2] * inv, o[3] * inv)};
       if (sum == 0.0f) w = u32x2_t{0, 0};
       *reinterpret_cast<u32x2_t*>(p.out + row * D + d) = w;
-      if (d == 0 && p.lse) p.lse[row] = sum == 0.0f ? kNegInf : (top + __log2f(sum)) * 0.6931471805599453f;
+      if (d == 0 && p.lse) p.lse[row] = sum == 0.0f ? kNegInf : (top + (p.lift + __log2f(sum))) * 0.6931471805599453f;
     };
     if (tile == 0 && tile_end == cur.seq.tiles) {
       for (int i = threadIdx.x * 4; i < heads * D; i += 4 * kThreads) {
@@ -875,6 +878,8 @@ hum_status hum_kv_attention(const hum_kv_desc* desc, const void* cache, size_t c
   p.window = (int32_t)(window < ((int64_t)1 << 30) ? window : (int64_t)1 << 30);
   p.seq_lens = seq_lens;
   p.scale_log2 = scale_log2;
+  const int64_t all = max_pages * desc->page_size, most = window > 0 && window < all ? window : all;
+  p.lift = 8.0f + (most > 1 ? 64 - __builtin_clzll((uint64_t)most - 1) : 0);
   p.out = static_cast<uint16_t*>(out_bf16);
   p.lse = lse;
   p.count = static_cast<uint32_t*>(workspace);
