@@ -517,8 +517,9 @@ hum_status hum_rotary_inv_freq(int32_t rotary_dim, double base, int32_t scaling,
  *   strides   : elements from token to token and from head to head (head
  *               elements are contiguous); any, as long as the rows of an
  *               output do not overlap
- *   out       : may be the input itself (same pointer and strides), but may
- *               not overlap it otherwise, nor the other input and output
+ *   out       : may be the input itself (same pointer and strides); one that
+ *               overlaps it otherwise, or the other input or output, is
+ *               refused (q and k as slices of one buffer do not overlap)
  * q (with q_out) or k (with k_out) may be NULL where its head count is 0.
  * At most 2^24 - 1 tokens in a call. */
 hum_status hum_rotary(const hum_rotary_desc* desc, int64_t num_tokens, const int64_t* positions,

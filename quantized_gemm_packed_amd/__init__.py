@@ -771,8 +771,9 @@ def rotary(q, k, positions, inv_freq, layout: str = "half", factor: float = 1.0,
     """q [T, Hq, D] and k [T, Hkv, D] (bf16 or float32; k may be None) turned
     by positions int64 [T] * inv_freq float64 [R / 2], the first R elements of
     each head -> (q, k), new tensors unless q_out / k_out are given (the
-    inputs themselves for a turn in place).  inverse turns back, which with
-    the same factor is the gradient."""
+    inputs themselves for a turn in place; outputs that overlap q or k
+    otherwise are refused).  inverse turns back, which with the same factor is
+    the gradient."""
     if layout not in _ROPE_LAYOUT:
         raise ValueError(f"layout must be one of {sorted(_ROPE_LAYOUT)}")
     return (_nat or _native()).rotary(q, k, positions, inv_freq, _ROPE_LAYOUT[layout], factor, inverse, q_out, k_out)

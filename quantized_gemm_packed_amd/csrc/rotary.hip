@@ -19,6 +19,7 @@
 
 #include "dev_common.h"
 #include "hum_internal.h"
+#include "rows.h"
 
 namespace hum {
 
@@ -284,6 +285,24 @@ hum_status hum_rotary(const hum_rotary_desc* d, int64_t num_tokens, const int64_
     all |= (int64_t)(reinterpret_cast<uintptr_t>(xs[i]) | reinterpret_cast<uintptr_t>(ys[i])) / size;
     for (int j = 0; j < 4; ++j) all |= st[i][j];
   }
+  // A workgroup's rows are read while others are stored: no output may lie in
+  // what is not its own input.
+  auto extent = [&](const void* at, int i, int out) {
+    return Rows{(int64_t)(intptr_t)at, num_tokens, heads[i], (wide_t)st[i][out] * size, (wide_t)st[i][out + 1] * size,
+                (int64_t)d->head_dim * size};
+  };
+  for (int i = 0; i < 2; ++i) {
+    if (!heads[i]) continue;
+    const Rows y = extent(ys[i], i, 2);
+    if (overlaps_itself(y)) return set_error(HUM_ERR_INVALID_ARG, "the rows of an output must not overlap");
+    for (int j = 0; j < 2; ++j) {
+      if (!heads[j] || (i == j && xs[i] == ys[i])) continue;
+      if (overlap(y, extent(xs[j], j, 0)) != Overlap::kNo)
+        return set_error(HUM_ERR_INVALID_ARG, "an output must not overlap q or k, unless it is the same tensor as its input");
+    }
+  }
+  if (heads[0] && heads[1] && overlap(extent(ys[0], 0, 2), extent(ys[1], 1, 2)) != Overlap::kNo)
+    return set_error(HUM_ERR_INVALID_ARG, "q's output and k's must not overlap");
   int v = 16 / size;
   while (all % v) v /= 2;
   p.tokens = num_tokens;
