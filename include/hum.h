@@ -556,7 +556,8 @@ size_t hum_kv_cache_bytes(const hum_kv_desc* desc);
  *   slots : i64 [T]; a slot outside [0, num_pages * page_size) is skipped.
  *           The others must differ: a slot that a call names twice holds
  *           parts of either row afterwards.
- *   strides in elements, head elements contiguous.
+ *   strides in elements, head elements contiguous.  k and v may be rows of
+ *   the cache itself (bf16), but not of a slot that the call writes.
  * An infinity or NaN is kept in bf16; in the other formats the row that it is
  * in (its block of 32, MX) holds no meaningful codes afterwards.
  * At most 2^24 - 1 tokens in a call (hum_kv_read too). */
@@ -567,7 +568,7 @@ hum_status hum_kv_write(const hum_kv_desc* desc, void* cache, size_t cache_bytes
 /* Reads slots[t] back: k_out, v_out bf16 [T][num_kv_heads][head_dim] =
  * bf16(code * scale).  A slot outside [0, num_pages * page_size) reads as
  * zeros; the same slot may be read more than once.  k_out and v_out must not
- * overlap. */
+ * overlap one another, the cache or the slots. */
 hum_status hum_kv_read(const hum_kv_desc* desc, const void* cache, size_t cache_bytes, int64_t num_tokens,
                        const int64_t* slots, void* k_out_bf16, void* v_out_bf16, void* stream);
 
@@ -597,8 +598,9 @@ size_t hum_kv_attention_workspace_bytes(const hum_kv_desc* desc, int32_t num_q_h
  *                 t / page_size of a row is the page of token t
  *   seq_lens    : i32 [batch], read by the kernel only (no device->host copy)
  *   out         : bf16 [batch][num_q_heads][head_dim], contiguous
- *   lse         : f32 [batch][num_q_heads] or NULL; out and lse must not
- *                 overlap the inputs
+ *   lse         : f32 [batch][num_q_heads] or NULL.  out may be q itself;
+ *                 out, lse and the workspace that overlap the inputs
+ *                 otherwise, or one another, are refused
  *   workspace   : hum_kv_attention_workspace_bytes(...) bytes, prepared as for
  *                 hum_linear (hum_prepare_workspace once).  Calls that may
  *                 overlap in time need different workspaces.

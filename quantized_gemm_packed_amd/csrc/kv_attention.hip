@@ -44,6 +44,7 @@
 // MXFP8 109 us (5.3 TB/s); one of 131072 in FP8 53 us (5.2 TB/s); 256 of 0 to
 // 515 in bf16 with 16 heads of 64 59 us (4.6 TB/s); one of 333 tokens 8.2 us.
 #include "kv_common.h"
+#include "rows.h"
 
 namespace hum {
 
@@ -859,6 +860,21 @@ hum_status hum_kv_attention(const hum_kv_desc* desc, const void* cache, size_t c
     return set_error(HUM_ERR_WORKSPACE, "cache of %zu bytes, the description takes %lld", cache_bytes, (long long)l.bytes);
   const size_t need = hum_kv_attention_workspace_bytes(desc, num_q_heads, batch, max_pages);
   if (ws_bytes < need) return set_error(HUM_ERR_WORKSPACE, "workspace of %zu bytes, %zu needed", ws_bytes, need);
+  // What is written may not lie in what other workgroups read; a row of out
+  // may be its own query (it is stored when the last reader has passed it).
+  const int64_t row = (int64_t)desc->head_dim * 2, rows = batch * num_q_heads;
+  const Rows q_rows{(int64_t)(intptr_t)q_bf16, batch, num_q_heads, (wide_t)q_ts * 2, (wide_t)q_hs * 2, row};
+  const bool same = q_bf16 == out_bf16 && (batch == 1 || q_ts == (int64_t)num_q_heads * desc->head_dim) &&
+                    (num_q_heads == 1 || q_hs == desc->head_dim);
+  const Rows in[4] = {bytes_at(cache, l.bytes), bytes_at(seq_lens, batch * 4),
+                      Rows{(int64_t)(intptr_t)block_table, batch, 1, (wide_t)table_stride * 4, 0, max_pages * 4}, q_rows};
+  const Rows out[3] = {bytes_at(workspace, (int64_t)need), bytes_at(lse, lse ? rows * 4 : 0), bytes_at(out_bf16, rows * row)};
+  for (int i = 0; i < 3; ++i) {
+    bool bad = false;
+    for (int j = 0; j < 4; ++j) bad |= !(same && i == 2 && j == 3) && overlap(out[i], in[j]) != Overlap::kNo;
+    for (int j = 0; j < i; ++j) bad |= overlap(out[i], out[j]) != Overlap::kNo;
+    if (bad) return set_error(HUM_ERR_INVALID_ARG, "out, lse and the workspace must not overlap the inputs or one another");
+  }
   KvAttnParams p{};
   p.cache = static_cast<const uint8_t*>(cache);
   p.unit = l.unit;

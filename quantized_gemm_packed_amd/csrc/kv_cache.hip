@@ -15,6 +15,7 @@
 // has the most arithmetic, 18.8 and 17.6.  256 tokens in FP8: 3.3 and 3.1 us,
 // a launch's own time.
 #include "kv_common.h"
+#include "rows.h"
 
 namespace hum {
 
@@ -409,6 +410,11 @@ hum_status hum_kv_read(const hum_kv_desc* desc, const void* cache, size_t cache_
     return set_error(HUM_ERR_INVALID_ARG, "k_out and v_out must not overlap");
   if ((ka | va) % 16)
     return set_error(HUM_ERR_INVALID_ARG, "k_out and v_out must be 16-byte aligned");
+  const int64_t bytes = num_tokens * desc->num_kv_heads * desc->head_dim * 2;
+  for (void* o : {k_out, v_out})
+    if (overlap(bytes_at(o, bytes), bytes_at(cache, hum_kv_cache_bytes(desc))) != Overlap::kNo ||
+        overlap(bytes_at(o, bytes), bytes_at(slots, num_tokens * 8)) != Overlap::kNo)
+      return set_error(HUM_ERR_INVALID_ARG, "k_out and v_out must not overlap the cache or the slots");
   p.out[0] = static_cast<uint16_t*>(k_out);
   p.out[1] = static_cast<uint16_t*>(v_out);
   const dim3 grid = kv_move_grid(desc, &p);
