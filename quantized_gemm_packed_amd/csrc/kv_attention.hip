@@ -21,12 +21,16 @@
 //   into them).  An FP8 row's f32 scale multiplies its score (K) or its
 //   probability (V) in f32.
 // * Scores stay in the exponent's base 2.  The reference maximum m of a head
-//   is only raised (to the next whole number) when a score exceeds it by more
-//   than 8: most tiles need no exchange for a maximum and no pass over the
-//   accumulators.  Probabilities are formed against m + lift, lift = 8 + log2
-//   of the tokens that may take part (known on the host): none passes 1 over
-//   their number, so no sum of finite V passes the largest of them; f32 sums
-//   and bf16 roundings do not care.  Sums, maxima and accumulators are f32.
+//   is only raised when a score exceeds it by more than 8: the probabilities
+//   stay below 2^8 times the wave's first, their f32 sums and bf16 roundings
+//   do not care, and most tiles need no exchange for a maximum and no pass
+//   over the accumulators.  Sums, maxima and accumulators are f32.
+// * What multiplies V is the probability times a power of two, 2^-8 over the
+//   tokens that may take part (known on the host), which the result's
+//   division takes out again: no weight then passes 1 over their number, and
+//   no sum of finite V passes the largest of them.  (Exact, where the same
+//   shift of m, which costs no product, rounds score - m in larger steps:
+//   log-sum-exps were up to ten times further off.)
 // * A probability goes into the second product as the sum of two bf16, its
 //   rounding and what that left (2^-16 of it in all): with one alone the
 //   result's error against float64 is 1.4 times that of its own rounding to
@@ -43,6 +47,8 @@
 // 128, 32 query heads, 2.4 GB) 400 us, 6.0 TB/s; 64 sequences of 1 to 8191 in
 // MXFP8 109 us (5.3 TB/s); one of 131072 in FP8 53 us (5.2 TB/s); 256 of 0 to
 // 515 in bf16 with 16 heads of 64 59 us (4.6 TB/s); one of 333 tokens 8.2 us.
+#include <cmath>
+
 #include "kv_common.h"
 #include "rows.h"
 
@@ -59,7 +65,7 @@ struct KvAttnParams {
   int32_t max_pages, batch, window;
   const int32_t* seq_lens;
   float scale_log2;  // scale * log2(e)
-  float lift;        // probabilities are 2^(score - m - lift)
+  float down, up;    // the power of two on V's weights, and its reciprocal
   uint16_t* out;
   float* lse;
   uint32_t* count;  // arrival counters (3 kAttnWgs, in the workspace's header), zero between calls
@@ -507,10 +513,10 @@ __global__ __launch_bounds__(kThreads, FMT == HUM_ACT_BF16 && D == 256 ? 1 : 2) 
       if (__ballot(top > m + 8.0f)) {
         top = __builtin_fmaxf(top, __shfl_xor(top, 16));
         top = __builtin_fmaxf(top, __shfl_xor(top, 32));
-        const float mn = __builtin_fmaxf(m, __builtin_ceilf(top));
+        const float mn = __builtin_fmaxf(m, top);
         const float a = rescale(m, mn);
         m = mn;
-        m_safe = mn == kNegInf ? 0.0f : mn + p.lift;
+        m_safe = mn == kNegInf ? 0.0f : mn;
         l *= a;
 #pragma unroll
         for (int i = 0; i < T::kVN * T::kVE; ++i) acc[i] *= a;
@@ -520,6 +526,7 @@ __global__ __launch_bounds__(kThreads, FMT == HUM_ACT_BF16 && D == 256 ? 1 : 2) 
       for (int i = 0; i < 8; ++i) {
         pr[i] = exp2_fast(x[i] - m_safe);
         l += pr[i];
+        pr[i] *= p.down;
         if constexpr (kFp8) pr[i] *= vf[i];
       }
       // probabilities as the sum of two bf16 (16 significant bits)
@@ -611,11 +618,11 @@ __global__ __launch_bounds__(kThreads, FMT == HUM_ACT_BF16 && D == 256 ? 1 : 2) 
     // the finished row of head h, elements d .. d + 3
     auto store_out = [&](int h, int d, f32x4_t o, float top, float sum) {
       const int64_t row = (int64_t)cur.b * p.kv_heads * p.group + q_head + h;
-      const float inv = 1.0f / sum;
+      const float inv = p.up / sum;
       u32x2_t w = {f32x2_to_bf16x2_bits(o[0] * inv, o[1] * inv), f32x2_to_bf16x2_bits(o[2] * inv, o[3] * inv)};
       if (sum == 0.0f) w = u32x2_t{0, 0};
       *reinterpret_cast<u32x2_t*>(p.out + row * D + d) = w;
-      if (d == 0 && p.lse) p.lse[row] = sum == 0.0f ? kNegInf : (top + (p.lift + __log2f(sum))) * 0.6931471805599453f;
+      if (d == 0 && p.lse) p.lse[row] = sum == 0.0f ? kNegInf : (top + __log2f(sum)) * 0.6931471805599453f;
     };
     if (tile == 0 && tile_end == cur.seq.tiles) {
       for (int i = threadIdx.x * 4; i < heads * D; i += 4 * kThreads) {
@@ -895,7 +902,9 @@ hum_status hum_kv_attention(const hum_kv_desc* desc, const void* cache, size_t c
   p.seq_lens = seq_lens;
   p.scale_log2 = scale_log2;
   const int64_t all = max_pages * desc->page_size, most = window > 0 && window < all ? window : all;
-  p.lift = 8.0f + (most > 1 ? 64 - __builtin_clzll((uint64_t)most - 1) : 0);
+  const int shift = 8 + (most > 1 ? 64 - __builtin_clzll((uint64_t)most - 1) : 0);
+  p.down = std::ldexp(1.0f, -shift);
+  p.up = std::ldexp(1.0f, shift);
   p.out = static_cast<uint16_t*>(out_bf16);
   p.lse = lse;
   p.count = static_cast<uint32_t*>(workspace);
