@@ -153,8 +153,9 @@ __global__ __launch_bounds__(256) void rotary_kernel(const RotaryParams p) {
           const int i0 = HALF ? i : 2 * i, i1 = HALF ? VEC + i : 2 * i + 1;
           const float x0 = ld1<T>(e[i0]), x1 = ld1<T>(e[i1]);
           const int at = HALF || kPair || i < VEC / 2 ? c0 + i : c1 + i - VEC / 2;
-          e[i0] = st1<T>(x0 * cs[at] - x1 * sn[at]);
-          e[i1] = st1<T>(x0 * sn[at] + x1 * cs[at]);
+          // (the fused product named: every instance gives the same bits)
+          e[i0] = st1<T>(__builtin_fmaf(x0, cs[at], -(x1 * sn[at])));
+          e[i1] = st1<T>(__builtin_fmaf(x0, sn[at], x1 * cs[at]));
         }
 #pragma unroll
         for (int i = 0; i < VEC; ++i) {

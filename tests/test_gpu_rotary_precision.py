@@ -37,3 +37,35 @@ def test_rotary_f32_coefficients(layout, inverse):
     for got, ref, what in ((y[:, first], np.cos(angle), "cos"), (y[:, second], np.sin(angle), "sin")):
         tol = (4 * 2.0 ** -23 + 2.0 ** -24) * np.abs(ref) + 2.0 ** -46 + 2.0 ** -51 * np.abs(angle)
         assert (np.abs(got - ref) <= tol).all(), (what, (np.abs(got - ref) / tol).max())
+
+
+@pytest.mark.parametrize("layout", ["half", "interleaved"])
+@pytest.mark.parametrize("factor", [1.0, 1.2772588])
+def test_rotary_f32_is_as_exact_as_its_plain_form(layout, factor):
+    """The plain form in f32, cosine and sine times the factor rounded once from float64, rounds four times to an
+    output: two coefficients (their two shares of the output make up one rounding of it), two products (one), the sum.
+    The kernel fuses a product with the sum: 2 1/2 roundings' variance where the plain form has 3, plus what the f32
+    functions add to a correctly rounded coefficient; a factor rounded by itself would add one more.  Up to 0.8 of a
+    rounding's variance is allowed to the functions: 3.3 / 3 = 1.05^2."""
+    g = np.random.default_rng(10)
+    t, half = 3001, 32
+    factor = float(np.float32(factor))
+    freq = 10000.0 ** (-np.arange(half) / half)
+    pos = g.integers(0, 1 << 20, t)
+    x = g.standard_normal((t, 4, 2 * half)).astype(np.float32)
+    y, _ = hum.rotary(torch.from_numpy(x).cuda(), None, torch.from_numpy(pos).cuda(), torch.from_numpy(freq).cuda(),
+                      layout=layout, factor=factor)
+    y = y.cpu().numpy()
+    angle = pos[:, None] * freq
+    c, s = (np.cos(angle) * factor)[:, None], (np.sin(angle) * factor)[:, None]
+    c32, s32 = c.astype(np.float32), s.astype(np.float32)
+    first = slice(0, half) if layout == "half" else slice(0, 2 * half, 2)
+    second = slice(half, 2 * half) if layout == "half" else slice(1, 2 * half, 2)
+    x0, x1 = x[..., first], x[..., second]
+    here = plain = 0.0
+    for got, p, ref in ((y[..., first], x0 * c32 - x1 * s32, x0.astype(np.float64) * c - x1.astype(np.float64) * s),
+                        (y[..., second], x0 * s32 + x1 * c32, x0.astype(np.float64) * s + x1.astype(np.float64) * c)):
+        assert p.dtype == np.float32
+        here += ((got - ref) ** 2).sum()
+        plain += ((p - ref) ** 2).sum()
+    assert here <= 3.3 / 3 * plain, (here / plain) ** 0.5
