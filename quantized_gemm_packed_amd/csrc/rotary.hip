@@ -131,8 +131,10 @@ __global__ __launch_bounds__(256) void rotary_kernel(const RotaryParams p) {
     const float r = (float)rem, lo = (float)(rem - r) * 6.28318531f;
     float s, c;
     sincospif(2.0f * r, &s, &c);
-    cs[i] = __builtin_fmaf(-s, lo, c) * p.factor;
-    sn[i] = __builtin_fmaf(c, lo, s) * p.factor * p.sign;
+    // (each rounded once, the factor included)
+    const float fs = p.factor * p.sign;
+    cs[i] = __builtin_fmaf(c, p.factor, -s * lo * p.factor);
+    sn[i] = __builtin_fmaf(s, fs, c * lo * fs);
   }
   __syncthreads();
 
