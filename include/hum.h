@@ -604,7 +604,10 @@ size_t hum_kv_attention_workspace_bytes(const hum_kv_desc* desc, int32_t num_q_h
  *   workspace   : hum_kv_attention_workspace_bytes(...) bytes, prepared as for
  *                 hum_linear (hum_prepare_workspace once).  Calls that may
  *                 overlap in time need different workspaces.
- * Products are f32 sums of bf16 values; the same call gives the same bits. */
+ * Products are f32 sums of bf16 values.  The same call gives the same bits; a
+ * sequence's own go by the lengths beside it, the batch and max_pages too
+ * (they decide into which parts its sums are cut): there is no batch-invariant
+ * form. */
 hum_status hum_kv_attention(const hum_kv_desc* desc, const void* cache, size_t cache_bytes, int32_t num_q_heads,
                             int64_t batch, const void* q_bf16, int64_t q_token_stride, int64_t q_head_stride,
                             const int32_t* block_table, int64_t table_stride, int64_t max_pages,

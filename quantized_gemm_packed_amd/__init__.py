@@ -820,7 +820,9 @@ def kv_attention(desc: KvDesc, cache, q, block_table, seq_lens, scale: float | N
     block_table int32 [B, max_pages] names.  scale defaults to D ** -0.5.
     workspace: uint8 of kv_attention_workspace_bytes(...), zeroed before its
     first call and not shared by calls that may overlap in time; by default
-    the current stream's own, or a captured graph's own."""
+    the current stream's own, or a captured graph's own.  The same call gives
+    the same bits; a sequence's own go by the batch around it too (its sums
+    are cut into other parts)."""
     return (_nat or _native()).kv_attention(desc, cache, q, block_table, seq_lens, scale, window, out, return_lse,
                                             workspace)
 
