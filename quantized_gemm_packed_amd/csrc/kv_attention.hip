@@ -17,8 +17,8 @@
 // * V arrives with a token's head elements side by side in a lane, and a lane
 //   holds 8 tokens: pairs of tokens are interleaved with one byte permute per
 //   two values to form V^T's rows.
-// * Codes become bf16 exactly on the way (hardware conversions; MX scales go
-//   into them).  An FP8 row's f32 scale multiplies its score (K) or its
+// * Codes become bf16 on the way (hardware conversions; MX scales go into
+//   them), exactly for every row that kv_write stores.  An FP8 row's f32 scale multiplies its score (K) or its
 //   probability (V) in f32.
 // * Scores stay in the exponent's base 2.  The reference maximum m of a head
 //   is only raised when a score exceeds it by more than 8: the probabilities
@@ -45,8 +45,8 @@
 //
 // Measured on MI355X: 48 sequences of 8192 to 16384 bf16 tokens (8 heads of
 // 128, 32 query heads, 2.4 GB) 400 us, 6.0 TB/s; 64 sequences of 1 to 8191 in
-// MXFP8 109 us (5.3 TB/s); one of 131072 in FP8 53 us (5.2 TB/s); 256 of 0 to
-// 515 in bf16 with 16 heads of 64 59 us (4.6 TB/s); one of 333 tokens 8.2 us.
+// MXFP8 110 us (5.2 TB/s); one of 131072 in FP8 53 us (5.2 TB/s); 256 of 0 to
+// 515 in bf16 with 16 heads of 64 60 us (4.5 TB/s); one of 333 tokens 8.2 us.
 #include <cmath>
 
 #include "kv_common.h"
@@ -134,8 +134,9 @@ __device__ __forceinline__ void to_bf16(const uint32_t* w, float scale, uint32_t
 }
 
 // Byte i of w, an E8M0 code, as the scale operand of the conversions.  They
-// read its exponent field only, so that also code 0 (2^-127, an f32 zero) is
-// exact: checked for every code of E4M3 and E2M1 and every scale.
+// read its exponent field only, so that code 0 (2^-127, an f32 zero) is right
+// too: checked for every code of E4M3 and E2M1 and every scale whose product
+// bf16 holds.
 __device__ __forceinline__ float mx_scale_bits(uint32_t w, int i) {
   return __uint_as_float((i < 3 ? w << (23 - 8 * i) : w >> 1) & 0x7F800000u);
 }
@@ -245,7 +246,9 @@ __global__ __launch_bounds__(kThreads, FMT == HUM_ACT_BF16 && D == 256 ? 1 : 2) 
   // No more workgroups than tiles (every share that counts is non-empty), and
   // where a head has up to three tiles on average, none than heads: two more
   // tiles in a row cost about as much as joining parts (16 sequences of 333
-  // FP8 tokens: 9.8 us cut, 8.2 whole; one of 200: 8.3 and 6.9).
+  // FP8 tokens: 9.8 us cut, 8.2 whole; one of 200: 8.3 and 6.9).  The shares
+  // are equal all the same: heads are whole where their lengths are, and
+  // ragged ones are cut where a border falls.
   const int32_t items = p.batch * items_per_seq, most = total <= 3 * (int64_t)items ? items : total;
   const int32_t nwg = most < p.wgs ? most : p.wgs;
   if (wg >= nwg) return;

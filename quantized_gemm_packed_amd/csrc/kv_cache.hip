@@ -4,9 +4,9 @@
 // A row (one token's K or V of one head) is quantized by the rules of
 // hum_quant_act: FP8 with one f32 scale per row (amax / 448), or MXFP8 /
 // MXFP4 with one E8M0 scale per 32.  D / 8 neighbouring lanes hold one row,
-// 16 bytes of bf16 each; the maximum is a shuffle inside them (a DPP quad
-// for an MX block), so nothing goes through LDS.  Memory bound: each row is
-// read once and its codes written once.
+// 16 bytes of bf16 each; the maximum moves between them (by DPP; the two
+// halves of an FP8 row of 256 by one permute), so nothing is stored in LDS.
+// Memory bound: each row is read once and its codes written once.
 //
 // Measured on MI355X, 16384 tokens of 8 heads of 128 in MXFP8, inputs that
 // change from call to call: written in 21.6 us (4.7 TB/s read + written; a

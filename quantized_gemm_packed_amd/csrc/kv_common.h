@@ -43,8 +43,11 @@ void kv_dispatch(const hum_kv_desc* d, F&& fn) {
 }
 
 // Eight codes of a row -> eight bf16 (packed pairs), times a power-of-two
-// scale: exact (at most four significant bits).  w: the codes' 8 (E4M3) or 4
-// (E2M1) bytes.
+// scale: at most four significant bits, so exact where the product lies in
+// bf16's range.  What kv_write stores does (its inputs are bf16, multiples of
+// 2^-133, and their codes times their scales are so too); other bytes may hold
+// products below 2^-133, which are rounded or lost, and past 2^128, which
+// become infinite.  w: the codes' 8 (E4M3) or 4 (E2M1) bytes.
 __device__ __forceinline__ u32x4_t e4m3x8_to_bf16(u32x2_t w, float scale) {
   u32x4_t o;
   o[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w[0], scale, false));
