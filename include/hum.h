@@ -186,6 +186,41 @@ hum_status hum_dequant_weight(const hum_weight_desc* desc, const void* packed,
 hum_status hum_quant_act(int32_t act_fmt, int64_t m, int64_t k, const void* x_bf16,
                          int64_t ld_x, void* q, void* scales, void* stream);
 
+/* ---- norm --------------------------------------------------------------- */
+
+typedef struct hum_norm_desc {
+  int32_t act_fmt;         /* hum_act_fmt of q; HUM_ACT_BF16: no codes */
+  int32_t residual_dtype;  /* HUM_BF16 | HUM_F32: the residual and its sum */
+  int32_t weight_dtype;    /* HUM_BF16 | HUM_F32 */
+  float eps;               /* above 0 */
+  float weight_offset;     /* added to every weight (1 for weights stored as their distance from one) */
+} hum_norm_desc;
+
+/* Root-mean-square norm of rows, with the residual's addition before it and
+ * the activation quantizer behind it, in one pass:
+ *   h = x + residual (f32),   residual_out = h rounded to its type,
+ *   y = h * (1 / sqrt(mean(h^2) + eps)) * (weight + weight_offset),
+ * y in f32 from the unrounded h, and rounded once: to bf16 (out), or to codes
+ * and scales by hum_quant_act's rules (q, scales: what hum_linear and
+ * hum_moe_grouped_gemm take as quantized activations), or both.
+ *   x            : bf16 [m][k]; ld_*: elements from row to row
+ *   residual     : [m][k] or NULL (h = x; residual_out is then NULL too)
+ *   weight       : [k]
+ *   out          : bf16 [m][k], or NULL where there are codes
+ *   q, scales    : contiguous, as hum_quant_act writes them (q 8-byte
+ *                  aligned); NULL for HUM_ACT_BF16
+ * k is at most 65536, and a multiple of 8 for FP8_TOKEN, of 32 for MXFP8 and
+ * MXFP4, of 128 for FP8_GROUP.  An output may take the place of x or of the
+ * residual (same pointer, row stride and element size); one that overlaps an
+ * input or an output otherwise is refused.  A row's bits depend on that row
+ * alone, not on m or on alignment.
+ * Magnitudes up to 2^55 are in range.  Past that the sum of squares may be
+ * infinite: such a row, and one that holds an infinity or NaN, gets y of
+ * zeros and NaN, and scales of NaN. */
+hum_status hum_rms_norm(const hum_norm_desc* desc, int64_t m, int64_t k, const void* x_bf16, int64_t ld_x,
+                        const void* residual, int64_t ld_residual, void* residual_out, int64_t ld_residual_out,
+                        const void* weight, void* out_bf16, int64_t ld_out, void* q, void* scales, void* stream);
+
 /* ---- dense layer --------------------------------------------------------- */
 
 /* Workspace bytes hum_linear needs for m rows (quantized activations,
@@ -387,6 +422,46 @@ hum_status hum_moe_gemm_masked(const hum_weight_desc* w13, const void* packed_w1
 size_t hum_moe_masked_workspace_bytes(const hum_weight_desc* w13, const hum_weight_desc* w2,
                                       int64_t max_m, int64_t expected_m,
                                       const hum_tile_config* cfg);
+
+/* Routing: logits [T][E] -> the topk_ids and topk_weights of hum_moe_gemm.
+ *   s_e = softmax(x)_e over all experts, or sigmoid: 1 / (1 + exp(-x_e))
+ *   Experts are ordered by s_e + bias_e; without a bias by x_e, which is the
+ *   same order (but no two of its values become equal by rounding).  Equal
+ *   ones: the lowest index first.
+ *   With num_groups > 1, only the experts of topk_groups groups take part:
+ *   groups are E / num_groups experts side by side, ordered by their best
+ *   expert (HUM_GROUP_MAX) or by the sum of their two best (HUM_GROUP_TOP2;
+ *   without a bias of their s), the lowest first among equal ones.
+ *   weights = s of the chosen (without the bias), divided by their sum where
+ *   renormalize, times scale.
+ * Scores are compared in f64.  Ids come best first.  An expert whose logit (or
+ * bias) is -inf takes no part; where fewer than topk are left, the other ids
+ * are -1 with weight 0, which hum_moe_gemm skips: a row of -inf (a padding
+ * token) routes nowhere.  A NaN logit comes first of all and its weight is NaN
+ * (with softmax or renormalize, every weight of its row; so it is where the
+ * softmax of a row meets an infinity, and the logits alone then order it); ids
+ * stay valid.
+ *   logits : [T][E], ld_logits elements from row to row
+ *   bias   : f32 [E] or NULL
+ *   topk_ids, topk_weights: contiguous [T][topk]
+ * E is at most 512, topk at most 64, num_groups at most 64. */
+typedef enum hum_route_score { HUM_SCORE_SOFTMAX = 0, HUM_SCORE_SIGMOID = 1 } hum_route_score;
+typedef enum hum_group_score { HUM_GROUP_MAX = 0, HUM_GROUP_TOP2 = 1 } hum_group_score;
+
+typedef struct hum_route_desc {
+  int32_t logits_dtype;  /* HUM_BF16 | HUM_F32 */
+  int32_t num_experts;
+  int32_t topk;
+  int32_t score;         /* hum_route_score */
+  int32_t num_groups;    /* divides num_experts; 1 for none */
+  int32_t topk_groups;   /* 1 .. num_groups */
+  int32_t group_score;   /* hum_group_score */
+  int32_t renormalize;   /* 0/1 */
+  float scale;
+} hum_route_desc;
+
+hum_status hum_moe_route(const hum_route_desc* desc, int64_t num_tokens, const void* logits, int64_t ld_logits,
+                         const float* bias, int32_t* topk_ids, float* topk_weights, void* stream);
 
 /* Stage export: sort the flat routing slots f = t*topk + j by expert.
  *   sorted  : i32 [T*topk + E*(block_m-1)]; segment of expert e starts at
@@ -613,6 +688,38 @@ hum_status hum_kv_attention(const hum_kv_desc* desc, const void* cache, size_t c
                             const int32_t* block_table, int64_t table_stride, int64_t max_pages,
                             const int32_t* seq_lens, int64_t window, float scale, void* out_bf16, float* lse,
                             void* workspace, size_t ws_bytes, void* stream);
+
+/* Rotary positions and the append to the cache in one launch: what
+ * hum_rotary of q and k and hum_kv_write of the turned k and of v do, with
+ *   q_out  : hum_rotary's, bit for bit (without a norm);
+ *   cache  : k's and v's rows, quantized as hum_kv_write does.  k is rounded
+ *            once, from the f32 turn to its codes (to bf16 and then to codes
+ *            by the two calls; in a bf16 cache the same bytes).
+ * Head norm, where norm and its weights are not NULL: before its turn, each
+ * head of q (q_weight) and of k (k_weight), [head_dim] weights, becomes
+ *   x * (1 / sqrt(mean(x^2) + eps)) * (w + weight_offset)    in f32.
+ * rot    : dtype HUM_BF16, inverse 0, head_dim and num_kv_heads the cache's;
+ *          num_q_heads may be 0 (q and q_out are then not read)
+ * slots  : as hum_kv_write's: those outside the cache are skipped (their q is
+ *          turned all the same), the others must differ
+ * strides: elements, any; q_out may be q itself (same pointer and strides).
+ * q_out or a cache that overlaps an input otherwise, or the other, is refused.
+ * At most 2^24 - 1 tokens in a call. */
+typedef struct hum_head_norm {
+  const void* q_weight;  /* [head_dim] on the device, or NULL: q's heads as they are */
+  const void* k_weight;  /* likewise for k */
+  int32_t weight_dtype;  /* HUM_BF16 | HUM_F32 */
+  float eps;             /* above 0 */
+  float weight_offset;   /* 1 for weights stored as their distance from one */
+} hum_head_norm;
+
+hum_status hum_rotary_kv_write(const hum_rotary_desc* rot, const hum_kv_desc* kv, const hum_head_norm* norm,
+                               void* cache, size_t cache_bytes, int64_t num_tokens, const int64_t* positions,
+                               const double* inv_freq, const int64_t* slots, const void* q, int64_t q_token_stride,
+                               int64_t q_head_stride, void* q_out, int64_t q_out_token_stride,
+                               int64_t q_out_head_stride, const void* k, int64_t k_token_stride,
+                               int64_t k_head_stride, const void* v, int64_t v_token_stride, int64_t v_head_stride,
+                               void* stream);
 
 /* ---- measurement -------------------------------------------------------- */
 

@@ -22,9 +22,10 @@ Modules:
   gemm     weight dequantization and the dense linear layer
   moe      routing align, per-expert GEMMs with SwiGLU, weighted reduce
   attention  rotary positions, the paged key-value cache, attention over it
+  layer    the norm with residual, the routing to experts, head norms
 
 Every function here is pinned by a CPU test against something other than
 itself (brute force, library routines, closed forms, invariants); see the
 ``tests/test_oracle_*.py`` files.
 """
-from . import formats, quant, gemm, moe, attention  # noqa: F401
+from . import formats, quant, gemm, moe, attention, layer  # noqa: F401

@@ -4,8 +4,9 @@ Argument marshalling only: every step of the computation runs in the HIP
 kernels of ``libhum.so``; PyTorch provides device memory and the current
 stream.  The names mirror the C ABI in ``include/hum.h``.  If the library is
 not built, every entry point raises -- there is no CPU fallback.  The
-decode-step calls (rotary, kv_write, kv_read, kv_attention) are marshalled by
-``_binding.so``, host code built beside it.
+calls around a layer's products (rms_norm, moe_route, rotary, rotary_kv_write,
+kv_write, kv_read, kv_attention) are marshalled by ``_binding.so``, host code
+built beside it.
 """
 from __future__ import annotations
 
@@ -24,7 +25,7 @@ __all__ = [
     "select_config", "linear_workspace_bytes", "linear", "moe_workspace_bytes",
     "moe_gemm", "moe_align", "moe_reduce", "Workspace", "header_functions",
     "KvDesc", "make_kv_desc", "rotary_inv_freq", "rotary", "kv_cache_bytes", "kv_write", "kv_read",
-    "kv_attention_workspace_bytes", "kv_attention",
+    "kv_attention_workspace_bytes", "kv_attention", "rms_norm", "moe_route", "rotary_kv_write",
 ]
 
 BF16, F32, INT4, UINT4, E2M1, E4M3, E8M0, INT8, INT3, UINT3, INT2, UINT2, INT1, UINT1, E2M3, E3M2 = range(16)
@@ -94,6 +95,28 @@ class KvDesc(ctypes.Structure):
         return "KvDesc(" + ", ".join(f"{f}={getattr(self, f)}" for f, _ in self._fields_) + ")"
 
 
+class NormDesc(ctypes.Structure):
+    _fields_ = [
+        ("act_fmt", ctypes.c_int32), ("residual_dtype", ctypes.c_int32), ("weight_dtype", ctypes.c_int32),
+        ("eps", ctypes.c_float), ("weight_offset", ctypes.c_float),
+    ]
+
+
+class RouteDesc(ctypes.Structure):
+    _fields_ = [
+        ("logits_dtype", ctypes.c_int32), ("num_experts", ctypes.c_int32), ("topk", ctypes.c_int32),
+        ("score", ctypes.c_int32), ("num_groups", ctypes.c_int32), ("topk_groups", ctypes.c_int32),
+        ("group_score", ctypes.c_int32), ("renormalize", ctypes.c_int32), ("scale", ctypes.c_float),
+    ]
+
+
+class HeadNorm(ctypes.Structure):
+    _fields_ = [
+        ("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p), ("weight_dtype", ctypes.c_int32),
+        ("eps", ctypes.c_float), ("weight_offset", ctypes.c_float),
+    ]
+
+
 _lib = None
 _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
@@ -145,6 +168,10 @@ _SIGS = {
     "hum_kv_attention_workspace_bytes": (_SZ, [_P, _I32, _I64, _I64]),
     "hum_kv_attention": (_I32, [_P, _P, _SZ, _I32, _I64, _P, _I64, _I64, _P, _I64, _I64, _P, _I64, ctypes.c_float,
                                 _P, _P, _P, _SZ, _P]),
+    "hum_rms_norm": (_I32, [_P, _I64, _I64, _P, _I64, _P, _I64, _P, _I64, _P, _P, _I64, _P, _P, _P]),
+    "hum_moe_route": (_I32, [_P, _I64, _P, _I64, _P, _P, _P, _P]),
+    "hum_rotary_kv_write": (_I32, [_P, _P, _P, _P, _SZ, _I64, _P, _P, _P, _P, _I64, _I64, _P, _I64, _I64, _P, _I64, _I64,
+                                   _P, _I64, _I64, _P]),
 }
 
 
@@ -708,7 +735,7 @@ def moe_grouped_gemm(w: WeightDesc, packed, a, sorted_ids, offsets, block_m: int
     return res[0] if len(res) == 1 else res
 
 
-# ---- attention side of a decode step --------------------------------------
+# ---- around a layer's products ---------------------------------------------
 
 _WS_HEADER = 64 << 10   # HUM_WS_HEADER_BYTES
 ROPE_HALF, ROPE_INTERLEAVED = range(2)
@@ -749,6 +776,51 @@ def _call_workspace(dev, need):
         ws[:_WS_HEADER].zero_()
         return ws
     return _workspace(device).get(need)
+
+
+def rms_norm(x, weight, eps: float = 1e-6, residual=None, act_fmt: str = "bf16", weight_offset: float = 0.0,
+             residual_out=None, out=None, with_bf16: bool = False):
+    """y = h / sqrt(mean(h^2) + eps) * (weight + weight_offset) of the rows of
+    h = x + residual (x bf16 [m, k], residual bf16 or float32 [m, k] or None,
+    weight bf16 or float32 [k]), in bf16, or quantized to act_fmt
+    ("fp8_token", "mxfp8", "mxfp4", "fp8_group") as quant_act does: the
+    (codes, scales) that linear takes as a and a_scales.
+
+    Returns y: a bf16 tensor, or (codes, scales), or with with_bf16 (codes,
+    scales, bf16 y).  With a residual: (y, residual_out), the sum h in the
+    residual's type.  residual_out may be the residual and out (of the bf16 y)
+    may be x, for results in place; outputs that overlap otherwise are
+    refused.  Rows may be strided."""
+    fmt = _AF.get(act_fmt, act_fmt)
+    return (_nat or _native()).rms_norm(x, weight, eps, residual, fmt, weight_offset, residual_out, out, with_bf16)
+
+
+SCORE_SOFTMAX, SCORE_SIGMOID = range(2)
+GROUP_MAX, GROUP_TOP2 = range(2)
+_SCORE = {"softmax": SCORE_SOFTMAX, "sigmoid": SCORE_SIGMOID}
+_GROUP_SCORE = {"max": GROUP_MAX, "top2": GROUP_TOP2}
+
+
+def moe_route(logits, topk: int, score: str = "softmax", bias=None, num_groups: int = 1, topk_groups: int = 1,
+              group_score: str = "max", renormalize: bool = True, scale: float = 1.0, topk_ids=None,
+              topk_weights=None):
+    """Router logits [T, E] (bf16 or float32) -> (topk_ids int32 [T, topk],
+    topk_weights float32 [T, topk]), what moe_gemm takes.
+
+    Scores are the softmax over all experts or the sigmoid of each logit.  The
+    topk experts are those of the largest score + bias (float32 [E] or None),
+    best first, the lowest index first of equal ones; with num_groups > 1 only
+    those of the topk_groups best groups of E / num_groups neighbours, by
+    their best expert ("max") or the sum of their two best ("top2").  Weights
+    are the scores (without the bias), divided by their sum if renormalize,
+    times scale.  Experts with logit -inf take no part; ids of -1 with weight
+    0 stand where none is left (moe_gemm skips them)."""
+    if score not in _SCORE:
+        raise ValueError(f"score must be one of {sorted(_SCORE)}")
+    if group_score not in _GROUP_SCORE:
+        raise ValueError(f"group_score must be one of {sorted(_GROUP_SCORE)}")
+    return (_nat or _native()).moe_route(logits, topk, _SCORE[score], bias, num_groups, topk_groups,
+                                         _GROUP_SCORE[group_score], renormalize, scale, topk_ids, topk_weights)
 
 
 def rotary_inv_freq(rotary_dim: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
@@ -802,6 +874,21 @@ def kv_read(desc: KvDesc, cache, slots, k_out=None, v_out=None):
     """slots int64 [T] of `cache` -> k, v bf16 [T, Hkv, D]; slots outside the
     cache (-1) read as zeros."""
     return (_nat or _native()).kv_read(desc, cache, slots, k_out, v_out)
+
+
+def rotary_kv_write(desc: KvDesc, cache, q, k, v, positions, inv_freq, slots, layout: str = "half", factor: float = 1.0,
+                    q_norm=None, k_norm=None, eps: float = 1e-6, weight_offset: float = 0.0, q_out=None):
+    """rotary(q, k, ...) and kv_write of the turned k and of v in one launch:
+    q bf16 [T, Hq, D] (or None) turned -> q_out, k and v bf16 [T, Hkv, D]
+    quantized into slots int64 [T] of `cache`; the turned k is rounded once,
+    to its codes.  q_norm, k_norm (bf16 or float32 [D], both of one type, or
+    None): each head of q or k first becomes
+    x / sqrt(mean(x^2) + eps) * (norm + weight_offset).  q_out may be q (a
+    turn in place); slots outside the cache (-1) are skipped."""
+    if layout not in _ROPE_LAYOUT:
+        raise ValueError(f"layout must be one of {sorted(_ROPE_LAYOUT)}")
+    return (_nat or _native()).rotary_kv_write(desc, cache, q, k, v, positions, inv_freq, slots, _ROPE_LAYOUT[layout],
+                                               factor, q_norm, k_norm, eps, weight_offset, q_out)
 
 
 def kv_attention_workspace_bytes(desc: KvDesc, num_q_heads: int, batch: int, max_pages: int) -> int:

@@ -1,5 +1,5 @@
 """Builds libhum.so (all HIP kernels + the C ABI) for gfx950 with hipcc, and
-_binding.so (host code: native marshalling of the decode-step calls).
+_binding.so (host code: native marshalling of the calls around a layer's products).
 
 The library is built in-tree, next to this file, so it travels with the
 source tree.  Every translation unit is compiled with packed-FP32 code
@@ -21,8 +21,8 @@ BUILD_DIR = os.path.join(HERE, "_build")
 # that they compile in parallel.
 GEMM_SOURCES = ["gemm.hip", "inst_dense_a.hip", "inst_dense_b.hip", "inst_dense_c.hip", "inst_dense_d.hip",
                 "inst_dense_sk.hip", "inst_moe_a.hip", "inst_moe_b.hip", "inst_moe_c.hip"]
-SOURCES = ["api.hip", "repack.hip", "act_moe.hip", "rotary.hip", "kv_cache.hip", "kv_attention.hip", "peaks.hip",
-           *GEMM_SOURCES]
+SOURCES = ["api.hip", "repack.hip", "act_moe.hip", "rms_norm.hip", "route.hip", "rotary.hip", "kv_cache.hip",
+           "kv_append.hip", "kv_attention.hip", "peaks.hip", *GEMM_SOURCES]
 ARCH = os.environ.get("HUM_OFFLOAD_ARCH", "gfx950")
 
 COMMON = [
@@ -56,7 +56,7 @@ def _compile(src: str) -> str:
 
 
 def _build_binding() -> None:
-    """_binding.so: the native marshalling of the decode-step calls (host code
+    """_binding.so: the native marshalling of the calls around a layer's products (host code
     against torch's headers; its HIP and hum symbols come with libhum.so)."""
     import sysconfig
 

@@ -1,5 +1,5 @@
-// Marshalling of the decode-step calls (rotary, cache, attention): the checks
-// of the tensors, the outputs and the call into libhum, as one native call.
+// Marshalling of the calls around a layer's products (norm, routing, rotary,
+// cache, attention): the checks of the tensors, the outputs and the call into libhum, as one native call.
 //
 // A decode step makes these calls once per layer with little work in each, so
 // the host side is what a small one costs: marshalled in Python a call took
@@ -376,6 +376,227 @@ PyObject* kv_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
+// A [rows, elements] tensor whose elements are contiguous; rows may be strided.
+void want_matrix(const at::Tensor& t, const char* name, int64_t n, int64_t k) {
+  if (t.is_neg()) fail("%s must hold its values (a negated view does not: resolve_neg())", name);
+  if (t.dim() != 2 || t.size(0) != n || t.size(1) != k) fail("%s must have shape (%lld, %lld)", name, (long long)n, (long long)k);
+  if (k > 1 && t.stride(1) != 1) fail("%s's rows must be contiguous", name);
+}
+void want_float(const at::Tensor& t, const char* name) {
+  if (t.scalar_type() != at::kBFloat16 && t.scalar_type() != at::kFloat)
+    fail("%s must be torch.bfloat16 or torch.float32, got %s", name, dtype_name(t.scalar_type()));
+}
+int32_t hum_dtype_of(const at::Tensor& t) { return t.scalar_type() == at::kFloat ? HUM_F32 : HUM_BF16; }
+int32_t whole32(PyObject* o, const char* name) {
+  const long long v = whole(o, name);
+  if (v < INT32_MIN || v > INT32_MAX) fail("%s is out of range", name);
+  return (int32_t)v;
+}
+PyObject* given_or(const at::Tensor& t, PyObject* given) {
+  if (given == Py_None) return THPVariable_Wrap(t);
+  Py_INCREF(given);
+  return given;
+}
+
+// rms_norm(x, weight, eps, residual, act_fmt, weight_offset, residual_out, out, with_bf16)
+PyObject* rms_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  want_args(n, 9);
+  const at::Tensor& x = tensor(a[0], "x", 2, "[m, k]");
+  const int64_t m = x.size(0), k = x.size(1);
+  want_dtype(x, "x", at::kBFloat16);
+  want_matrix(x, "x", m, k);
+  const at::Tensor& w = tensor(a[1], "weight", 1, "[k]");
+  want_float(w, "weight");
+  want_vec(&w, "weight", w.scalar_type(), k);
+  const at::Tensor *res = maybe(a[3], "residual"), *res_out = maybe(a[6], "residual_out"), *out = maybe(a[7], "out");
+  if (res) {
+    want_float(*res, "residual");
+    want_matrix(*res, "residual", m, k);
+  }
+  if (res_out) {
+    if (!res) fail("residual_out without residual");
+    want_dtype(*res_out, "residual_out", res->scalar_type());
+    want_matrix(*res_out, "residual_out", m, k);
+    want_spread(*res_out, "residual_out");
+  }
+  if (PyUnicode_Check(a[4])) fail("act_fmt must be bf16, fp8_token, mxfp8, mxfp4 or fp8_group");
+  const int32_t fmt = whole32(a[4], "act_fmt");
+  if (fmt < HUM_ACT_BF16 || fmt > HUM_ACT_FP8_GROUP) fail("act_fmt must be bf16, fp8_token, mxfp8, mxfp4 or fp8_group");
+  const bool quant = fmt != HUM_ACT_BF16, with_bf16 = truth(a[8]);
+  if (out) {
+    if (quant && !with_bf16) fail("out is of the bf16 result: give with_bf16 too");
+    want_dtype(*out, "out", at::kBFloat16);
+    want_matrix(*out, "out", m, k);
+    want_spread(*out, "out");
+  }
+  const int dev = device_of("x", {&x, &w, res, res_out, out});
+  const int64_t unit = fmt == HUM_ACT_FP8_TOKEN ? 8 : fmt == HUM_ACT_FP8_GROUP ? 128 : quant ? 32 : 1;
+  if (k < 1 || k % unit) fail("x must have a multiple of %lld columns", (long long)unit);
+  hum_norm_desc desc{};
+  desc.act_fmt = fmt;
+  desc.residual_dtype = res ? hum_dtype_of(*res) : HUM_BF16;
+  desc.weight_dtype = hum_dtype_of(w);
+  desc.eps = (float)real(a[2]);
+  desc.weight_offset = (float)real(a[5]);
+  at::Tensor q, scales, fresh, fresh_res;
+  if (quant) {
+    const auto bytes = x.options().dtype(at::kByte);
+    const auto f32 = x.options().dtype(at::kFloat);
+    q = at::empty({m, fmt == HUM_ACT_MXFP4 ? k / 2 : k}, bytes);
+    scales = fmt == HUM_ACT_FP8_TOKEN ? at::empty({m}, f32) : fmt == HUM_ACT_FP8_GROUP ? at::empty({m, k / 128}, f32) : at::empty({m, k / 32}, bytes);
+  }
+  if (!out && (!quant || with_bf16)) {
+    fresh = at::empty({m, k}, x.options());
+    out = &fresh;
+  }
+  if (res && !res_out) {
+    fresh_res = at::empty({m, k}, res->options());
+    res_out = &fresh_res;
+  }
+  const DeviceGuard guard(dev);
+  const hum_status st = hum_rms_norm(
+      &desc, m, k, x.data_ptr(), x.stride(0), res ? res->data_ptr() : nullptr, res ? res->stride(0) : 0,
+      res ? res_out->data_ptr() : nullptr, res ? res_out->stride(0) : 0, w.data_ptr(), out ? out->data_ptr() : nullptr,
+      out ? out->stride(0) : 0, quant ? q.data_ptr() : nullptr, quant ? scales.data_ptr() : nullptr, stream_of(dev));
+  if (st != HUM_OK) raise_status(st);
+  PyObject* y;
+  if (!quant) {
+    y = given_or(*out, a[7]);
+  } else {
+    const Ref c(THPVariable_Wrap(q)), s(THPVariable_Wrap(scales));
+    if (with_bf16) {
+      const Ref b(given_or(*out, a[7]));
+      y = PyTuple_Pack(3, c.o, s.o, b.o);
+    } else {
+      y = PyTuple_Pack(2, c.o, s.o);
+    }
+  }
+  if (!res) return y;
+  const Ref yr(y), rr(given_or(*res_out, a[6]));
+  return PyTuple_Pack(2, yr.o, rr.o);
+  END_HANDLE_TH_ERRORS
+}
+
+// moe_route(logits, topk, score, bias, num_groups, topk_groups, group_score, renormalize, scale, topk_ids, topk_weights)
+PyObject* moe_route(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  want_args(n, 11);
+  const at::Tensor& x = tensor(a[0], "logits", 2, "[T, E]");
+  const int64_t t = x.size(0), e = x.size(1);
+  want_float(x, "logits");
+  want_matrix(x, "logits", t, e);
+  hum_route_desc desc{};
+  desc.logits_dtype = hum_dtype_of(x);
+  desc.num_experts = (int32_t)(e < INT32_MAX ? e : INT32_MAX);
+  desc.topk = whole32(a[1], "topk");
+  desc.score = whole32(a[2], "score");
+  desc.num_groups = whole32(a[4], "num_groups");
+  desc.topk_groups = whole32(a[5], "topk_groups");
+  desc.group_score = whole32(a[6], "group_score");
+  desc.renormalize = truth(a[7]);
+  desc.scale = (float)real(a[8]);
+  if (desc.topk < 1 || desc.topk > e) fail("topk must be 1 .. the number of experts");
+  const at::Tensor *bias = maybe(a[3], "bias"), *ids = maybe(a[9], "topk_ids"), *weights = maybe(a[10], "topk_weights");
+  if (bias) want_vec(bias, "bias", at::kFloat, e);
+  if (ids) {
+    want_dtype(*ids, "topk_ids", at::kInt);
+    want_matrix(*ids, "topk_ids", t, desc.topk);
+    want_contiguous(*ids, "topk_ids");
+  }
+  if (weights) {
+    want_dtype(*weights, "topk_weights", at::kFloat);
+    want_matrix(*weights, "topk_weights", t, desc.topk);
+    want_contiguous(*weights, "topk_weights");
+  }
+  const int dev = device_of("logits", {&x, bias, ids, weights});
+  at::Tensor new_ids, new_weights;
+  if (!ids) {
+    new_ids = at::empty({t, desc.topk}, x.options().dtype(at::kInt));
+    ids = &new_ids;
+  }
+  if (!weights) {
+    new_weights = at::empty({t, desc.topk}, x.options().dtype(at::kFloat));
+    weights = &new_weights;
+  }
+  const DeviceGuard guard(dev);
+  const hum_status st = hum_moe_route(&desc, t, x.data_ptr(), x.stride(0), bias ? static_cast<const float*>(bias->data_ptr()) : nullptr,
+                                      static_cast<int32_t*>(ids->data_ptr()), static_cast<float*>(weights->data_ptr()), stream_of(dev));
+  if (st != HUM_OK) raise_status(st);
+  return pair(*ids, a[9], weights, a[10]);
+  END_HANDLE_TH_ERRORS
+}
+
+// rotary_kv_write(desc, cache, q, k, v, positions, inv_freq, slots, layout, factor, q_norm, k_norm, eps, weight_offset, q_out)
+PyObject* rotary_kv_write(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  want_args(n, 15);
+  const KvDesc desc(a[0]);
+  const at::Tensor* cache = maybe(a[1], "cache");
+  want_cache(cache);
+  const char* heads = "[T, heads, head_dim]";
+  const at::Tensor* q = a[2] == Py_None ? nullptr : &tensor(a[2], "q", 3, heads);
+  const at::Tensor &k = tensor(a[3], "k", 3, heads), &v = tensor(a[4], "v", 3, heads);
+  const int64_t t = k.size(0), hq = q ? q->size(1) : 0, hk = desc->num_kv_heads, d = desc->head_dim;
+  if (q) want_rows(*q, "q", at::kBFloat16, t, hq, d);
+  want_rows(k, "k", at::kBFloat16, t, hk, d);
+  want_rows(v, "v", at::kBFloat16, t, hk, d);
+  const at::Tensor *pos = maybe(a[5], "positions"), *slots = maybe(a[7], "slots");
+  want_vec(pos, "positions", at::kLong, t);
+  want_vec(slots, "slots", at::kLong, t);
+  const at::Tensor& freq = tensor(a[6], "inv_freq", 1, "of float64");
+  const int64_t half = freq.size(0);
+  want_vec(&freq, "inv_freq", at::kDouble, half);
+  const at::Tensor *norm[2] = {maybe(a[10], "q_norm"), maybe(a[11], "k_norm")}, *qo = maybe(a[14], "q_out");
+  const char* names[2] = {"q_norm", "k_norm"};
+  for (int i = 0; i < 2; ++i) {
+    if (!norm[i]) continue;
+    want_float(*norm[i], names[i]);
+    want_vec(norm[i], names[i], norm[i]->scalar_type(), d);
+  }
+  if (norm[0] && norm[1]) want_dtype(*norm[1], "k_norm", norm[0]->scalar_type());
+  if (norm[0] && !q) fail("q_norm without q");
+  if (qo) {
+    if (!q) fail("q_out without q");
+    want_rows(*qo, "q_out", at::kBFloat16, t, hq, d);
+    want_spread(*qo, "q_out");
+  }
+  const int dev = device_of("cache", {cache, q, &k, &v, pos, slots, &freq, norm[0], norm[1], qo});
+  hum_rotary_desc rot{};
+  rot.dtype = HUM_BF16;
+  rot.layout = whole32(a[8], "layout");
+  rot.head_dim = (int32_t)d;
+  rot.rotary_dim = (int32_t)(half < INT32_MAX / 2 ? 2 * half : INT32_MAX - 1);
+  rot.num_q_heads = (int32_t)(hq < INT32_MAX ? hq : INT32_MAX);
+  rot.num_kv_heads = (int32_t)hk;
+  rot.factor = (float)real(a[9]);
+  hum_head_norm hn{};
+  const at::Tensor* any = norm[0] ? norm[0] : norm[1];
+  if (any) {
+    hn.q_weight = norm[0] ? norm[0]->data_ptr() : nullptr;
+    hn.k_weight = norm[1] ? norm[1]->data_ptr() : nullptr;
+    hn.weight_dtype = hum_dtype_of(*any);
+    hn.eps = (float)real(a[12]);
+    hn.weight_offset = (float)real(a[13]);
+  }
+  at::Tensor fresh;
+  if (q && !qo) {
+    fresh = at::empty({t, hq, d}, q->options());
+    qo = &fresh;
+  }
+  const DeviceGuard guard(dev);
+  const hum_status st = hum_rotary_kv_write(
+      &rot, desc.d, any ? &hn : nullptr, cache->data_ptr(), (size_t)cache->numel(), t,
+      static_cast<const int64_t*>(pos->data_ptr()), static_cast<const double*>(freq.data_ptr()),
+      static_cast<const int64_t*>(slots->data_ptr()), q ? q->data_ptr() : nullptr, q ? q->stride(0) : 0,
+      q ? q->stride(1) : 0, q ? qo->data_ptr() : nullptr, q ? qo->stride(0) : 0, q ? qo->stride(1) : 0, k.data_ptr(),
+      k.stride(0), k.stride(1), v.data_ptr(), v.stride(0), v.stride(1), stream_of(dev));
+  if (st != HUM_OK) raise_status(st);
+  if (!q) Py_RETURN_NONE;
+  return given_or(*qo, a[14]);
+  END_HANDLE_TH_ERRORS
+}
+
 // setup(HumError, raw stream function, workspace function, workspaces)
 PyObject* setup(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
@@ -391,9 +612,10 @@ PyObject* setup(PyObject*, PyObject* const* a, Py_ssize_t n) {
 }
 
 #define HUM_METHOD(f) {#f, (PyCFunction)(void (*)(void))f, METH_FASTCALL, nullptr}
-PyMethodDef g_methods[] = {HUM_METHOD(rotary),       HUM_METHOD(kv_write), HUM_METHOD(kv_read),
-                           HUM_METHOD(kv_attention), HUM_METHOD(setup),    {nullptr, nullptr, 0, nullptr}};
-PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_binding", "Marshalling of the decode-step calls.", -1, g_methods,
+PyMethodDef g_methods[] = {HUM_METHOD(rms_norm), HUM_METHOD(moe_route),    HUM_METHOD(rotary),
+                           HUM_METHOD(kv_write), HUM_METHOD(kv_read),      HUM_METHOD(rotary_kv_write),
+                           HUM_METHOD(setup),    HUM_METHOD(kv_attention), {nullptr, nullptr, 0, nullptr}};
+PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_binding", "Marshalling of the calls around a layer's products.", -1, g_methods,
                         nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

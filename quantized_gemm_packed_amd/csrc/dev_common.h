@@ -117,4 +117,29 @@ __device__ __forceinline__ float mx_inv_scale(int e) {
   return __uint_as_float(0x00400000u);  // 2^-127
 }
 
+// Eight floats over a power of two -> eight codes, nearest even, saturated
+// (the hardware conversions; E2M1 saturates by itself, E4M3 becomes NaN past
+// 448, so what the rule saturates is clamped first).
+__device__ __forceinline__ u32x2_t mx_e4m3x8(const float (&f)[8], float scale) {
+  typedef short s16x2_v __attribute__((ext_vector_type(2)));
+  const float top = 448.0f * scale;
+  float c[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) c[i] = __builtin_fminf(__builtin_fmaxf(f[i], -top), top);
+  s16x2_v o[2] = {{0, 0}, {0, 0}};
+  o[0] = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(o[0], c[0], c[1], scale, false);
+  o[0] = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(o[0], c[2], c[3], scale, true);
+  o[1] = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(o[1], c[4], c[5], scale, false);
+  o[1] = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(o[1], c[6], c[7], scale, true);
+  return u32x2_t{__builtin_bit_cast(uint32_t, o[0]), __builtin_bit_cast(uint32_t, o[1])};
+}
+__device__ __forceinline__ uint32_t mx_e2m1x8(const float (&f)[8], float scale) {
+  uint32_t o = 0;
+  o = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(o, f[0], f[1], scale, 0);
+  o = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(o, f[2], f[3], scale, 1);
+  o = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(o, f[4], f[5], scale, 2);
+  o = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(o, f[6], f[7], scale, 3);
+  return o;
+}
+
 }  // namespace hum

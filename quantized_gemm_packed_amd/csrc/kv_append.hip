@@ -1,0 +1,349 @@
+// Rotary positions and the paged cache in one launch: q is turned, k is
+// turned, quantized and written to its slots beside v.
+//
+// Per row (one head of one token): the head's norm, where there is one,
+//   x' = x * (1 / sqrt(mean(x^2) + eps)) * (w + offset),
+// the turn of its first rotary_dim elements (hum_rotary's coefficients and
+// products: the same bits), and for k and v the cache's quantizer; f32 between
+// them, rounded once at the end.  D / 8 neighbouring lanes have one row, 8
+// elements each.  Memory bound: q is read and written once, k and v are read
+// once and their codes written once; apart, the turned k would be written and
+// read once more, and a launch paid twice.
+#include <cmath>
+
+#include "kv_common.h"
+#include "rotary_common.h"
+#include "rows.h"
+
+namespace hum {
+
+struct AppendParams {
+  uint8_t* cache;
+  uint32_t unit, page_stride;
+  int64_t slots_all;
+  int32_t page_shift;
+  int32_t heads[2];  // of q, of k and v
+  const int64_t *slots, *positions;
+  const double* inv_freq;
+  const uint16_t* x[3];  // q, k, v
+  int64_t ts[3], hs[3];
+  uint16_t* q_out;
+  int64_t qo_ts, qo_hs;
+  const void* w[2];  // head norms of q, of k
+  int64_t tokens;
+  int32_t half;        // rotary_dim / 2
+  int32_t tok_per_wg;
+  int32_t row_step;    // rows (q's heads, k's, v's) per workgroup (grid.y slices them)
+  int32_t w_f32;
+  float factor, eps, offset;
+};
+
+constexpr int kAppendRows = 4;  // rows that a thread has in flight at once
+
+// Sum over the N lanes (8, 16 or 32) that hold one row.
+template <int N>
+__device__ __forceinline__ float row_sum(float v) {
+  auto with = [&](auto ctrl) {
+    v += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), decltype(ctrl)::value, 0xF, 0xF, false));
+  };
+  with(std::integral_constant<int, 0xB1>{});   // quad_perm 1,0,3,2
+  with(std::integral_constant<int, 0x4E>{});   // quad_perm 2,3,0,1
+  with(std::integral_constant<int, 0x141>{});  // row_half_mirror
+  if constexpr (N >= 16) with(std::integral_constant<int, 0x140>{});
+  if constexpr (N >= 32) v += __shfl_xor(v, 16);
+  return v;
+}
+
+__device__ __forceinline__ void unpack8(const u32x4_t v, float (&f)[8]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f[2 * i] = bf16_bits_to_f32(v[i] & 0xFFFF);
+    f[2 * i + 1] = bf16_bits_to_f32(v[i] >> 16);
+  }
+}
+
+// FAST: every piece of 8 elements lies at 16 bytes and turns as a whole, with
+// another whole piece (half layout: the half a multiple of 8 elements) or
+// within itself (interleaved: rotary_dim a multiple of 8).
+template <int FMT, int D, bool HALF, bool FAST, bool NORM>
+__global__ __launch_bounds__(256) void append_kernel(const AppendParams p) {
+  using U = KvUnit<FMT, D>;
+  constexpr int kLanes = D / 8;
+  constexpr int kStep = 256 / kLanes;  // rows a workgroup moves at once
+  constexpr int kB = 8 * U::kRow / D;
+  extern __shared__ float lds[];
+  const int tid = threadIdx.x, lane = tid % kLanes;
+  const int64_t t0 = (int64_t)blockIdx.x * p.tok_per_wg;
+  const int nt = (int)(p.tokens - t0 < p.tok_per_wg ? p.tokens - t0 : p.tok_per_wg);
+  float* cs = lds;
+  float* sn = lds + p.tok_per_wg * p.half;
+  const int all = p.heads[0] + 2 * p.heads[1];
+  const int r0 = (int)blockIdx.y * p.row_step;
+  const int nr = all - r0 < p.row_step ? all - r0 : p.row_step;
+  const float inv_nr = 1.0f / (float)nr;  // items below 2^17: (item + 1/2) inv_nr is never a whole step off
+  const int items = nt * nr;
+  const int page_size = 1 << p.page_shift;
+
+  u32x4_t own[kAppendRows], other[kAppendRows];
+  int tok[kAppendRows], kind[kAppendRows], head[kAppendRows];
+  auto load = [&](int base) {
+#pragma unroll
+    for (int n = 0; n < kAppendRows; ++n) {
+      const int item = base + n * kStep + tid / kLanes;
+      own[n] = other[n] = u32x4_t{0, 0, 0, 0};
+      kind[n] = -1;
+      if (item >= items) continue;
+      tok[n] = (int)(((float)item + 0.5f) * inv_nr);
+      const int row = r0 + item - tok[n] * nr;
+      kind[n] = row < p.heads[0] ? 0 : row < p.heads[0] + p.heads[1] ? 1 : 2;
+      head[n] = row - (kind[n] ? p.heads[0] : 0) - (kind[n] == 2 ? p.heads[1] : 0);
+      const uint16_t* x = (kind[n] == 0 ? p.x[0] : kind[n] == 1 ? p.x[1] : p.x[2]) +
+                          (t0 + tok[n]) * (kind[n] == 0 ? p.ts[0] : kind[n] == 1 ? p.ts[1] : p.ts[2]) +
+                          head[n] * (kind[n] == 0 ? p.hs[0] : kind[n] == 1 ? p.hs[1] : p.hs[2]);
+      if constexpr (FAST) {
+        own[n] = *reinterpret_cast<const u32x4_t*>(x + lane * 8);
+        if constexpr (HALF) {
+          const int m = p.half / 8;
+          if (kind[n] < 2 && lane < 2 * m) other[n] = *reinterpret_cast<const u32x4_t*>(x + (lane < m ? lane + m : lane - m) * 8);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) own[n][i] = (uint32_t)x[lane * 8 + 2 * i] | ((uint32_t)x[lane * 8 + 2 * i + 1] << 16);
+        if (HALF && kind[n] < 2) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int e = lane * 8 + i;
+            const uint32_t b = e < p.half ? x[e + p.half] : e < 2 * p.half ? x[e - p.half] : 0;
+            other[n][i / 2] |= b << (16 * (i & 1));
+          }
+        }
+      }
+    }
+  };
+  load(0);
+
+  for (int i = tid; i < nt * p.half; i += 256) {
+    const int t = i / p.half;
+    rotary_coefficients(p.positions[t0 + t], p.inv_freq[i - t * p.half], p.factor, 1.0f, cs + i, sn + i);
+  }
+  __syncthreads();
+
+  for (int base = 0; base < items; base += kAppendRows * kStep) {
+    if (base) load(base);
+#pragma unroll
+    for (int n = 0; n < kAppendRows; ++n) {
+      if (kind[n] < 0) continue;
+      float f[8], g[8];
+      unpack8(own[n], f);
+      unpack8(other[n], g);
+      if (kind[n] < 2) {
+        const void* w = kind[n] ? p.w[1] : p.w[0];
+        if (NORM && w) {
+          float sum = 0.0f;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) sum = __builtin_fmaf(f[i], f[i], sum);
+          const float r = 1.0f / __builtin_sqrtf(row_sum<kLanes>(sum) * (1.0f / D) + p.eps);
+          auto weight = [&](int e) {
+            return (p.w_f32 ? static_cast<const float*>(w)[e] : bf16_bits_to_f32(static_cast<const uint16_t*>(w)[e])) + p.offset;
+          };
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int e = lane * 8 + i;
+            f[i] = f[i] * r * weight(e);
+            if (HALF && e < 2 * p.half) g[i] = g[i] * r * weight(e < p.half ? e + p.half : e - p.half);
+          }
+        }
+        const float *c = cs + tok[n] * p.half, *s = sn + tok[n] * p.half;
+        if constexpr (HALF) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int e = lane * 8 + i;
+            if (e < p.half) f[i] = rotary_first(f[i], g[i], c[e], s[e]);
+            else if (e < 2 * p.half) f[i] = rotary_second(g[i], f[i], c[e - p.half], s[e - p.half]);
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int pr = lane * 4 + i;
+            if (pr < p.half) {
+              const float a = f[2 * i], b = f[2 * i + 1];
+              f[2 * i] = rotary_first(a, b, c[pr], s[pr]);
+              f[2 * i + 1] = rotary_second(a, b, c[pr], s[pr]);
+            }
+          }
+        }
+      }
+      if (kind[n] == 0) {
+        uint16_t* y = p.q_out + (t0 + tok[n]) * p.qo_ts + head[n] * p.qo_hs + lane * 8;
+        if constexpr (FAST) {
+          u32x4_t o;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) o[i] = f32x2_to_bf16x2_bits(f[2 * i], f[2 * i + 1]);
+          *reinterpret_cast<u32x4_t*>(y) = o;
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) y[i] = (uint16_t)f32_to_bf16_bits(f[i]);
+        }
+        continue;
+      }
+      const int which = kind[n] - 1;
+      const int64_t slot = p.slots[t0 + tok[n]];
+      // (unsigned: negative slots are past the end too)
+      const bool live = (uint64_t)slot < (uint64_t)p.slots_all;
+      const uint32_t page = (uint32_t)(slot >> p.page_shift);
+      const int at = (int)(slot & (page_size - 1));
+      const KvOffsets<FMT, D> off(which, at, page_size);
+      uint8_t* unit = p.cache + (uint64_t)head[n] * p.unit + (uint64_t)page * p.page_stride;
+      if (which) kv_store_row<FMT, D, false>(f, lane, unit + off.code + lane * kB, unit + off.scale, off.scale_step, live);
+      else kv_store_row<FMT, D, true>(f, lane, unit + off.code + lane * kB, unit + off.scale, off.scale_step, live);
+    }
+  }
+}
+
+}  // namespace hum
+
+using namespace hum;
+
+extern "C" hum_status hum_rotary_kv_write(const hum_rotary_desc* rot, const hum_kv_desc* kv, const hum_head_norm* norm,
+                                          void* cache, size_t cache_bytes, int64_t num_tokens, const int64_t* positions,
+                                          const double* inv_freq, const int64_t* slots, const void* q, int64_t q_ts,
+                                          int64_t q_hs, void* q_out, int64_t qo_ts, int64_t qo_hs, const void* k,
+                                          int64_t k_ts, int64_t k_hs, const void* v, int64_t v_ts, int64_t v_hs,
+                                          void* stream) {
+  clear_error();
+  if (!rot) return set_error(HUM_ERR_INVALID_ARG, "the rotary description is NULL");
+  KvLayout l;
+  const hum_status st = kv_layout(kv, &l);
+  if (st != HUM_OK) return st;
+  if (rot->dtype != HUM_BF16) return set_error(HUM_ERR_UNSUPPORTED, "dtype must be bf16");
+  if (rot->layout != HUM_ROPE_HALF && rot->layout != HUM_ROPE_INTERLEAVED)
+    return set_error(HUM_ERR_INVALID_ARG, "bad layout");
+  if (rot->head_dim != kv->head_dim || rot->num_kv_heads != kv->num_kv_heads)
+    return set_error(HUM_ERR_INVALID_ARG, "head_dim and num_kv_heads must be the cache's");
+  if (rot->rotary_dim < 2 || rot->rotary_dim % 2 || rot->rotary_dim > rot->head_dim)
+    return set_error(HUM_ERR_INVALID_ARG, "rotary_dim must be even, 2 .. head_dim");
+  if (rot->num_q_heads < 0 || rot->num_q_heads > 4096) return set_error(HUM_ERR_INVALID_ARG, "num_q_heads must be 0 .. 4096");
+  if (rot->inverse != 0) return set_error(HUM_ERR_INVALID_ARG, "inverse must be 0");
+  if (norm) {
+    if (norm->weight_dtype != HUM_BF16 && norm->weight_dtype != HUM_F32)
+      return set_error(HUM_ERR_UNSUPPORTED, "weight_dtype must be bf16 or f32");
+    if (!(norm->eps > 0.0f) || !std::isfinite(norm->eps)) return set_error(HUM_ERR_INVALID_ARG, "eps must be a number above 0");
+    if (!std::isfinite(norm->weight_offset)) return set_error(HUM_ERR_INVALID_ARG, "weight_offset must be finite");
+  }
+  if (num_tokens < 0) return set_error(HUM_ERR_INVALID_ARG, "num_tokens must be >= 0");
+  // (a grid holds at most 2^32 - 1 threads)
+  if (num_tokens >= (int64_t)1 << 24) return set_error(HUM_ERR_UNSUPPORTED, "at most 2^24 - 1 tokens in a call");
+  if (num_tokens == 0) return HUM_OK;
+  const int hq = rot->num_q_heads, hk = kv->num_kv_heads, d = kv->head_dim;
+  if (!cache || !positions || !inv_freq || !slots || !k || !v || (hq && (!q || !q_out)))
+    return set_error(HUM_ERR_INVALID_ARG, "NULL pointer");
+  auto addr = [](const void* x) { return reinterpret_cast<uintptr_t>(x); };
+  if (addr(cache) % 16) return set_error(HUM_ERR_INVALID_ARG, "the cache must be 16-byte aligned");
+  if ((addr(positions) | addr(inv_freq) | addr(slots)) % 8)
+    return set_error(HUM_ERR_INVALID_ARG, "positions, inv_freq and slots must be aligned to their elements");
+  if (cache_bytes < (size_t)l.bytes)
+    return set_error(HUM_ERR_WORKSPACE, "cache of %zu bytes, the description takes %lld", cache_bytes, (long long)l.bytes);
+  if ((addr(k) | addr(v) | (hq ? addr(q) | addr(q_out) : 0)) % 2)
+    return set_error(HUM_ERR_INVALID_ARG, "q, q_out, k and v must be aligned to their elements");
+  const int wsize = norm && norm->weight_dtype == HUM_F32 ? 4 : 2;
+  if (norm && (addr(norm->q_weight) | addr(norm->k_weight)) % wsize)
+    return set_error(HUM_ERR_INVALID_ARG, "the norms' weights must be aligned to their elements");
+  const bool in_place = q == q_out && ((q_ts == qo_ts) || num_tokens == 1) && (q_hs == qo_hs || hq == 1);
+  // q_out and the cache are stored while other workgroups still read: neither
+  // may lie in an input, but q_out in q's place, row by row.
+  auto rows = [&](const void* at, int heads, int64_t ts, int64_t hs) {
+    return Rows{(int64_t)(intptr_t)at, num_tokens, heads, (wide_t)ts * 2, (wide_t)hs * 2, (int64_t)d * 2};
+  };
+  struct In {
+    const char* name;
+    Rows at;
+  };
+  const In in[] = {{"q", rows(q, hq, q_ts, q_hs)},
+                   {"k", rows(k, hk, k_ts, k_hs)},
+                   {"v", rows(v, hk, v_ts, v_hs)},
+                   {"positions", bytes_at(positions, num_tokens * 8)},
+                   {"slots", bytes_at(slots, num_tokens * 8)},
+                   {"inv_freq", bytes_at(inv_freq, rot->rotary_dim / 2 * 8)},
+                   {"q_weight", bytes_at(norm ? norm->q_weight : nullptr, norm && norm->q_weight ? d * wsize : 0)},
+                   {"k_weight", bytes_at(norm ? norm->k_weight : nullptr, norm && norm->k_weight ? d * wsize : 0)}};
+  const Rows of_q = rows(q_out, hq, qo_ts, qo_hs), of_cache = bytes_at(cache, l.bytes);
+  if (overlaps_itself(of_q)) return set_error(HUM_ERR_INVALID_ARG, "the rows of q_out must not overlap");
+  if (overlap(of_q, of_cache) != Overlap::kNo) return set_error(HUM_ERR_INVALID_ARG, "q_out and the cache must not overlap");
+  for (const In& i : in) {
+    if (!(i.at.at == of_q.at && in_place && &i == in) && overlap(of_q, i.at) != Overlap::kNo)
+      return set_error(HUM_ERR_INVALID_ARG, "q_out and %s must not overlap", i.name);
+    if (overlap(of_cache, i.at) != Overlap::kNo)
+      return set_error(HUM_ERR_INVALID_ARG, "the cache and %s must not overlap", i.name);
+  }
+  AppendParams p{};
+  p.cache = static_cast<uint8_t*>(cache);
+  p.unit = (uint32_t)l.unit;
+  p.page_stride = (uint32_t)(l.unit * hk);
+  p.slots_all = kv->num_pages * kv->page_size;
+  p.page_shift = __builtin_ctz((unsigned)kv->page_size);
+  p.heads[0] = hq;
+  p.heads[1] = hk;
+  p.slots = slots;
+  p.positions = positions;
+  p.inv_freq = inv_freq;
+  const void* xs[3] = {q, k, v};
+  const int64_t strides[3][2] = {{q_ts, q_hs}, {k_ts, k_hs}, {v_ts, v_hs}};
+  int64_t any = hq ? (int64_t)(addr(q) | addr(q_out)) / 2 | q_ts | q_hs | qo_ts | qo_hs : 0;
+  any |= (int64_t)(addr(k) | addr(v)) / 2 | k_ts | k_hs | v_ts | v_hs;
+  for (int i = 0; i < 3; ++i) {
+    p.x[i] = static_cast<const uint16_t*>(xs[i]);
+    p.ts[i] = strides[i][0];
+    p.hs[i] = strides[i][1];
+  }
+  p.q_out = static_cast<uint16_t*>(q_out);
+  p.qo_ts = qo_ts;
+  p.qo_hs = qo_hs;
+  p.tokens = num_tokens;
+  p.half = rot->rotary_dim / 2;
+  p.factor = rot->factor;
+  if (norm) {
+    p.w[0] = norm->q_weight;
+    p.w[1] = norm->k_weight;
+    p.w_f32 = wsize == 4;
+    p.eps = norm->eps;
+    p.offset = norm->weight_offset;
+  }
+  const bool half = rot->layout == HUM_ROPE_HALF;
+  const bool fast = any % 8 == 0 && p.half % (half ? 8 : 4) == 0;
+  // Tokens per workgroup: as many as give 256 threads a coefficient each, as
+  // long as that leaves a thousand workgroups; rows are sliced over grid.y
+  // where the tokens alone would leave compute units without one.
+  int64_t tok = 256 / p.half;
+  tok = tok < 1 ? 1 : tok > 8 ? 8 : tok;
+  while (tok > 1 && (num_tokens + tok - 1) / tok < 1024) tok /= 2;
+  const int all = hq + 2 * hk, at_once = 256 / (d / 8);
+  p.tok_per_wg = (int)tok;
+  const int64_t gx = (num_tokens + tok - 1) / tok;
+  int64_t gy = 1;
+  if (gx < 512) {
+    gy = (512 + gx - 1) / gx;
+    const int64_t most = (all + at_once - 1) / at_once;
+    if (gy > most) gy = most;
+  }
+  p.row_step = (int)((all + gy - 1) / gy);
+  gy = (all + p.row_step - 1) / p.row_step;
+  const size_t lds = (size_t)tok * p.half * 2 * sizeof(float);
+  const dim3 grid((unsigned)gx, (unsigned)gy);
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  const bool normed = p.w[0] || p.w[1];
+  kv_dispatch(kv, [&](auto fmt, auto dim) {
+    constexpr int F = decltype(fmt)::value, D = decltype(dim)::value;
+    auto by = [&](auto h, auto f) {
+      constexpr bool H = decltype(h)::value, FA = decltype(f)::value;
+      if (normed) append_kernel<F, D, H, FA, true><<<grid, 256, lds, s>>>(p);
+      else append_kernel<F, D, H, FA, false><<<grid, 256, lds, s>>>(p);
+    };
+    if (half && fast) by(std::true_type{}, std::true_type{});
+    else if (half) by(std::true_type{}, std::false_type{});
+    else if (fast) by(std::false_type{}, std::true_type{});
+    else by(std::false_type{}, std::false_type{});
+  });
+  hipError_t err = hipGetLastError();
+  if (err != hipSuccess) return set_error(HUM_ERR_HIP, "rotary_kv_write launch: %s", hipGetErrorString(err));
+  return HUM_OK;
+}

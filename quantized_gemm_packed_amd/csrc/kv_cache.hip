@@ -61,72 +61,6 @@ struct KvPlace {
   }
 };
 
-// Max over the N lanes (8, 16 or 32) that hold one row.
-template <int N>
-__device__ __forceinline__ float row_max(float v) {
-  v = quad_max(v);
-  auto with = [&](auto ctrl) {
-    v = __builtin_fmaxf(v, __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), decltype(ctrl)::value, 0xF, 0xF, false)));
-  };
-  with(std::integral_constant<int, 0x141>{});                         // row_half_mirror: the other quad of eight
-  if constexpr (N >= 16) with(std::integral_constant<int, 0x140>{});  // row_mirror: the other eight of sixteen
-  if constexpr (N >= 32) v = __builtin_fmaxf(v, __shfl_xor(v, 16));
-  return v;
-}
-
-// x / d as an IEEE f32 division rounds it, from y = RN(1 / d): with
-// q = RN(x y) and the exact remainder r = q d - x, RN(q - r y) (Markstein,
-// "Computation of elementary functions on the IBM RISC System/6000
-// processor", 1990), three instructions where the division takes eleven.
-// That holds while nothing over- or underflows (fp8_row says where).  A zero
-// keeps its sign: r is then +0, and q - 0 is q.
-__device__ __forceinline__ float divide_by(float x, float d, float y) {
-  const float q = x * y;
-  return __builtin_fmaf(-__builtin_fmaf(q, d, -x), y, q);
-}
-
-// A row's scale by the FP8 rule, amax / 448 (1 for a row of zeros), and the
-// lane's eight values over it, as IEEE f32 divisions give them (a code can
-// hang on the quotient's last bit).  Maxima outside [2^-70, 2^120] divide;
-// inside, values below 2^-10 of the scale, whose remainder may underflow,
-// become zero codes either way.  A bf16 maximum has 128 mantissas, so have
-// the scales: the quotients of all of them were compared with the division's.
-__device__ __forceinline__ float fp8_row(float (&f)[8], float amax) {
-  float s = 1.0f;
-  if (amax >= 0x1p-70f && amax <= 0x1p120f) {
-    s = divide_by(amax, 448.0f, 1.0f / 448.0f);
-    const float y0 = __builtin_amdgcn_rcpf(s);
-    const float y = __builtin_fmaf(__builtin_fmaf(-s, y0, 1.0f), y0, y0);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = divide_by(f[i], s, y);
-  } else if (amax > 0.0f) {  // (lanes without a row hold zeros)
-    s = amax / 448.0f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = f[i] / s;
-  }
-  return s;
-}
-
-// Byte offsets of token `at` of a page inside its (page, head) unit: its code
-// row, and its scale (or the first of them) with the step to the next.
-template <int FMT, int D>
-struct KvOffsets {
-  int64_t code, scale;
-  int32_t scale_step;
-  __device__ __forceinline__ KvOffsets(int which, int at, int page_size) {
-    using U = KvUnit<FMT, D>;
-    code = (int64_t)(which * page_size + at) * U::kRow;
-    const int64_t scales = (int64_t)2 * page_size * U::kRow + which * page_size * U::kScale;
-    if (U::kMx && which) {
-      scale = scales + at;
-      scale_step = page_size;
-    } else {
-      scale = scales + at * U::kScale;
-      scale_step = 1;
-    }
-  }
-};
-
 template <int FMT, int D, bool VEC>
 __global__ __launch_bounds__(256) void kv_write_kernel(const KvMoveParams p) {
   using U = KvUnit<FMT, D>;
@@ -177,49 +111,7 @@ __global__ __launch_bounds__(256) void kv_write_kernel(const KvMoveParams p) {
           f[2 * i] = bf16_bits_to_f32(v[k][i] & 0xFFFF);
           f[2 * i + 1] = bf16_bits_to_f32(v[k][i] >> 16);
         }
-        float amax = 0.0f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) amax = __builtin_fmaxf(amax, __builtin_fabsf(f[i]));
-        if constexpr (FMT == HUM_ACT_FP8_TOKEN) {
-          amax = row_max<D / 8>(amax);
-          const float sc = fp8_row(f, amax);
-          u32x2_t o;
-          o[0] = f32x2_to_e4m3x2(f[0], f[1]) | (f32x2_to_e4m3x2(f[2], f[3]) << 16);
-          o[1] = f32x2_to_e4m3x2(f[4], f[5]) | (f32x2_to_e4m3x2(f[6], f[7]) << 16);
-          if (live) {
-            *reinterpret_cast<u32x2_t*>(code) = o;
-            if (me.lane == 0) *reinterpret_cast<float*>(scale) = sc;
-          }
-        } else {
-          amax = quad_max(amax);  // four lanes hold one block of 32
-          const int e = mx_scale_code_emax(amax, FMT == HUM_ACT_MXFP8 ? 8 : 2);
-          // The hardware conversions, two floats over a power of two to two
-          // codes, nearest even.  E2M1 saturates by itself; E4M3 becomes NaN
-          // past 448, so what the rule saturates is clamped first.
-          const float sc = e8m0_to_f32((uint32_t)e);
-          if (live) {
-            if constexpr (FMT == HUM_ACT_MXFP8) {
-              const float top = 448.0f * sc;
-              typedef short s16x2_v __attribute__((ext_vector_type(2)));
-              s16x2_v o[2] = {{0, 0}, {0, 0}};
-#pragma unroll
-              for (int i = 0; i < 8; ++i) f[i] = __builtin_fminf(__builtin_fmaxf(f[i], -top), top);
-              o[0] = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(o[0], f[0], f[1], sc, false);
-              o[0] = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(o[0], f[2], f[3], sc, true);
-              o[1] = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(o[1], f[4], f[5], sc, false);
-              o[1] = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(o[1], f[6], f[7], sc, true);
-              *reinterpret_cast<u32x2_t*>(code) = u32x2_t{__builtin_bit_cast(uint32_t, o[0]), __builtin_bit_cast(uint32_t, o[1])};
-            } else {
-              uint32_t o = 0;
-              o = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(o, f[0], f[1], sc, 0);
-              o = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(o, f[2], f[3], sc, 1);
-              o = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(o, f[4], f[5], sc, 2);
-              o = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(o, f[6], f[7], sc, 3);
-              *reinterpret_cast<uint32_t*>(code) = o;
-            }
-            if ((me.lane & 3) == 0) scale[(me.lane >> 2) * off0.scale_step] = (uint8_t)e;
-          }
-        }
+        kv_store_row<FMT, D, false>(f, me.lane, code, scale, off0.scale_step, live);
       }
     }
   }

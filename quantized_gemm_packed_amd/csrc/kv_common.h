@@ -65,4 +65,111 @@ __device__ __forceinline__ u32x4_t e2m1x8_to_bf16(uint32_t w, float scale) {
   return o;
 }
 
+// Max over the N lanes (8, 16 or 32) that hold one row.
+template <int N>
+__device__ __forceinline__ float row_max(float v) {
+  v = quad_max(v);
+  auto with = [&](auto ctrl) {
+    v = __builtin_fmaxf(v, __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), decltype(ctrl)::value, 0xF, 0xF, false)));
+  };
+  with(std::integral_constant<int, 0x141>{});                         // row_half_mirror: the other quad of eight
+  if constexpr (N >= 16) with(std::integral_constant<int, 0x140>{});  // row_mirror: the other eight of sixteen
+  if constexpr (N >= 32) v = __builtin_fmaxf(v, __shfl_xor(v, 16));
+  return v;
+}
+
+// x / d as an IEEE f32 division rounds it, from y = RN(1 / d): with
+// q = RN(x y) and the exact remainder r = q d - x, RN(q - r y) (Markstein,
+// "Computation of elementary functions on the IBM RISC System/6000
+// processor", 1990), three instructions where the division takes eleven.
+// That holds while nothing over- or underflows (fp8_row says where).  A zero
+// keeps its sign: r is then +0, and q - 0 is q.
+__device__ __forceinline__ float divide_by(float x, float d, float y) {
+  const float q = x * y;
+  return __builtin_fmaf(-__builtin_fmaf(q, d, -x), y, q);
+}
+
+// A row's scale by the FP8 rule, amax / 448 (1 for a row of zeros), and the
+// lane's eight values over it, as IEEE f32 divisions give them (a code can
+// hang on the quotient's last bit).  Maxima outside [2^-70, 2^120] divide;
+// inside, values below 2^-10 of the scale, whose remainder may underflow,
+// become zero codes either way.  A bf16 maximum has 128 mantissas, so have
+// the scales: the quotients of all of them were compared with the division's.
+// ANY: of other values only the division itself is known to be right.
+template <bool ANY>
+__device__ __forceinline__ float fp8_row(float (&f)[8], float amax) {
+  float s = 1.0f;
+  if (!ANY && amax >= 0x1p-70f && amax <= 0x1p120f) {
+    s = divide_by(amax, 448.0f, 1.0f / 448.0f);
+    const float y0 = __builtin_amdgcn_rcpf(s);
+    const float y = __builtin_fmaf(__builtin_fmaf(-s, y0, 1.0f), y0, y0);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = divide_by(f[i], s, y);
+  } else if (amax > 0.0f) {  // (lanes without a row hold zeros)
+    s = amax / 448.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = f[i] / s;
+  }
+  return s;
+}
+
+// Byte offsets of token `at` of a page inside its (page, head) unit: its code
+// row, and its scale (or the first of them) with the step to the next.
+template <int FMT, int D>
+struct KvOffsets {
+  int64_t code, scale;
+  int32_t scale_step;
+  __device__ __forceinline__ KvOffsets(int which, int at, int page_size) {
+    using U = KvUnit<FMT, D>;
+    code = (int64_t)(which * page_size + at) * U::kRow;
+    const int64_t scales = (int64_t)2 * page_size * U::kRow + which * page_size * U::kScale;
+    if (U::kMx && which) {
+      scale = scales + at;
+      scale_step = page_size;
+    } else {
+      scale = scales + at * U::kScale;
+      scale_step = 1;
+    }
+  }
+};
+
+// Quantizes one row, of which the lane has the eight values f, and stores the
+// lane's codes at `code` and the row's scale (of the lane's block of 32:
+// block b's at b * scale_step) at `scale`, where `live`.  Every lane of the
+// row calls it together.  ANY: the values are any f32 (fp8_row says what that
+// changes), not bf16.
+template <int FMT, int D, bool ANY>
+__device__ __forceinline__ void kv_store_row(float (&f)[8], int lane, uint8_t* code, uint8_t* scale, int32_t scale_step, bool live) {
+  if constexpr (FMT == HUM_ACT_BF16) {
+    u32x4_t o;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[i] = f32x2_to_bf16x2_bits(f[2 * i], f[2 * i + 1]);
+    if (live) *reinterpret_cast<u32x4_t*>(code) = o;
+  } else {
+    float amax = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) amax = __builtin_fmaxf(amax, __builtin_fabsf(f[i]));
+    if constexpr (FMT == HUM_ACT_FP8_TOKEN) {
+      amax = row_max<D / 8>(amax);
+      const float sc = fp8_row<ANY>(f, amax);
+      u32x2_t o;
+      o[0] = f32x2_to_e4m3x2(f[0], f[1]) | (f32x2_to_e4m3x2(f[2], f[3]) << 16);
+      o[1] = f32x2_to_e4m3x2(f[4], f[5]) | (f32x2_to_e4m3x2(f[6], f[7]) << 16);
+      if (live) {
+        *reinterpret_cast<u32x2_t*>(code) = o;
+        if (lane == 0) *reinterpret_cast<float*>(scale) = sc;
+      }
+    } else {
+      amax = quad_max(amax);  // four lanes hold one block of 32
+      const int e = mx_scale_code_emax(amax, FMT == HUM_ACT_MXFP8 ? 8 : 2);
+      const float sc = e8m0_to_f32((uint32_t)e);
+      if (live) {
+        if constexpr (FMT == HUM_ACT_MXFP8) *reinterpret_cast<u32x2_t*>(code) = mx_e4m3x8(f, sc);
+        else *reinterpret_cast<uint32_t*>(code) = mx_e2m1x8(f, sc);
+        if ((lane & 3) == 0) scale[(lane >> 2) * scale_step] = (uint8_t)e;
+      }
+    }
+  }
+}
+
 }  // namespace hum

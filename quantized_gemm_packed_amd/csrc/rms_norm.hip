@@ -1,0 +1,410 @@
+// Root-mean-square norm of rows, with the residual's addition before it and
+// the activation quantizer behind it, in one pass:
+//   h = x + residual, residual' = round(h),
+//   y = h * r * (w + offset),  r = 1 / sqrt(mean(h^2) + eps),
+// y in f32, rounded once: to bf16, or to the codes of hum_quant_act's rules.
+//
+// Memory bound: x and the residual are read once, everything that is written
+// is written once.  A row stays in the registers of its workgroup between the
+// two passes over it (the sum of squares, then y), 8 elements of a thread side
+// by side.  Which elements a thread has, and so the order of the sums, goes by
+// k alone: a row's bits are the same in every batch and at every alignment.
+#include <cmath>
+
+#include "dev_common.h"
+#include "hum_internal.h"
+#include "rows.h"
+
+namespace hum {
+
+struct NormParams {
+  const uint16_t* x;
+  const void* res;
+  void* res_out;
+  const void* w;
+  uint16_t* out;
+  uint8_t* q;
+  void* scales;
+  int64_t m, ld_x, ld_res, ld_res_out, ld_out;
+  int32_t k;
+  int32_t vec;     // elements per access where not all are 16 bytes: 4, 2 or 1
+  int32_t w_f32;
+  float inv_k, eps, offset;
+};
+
+// What a row's residual is.
+enum { kNoRes = 0, kResBf16 = 1, kResF32 = 2 };
+
+template <typename T>
+__device__ __forceinline__ float norm_ld(T v) {
+  if constexpr (sizeof(T) == 2) return bf16_bits_to_f32(v);
+  else return v;
+}
+
+// Eight elements at `at` of a row -> f32 (zeros past k).
+template <typename T, bool FAST>
+__device__ __forceinline__ void load8(const T* row, int at, int k, int vec, float (&f)[8]) {
+  if constexpr (FAST) {
+    if (at < k) {
+      if constexpr (sizeof(T) == 2) {
+        const u32x4_t v = *reinterpret_cast<const u32x4_t*>(row + at);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          f[2 * i] = bf16_bits_to_f32(v[i] & 0xFFFF);
+          f[2 * i + 1] = bf16_bits_to_f32(v[i] >> 16);
+        }
+      } else {
+        const f32x4_t a = *reinterpret_cast<const f32x4_t*>(row + at), b = *reinterpret_cast<const f32x4_t*>(row + at + 4);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          f[i] = a[i];
+          f[4 + i] = b[i];
+        }
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) f[i] = 0.0f;
+    }
+  } else {
+    auto pieces = [&](auto n) {
+      constexpr int N = decltype(n)::value;
+      typedef T P __attribute__((ext_vector_type(N)));
+#pragma unroll
+      for (int i = 0; i < 8; i += N) {
+        if (at + i < k) {
+          if constexpr (N == 1) {
+            f[i] = norm_ld<T>(row[at + i]);
+          } else {
+            const P v = *reinterpret_cast<const P*>(row + at + i);
+#pragma unroll
+            for (int e = 0; e < N; ++e) f[i + e] = norm_ld<T>((T)v[e]);
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < N; ++e) f[i + e] = 0.0f;
+        }
+      }
+    };
+    if (vec == 4) pieces(std::integral_constant<int, 4>{});
+    else if (vec == 2) pieces(std::integral_constant<int, 2>{});
+    else pieces(std::integral_constant<int, 1>{});
+  }
+}
+
+template <typename T, bool FAST>
+__device__ __forceinline__ void store8(T* row, int at, int k, int vec, const float (&f)[8]) {
+  if constexpr (FAST) {
+    if (at >= k) return;
+    if constexpr (sizeof(T) == 2) {
+      u32x4_t v;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = f32x2_to_bf16x2_bits(f[2 * i], f[2 * i + 1]);
+      *reinterpret_cast<u32x4_t*>(row + at) = v;
+    } else {
+      *reinterpret_cast<f32x4_t*>(row + at) = f32x4_t{f[0], f[1], f[2], f[3]};
+      *reinterpret_cast<f32x4_t*>(row + at + 4) = f32x4_t{f[4], f[5], f[6], f[7]};
+    }
+  } else {
+    auto pieces = [&](auto n) {
+      constexpr int N = decltype(n)::value;
+      typedef T P __attribute__((ext_vector_type(N)));
+#pragma unroll
+      for (int i = 0; i < 8; i += N) {
+        if (at + i >= k) continue;
+        T e[N];
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+          if constexpr (sizeof(T) == 2) e[j] = (T)f32_to_bf16_bits(f[i + j]);
+          else e[j] = f[i + j];
+        }
+        if constexpr (N == 1) {
+          row[at + i] = e[0];
+        } else {
+          P v;
+#pragma unroll
+          for (int j = 0; j < N; ++j) v[j] = e[j];
+          *reinterpret_cast<P*>(row + at + i) = v;
+        }
+      }
+    };
+    if (vec == 4) pieces(std::integral_constant<int, 4>{});
+    else if (vec == 2) pieces(std::integral_constant<int, 2>{});
+    else pieces(std::integral_constant<int, 1>{});
+  }
+}
+
+// Sum / max over the row: the wave's lanes, then the WAVES waves in order.
+template <int WAVES, bool MAX>
+__device__ __forceinline__ float over_row(float v, float* red) {
+  auto join = [](float a, float b) { return MAX ? __builtin_fmaxf(a, b) : a + b; };
+  v = MAX ? row16_max(v) : row16_sum(v);
+  v = join(v, __shfl_xor(v, 16));
+  v = join(v, __shfl_xor(v, 32));
+  if constexpr (WAVES > 1) {
+    if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
+    __syncthreads();
+    v = red[0];
+#pragma unroll
+    for (int i = 1; i < WAVES; ++i) v = join(v, red[i]);
+  }
+  return v;
+}
+
+// The scale of a maximum by the FP8 rule, and codes of eight values over it.
+__device__ __forceinline__ float fp8_scale(float amax) { return amax > 0.0f ? amax / 448.0f : 1.0f; }
+__device__ __forceinline__ u32x2_t fp8_codes(const float (&f)[8], float s) {
+  u32x2_t o;
+  o[0] = f32x2_to_e4m3x2(f[0] / s, f[1] / s) | (f32x2_to_e4m3x2(f[2] / s, f[3] / s) << 16);
+  o[1] = f32x2_to_e4m3x2(f[4] / s, f[5] / s) | (f32x2_to_e4m3x2(f[6] / s, f[7] / s) << 16);
+  return o;
+}
+__device__ __forceinline__ float max8(const float (&f)[8]) {
+  float a = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) a = __builtin_fmaxf(a, __builtin_fabsf(f[i]));
+  return a;
+}
+
+// WAVES waves have a row (one: a workgroup has four rows), NV pieces of 8
+// elements each thread.
+template <int FMT, int RES, bool FAST, int WAVES, int NV>
+__global__ __launch_bounds__(WAVES == 1 ? 256 : WAVES * 64) void norm_kernel(const NormParams p) {
+  constexpr int kLanes = WAVES * 64;
+  __shared__ float red[2][2][WAVES];
+  const int lane = WAVES == 1 ? threadIdx.x & 63 : threadIdx.x;
+  const int rows = WAVES == 1 ? 4 : 1;
+  const int k = p.k;
+  int turn = 0;  // (the rows' exchanges alternate between two places: one barrier each)
+  for (int64_t row = (int64_t)blockIdx.x * rows + (WAVES == 1 ? threadIdx.x >> 6 : 0); row < p.m;
+       row += (int64_t)gridDim.x * rows, turn ^= 1) {
+    float h[NV][8];
+#pragma unroll
+    for (int j = 0; j < NV; ++j) load8<uint16_t, FAST>(p.x + row * p.ld_x, (j * kLanes + lane) * 8, k, p.vec, h[j]);
+    if constexpr (RES != kNoRes) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        const int at = (j * kLanes + lane) * 8;
+        float b[8];
+        if constexpr (RES == kResBf16) load8<uint16_t, FAST>(static_cast<const uint16_t*>(p.res) + row * p.ld_res, at, k, p.vec, b);
+        else load8<float, FAST>(static_cast<const float*>(p.res) + row * p.ld_res, at, k, p.vec, b);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) h[j][i] += b[i];
+      }
+    }
+    float sum = 0.0f;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      if constexpr (RES == kResBf16) store8<uint16_t, FAST>(static_cast<uint16_t*>(p.res_out) + row * p.ld_res_out, (j * kLanes + lane) * 8, k, p.vec, h[j]);
+      if constexpr (RES == kResF32) store8<float, FAST>(static_cast<float*>(p.res_out) + row * p.ld_res_out, (j * kLanes + lane) * 8, k, p.vec, h[j]);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sum = __builtin_fmaf(h[j][i], h[j][i], sum);
+    }
+    sum = over_row<WAVES, false>(sum, red[0][turn]);
+    const float r = 1.0f / __builtin_sqrtf(sum * p.inv_k + p.eps);
+    const bool fine = sum < __builtin_inff();  // (false for a NaN too)
+    float amax = 0.0f;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int at = (j * kLanes + lane) * 8;
+      float w[8];
+      if (p.w_f32) load8<float, FAST>(static_cast<const float*>(p.w), at, k, p.vec, w);
+      else load8<uint16_t, FAST>(static_cast<const uint16_t*>(p.w), at, k, p.vec, w);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) h[j][i] = h[j][i] * r * (w[i] + p.offset);
+      if (p.out) store8<uint16_t, FAST>(p.out + row * p.ld_out, at, k, p.vec, h[j]);
+      if constexpr (FMT == HUM_ACT_FP8_TOKEN) amax = __builtin_fmaxf(amax, max8(h[j]));
+    }
+    if constexpr (FMT == HUM_ACT_FP8_TOKEN) {
+      amax = over_row<WAVES, true>(amax, red[1][turn]);
+      const float s = fp8_scale(amax);
+      if (lane == 0) static_cast<float*>(p.scales)[row] = fine ? s : __builtin_nanf("");
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        const int at = (j * kLanes + lane) * 8;
+        if (at < k) *reinterpret_cast<u32x2_t*>(p.q + row * k + at) = fp8_codes(h[j], s);
+      }
+    }
+    if constexpr (FMT == HUM_ACT_FP8_GROUP) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        const int at = (j * kLanes + lane) * 8;
+        const float s = fp8_scale(row16_max(max8(h[j])));  // 16 lanes have a group of 128
+        if (at < k) {
+          *reinterpret_cast<u32x2_t*>(p.q + row * k + at) = fp8_codes(h[j], s);
+          if ((lane & 15) == 0) static_cast<float*>(p.scales)[row * (k / 128) + at / 128] = fine ? s : __builtin_nanf("");
+        }
+      }
+    }
+    if constexpr (FMT == HUM_ACT_MXFP8 || FMT == HUM_ACT_MXFP4) {
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        const int at = (j * kLanes + lane) * 8;
+        const int e = mx_scale_code_emax(quad_max(max8(h[j])), FMT == HUM_ACT_MXFP8 ? 8 : 2);  // 4 lanes have a block of 32
+        if (at >= k) continue;
+        const float sc = e8m0_to_f32((uint32_t)e);
+        if constexpr (FMT == HUM_ACT_MXFP8) *reinterpret_cast<u32x2_t*>(p.q + row * k + at) = mx_e4m3x8(h[j], sc);
+        else *reinterpret_cast<uint32_t*>(p.q + (row * k + at) / 2) = mx_e2m1x8(h[j], sc);
+        if ((lane & 3) == 0) static_cast<uint8_t*>(p.scales)[row * (k / 32) + at / 32] = fine ? (uint8_t)e : 255;
+      }
+    }
+  }
+}
+
+// Waves per row and pieces per thread, by the row's length alone.
+template <int FMT, int RES, bool FAST>
+static void launch_norm(const NormParams& p, hipStream_t s) {
+  auto go = [&](auto waves, auto nv) {
+    constexpr int W = decltype(waves)::value;
+    const int64_t wgs = W == 1 ? (p.m + 3) / 4 : p.m;
+    const int64_t most = (int64_t)1 << 20;
+    norm_kernel<FMT, RES, FAST, W, decltype(nv)::value><<<(unsigned)(wgs < most ? wgs : most), W == 1 ? 256 : W * 64, 0, s>>>(p);
+  };
+  using I1 = std::integral_constant<int, 1>;
+  using I2 = std::integral_constant<int, 2>;
+  using I4 = std::integral_constant<int, 4>;
+  using I8 = std::integral_constant<int, 8>;
+  using I16 = std::integral_constant<int, 16>;
+  if (p.k <= 512) go(I1{}, I1{});
+  else if (p.k <= 2048) go(I4{}, I1{});
+  else if (p.k <= 4096) go(I4{}, I2{});
+  else if (p.k <= 8192) go(I4{}, I4{});
+  else if (p.k <= 16384) go(I16{}, I2{});
+  else if (p.k <= 32768) go(I16{}, I4{});
+  else go(I16{}, I8{});
+}
+
+constexpr int64_t kNormMaxK = 65536;
+
+}  // namespace hum
+
+using namespace hum;
+
+extern "C" hum_status hum_rms_norm(const hum_norm_desc* d, int64_t m, int64_t k, const void* x, int64_t ld_x,
+                                   const void* residual, int64_t ld_res, void* residual_out, int64_t ld_res_out,
+                                   const void* weight, void* out, int64_t ld_out, void* q, void* scales, void* stream) {
+  clear_error();
+  if (!d) return set_error(HUM_ERR_INVALID_ARG, "desc is NULL");
+  const int32_t fmt = d->act_fmt;
+  if (fmt < HUM_ACT_BF16 || fmt > HUM_ACT_FP8_GROUP) return set_error(HUM_ERR_INVALID_ARG, "bad act_fmt");
+  if (d->residual_dtype != HUM_BF16 && d->residual_dtype != HUM_F32)
+    return set_error(HUM_ERR_UNSUPPORTED, "residual_dtype must be bf16 or f32");
+  if (d->weight_dtype != HUM_BF16 && d->weight_dtype != HUM_F32)
+    return set_error(HUM_ERR_UNSUPPORTED, "weight_dtype must be bf16 or f32");
+  if (!(d->eps > 0.0f) || !std::isfinite(d->eps)) return set_error(HUM_ERR_INVALID_ARG, "eps must be a number above 0");
+  if (!std::isfinite(d->weight_offset)) return set_error(HUM_ERR_INVALID_ARG, "weight_offset must be finite");
+  if (m < 0 || k < 1) return set_error(HUM_ERR_INVALID_ARG, "m must be >= 0 and k >= 1");
+  if (k > kNormMaxK) return set_error(HUM_ERR_UNSUPPORTED, "k must be at most %lld", (long long)kNormMaxK);
+  const int unit = fmt == HUM_ACT_FP8_TOKEN ? 8 : fmt == HUM_ACT_FP8_GROUP ? 128 : fmt == HUM_ACT_BF16 ? 1 : 32;
+  if (k % unit) return set_error(HUM_ERR_UNSUPPORTED, "k must be a multiple of %d for this format", unit);
+  if (m >= (int64_t)1 << 40) return set_error(HUM_ERR_UNSUPPORTED, "at most 2^40 - 1 rows in a call");
+  if (m == 0) return HUM_OK;
+  const bool quant = fmt != HUM_ACT_BF16;
+  if (quant != (q != nullptr) || quant != (scales != nullptr))
+    return set_error(HUM_ERR_INVALID_ARG, quant ? "q and scales must be given for this format" : "q and scales must be NULL for bf16");
+  if (!quant && !out) return set_error(HUM_ERR_INVALID_ARG, "out must be given for bf16");
+  if ((residual != nullptr) != (residual_out != nullptr))
+    return set_error(HUM_ERR_INVALID_ARG, "residual and residual_out go together");
+  if (!x || !weight) return set_error(HUM_ERR_INVALID_ARG, "NULL pointer");
+  const int rsize = d->residual_dtype == HUM_BF16 ? 2 : 4, wsize = d->weight_dtype == HUM_BF16 ? 2 : 4;
+  auto addr = [](const void* p) { return reinterpret_cast<uintptr_t>(p); };
+  const int ssize = fmt == HUM_ACT_MXFP8 || fmt == HUM_ACT_MXFP4 ? 1 : 4;
+  if (addr(x) % 2 || addr(out) % 2 || addr(weight) % wsize || (addr(residual) | addr(residual_out)) % rsize || addr(scales) % ssize)
+    return set_error(HUM_ERR_INVALID_ARG, "tensors must be aligned to their elements");
+  if (addr(q) % 8) return set_error(HUM_ERR_INVALID_ARG, "q must be 8-byte aligned");
+  // What workgroups store while others read: no output may lie in an input or
+  // another output, but for whole rows in place (a thread stores what it has
+  // read itself).
+  auto extent = [&](const void* at, int64_t ld, int64_t row_bytes, int size) {
+    return Rows{(int64_t)(intptr_t)at, m, 1, (wide_t)ld * size, 0, row_bytes};
+  };
+  struct Part {
+    const char* name;
+    Rows at;
+    bool output;
+    int64_t ld;
+    int size;
+  };
+  Part parts[7];
+  int n = 0;
+  auto add = [&](const char* name, const void* p, int64_t ld, int size, bool output) {
+    if (p) parts[n++] = Part{name, extent(p, ld, k * size, size), output, ld, size};
+  };
+  add("x", x, ld_x, 2, false);
+  add("residual", residual, ld_res, rsize, false);
+  add("residual_out", residual_out, ld_res_out, rsize, true);
+  add("out", out, ld_out, 2, true);
+  parts[n++] = Part{"weight", bytes_at(weight, k * wsize), false, 0, 0};
+  if (quant) {
+    const int64_t qrow = fmt == HUM_ACT_MXFP4 ? k / 2 : k;
+    const int64_t srow = fmt == HUM_ACT_FP8_TOKEN ? 4 : fmt == HUM_ACT_FP8_GROUP ? k / 128 * 4 : k / 32;
+    parts[n++] = Part{"q", bytes_at(q, m * qrow), true, 0, 0};
+    parts[n++] = Part{"scales", bytes_at(scales, m * srow), true, 0, 0};
+  }
+  for (int i = 0; i < n; ++i) {
+    if (!parts[i].output) continue;
+    if (overlaps_itself(parts[i].at)) return set_error(HUM_ERR_INVALID_ARG, "the rows of %s must not overlap", parts[i].name);
+    for (int j = 0; j < n; ++j) {
+      if (j == i || (parts[j].output && j > i)) continue;
+      const bool in_place = !parts[j].output && parts[i].size && parts[i].size == parts[j].size && parts[i].at.at == parts[j].at.at &&
+                            (parts[i].ld == parts[j].ld || m == 1);
+      if (!in_place && overlap(parts[i].at, parts[j].at) != Overlap::kNo)
+        return set_error(HUM_ERR_INVALID_ARG, "%s and %s must not overlap", parts[i].name, parts[j].name);
+    }
+  }
+  NormParams p{};
+  p.x = static_cast<const uint16_t*>(x);
+  p.res = residual;
+  p.res_out = residual_out;
+  p.w = weight;
+  p.out = static_cast<uint16_t*>(out);
+  p.q = static_cast<uint8_t*>(q);
+  p.scales = scales;
+  p.m = m;
+  p.k = (int32_t)k;
+  p.ld_x = ld_x;
+  p.ld_res = ld_res;
+  p.ld_res_out = ld_res_out;
+  p.ld_out = ld_out;
+  p.w_f32 = wsize == 4;
+  p.inv_k = (float)(1.0 / (double)k);
+  p.eps = d->eps;
+  p.offset = d->weight_offset;
+  // Elements that every access can take at once: what divides the length, the
+  // strides and the addresses (f32: at most the 16 bytes of four).
+  int64_t all = k | (int64_t)(addr(x) / 2) | (int64_t)(addr(out) / 2);
+  if (m > 1) all |= ld_x | (out ? ld_out : 0);
+  int64_t wide = (int64_t)(addr(weight) / wsize);  // of f32 tensors, in pieces of 4
+  if (wsize == 2) {
+    all |= wide;
+    wide = 0;
+  }
+  if (residual) {
+    const int64_t r = (int64_t)(addr(residual) / rsize) | (int64_t)(addr(residual_out) / rsize) | (m > 1 ? ld_res | ld_res_out : 0);
+    (rsize == 2 ? all : wide) |= r;
+  }
+  const bool fast = all % 8 == 0 && wide % 4 == 0;
+  all |= wide;
+  p.vec = all % 4 == 0 ? 4 : all % 2 == 0 ? 2 : 1;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  auto by_res = [&](auto f) {
+    constexpr int F = decltype(f)::value;
+    auto by_fast = [&](auto res) {
+      constexpr int R = decltype(res)::value;
+      if (fast) launch_norm<F, R, true>(p, s);
+      else launch_norm<F, R, false>(p, s);
+    };
+    if (!residual) by_fast(std::integral_constant<int, kNoRes>{});
+    else if (rsize == 2) by_fast(std::integral_constant<int, kResBf16>{});
+    else by_fast(std::integral_constant<int, kResF32>{});
+  };
+  switch (fmt) {
+    case HUM_ACT_BF16: by_res(std::integral_constant<int, HUM_ACT_BF16>{}); break;
+    case HUM_ACT_FP8_TOKEN: by_res(std::integral_constant<int, HUM_ACT_FP8_TOKEN>{}); break;
+    case HUM_ACT_MXFP8: by_res(std::integral_constant<int, HUM_ACT_MXFP8>{}); break;
+    case HUM_ACT_MXFP4: by_res(std::integral_constant<int, HUM_ACT_MXFP4>{}); break;
+    default: by_res(std::integral_constant<int, HUM_ACT_FP8_GROUP>{}); break;
+  }
+  hipError_t err = hipGetLastError();
+  if (err != hipSuccess) return set_error(HUM_ERR_HIP, "rms_norm launch: %s", hipGetErrorString(err));
+  return HUM_OK;
+}

@@ -19,6 +19,7 @@
 
 #include "dev_common.h"
 #include "hum_internal.h"
+#include "rotary_common.h"
 #include "rows.h"
 
 namespace hum {
@@ -126,15 +127,7 @@ __global__ __launch_bounds__(256) void rotary_kernel(const RotaryParams p) {
 
   for (int i = tid; i < nt * p.half; i += 256) {
     const int t = i / p.half;
-    const double turns = (double)p.positions[t0 + t] * (p.inv_freq[i - t * p.half] * 0.15915494309189535);
-    const double rem = turns - __builtin_rint(turns);
-    const float r = (float)rem, lo = (float)(rem - r) * 6.28318531f;
-    float s, c;
-    sincospif(2.0f * r, &s, &c);
-    // (each rounded once, the factor included)
-    const float fs = p.factor * p.sign;
-    cs[i] = __builtin_fmaf(c, p.factor, -s * lo * p.factor);
-    sn[i] = __builtin_fmaf(s, fs, c * lo * fs);
+    rotary_coefficients(p.positions[t0 + t], p.inv_freq[i - t * p.half], p.factor, p.sign, cs + i, sn + i);
   }
   __syncthreads();
 
@@ -155,9 +148,8 @@ __global__ __launch_bounds__(256) void rotary_kernel(const RotaryParams p) {
           const int i0 = HALF ? i : 2 * i, i1 = HALF ? VEC + i : 2 * i + 1;
           const float x0 = ld1<T>(e[i0]), x1 = ld1<T>(e[i1]);
           const int at = HALF || kPair || i < VEC / 2 ? c0 + i : c1 + i - VEC / 2;
-          // (the fused product named: every instance gives the same bits)
-          e[i0] = st1<T>(__builtin_fmaf(x0, cs[at], -(x1 * sn[at])));
-          e[i1] = st1<T>(__builtin_fmaf(x0, sn[at], x1 * cs[at]));
+          e[i0] = st1<T>(rotary_first(x0, x1, cs[at], sn[at]));
+          e[i1] = st1<T>(rotary_second(x0, x1, cs[at], sn[at]));
         }
 #pragma unroll
         for (int i = 0; i < VEC; ++i) {
