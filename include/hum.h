@@ -444,7 +444,8 @@ size_t hum_moe_masked_workspace_bytes(const hum_weight_desc* w13, const hum_weig
  *   logits : [T][E], ld_logits elements from row to row
  *   bias   : f32 [E] or NULL
  *   topk_ids, topk_weights: contiguous [T][topk]
- * E is at most 512, topk at most 64, num_groups at most 64. */
+ * E is at most 512, topk at most 64, num_groups at most 64; at most 2^24 - 1
+ * tokens in a call. */
 typedef enum hum_route_score { HUM_SCORE_SOFTMAX = 0, HUM_SCORE_SIGMOID = 1 } hum_route_score;
 typedef enum hum_group_score { HUM_GROUP_MAX = 0, HUM_GROUP_TOP2 = 1 } hum_group_score;
 

@@ -25,7 +25,11 @@ struct RouteParams {
   int64_t tokens, ld;
   int32_t experts, topk, groups, topk_groups, per_group;
   int32_t sigmoid, bf16, top2, renormalize;
-  float scale;
+  int32_t vec;         // four logits at once
+  int32_t candidates;  // topk, and two more where a cut key is not exact
+  int32_t exact_cut;   // a cut key holds the whole of its key
+  uint32_t low_mask;   // of a cut key: the expert's number
+  float inv_quads, scale;
 };
 
 __device__ __forceinline__ double wave_max(double v) {
@@ -53,119 +57,392 @@ __device__ __forceinline__ void wave_best(double& key, int& idx) {
   }
 }
 
-// One wave per token; lane l has the experts l, l + 64, ...
-__global__ __launch_bounds__(256) void route_kernel(const RouteParams p) {
-  constexpr int N = kRouteMaxExperts / 64;
-  __shared__ double keys[4][kRouteMaxExperts];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+// One token by one wave, all in f64; lane l has the experts l, l + 64, ...
+// keys: LDS of this wave alone.  Loops stay rolled: it runs seldom, and what it
+// holds in registers the kernel around it does not have.
+__device__ __forceinline__ void route_exactly(const RouteParams& p, int64_t t, double* keys) {
+  const int lane = threadIdx.x & 63;
   const double none = -__builtin_inf();
-  for (int64_t t = (int64_t)blockIdx.x * 4 + wave; t < p.tokens; t += (int64_t)gridDim.x * 4) {
-    double s[N], key[N];
-    double top = none;
-#pragma unroll
-    for (int j = 0; j < N; ++j) {
-      const int e = j * 64 + lane;
-      key[j] = none;
-      if (e < p.experts)
-        key[j] = p.bf16 ? bf16_bits_to_f32(static_cast<const uint16_t*>(p.logits)[t * p.ld + e]) : static_cast<const float*>(p.logits)[t * p.ld + e];
-      top = fmax(top, key[j]);
+  auto logit = [&](int e) {
+    return (double)(p.bf16 ? bf16_bits_to_f32(static_cast<const uint16_t*>(p.logits)[t * p.ld + e]) : static_cast<const float*>(p.logits)[t * p.ld + e]);
+  };
+  auto fence = [] {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+  };
+  double top = none, sum = 0.0;
+  if (!p.sigmoid) {
+#pragma unroll 1
+    for (int e = lane; e < p.experts; e += 64) top = fmax(top, logit(e));
+    top = wave_max(top);
+#pragma unroll 1
+    for (int e = lane; e < p.experts; e += 64) {
+      const double x = logit(e);
+      if (x != none) sum += exp(x - top);
     }
-    bool by_score = p.bias || (p.groups > 1 && p.top2);
-    if (!p.sigmoid) {
-      top = wave_max(top);
-      double sum = 0.0;
-#pragma unroll
-      for (int j = 0; j < N; ++j) {
-        s[j] = key[j] == none ? 0.0 : exp(key[j] - top);
-        sum += s[j];
+    sum = wave_sum(sum);
+  }
+  auto score = [&](double x) {
+    const double v = exp(p.sigmoid ? -x : x - top);
+    return p.sigmoid ? 1.0 / (1.0 + v) : v / sum;
+  };
+  // (where a NaN leaves no softmax, the logits order)
+  const bool scored = sum == sum, by_bias = p.bias && scored;
+  // what an expert is ordered by; a NaN comes first
+  auto key_of = [&](int e, bool value) {
+    const double x = logit(e);
+    double k = x;
+    if (x != none && (by_bias || (value && p.top2 && !p.bias && scored))) k = score(x) + (by_bias ? (double)p.bias[e] : 0.0);
+    return k == k ? k : -none;
+  };
+  uint64_t kept = ~0ull;
+  if (p.groups > 1) {
+#pragma unroll 1
+    for (int e = lane; e < p.experts; e += 64) keys[e] = key_of(e, true);
+    fence();
+    // lane g looks at group g (at most 64 of them)
+    double a = none, b = none;
+    if (lane < p.groups) {
+#pragma unroll 1
+      for (int i = 0; i < p.per_group; ++i) {
+        const double v = keys[lane * p.per_group + i];
+        b = fmax(b, fmin(a, v));
+        a = fmax(a, v);
       }
-      sum = wave_sum(sum);
+      if (p.top2 && b != none) a += b;
+    }
+    fence();
+    kept = 0;
+#pragma unroll 1
+    for (int n = 0; n < p.topk_groups; ++n) {
+      const bool open = lane < p.groups && !((kept >> lane) & 1);
+      double best = open ? a : none;
+      int at = open ? lane : 64 + lane;
+      wave_best(best, at);
+      kept |= 1ull << at;  // (there are more groups than are kept: some lane's is open)
+    }
+  }
+#pragma unroll 1
+  for (int e = lane; e < p.experts; e += 64) keys[e] = (kept >> (p.groups > 1 ? e / p.per_group : 0)) & 1 ? key_of(e, false) : none;
+  fence();
+  int id = -1;  // lane n: the n-th choice
+#pragma unroll 1
+  for (int n = 0; n < p.topk; ++n) {
+    double best = none;
+    int at = 1 << 20;
+#pragma unroll 1
+    for (int e = lane; e < p.experts; e += 64)
+      if (keys[e] > best) {
+        best = keys[e];
+        at = e;
+      }
+    wave_best(best, at);
+    if (best == none) break;  // nothing is left (the same in every lane)
+    if (lane == (at & 63)) keys[at] = none;
+    fence();
+    if (lane == n) id = at;
+  }
+  double w = id < 0 ? 0.0 : score(logit(id));
+  if (p.renormalize) {
+    const double all = wave_sum(w);
+    if (all != 0.0) w /= all;
+  }
+  if (lane < p.topk) {
+    p.ids[t * p.topk + lane] = id;
+    p.weights[t * p.topk + lane] = (float)(w * p.scale);
+  }
+}
+
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, false);
+}
+template <int CTRL>
+__device__ __forceinline__ double dpp(double v) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, v);
+  return __builtin_bit_cast(double, (uint64_t)dpp<CTRL>((uint32_t)b) | ((uint64_t)dpp<CTRL>((uint32_t)(b >> 32)) << 32));
+}
+// Over the 16 lanes of a token.
+__device__ __forceinline__ uint32_t row16_max(uint32_t v) {
+  auto up = [](uint32_t a, uint32_t b) { return a > b ? a : b; };
+  v = up(v, dpp<0x128>(v));
+  v = up(v, dpp<0x124>(v));
+  v = up(v, dpp<0x122>(v));
+  return up(v, dpp<0x121>(v));
+}
+__device__ __forceinline__ double row16_sum(double v) {
+  v += dpp<0x128>(v);
+  v += dpp<0x124>(v);
+  v += dpp<0x122>(v);
+  return v + dpp<0x121>(v);
+}
+// Calls fn with lane I of the token's lanes broadcast by `DPP row_newbcast`,
+// I = 0 .. n - 1 (n the same in the whole wave).
+template <int I, typename F>
+__device__ __forceinline__ void each_lane(int n, F&& fn) {
+  if constexpr (I < 16) {
+    if (I < n) {
+      fn(std::integral_constant<int, 0x150 + I>{});
+      each_lane<I + 1>(n, fn);
+    }
+  }
+}
+
+// f32 bits that compare as unsigned numbers as the values do, and back.
+__device__ __forceinline__ uint32_t ordered(float v) {
+  const uint32_t b = __float_as_uint(v);
+  return b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float from_ordered(uint32_t u) {
+  return __uint_as_float(u ^ ((u >> 31) ? 0x80000000u : 0xFFFFFFFFu));
+}
+
+// 16 lanes per token, four tokens per wave.  Lane l has the experts 64 b + 4 l
+// .. + 3 of NB blocks.  Keys are formed in f32 and cut to what leaves room for
+// the expert's number below them, so that one maximum finds both; topk + 2 of
+// them are taken.  Those candidates then get f64 keys, a lane each, and their
+// exact order; the first topk stand if the last of them is above whatever was
+// not taken can be, and a token for which that (or the choice of groups) is
+// too near to tell is done again by route_exactly.
+template <typename T, int NB>
+__global__ __launch_bounds__(256) void route_kernel(const RouteParams p) {
+  __shared__ double keys[4][kRouteMaxExperts];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, l = lane & 15;
+  const float none = -__builtin_inff();
+  const uint32_t low = p.low_mask;
+  const int64_t tw = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 4;
+  const bool have = tw < p.tokens;
+  const int64_t t = have ? tw : p.tokens - 1;
+  const T* row = static_cast<const T*>(p.logits) + t * p.ld;
+  float x[NB][4];
 #pragma unroll
-      for (int j = 0; j < N; ++j) s[j] = sum == 0.0 ? 0.0 : s[j] / sum;
-      by_score = by_score && sum == sum;  // (where a NaN leaves no score, the logits order)
+  for (int b = 0; b < NB; ++b) {
+    const int e = b * 64 + l * 4;
+    if (p.vec) {
+      if (e < p.experts) {
+        if constexpr (sizeof(T) == 2) {
+          const u32x2_t v = *reinterpret_cast<const u32x2_t*>(row + e);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) x[b][i] = i & 1 ? __uint_as_float(v[i / 2] & 0xFFFF0000u) : __uint_as_float(v[i / 2] << 16);
+        } else {
+          const f32x4_t v = *reinterpret_cast<const f32x4_t*>(row + e);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) x[b][i] = v[i];
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x[b][i] = none;
+      }
     } else {
 #pragma unroll
-      for (int j = 0; j < N; ++j) s[j] = 1.0 / (1.0 + exp(-key[j]));
-    }
-    // what the experts are ordered by; a NaN comes first
-#pragma unroll
-    for (int j = 0; j < N; ++j) {
-      const int e = j * 64 + lane;
-      if (p.bias && by_score && e < p.experts && key[j] != none) key[j] = s[j] + (double)p.bias[e];
-      if (key[j] != key[j]) key[j] = -none;
-    }
-    if (p.groups > 1) {
-      // (one wave's own part of LDS: no other wave reads it)
-#pragma unroll
-      for (int j = 0; j < N; ++j) {
-        const int e = j * 64 + lane;
-        if (e < p.experts) keys[wave][e] = key[j] == none || !by_score || p.bias ? key[j] : s[j] == s[j] ? s[j] : -none;
-      }
-      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-      __builtin_amdgcn_wave_barrier();
-      // lane g looks at group g (at most 64 of them)
-      double a = none, b = none;
-      if (lane < p.groups) {
-        for (int i = 0; i < p.per_group; ++i) {
-          const double v = keys[wave][lane * p.per_group + i];
-          if (v > a) {
-            b = a;
-            a = v;
-          } else if (v > b) {
-            b = v;
-          }
+      for (int i = 0; i < 4; ++i) {
+        x[b][i] = none;
+        if (e + i < p.experts) {
+          if constexpr (sizeof(T) == 2) x[b][i] = bf16_bits_to_f32(row[e + i]);
+          else x[b][i] = row[e + i];
         }
-        if (p.top2 && b != none) a += b;
       }
-      uint64_t kept = 0;
-      for (int n = 0; n < p.topk_groups; ++n) {
-        double best = lane < p.groups && !((kept >> lane) & 1) ? a : none;
-        int at = lane < p.groups && !((kept >> lane) & 1) ? lane : 64 + lane;
-        wave_best(best, at);
-        if (at < 64) kept |= 1ull << at;
-      }
+    }
+  }
+  bool ok = true;
+  // the largest logit, and whether one is a NaN or +inf
+  float top = none;
+  bool odd = false;
 #pragma unroll
-      for (int j = 0; j < N; ++j) {
-        const int e = j * 64 + lane;
-        if (e < p.experts && !((kept >> (e / p.per_group)) & 1)) key[j] = none;
-      }
-      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-      __builtin_amdgcn_wave_barrier();
-    }
-    int id = -1;       // lane n: the n-th choice
-    double w = 0.0;
-    for (int n = 0; n < p.topk; ++n) {
-      double best = none;
-      int at = 1 << 20;
+  for (int b = 0; b < NB; ++b)
 #pragma unroll
-      for (int j = 0; j < N; ++j)
-        if (key[j] > best) {
-          best = key[j];
-          at = j * 64 + lane;
-        }
-      wave_best(best, at);
-      if (best == none) break;  // nothing is left (the same in every lane)
-      double sc = 0.0;
+    for (int i = 0; i < 4; ++i) {
+      top = __builtin_fmaxf(top, x[b][i]);
+      odd = odd || !(x[b][i] < __builtin_inff());
+    }
+  top = row16_max(top);
+  float sum = 0.0f;  // of exp(x - top)
+  if (!p.sigmoid) {
+    const float shift = top > none ? top : 0.0f;
 #pragma unroll
-      for (int j = 0; j < N; ++j)
-        if (j * 64 + lane == at) {
-          key[j] = none;
-          sc = s[j];
-        }
-      sc = __shfl(sc, at & 63);
-      if (lane == n) {
-        id = at;
-        w = sc;
+    for (int b = 0; b < NB; ++b) {
+      float e[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) e[i] = __builtin_amdgcn_exp2f((x[b][i] - shift) * 1.44269504f);
+      sum += (e[0] + e[1]) + (e[2] + e[3]);
+    }
+    sum = row16_sum(sum);
+  }
+  auto score = [&](float v) {
+    if (p.sigmoid) return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(v * -1.44269504f));
+    return __builtin_amdgcn_exp2f((v - top) * 1.44269504f) * __builtin_amdgcn_rcpf(sum);
+  };
+  // what the experts are ordered by (-inf for those that take no part)
+  float key[NB][4];
+#pragma unroll
+  for (int b = 0; b < NB; ++b) {
+    const int e = b * 64 + l * 4;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      key[b][i] = x[b][i];
+      if (p.bias && e + i < p.experts && x[b][i] > none) {
+        key[b][i] = score(x[b][i]) + p.bias[e + i];
+        odd = odd || !(key[b][i] < __builtin_inff());
       }
     }
-    if (p.renormalize) {
-      const double sum = wave_sum(w);
-      if (sum != 0.0) w /= sum;
+  }
+  if (p.groups > 1) {
+    // each lane's four experts to LDS: their best two
+    float* mine = reinterpret_cast<float*>(keys[wave]) + (lane >> 4) * (kRouteMaxExperts / 2);
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      float a = none, c = none;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float v = key[b][i];
+        if (p.top2 && !p.bias && v > none) v = score(v);
+        c = __builtin_fmaxf(c, __builtin_fminf(a, v));
+        a = __builtin_fmaxf(a, v);
+      }
+      mine[(b * 16 + l) * 2] = a;
+      mine[(b * 16 + l) * 2 + 1] = c;
     }
-    if (lane < p.topk) {
-      p.ids[t * p.topk + lane] = id;
-      p.weights[t * p.topk + lane] = (float)(w * p.scale);
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    float a = none, c = none;  // lane g: group g's best two
+    const int quads = p.per_group / 4;
+    if (l < p.groups) {
+      for (int i = 0; i < quads; ++i) {
+        const float u = mine[(l * quads + i) * 2], v = mine[(l * quads + i) * 2 + 1];
+        c = __builtin_fmaxf(__builtin_fmaxf(c, v), __builtin_fminf(a, u));
+        a = __builtin_fmaxf(a, u);
+      }
     }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    if (p.top2 && c > none) a += c;
+    int rank = 0;
+    each_lane<0>(p.groups, [&](auto ctrl) {
+      constexpr int C = decltype(ctrl)::value;
+      const float o = __uint_as_float(dpp<C>(__float_as_uint(a)));
+      rank += o > a || (o == a && C - 0x150 < l);
+    });
+    const bool keep = l < p.groups && rank < p.topk_groups;
+    // the worst that stays and the best that does not
+    const float worst = -row16_max(keep ? -a : none), best = row16_max(keep ? none : a);
+    // (by logits the comparison is exact)
+    if ((p.bias || p.top2) && worst > none) ok = ok && worst - best > (__builtin_fabsf(worst) + 4.0f) * 0x1p-19f;
+    const uint32_t kept = (uint32_t)(__ballot(keep) >> (lane & 48)) & 0xFFFFu;
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      const int g = (int)(((float)(b * 16 + l) + 0.5f) * p.inv_quads);
+      if (!((kept >> g) & 1)) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) key[b][i] = none;
+      }
+    }
+  }
+  uint32_t cut[NB][4];
+#pragma unroll
+  for (int b = 0; b < NB; ++b)
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      cut[b][i] = key[b][i] > none ? (ordered(key[b][i]) & ~low) | (low - (uint32_t)(b * 64 + l * 4 + i)) : 0u;
+  // the candidates, lane n the n-th
+  const int n_cand = p.candidates;
+  uint32_t best = 0, mine = 0;
+#pragma unroll
+  for (int b = 0; b < NB; ++b)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) best = cut[b][i] > best ? cut[b][i] : best;
+  best = row16_max(best);
+  for (int n = 0;; ++n) {
+    if (l == n) mine = best;
+    if (n + 1 == n_cand) break;
+    // The largest below `best`: keys minus it wrap to the top of the range,
+    // those already taken to its bottom.
+    uint32_t next = 0;
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t d = cut[b][i] - best;
+        next = d > next ? d : next;
+      }
+    next = row16_max(next);
+    best = best ? best + next : 0u;
+  }
+  // their exact keys
+  const int id = mine ? (int)(low - (mine & low)) : -1;
+  double s = 0.0, k = -__builtin_inf();
+  float b = 0.0f;
+  if (id >= 0) {
+    float v;
+    if constexpr (sizeof(T) == 2) v = bf16_bits_to_f32(row[id]);
+    else v = row[id];
+    if (p.sigmoid) s = 1.0 / (1.0 + exp(-(double)v));
+    else s = exp((double)v - (double)top) / (double)sum;
+    k = v;
+    if (p.bias) {
+      b = p.bias[id];
+      k = s + (double)b;
+    }
+  }
+  const bool soft = !p.sigmoid && p.bias;
+  const int place = id >= 0 ? id : kRouteMaxExperts + l;  // (what is no candidate comes last, in order)
+  uint32_t last = 0;
+  int rank = 0;
+  each_lane<0>(n_cand, [&](auto ctrl) {
+    constexpr int C = decltype(ctrl)::value;
+    const double o = dpp<C>(k);
+    const int other = (int)dpp<C>((uint32_t)place);
+    rank += o > k || (o == k && other < place);
+    if (soft) {
+      // the softmax's sum is an f32 one: scores are off by up to 2^-19 of themselves
+      const double os = dpp<C>(s);
+      if (id >= 0 && other < kRouteMaxExperts && !(os == s && o == k) && __builtin_fabs(o - k) <= (os + s) * 0x1p-18) ok = false;
+    }
+    last = dpp<C>(mine);
+  });
+  // What was not taken is below the last candidate's cut key and a step of it.
+  if (!p.exact_cut && last) {
+    const float hi = from_ordered(last | low);
+    const double err = p.bias ? ((double)__builtin_fabsf(hi) + 2.0) * 0x1p-18 : 0.0;
+    if (rank == p.topk - 1 && !(k > (double)hi + err)) ok = false;
+  }
+  if (odd) ok = false;
+  const bool chosen = rank < p.topk && id >= 0;
+  if (p.renormalize) {
+    const double all = row16_sum(chosen ? s : 0.0);
+    if (all != 0.0) s /= all;
+  }
+  const uint64_t bad = __ballot(have && !ok);
+  if (have && !((bad >> (lane & 48)) & 0xFFFF)) {
+    if (rank < p.topk && l < n_cand) {
+      p.ids[t * p.topk + rank] = id;
+      p.weights[t * p.topk + rank] = chosen ? (float)(s * p.scale) : 0.0f;
+    }
+  }
+#pragma unroll 1
+  for (int n = 0; n < 4; ++n)
+    if ((bad >> (16 * n)) & 0xFFFF) route_exactly(p, tw - (lane >> 4) + n, keys[wave]);
+}
+
+// Whatever the kernel above does not take: one wave per token.
+__global__ __launch_bounds__(256) void route_exact_kernel(const RouteParams p) {
+  __shared__ double keys[4][kRouteMaxExperts];
+  const int wave = threadIdx.x >> 6;
+  const int64_t t = (int64_t)blockIdx.x * 4 + wave;
+  if (t < p.tokens) route_exactly(p, t, keys[wave]);
+}
+
+template <typename T>
+static void launch_route(const RouteParams& p, hipStream_t s) {
+  const int block = p.tokens >= 4096 ? 256 : 64;
+  const unsigned grid = (unsigned)((p.tokens * 16 + block - 1) / block);
+  switch ((p.experts + 63) / 64) {
+    case 1: route_kernel<T, 1><<<grid, block, 0, s>>>(p); break;
+    case 2: route_kernel<T, 2><<<grid, block, 0, s>>>(p); break;
+    case 3: route_kernel<T, 3><<<grid, block, 0, s>>>(p); break;
+    case 4: route_kernel<T, 4><<<grid, block, 0, s>>>(p); break;
+    case 5:
+    case 6: route_kernel<T, 6><<<grid, block, 0, s>>>(p); break;
+    default: route_kernel<T, 8><<<grid, block, 0, s>>>(p); break;
   }
 }
 
@@ -190,7 +467,8 @@ extern "C" hum_status hum_moe_route(const hum_route_desc* d, int64_t num_tokens,
   if (d->renormalize != 0 && d->renormalize != 1) return set_error(HUM_ERR_INVALID_ARG, "renormalize must be 0/1");
   if (!std::isfinite(d->scale)) return set_error(HUM_ERR_INVALID_ARG, "scale must be finite");
   if (num_tokens < 0) return set_error(HUM_ERR_INVALID_ARG, "num_tokens must be >= 0");
-  if (num_tokens >= (int64_t)1 << 31) return set_error(HUM_ERR_UNSUPPORTED, "at most 2^31 - 1 tokens in a call");
+  // (a grid holds at most 2^32 - 1 threads)
+  if (num_tokens >= (int64_t)1 << 24) return set_error(HUM_ERR_UNSUPPORTED, "at most 2^24 - 1 tokens in a call");
   if (num_tokens == 0) return HUM_OK;
   if (!logits || !topk_ids || !topk_weights) return set_error(HUM_ERR_INVALID_ARG, "NULL pointer");
   const int size = d->logits_dtype == HUM_BF16 ? 2 : 4;
@@ -221,8 +499,23 @@ extern "C" hum_status hum_moe_route(const hum_route_desc* d, int64_t num_tokens,
   p.top2 = d->group_score == HUM_GROUP_TOP2;
   p.renormalize = d->renormalize;
   p.scale = d->scale;
-  const int64_t wgs = (num_tokens + 3) / 4;
-  route_kernel<<<(unsigned)(wgs < 1 << 20 ? wgs : 1 << 20), 256, 0, static_cast<hipStream_t>(stream)>>>(p);
+  const int quad = 4 * size;
+  p.vec = addr(logits) % quad == 0 && (num_tokens == 1 || ld_logits % 4 == 0) && d->num_experts % 4 == 0;
+  p.exact_cut = size == 2 && !bias;
+  p.candidates = d->topk + (p.exact_cut ? 0 : 2);
+  int bits = 0;
+  while (1 << bits < d->num_experts) ++bits;
+  p.low_mask = (1u << bits) - 1u;
+  p.inv_quads = 4.0f / (float)p.per_group;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  // The fast kernel holds topk + 2 candidates in 16 lanes, and groups of whole
+  // lanes' experts in 16 more.
+  if (d->topk <= 14 && (p.groups == 1 || (p.groups <= 16 && p.per_group % 4 == 0))) {
+    if (p.bf16) launch_route<uint16_t>(p, s);
+    else launch_route<float>(p, s);
+  } else {
+    route_exact_kernel<<<(unsigned)((num_tokens + 3) / 4), 256, 0, s>>>(p);
+  }
   hipError_t err = hipGetLastError();
   if (err != hipSuccess) return set_error(HUM_ERR_HIP, "moe_route launch: %s", hipGetErrorString(err));
   return HUM_OK;

@@ -90,7 +90,7 @@ def _route(lib, t=4, x=P(BIG), ld=16, bias=None, ids=P(2 * BIG), w=P(3 * BIG), *
 def test_route_abi_refusals(lib):
     r = lambda **kw: _route(lib, **kw)  # noqa: E731
     assert r(t=0) == 0 and r(t=0, x=None) == 0 and lib.hum_moe_route(None, 0, None, 0, None, None, None, None) == 1
-    assert r(t=-1) == 1 and r(t=1 << 31) == 2 and r(logits_dtype=hum.INT8) == 2
+    assert r(t=-1) == 1 and r(t=1 << 24) == 2 and r(logits_dtype=hum.INT8) == 2
     assert r(num_experts=0) == 2 and r(num_experts=513) == 2 and r(topk=0) == 1 and r(topk=17) == 1
     assert r(num_experts=128, topk=65) == 1 and r(score=2) == 1 and r(group_score=2) == 1 and r(renormalize=2) == 1
     assert r(num_groups=0) == 1 and r(num_groups=3) == 1 and r(num_groups=4, topk_groups=5) == 1 and r(topk_groups=0) == 1
