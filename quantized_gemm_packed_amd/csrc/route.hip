@@ -32,35 +32,55 @@ struct RouteParams {
   float inv_quads, scale;
 };
 
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, false);
+}
+template <int CTRL>
+__device__ __forceinline__ double dpp(double v) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, v);
+  return __builtin_bit_cast(double, (uint64_t)dpp<CTRL>((uint32_t)b) | ((uint64_t)dpp<CTRL>((uint32_t)(b >> 32)) << 32));
+}
+// Over the 16 lanes of a token.
+__device__ __forceinline__ uint32_t row16_max(uint32_t v) {
+  auto up = [](uint32_t a, uint32_t b) { return a > b ? a : b; };
+  v = up(v, dpp<0x128>(v));
+  v = up(v, dpp<0x124>(v));
+  v = up(v, dpp<0x122>(v));
+  return up(v, dpp<0x121>(v));
+}
+__device__ __forceinline__ double row16_sum(double v) {
+  v += dpp<0x128>(v);
+  v += dpp<0x124>(v);
+  v += dpp<0x122>(v);
+  return v + dpp<0x121>(v);
+}
+__device__ __forceinline__ double row16_max(double v) {
+  v = fmax(v, dpp<0x128>(v));
+  v = fmax(v, dpp<0x124>(v));
+  v = fmax(v, dpp<0x122>(v));
+  return fmax(v, dpp<0x121>(v));
+}
+__device__ __forceinline__ double lane_of(double v, int lane) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = __builtin_amdgcn_readlane((int)(uint32_t)b, lane), hi = __builtin_amdgcn_readlane((int)(uint32_t)(b >> 32), lane);
+  return __builtin_bit_cast(double, (uint64_t)lo | (uint64_t)hi << 32);
+}
+// Over the 64 lanes of a wave, the same in all of them.
 __device__ __forceinline__ double wave_max(double v) {
-#pragma unroll
-  for (int o = 1; o < 64; o *= 2) v = fmax(v, __shfl_xor(v, o));
-  return v;
+  v = row16_max(v);
+  return fmax(fmax(lane_of(v, 0), lane_of(v, 16)), fmax(lane_of(v, 32), lane_of(v, 48)));
 }
 __device__ __forceinline__ double wave_sum(double v) {
-#pragma unroll
-  for (int o = 1; o < 64; o *= 2) v += __shfl_xor(v, o);
-  return v;
-}
-
-// The largest key of the wave, of equal ones that of the lowest index: every
-// lane gets both.
-__device__ __forceinline__ void wave_best(double& key, int& idx) {
-#pragma unroll
-  for (int o = 1; o < 64; o *= 2) {
-    const double k = __shfl_xor(key, o);
-    const int i = __shfl_xor(idx, o);
-    if (k > key || (k == key && i < idx)) {
-      key = k;
-      idx = i;
-    }
-  }
+  v = row16_sum(v);
+  return (lane_of(v, 0) + lane_of(v, 16)) + (lane_of(v, 32) + lane_of(v, 48));
 }
 
 // One token by one wave, all in f64; lane l has the experts l, l + 64, ...
-// keys: LDS of this wave alone.  Loops stay rolled: it runs seldom, and what it
-// holds in registers the kernel around it does not have.
+// keys: LDS of this wave alone.  What calls exp stays rolled: it runs seldom,
+// and what it holds in registers the kernel around it does not have.
 __device__ __forceinline__ void route_exactly(const RouteParams& p, int64_t t, double* keys) {
+  constexpr int N = kRouteMaxExperts / 64;
   const int lane = threadIdx.x & 63;
   const double none = -__builtin_inf();
   auto logit = [&](int e) {
@@ -87,59 +107,62 @@ __device__ __forceinline__ void route_exactly(const RouteParams& p, int64_t t, d
     return p.sigmoid ? 1.0 / (1.0 + v) : v / sum;
   };
   // (where a NaN leaves no softmax, the logits order)
-  const bool scored = sum == sum, by_bias = p.bias && scored;
-  // what an expert is ordered by; a NaN comes first
-  auto key_of = [&](int e, bool value) {
-    const double x = logit(e);
-    double k = x;
-    if (x != none && (by_bias || (value && p.top2 && !p.bias && scored))) k = score(x) + (by_bias ? (double)p.bias[e] : 0.0);
-    return k == k ? k : -none;
-  };
-  uint64_t kept = ~0ull;
-  if (p.groups > 1) {
+  const bool by_bias = p.bias && sum == sum, by_score = p.groups > 1 && p.top2 && !p.bias && sum == sum;
+  // what an expert is ordered by, and its group (by its score then); a NaN first
 #pragma unroll 1
-    for (int e = lane; e < p.experts; e += 64) keys[e] = key_of(e, true);
-    fence();
+  for (int e = lane; e < p.experts; e += 64) {
+    double k = logit(e);
+    if (k != none && (by_bias || by_score)) k = score(k) + (by_bias ? (double)p.bias[e] : 0.0);
+    keys[e] = k == k ? k : -none;
+  }
+  fence();
+  double key[N];
+#pragma unroll
+  for (int j = 0; j < N; ++j) key[j] = j * 64 + lane < p.experts ? keys[j * 64 + lane] : none;
+  if (p.groups > 1) {
     // lane g looks at group g (at most 64 of them)
     double a = none, b = none;
-    if (lane < p.groups) {
-#pragma unroll 1
-      for (int i = 0; i < p.per_group; ++i) {
-        const double v = keys[lane * p.per_group + i];
-        b = fmax(b, fmin(a, v));
-        a = fmax(a, v);
-      }
-      if (p.top2 && b != none) a += b;
+    const int from = lane < p.groups ? lane * p.per_group : 0;
+#pragma unroll 4
+    for (int i = 0; i < p.per_group; ++i) {
+      const double v = keys[from + i];
+      b = fmax(b, fmin(a, v));
+      a = fmax(a, v);
     }
-    fence();
-    kept = 0;
-#pragma unroll 1
-    for (int n = 0; n < p.topk_groups; ++n) {
-      const bool open = lane < p.groups && !((kept >> lane) & 1);
-      double best = open ? a : none;
-      int at = open ? lane : 64 + lane;
-      wave_best(best, at);
-      kept |= 1ull << at;  // (there are more groups than are kept: some lane's is open)
+    if (p.top2 && b != none) a += b;
+    int rank = 0;
+    for (int g = 0; g < p.groups; ++g) {
+      const double o = lane_of(a, g);
+      rank += (int)(o > a) | ((int)(o == a) & (int)(g < lane));
+    }
+    const uint64_t kept = __ballot(lane < p.groups && rank < p.topk_groups);
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      const int e = j * 64 + lane;
+      if (e >= p.experts) continue;
+      if (by_score && key[j] != none) {  // (their own order is that of the logits)
+        const double x = logit(e);
+        key[j] = x == x ? x : -none;
+      }
+      if (!((kept >> (e / p.per_group)) & 1)) key[j] = none;
     }
   }
-#pragma unroll 1
-  for (int e = lane; e < p.experts; e += 64) keys[e] = (kept >> (p.groups > 1 ? e / p.per_group : 0)) & 1 ? key_of(e, false) : none;
-  fence();
   int id = -1;  // lane n: the n-th choice
-#pragma unroll 1
   for (int n = 0; n < p.topk; ++n) {
     double best = none;
-    int at = 1 << 20;
-#pragma unroll 1
-    for (int e = lane; e < p.experts; e += 64)
-      if (keys[e] > best) {
-        best = keys[e];
-        at = e;
-      }
-    wave_best(best, at);
+#pragma unroll
+    for (int j = 0; j < N; ++j) best = fmax(best, key[j]);
+    best = wave_max(best);
     if (best == none) break;  // nothing is left (the same in every lane)
-    if (lane == (at & 63)) keys[at] = none;
-    fence();
+    int at = -1;              // the lowest of those that have it
+#pragma unroll
+    for (int j = N - 1; j >= 0; --j) {
+      const uint64_t have = __ballot(key[j] == best);
+      if (have) at = j * 64 + __builtin_ctzll(have);
+    }
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+      if (at == j * 64 + lane) key[j] = none;
     if (lane == n) id = at;
   }
   double w = id < 0 ? 0.0 : score(logit(id));
@@ -151,31 +174,9 @@ __device__ __forceinline__ void route_exactly(const RouteParams& p, int64_t t, d
     p.ids[t * p.topk + lane] = id;
     p.weights[t * p.topk + lane] = (float)(w * p.scale);
   }
+  fence();
 }
 
-template <int CTRL>
-__device__ __forceinline__ uint32_t dpp(uint32_t v) {
-  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, false);
-}
-template <int CTRL>
-__device__ __forceinline__ double dpp(double v) {
-  const uint64_t b = __builtin_bit_cast(uint64_t, v);
-  return __builtin_bit_cast(double, (uint64_t)dpp<CTRL>((uint32_t)b) | ((uint64_t)dpp<CTRL>((uint32_t)(b >> 32)) << 32));
-}
-// Over the 16 lanes of a token.
-__device__ __forceinline__ uint32_t row16_max(uint32_t v) {
-  auto up = [](uint32_t a, uint32_t b) { return a > b ? a : b; };
-  v = up(v, dpp<0x128>(v));
-  v = up(v, dpp<0x124>(v));
-  v = up(v, dpp<0x122>(v));
-  return up(v, dpp<0x121>(v));
-}
-__device__ __forceinline__ double row16_sum(double v) {
-  v += dpp<0x128>(v);
-  v += dpp<0x124>(v);
-  v += dpp<0x122>(v);
-  return v + dpp<0x121>(v);
-}
 // Calls fn with lane I of the token's lanes broadcast by `DPP row_newbcast`,
 // I = 0 .. n - 1 (n the same in the whole wave).
 template <int I, typename F>
@@ -204,7 +205,7 @@ __device__ __forceinline__ float from_ordered(uint32_t u) {
 // exact order; the first topk stand if the last of them is above whatever was
 // not taken can be, and a token for which that (or the choice of groups) is
 // too near to tell is done again by route_exactly.
-template <typename T, int NB>
+template <typename T, int NB, bool BIAS, bool GROUPS>
 __global__ __launch_bounds__(256) void route_kernel(const RouteParams p) {
   __shared__ double keys[4][kRouteMaxExperts];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, l = lane & 15;
@@ -214,50 +215,55 @@ __global__ __launch_bounds__(256) void route_kernel(const RouteParams p) {
   const bool have = tw < p.tokens;
   const int64_t t = have ? tw : p.tokens - 1;
   const T* row = static_cast<const T*>(p.logits) + t * p.ld;
-  float x[NB][4];
+  float x[NB][4], bias[NB][4];
+  if (p.vec) {
 #pragma unroll
-  for (int b = 0; b < NB; ++b) {
-    const int e = b * 64 + l * 4;
-    if (p.vec) {
-      if (e < p.experts) {
-        if constexpr (sizeof(T) == 2) {
-          const u32x2_t v = *reinterpret_cast<const u32x2_t*>(row + e);
+    for (int b = 0; b < NB; ++b) {
+      const int e = b * 64 + l * 4;
+      const bool in = e < p.experts;
+      if constexpr (sizeof(T) == 2) {
+        u32x2_t v = {0xFF80FF80u, 0xFF80FF80u};
+        if (in) v = *reinterpret_cast<const u32x2_t*>(row + e);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) x[b][i] = i & 1 ? __uint_as_float(v[i / 2] & 0xFFFF0000u) : __uint_as_float(v[i / 2] << 16);
-        } else {
-          const f32x4_t v = *reinterpret_cast<const f32x4_t*>(row + e);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) x[b][i] = v[i];
-        }
+        for (int i = 0; i < 4; ++i) x[b][i] = __uint_as_float(i & 1 ? v[i / 2] & 0xFFFF0000u : v[i / 2] << 16);
       } else {
+        f32x4_t v = {none, none, none, none};
+        if (in) v = *reinterpret_cast<const f32x4_t*>(row + e);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) x[b][i] = none;
+        for (int i = 0; i < 4; ++i) x[b][i] = v[i];
       }
-    } else {
+      if constexpr (BIAS) {
+        f32x4_t v = {0.0f, 0.0f, 0.0f, 0.0f};
+        if (in) v = *reinterpret_cast<const f32x4_t*>(p.bias + e);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) bias[b][i] = v[i];
+      }
+    }
+  } else {
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
+        const int e = b * 64 + l * 4 + i;
+        const bool in = e < p.experts;
         x[b][i] = none;
-        if (e + i < p.experts) {
-          if constexpr (sizeof(T) == 2) x[b][i] = bf16_bits_to_f32(row[e + i]);
-          else x[b][i] = row[e + i];
+        bias[b][i] = 0.0f;
+        if (in) {
+          if constexpr (sizeof(T) == 2) x[b][i] = bf16_bits_to_f32(row[e]);
+          else x[b][i] = row[e];
+          if constexpr (BIAS) bias[b][i] = p.bias[e];
         }
       }
-    }
   }
   bool ok = true;
-  // the largest logit, and whether one is a NaN or +inf
-  float top = none;
-  bool odd = false;
-#pragma unroll
-  for (int b = 0; b < NB; ++b)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      top = __builtin_fmaxf(top, x[b][i]);
-      odd = odd || !(x[b][i] < __builtin_inff());
-    }
-  top = row16_max(top);
-  float sum = 0.0f;  // of exp(x - top)
+  // the largest logit, and the sum of exp(x - top)
+  float top = none, sum = 0.0f;
   if (!p.sigmoid) {
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) top = __builtin_fmaxf(top, x[b][i]);
+    top = row16_max(top);
     const float shift = top > none ? top : 0.0f;
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
@@ -272,69 +278,72 @@ __global__ __launch_bounds__(256) void route_kernel(const RouteParams p) {
     if (p.sigmoid) return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(v * -1.44269504f));
     return __builtin_amdgcn_exp2f((v - top) * 1.44269504f) * __builtin_amdgcn_rcpf(sum);
   };
-  // what the experts are ordered by (-inf for those that take no part)
+  // what the experts are ordered by: -inf for those that take no part; whether
+  // a NaN or +inf is among them
   float key[NB][4];
+  bool odd = false;
 #pragma unroll
-  for (int b = 0; b < NB; ++b) {
-    const int e = b * 64 + l * 4;
+  for (int b = 0; b < NB; ++b)
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       key[b][i] = x[b][i];
-      if (p.bias && e + i < p.experts && x[b][i] > none) {
-        key[b][i] = score(x[b][i]) + p.bias[e + i];
+      odd = odd || !(x[b][i] < __builtin_inff());
+      if constexpr (BIAS) {
+        const float v = score(x[b][i]) + bias[b][i];
+        key[b][i] = x[b][i] > none ? v : none;
         odd = odd || !(key[b][i] < __builtin_inff());
       }
     }
-  }
-  if (p.groups > 1) {
+  if constexpr (GROUPS) {
     // each lane's four experts to LDS: their best two
-    float* mine = reinterpret_cast<float*>(keys[wave]) + (lane >> 4) * (kRouteMaxExperts / 2);
+    typedef float f32x2_t __attribute__((ext_vector_type(2)));
+    f32x2_t* mine = reinterpret_cast<f32x2_t*>(keys[wave]) + (lane >> 4) * (kRouteMaxExperts / 4);
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
-      float a = none, c = none;
+      float v[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        float v = key[b][i];
-        if (p.top2 && !p.bias && v > none) v = score(v);
-        c = __builtin_fmaxf(c, __builtin_fminf(a, v));
-        a = __builtin_fmaxf(a, v);
-      }
-      mine[(b * 16 + l) * 2] = a;
-      mine[(b * 16 + l) * 2 + 1] = c;
+      for (int i = 0; i < 4; ++i) v[i] = !BIAS && p.top2 && key[b][i] > none ? score(key[b][i]) : key[b][i];
+      const float a0 = __builtin_fmaxf(v[0], v[1]), c0 = __builtin_fminf(v[0], v[1]);
+      const float a1 = __builtin_fmaxf(v[2], v[3]), c1 = __builtin_fminf(v[2], v[3]);
+      mine[b * 16 + l] = f32x2_t{__builtin_fmaxf(a0, a1), __builtin_fmaxf(__builtin_fminf(a0, a1), __builtin_fmaxf(c0, c1))};
     }
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     __builtin_amdgcn_wave_barrier();
     float a = none, c = none;  // lane g: group g's best two
-    const int quads = p.per_group / 4;
-    if (l < p.groups) {
-      for (int i = 0; i < quads; ++i) {
-        const float u = mine[(l * quads + i) * 2], v = mine[(l * quads + i) * 2 + 1];
-        c = __builtin_fmaxf(__builtin_fmaxf(c, v), __builtin_fminf(a, u));
-        a = __builtin_fmaxf(a, u);
-      }
+    const int quads = p.per_group / 4, mine0 = l < p.groups ? l * quads : 0;
+#pragma unroll 4
+    for (int i = 0; i < quads; ++i) {
+      const f32x2_t v = mine[mine0 + i];
+      c = __builtin_fmaxf(__builtin_fmaxf(c, v[1]), __builtin_fminf(a, v[0]));
+      a = __builtin_fmaxf(a, v[0]);
     }
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     __builtin_amdgcn_wave_barrier();
+    // How far a group's f32 score may be off: a score 2^-22 (the exponential, its
+    // argument's rounding, the sum and the reciprocal), a softmax's its sum's
+    // 2^-19 of itself, a sum with the bias half an ulp.
+    float err = 0x1p-20f + (__builtin_fabsf(a) + (c > none ? __builtin_fabsf(c) : 0.0f)) * (p.sigmoid ? 0x1p-23f : 0x1p-18f);
     if (p.top2 && c > none) a += c;
+    if (l >= p.groups) a = none;
+    err = row16_max(a > none ? err : 0.0f);
     int rank = 0;
     each_lane<0>(p.groups, [&](auto ctrl) {
       constexpr int C = decltype(ctrl)::value;
       const float o = __uint_as_float(dpp<C>(__float_as_uint(a)));
-      rank += o > a || (o == a && C - 0x150 < l);
+      rank += (int)(o > a) | ((int)(o == a) & (int)(C - 0x150 < l));
     });
     const bool keep = l < p.groups && rank < p.topk_groups;
     // the worst that stays and the best that does not
     const float worst = -row16_max(keep ? -a : none), best = row16_max(keep ? none : a);
     // (by logits the comparison is exact)
-    if ((p.bias || p.top2) && worst > none) ok = ok && worst - best > (__builtin_fabsf(worst) + 4.0f) * 0x1p-19f;
+    if ((BIAS || p.top2) && worst > none) ok = worst - best > 2.0f * err;
     const uint32_t kept = (uint32_t)(__ballot(keep) >> (lane & 48)) & 0xFFFFu;
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
       const int g = (int)(((float)(b * 16 + l) + 0.5f) * p.inv_quads);
-      if (!((kept >> g) & 1)) {
+      const bool out = !((kept >> (g & 31)) & 1);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) key[b][i] = none;
-      }
+      for (int i = 0; i < 4; ++i) key[b][i] = out ? none : key[b][i];
     }
   }
   uint32_t cut[NB][4];
@@ -370,20 +379,16 @@ __global__ __launch_bounds__(256) void route_kernel(const RouteParams p) {
   // their exact keys
   const int id = mine ? (int)(low - (mine & low)) : -1;
   double s = 0.0, k = -__builtin_inf();
-  float b = 0.0f;
   if (id >= 0) {
     float v;
     if constexpr (sizeof(T) == 2) v = bf16_bits_to_f32(row[id]);
     else v = row[id];
-    if (p.sigmoid) s = 1.0 / (1.0 + exp(-(double)v));
-    else s = exp((double)v - (double)top) / (double)sum;
-    k = v;
-    if (p.bias) {
-      b = p.bias[id];
-      k = s + (double)b;
-    }
+    const double by = BIAS ? (double)p.bias[id] : 0.0;
+    const double e = exp(p.sigmoid ? -(double)v : (double)v - (double)top);
+    s = p.sigmoid ? 1.0 / (1.0 + e) : e / (double)sum;
+    k = BIAS ? s + by : (double)v;
   }
-  const bool soft = !p.sigmoid && p.bias;
+  const bool soft = BIAS && !p.sigmoid;
   const int place = id >= 0 ? id : kRouteMaxExperts + l;  // (what is no candidate comes last, in order)
   uint32_t last = 0;
   int rank = 0;
@@ -391,7 +396,7 @@ __global__ __launch_bounds__(256) void route_kernel(const RouteParams p) {
     constexpr int C = decltype(ctrl)::value;
     const double o = dpp<C>(k);
     const int other = (int)dpp<C>((uint32_t)place);
-    rank += o > k || (o == k && other < place);
+    rank += (int)(o > k) | ((int)(o == k) & (int)(other < place));
     if (soft) {
       // the softmax's sum is an f32 one: scores are off by up to 2^-19 of themselves
       const double os = dpp<C>(s);
@@ -402,7 +407,7 @@ __global__ __launch_bounds__(256) void route_kernel(const RouteParams p) {
   // What was not taken is below the last candidate's cut key and a step of it.
   if (!p.exact_cut && last) {
     const float hi = from_ordered(last | low);
-    const double err = p.bias ? ((double)__builtin_fabsf(hi) + 2.0) * 0x1p-18 : 0.0;
+    const double err = BIAS ? ((double)__builtin_fabsf(hi) + 2.0) * 0x1p-18 : 0.0;
     if (rank == p.topk - 1 && !(k > (double)hi + err)) ok = false;
   }
   if (odd) ok = false;
@@ -431,19 +436,27 @@ __global__ __launch_bounds__(256) void route_exact_kernel(const RouteParams p) {
   if (t < p.tokens) route_exactly(p, t, keys[wave]);
 }
 
-template <typename T>
+template <typename T, bool BIAS, bool GROUPS>
 static void launch_route(const RouteParams& p, hipStream_t s) {
   const int block = p.tokens >= 4096 ? 256 : 64;
   const unsigned grid = (unsigned)((p.tokens * 16 + block - 1) / block);
   switch ((p.experts + 63) / 64) {
-    case 1: route_kernel<T, 1><<<grid, block, 0, s>>>(p); break;
-    case 2: route_kernel<T, 2><<<grid, block, 0, s>>>(p); break;
-    case 3: route_kernel<T, 3><<<grid, block, 0, s>>>(p); break;
-    case 4: route_kernel<T, 4><<<grid, block, 0, s>>>(p); break;
+    case 1: route_kernel<T, 1, BIAS, GROUPS><<<grid, block, 0, s>>>(p); break;
+    case 2: route_kernel<T, 2, BIAS, GROUPS><<<grid, block, 0, s>>>(p); break;
+    case 3: route_kernel<T, 3, BIAS, GROUPS><<<grid, block, 0, s>>>(p); break;
+    case 4: route_kernel<T, 4, BIAS, GROUPS><<<grid, block, 0, s>>>(p); break;
     case 5:
-    case 6: route_kernel<T, 6><<<grid, block, 0, s>>>(p); break;
-    default: route_kernel<T, 8><<<grid, block, 0, s>>>(p); break;
+    case 6: route_kernel<T, 6, BIAS, GROUPS><<<grid, block, 0, s>>>(p); break;
+    default: route_kernel<T, 8, BIAS, GROUPS><<<grid, block, 0, s>>>(p); break;
   }
+}
+
+template <typename T>
+static void launch_route(const RouteParams& p, hipStream_t s) {
+  if (p.bias && p.groups > 1) launch_route<T, true, true>(p, s);
+  else if (p.bias) launch_route<T, true, false>(p, s);
+  else if (p.groups > 1) launch_route<T, false, true>(p, s);
+  else launch_route<T, false, false>(p, s);
 }
 
 }  // namespace hum
@@ -500,7 +513,7 @@ extern "C" hum_status hum_moe_route(const hum_route_desc* d, int64_t num_tokens,
   p.renormalize = d->renormalize;
   p.scale = d->scale;
   const int quad = 4 * size;
-  p.vec = addr(logits) % quad == 0 && (num_tokens == 1 || ld_logits % 4 == 0) && d->num_experts % 4 == 0;
+  p.vec = addr(logits) % quad == 0 && addr(bias) % 16 == 0 && (num_tokens == 1 || ld_logits % 4 == 0) && d->num_experts % 4 == 0;
   p.exact_cut = size == 2 && !bias;
   p.candidates = d->topk + (p.exact_cut ? 0 : 2);
   int bits = 0;
