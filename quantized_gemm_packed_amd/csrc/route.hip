@@ -109,7 +109,7 @@ __device__ __forceinline__ void route_exactly(const RouteParams& p, int64_t t, d
   // (where a NaN leaves no softmax, the logits order)
   const bool by_bias = p.bias && sum == sum, by_score = p.groups > 1 && p.top2 && !p.bias && sum == sum;
   // what an expert is ordered by, and its group (by its score then); a NaN first
-#pragma unroll 1
+#pragma unroll 2
   for (int e = lane; e < p.experts; e += 64) {
     double k = logit(e);
     if (k != none && (by_bias || by_score)) k = score(k) + (by_bias ? (double)p.bias[e] : 0.0);
@@ -198,6 +198,18 @@ __device__ __forceinline__ float from_ordered(uint32_t u) {
   return __uint_as_float(u ^ ((u >> 31) ? 0x80000000u : 0xFFFFFFFFu));
 }
 
+// The cut key of -inf is below this, that of any number above.
+constexpr uint32_t kNoKey = 0x00800000u;
+constexpr int kRowShl1 = 0x101;  // DPP row_shl:1, a lane gets the next one's
+
+// 1 / d to f64's last bit or two, d in [2^-1000, 2^1000]: the instruction's
+// estimate and two Newton steps.
+__device__ __forceinline__ double reciprocal(double d) {
+  double y = __builtin_amdgcn_rcp(d);
+  y = __builtin_fma(__builtin_fma(-d, y, 1.0), y, y);
+  return __builtin_fma(__builtin_fma(-d, y, 1.0), y, y);
+}
+
 // 16 lanes per token, four tokens per wave.  Lane l has the experts 64 b + 4 l
 // .. + 3 of NB blocks.  Keys are formed in f32 and cut to what leaves room for
 // the expert's number below them, so that one maximum finds both; topk + 2 of
@@ -206,7 +218,7 @@ __device__ __forceinline__ float from_ordered(uint32_t u) {
 // not taken can be, and a token for which that (or the choice of groups) is
 // too near to tell is done again by route_exactly.
 template <typename T, int NB, bool BIAS, bool GROUPS>
-__global__ __launch_bounds__(256) void route_kernel(const RouteParams p) {
+__global__ __launch_bounds__(256, NB <= 4 ? 5 : 4) void route_kernel(const RouteParams p) {
   __shared__ double keys[4][kRouteMaxExperts];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, l = lane & 15;
   const float none = -__builtin_inff();
@@ -221,20 +233,18 @@ __global__ __launch_bounds__(256) void route_kernel(const RouteParams p) {
     for (int b = 0; b < NB; ++b) {
       const int e = b * 64 + l * 4;
       const bool in = e < p.experts;
+      const int at = in ? e : 0;  // (no branch between the loads)
       if constexpr (sizeof(T) == 2) {
-        u32x2_t v = {0xFF80FF80u, 0xFF80FF80u};
-        if (in) v = *reinterpret_cast<const u32x2_t*>(row + e);
+        const u32x2_t v = *reinterpret_cast<const u32x2_t*>(row + at);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) x[b][i] = __uint_as_float(i & 1 ? v[i / 2] & 0xFFFF0000u : v[i / 2] << 16);
+        for (int i = 0; i < 4; ++i) x[b][i] = in ? __uint_as_float(i & 1 ? v[i / 2] & 0xFFFF0000u : v[i / 2] << 16) : none;
       } else {
-        f32x4_t v = {none, none, none, none};
-        if (in) v = *reinterpret_cast<const f32x4_t*>(row + e);
+        const f32x4_t v = *reinterpret_cast<const f32x4_t*>(row + at);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) x[b][i] = v[i];
+        for (int i = 0; i < 4; ++i) x[b][i] = in ? v[i] : none;
       }
       if constexpr (BIAS) {
-        f32x4_t v = {0.0f, 0.0f, 0.0f, 0.0f};
-        if (in) v = *reinterpret_cast<const f32x4_t*>(p.bias + e);
+        const f32x4_t v = *reinterpret_cast<const f32x4_t*>(p.bias + at);
 #pragma unroll
         for (int i = 0; i < 4; ++i) bias[b][i] = v[i];
       }
@@ -274,37 +284,60 @@ __global__ __launch_bounds__(256) void route_kernel(const RouteParams p) {
     }
     sum = row16_sum(sum);
   }
-  auto score = [&](float v) {
-    if (p.sigmoid) return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(v * -1.44269504f));
-    return __builtin_amdgcn_exp2f((v - top) * 1.44269504f) * __builtin_amdgcn_rcpf(sum);
+  // scores of logits (of -inf: 0)
+  auto scores = [&](float (&v)[NB][4]) {
+    if (p.sigmoid) {
+#pragma unroll
+      for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[b][i] = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(v[b][i] * -1.44269504f));
+    } else {
+      const float r = __builtin_amdgcn_rcpf(sum);
+#pragma unroll
+      for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[b][i] = __builtin_amdgcn_exp2f((v[b][i] - top) * 1.44269504f) * r;
+    }
   };
   // what the experts are ordered by: -inf for those that take no part; whether
   // a NaN or +inf is among them
   float key[NB][4];
+#pragma unroll
+  for (int b = 0; b < NB; ++b)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) key[b][i] = x[b][i];
+  if constexpr (BIAS) {
+    scores(key);
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) key[b][i] = x[b][i] == none ? none : key[b][i] + bias[b][i];
+  }
   bool odd = false;
 #pragma unroll
   for (int b = 0; b < NB; ++b)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      key[b][i] = x[b][i];
-      odd = odd || !(x[b][i] < __builtin_inff());
-      if constexpr (BIAS) {
-        const float v = score(x[b][i]) + bias[b][i];
-        key[b][i] = x[b][i] > none ? v : none;
-        odd = odd || !(key[b][i] < __builtin_inff());
-      }
-    }
+    for (int i = 0; i < 4; ++i) odd = odd || !(key[b][i] < __builtin_inff());
   if constexpr (GROUPS) {
     // each lane's four experts to LDS: their best two
     typedef float f32x2_t __attribute__((ext_vector_type(2)));
     f32x2_t* mine = reinterpret_cast<f32x2_t*>(keys[wave]) + (lane >> 4) * (kRouteMaxExperts / 4);
+    float v[NB][4];
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[b][i] = key[b][i];
+    if (!BIAS && p.top2) {
+      scores(v);
+#pragma unroll
+      for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[b][i] = key[b][i] > none ? v[b][i] : none;
+    }
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
-      float v[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] = !BIAS && p.top2 && key[b][i] > none ? score(key[b][i]) : key[b][i];
-      const float a0 = __builtin_fmaxf(v[0], v[1]), c0 = __builtin_fminf(v[0], v[1]);
-      const float a1 = __builtin_fmaxf(v[2], v[3]), c1 = __builtin_fminf(v[2], v[3]);
+      const float a0 = __builtin_fmaxf(v[b][0], v[b][1]), c0 = __builtin_fminf(v[b][0], v[b][1]);
+      const float a1 = __builtin_fmaxf(v[b][2], v[b][3]), c1 = __builtin_fminf(v[b][2], v[b][3]);
       mine[b * 16 + l] = f32x2_t{__builtin_fmaxf(a0, a1), __builtin_fmaxf(__builtin_fminf(a0, a1), __builtin_fmaxf(c0, c1))};
     }
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
@@ -319,10 +352,11 @@ __global__ __launch_bounds__(256) void route_kernel(const RouteParams p) {
     }
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     __builtin_amdgcn_wave_barrier();
-    // How far a group's f32 score may be off: a score 2^-22 (the exponential, its
-    // argument's rounding, the sum and the reciprocal), a softmax's its sum's
-    // 2^-19 of itself, a sum with the bias half an ulp.
-    float err = 0x1p-20f + (__builtin_fabsf(a) + (c > none ? __builtin_fabsf(c) : 0.0f)) * (p.sigmoid ? 0x1p-23f : 0x1p-18f);
+    // How far a group's f32 score may be off: each score by 2^-22 (the
+    // exponential, its argument's rounding, the sum and the reciprocal; a
+    // softmax's by its sum's 2^-19 of itself), its sum with the bias by half an
+    // ulp.
+    float err = 0x1p-21f + (__builtin_fabsf(a) + (c > none ? __builtin_fabsf(c) : 0.0f)) * (p.sigmoid ? 0x1p-23f : 0x1p-18f);
     if (p.top2 && c > none) a += c;
     if (l >= p.groups) a = none;
     err = row16_max(a > none ? err : 0.0f);
@@ -346,12 +380,12 @@ __global__ __launch_bounds__(256) void route_kernel(const RouteParams p) {
       for (int i = 0; i < 4; ++i) key[b][i] = out ? none : key[b][i];
     }
   }
+  // Cut keys: what takes no part lies below kNoKey.
   uint32_t cut[NB][4];
 #pragma unroll
   for (int b = 0; b < NB; ++b)
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      cut[b][i] = key[b][i] > none ? (ordered(key[b][i]) & ~low) | (low - (uint32_t)(b * 64 + l * 4 + i)) : 0u;
+    for (int i = 0; i < 4; ++i) cut[b][i] = (ordered(key[b][i]) & ~low) | ((low - (uint32_t)(l * 4) - (uint32_t)(b * 64 + i)) & low);
   // the candidates, lane n the n-th
   const int n_cand = p.candidates;
   uint32_t best = 0, mine = 0;
@@ -361,7 +395,7 @@ __global__ __launch_bounds__(256) void route_kernel(const RouteParams p) {
     for (int i = 0; i < 4; ++i) best = cut[b][i] > best ? cut[b][i] : best;
   best = row16_max(best);
   for (int n = 0;; ++n) {
-    if (l == n) mine = best;
+    mine = l == n ? best : mine;
     if (n + 1 == n_cand) break;
     // The largest below `best`: keys minus it wrap to the top of the range,
     // those already taken to its bottom.
@@ -374,10 +408,10 @@ __global__ __launch_bounds__(256) void route_kernel(const RouteParams p) {
         next = d > next ? d : next;
       }
     next = row16_max(next);
-    best = best ? best + next : 0u;
+    best = best < kNoKey ? best : best + next;
   }
   // their exact keys
-  const int id = mine ? (int)(low - (mine & low)) : -1;
+  const int id = mine >= kNoKey ? (int)(low - (mine & low)) : -1;
   double s = 0.0, k = -__builtin_inf();
   if (id >= 0) {
     float v;
@@ -385,36 +419,47 @@ __global__ __launch_bounds__(256) void route_kernel(const RouteParams p) {
     else v = row[id];
     const double by = BIAS ? (double)p.bias[id] : 0.0;
     const double e = exp(p.sigmoid ? -(double)v : (double)v - (double)top);
-    s = p.sigmoid ? 1.0 / (1.0 + e) : e / (double)sum;
+    if (!p.sigmoid) s = e * reciprocal((double)sum);
+    else s = e < 0x1p1000 ? reciprocal(1.0 + e) : 1.0 / e;
     k = BIAS ? s + by : (double)v;
   }
-  const bool soft = BIAS && !p.sigmoid;
+  // Their exact order: mostly that of the cut keys.
   const int place = id >= 0 ? id : kRouteMaxExperts + l;  // (what is no candidate comes last, in order)
-  uint32_t last = 0;
-  int rank = 0;
-  each_lane<0>(n_cand, [&](auto ctrl) {
-    constexpr int C = decltype(ctrl)::value;
-    const double o = dpp<C>(k);
-    const int other = (int)dpp<C>((uint32_t)place);
-    rank += (int)(o > k) | ((int)(o == k) & (int)(other < place));
-    if (soft) {
-      // the softmax's sum is an f32 one: scores are off by up to 2^-19 of themselves
-      const double os = dpp<C>(s);
-      if (id >= 0 && other < kRouteMaxExperts && !(os == s && o == k) && __builtin_fabs(o - k) <= (os + s) * 0x1p-18) ok = false;
-    }
-    last = dpp<C>(mine);
-  });
+  int rank = l;
+  const bool inside = l + 1 < n_cand;
+  const double after = dpp<kRowShl1>(k);
+  const int place_after = (int)dpp<kRowShl1>((uint32_t)place);
+  const bool sorted = !inside || k > after || (k == after && place < place_after);
+  if (__ballot(!sorted)) {
+    rank = 0;
+    each_lane<0>(n_cand, [&](auto ctrl) {
+      constexpr int C = decltype(ctrl)::value;
+      const double o = dpp<C>(k);
+      const int other = (int)dpp<C>((uint32_t)place);
+      rank += (int)(o > k) | ((int)(o == k) & (int)(other < place));
+    });
+  }
+  if (BIAS && !p.sigmoid) {
+    // The softmax's sum is an f32 one, its scores are off by up to 2^-19 of
+    // themselves: neighbours (in cut order; tokens out of it are done again)
+    // have to differ by more.
+    const double s_after = dpp<kRowShl1>(s);
+    if (inside && place_after < kRouteMaxExperts && !(s == s_after && k == after) && !(k - after > (s + s_after) * 0x1p-18)) ok = false;
+  }
   // What was not taken is below the last candidate's cut key and a step of it.
-  if (!p.exact_cut && last) {
-    const float hi = from_ordered(last | low);
+  if (!p.exact_cut) {
+    const float hi = from_ordered(mine | low);
     const double err = BIAS ? ((double)__builtin_fabsf(hi) + 2.0) * 0x1p-18 : 0.0;
-    if (rank == p.topk - 1 && !(k > (double)hi + err)) ok = false;
+    // (the last candidate's lane asks for the worst of the chosen)
+    const double worst = -row16_max(rank < p.topk && id >= 0 ? -k : -__builtin_inf());
+    if (l == n_cand - 1 && id >= 0 && !(worst > (double)hi + err)) ok = false;
   }
   if (odd) ok = false;
   const bool chosen = rank < p.topk && id >= 0;
   if (p.renormalize) {
     const double all = row16_sum(chosen ? s : 0.0);
-    if (all != 0.0) s /= all;
+    if (all > 0x1p-1000) s *= reciprocal(all);
+    else if (all != 0.0) s /= all;
   }
   const uint64_t bad = __ballot(have && !ok);
   if (have && !((bad >> (lane & 48)) & 0xFFFF)) {
