@@ -468,9 +468,11 @@ __global__ __launch_bounds__(256, NB <= 4 ? 5 : 4) void route_kernel(const Route
       p.weights[t * p.topk + rank] = chosen ? (float)(s * p.scale) : 0.0f;
     }
   }
+  if (__builtin_expect(bad != 0, 0)) {  // (so that the loop's invariants are formed in here)
 #pragma unroll 1
-  for (int n = 0; n < 4; ++n)
-    if ((bad >> (16 * n)) & 0xFFFF) route_exactly(p, tw - (lane >> 4) + n, keys[wave]);
+    for (int n = 0; n < 4; ++n)
+      if ((bad >> (16 * n)) & 0xFFFF) route_exactly(p, tw - (lane >> 4) + n, keys[wave]);
+  }
 }
 
 // Whatever the kernel above does not take: one wave per token.
