@@ -57,64 +57,86 @@ __device__ __forceinline__ float row_sum(float v) {
 __device__ __forceinline__ void unpack8(const u32x4_t v, float (&f)[8]) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    f[2 * i] = bf16_bits_to_f32(v[i] & 0xFFFF);
-    f[2 * i + 1] = bf16_bits_to_f32(v[i] >> 16);
+    f[2 * i] = __uint_as_float(v[i] << 16);
+    f[2 * i + 1] = __uint_as_float(v[i] & 0xFFFF0000u);
+  }
+}
+// Eight floats of LDS (16-byte aligned).
+__device__ __forceinline__ void lds8(const float* at, float (&f)[8]) {
+  const f32x4_t a = *reinterpret_cast<const f32x4_t*>(at), b = *reinterpret_cast<const f32x4_t*>(at + 4);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f[i] = a[i];
+    f[4 + i] = b[i];
   }
 }
 
 // FAST: every piece of 8 elements lies at 16 bytes and turns as a whole, with
 // another whole piece (half layout: the half a multiple of 8 elements) or
-// within itself (interleaved: rotary_dim a multiple of 8).
+// within itself (interleaved: rotary_dim a multiple of 8), and the offsets in
+// a workgroup's tokens fit 32 bits.  In the half layout the two lanes of a
+// pair of pieces then load the same two, x0 and x1, and form one result each:
+//   y0 = x0 c + (-x1) s,   y1 = x0 s + x1 c,
+// the same products with the coefficients exchanged.
 template <int FMT, int D, bool HALF, bool FAST, bool NORM>
 __global__ __launch_bounds__(256) void append_kernel(const AppendParams p) {
   using U = KvUnit<FMT, D>;
+  using off_t = std::conditional_t<FAST, int32_t, int64_t>;
   constexpr int kLanes = D / 8;
   constexpr int kStep = 256 / kLanes;  // rows a workgroup moves at once
   constexpr int kB = 8 * U::kRow / D;
-  extern __shared__ float lds[];
+  extern __shared__ __attribute__((aligned(16))) float lds[];
   const int tid = threadIdx.x, lane = tid % kLanes;
   const int64_t t0 = (int64_t)blockIdx.x * p.tok_per_wg;
   const int nt = (int)(p.tokens - t0 < p.tok_per_wg ? p.tokens - t0 : p.tok_per_wg);
   float* cs = lds;
   float* sn = lds + p.tok_per_wg * p.half;
-  const int all = p.heads[0] + 2 * p.heads[1];
+  float* wt = lds + 2 * p.tok_per_wg * p.half;  // the norms' weights, q's and k's
+  const int hq = p.heads[0], hk = p.heads[1], all = hq + 2 * hk;
   const int r0 = (int)blockIdx.y * p.row_step;
   const int nr = all - r0 < p.row_step ? all - r0 : p.row_step;
   const float inv_nr = 1.0f / (float)nr;  // items below 2^17: (item + 1/2) inv_nr is never a whole step off
   const int items = nt * nr;
   const int page_size = 1 << p.page_shift;
 
-  u32x4_t own[kAppendRows], other[kAppendRows];
+  // a lane's place among the pieces of the turned part
+  const int m = p.half / 8;
+  const bool first = lane < m, turn = lane < (HALF ? 2 * m : p.half / 4);
+  const int at0 = FAST && HALF && turn ? (first ? lane : lane - m) * 8 : lane * 8;  // x0's piece, or its own
+  const uint32_t flip = first ? 0x80008000u : 0u;
+  const uint16_t* const base[3] = {p.x[0] + t0 * p.ts[0] + at0, p.x[1] + t0 * p.ts[1] + at0, p.x[2] + t0 * p.ts[2] + lane * 8};
+
+  u32x4_t x0[kAppendRows], x1[kAppendRows];
   int tok[kAppendRows], kind[kAppendRows], head[kAppendRows];
-  auto load = [&](int base) {
+  int64_t slot[kAppendRows];
+  auto load = [&](int from) {
 #pragma unroll
     for (int n = 0; n < kAppendRows; ++n) {
-      const int item = base + n * kStep + tid / kLanes;
-      own[n] = other[n] = u32x4_t{0, 0, 0, 0};
+      const int item = from + n * kStep + tid / kLanes;
       kind[n] = -1;
       if (item >= items) continue;
       tok[n] = (int)(((float)item + 0.5f) * inv_nr);
       const int row = r0 + item - tok[n] * nr;
-      kind[n] = row < p.heads[0] ? 0 : row < p.heads[0] + p.heads[1] ? 1 : 2;
-      head[n] = row - (kind[n] ? p.heads[0] : 0) - (kind[n] == 2 ? p.heads[1] : 0);
-      const uint16_t* x = (kind[n] == 0 ? p.x[0] : kind[n] == 1 ? p.x[1] : p.x[2]) +
-                          (t0 + tok[n]) * (kind[n] == 0 ? p.ts[0] : kind[n] == 1 ? p.ts[1] : p.ts[2]) +
-                          head[n] * (kind[n] == 0 ? p.hs[0] : kind[n] == 1 ? p.hs[1] : p.hs[2]);
+      kind[n] = (row >= hq) + (row >= hq + hk);
+      head[n] = row - (kind[n] ? hq : 0) - (kind[n] == 2 ? hk : 0);
+      const off_t ts = (off_t)(kind[n] == 0 ? p.ts[0] : kind[n] == 1 ? p.ts[1] : p.ts[2]);
+      const off_t hs = (off_t)(kind[n] == 0 ? p.hs[0] : kind[n] == 1 ? p.hs[1] : p.hs[2]);
+      const uint16_t* x = (kind[n] == 0 ? base[0] : kind[n] == 1 ? base[1] : base[2]) + (tok[n] * ts + head[n] * hs);
+      if (kind[n]) slot[n] = p.slots[t0 + tok[n]];
       if constexpr (FAST) {
-        own[n] = *reinterpret_cast<const u32x4_t*>(x + lane * 8);
-        if constexpr (HALF) {
-          const int m = p.half / 8;
-          if (kind[n] < 2 && lane < 2 * m) other[n] = *reinterpret_cast<const u32x4_t*>(x + (lane < m ? lane + m : lane - m) * 8);
-        }
+        x0[n] = *reinterpret_cast<const u32x4_t*>(x);
+        if (HALF && kind[n] < 2 && turn) x1[n] = *reinterpret_cast<const u32x4_t*>(x + p.half);
       } else {
+        // its own elements, and in the half layout the other one of each pair
 #pragma unroll
-        for (int i = 0; i < 4; ++i) own[n][i] = (uint32_t)x[lane * 8 + 2 * i] | ((uint32_t)x[lane * 8 + 2 * i + 1] << 16);
+        for (int i = 0; i < 4; ++i) x0[n][i] = (uint32_t)x[2 * i] | ((uint32_t)x[2 * i + 1] << 16);
+        x1[n] = u32x4_t{0, 0, 0, 0};
         if (HALF && kind[n] < 2) {
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             const int e = lane * 8 + i;
-            const uint32_t b = e < p.half ? x[e + p.half] : e < 2 * p.half ? x[e - p.half] : 0;
-            other[n][i / 2] |= b << (16 * (i & 1));
+            const uint32_t b = e < p.half ? x[i + p.half] : e < 2 * p.half ? x[i - p.half] : 0;
+            x1[n][i / 2] |= b << (16 * (i & 1));
           }
         }
       }
@@ -122,39 +144,73 @@ __global__ __launch_bounds__(256) void append_kernel(const AppendParams p) {
   };
   load(0);
 
+  if constexpr (NORM) {
+    for (int i = tid; i < 2 * D; i += 256) {
+      const void* w = i < D ? p.w[0] : p.w[1];
+      const int e = i < D ? i : i - D;
+      if (w) wt[i] = (p.w_f32 ? static_cast<const float*>(w)[e] : bf16_bits_to_f32(static_cast<const uint16_t*>(w)[e])) + p.offset;
+    }
+  }
   for (int i = tid; i < nt * p.half; i += 256) {
     const int t = i / p.half;
     rotary_coefficients(p.positions[t0 + t], p.inv_freq[i - t * p.half], p.factor, 1.0f, cs + i, sn + i);
   }
   __syncthreads();
 
-  for (int base = 0; base < items; base += kAppendRows * kStep) {
-    if (base) load(base);
+  for (int from = 0; from < items; from += kAppendRows * kStep) {
+    if (from) load(from);
 #pragma unroll
     for (int n = 0; n < kAppendRows; ++n) {
       if (kind[n] < 0) continue;
-      float f[8], g[8];
-      unpack8(own[n], f);
-      unpack8(other[n], g);
+      float f[8];
+      unpack8(x0[n], f);
       if (kind[n] < 2) {
-        const void* w = kind[n] ? p.w[1] : p.w[0];
-        if (NORM && w) {
+        float g[8];
+        if constexpr (HALF && FAST) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) x1[n][i] ^= flip;
+        }
+        if constexpr (HALF) unpack8(x1[n], g);
+        const float* w = wt + (kind[n] ? D : 0);
+        if (NORM && p.w[kind[n]]) {
           float sum = 0.0f;
+          if (FAST && HALF && turn && !first) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) sum = __builtin_fmaf(f[i], f[i], sum);
+            for (int i = 0; i < 8; ++i) sum = __builtin_fmaf(g[i], g[i], sum);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) sum = __builtin_fmaf(f[i], f[i], sum);
+          }
           const float r = 1.0f / __builtin_sqrtf(row_sum<kLanes>(sum) * (1.0f / D) + p.eps);
-          auto weight = [&](int e) {
-            return (p.w_f32 ? static_cast<const float*>(w)[e] : bf16_bits_to_f32(static_cast<const uint16_t*>(w)[e])) + p.offset;
-          };
+          if constexpr (FAST) {
+            float v[8];
+            lds8(w + at0, v);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int e = lane * 8 + i;
-            f[i] = f[i] * r * weight(e);
-            if (HALF && e < 2 * p.half) g[i] = g[i] * r * weight(e < p.half ? e + p.half : e - p.half);
+            for (int i = 0; i < 8; ++i) f[i] = f[i] * r * v[i];
+            if (HALF && turn) {
+              lds8(w + at0 + p.half, v);
+#pragma unroll
+              for (int i = 0; i < 8; ++i) g[i] = g[i] * r * v[i];
+            }
+          } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const int e = lane * 8 + i;
+              f[i] = f[i] * r * w[e];
+              if (HALF && e < 2 * p.half) g[i] = g[i] * r * w[e < p.half ? e + p.half : e - p.half];
+            }
           }
         }
         const float *c = cs + tok[n] * p.half, *s = sn + tok[n] * p.half;
-        if constexpr (HALF) {
+        if constexpr (FAST && HALF) {
+          if (turn) {
+            float ca[8], cb[8];
+            lds8((first ? c : s) + at0, ca);
+            lds8((first ? s : c) + at0, cb);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) f[i] = __builtin_fmaf(f[i], ca[i], g[i] * cb[i]);
+          }
+        } else if constexpr (HALF) {
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             const int e = lane * 8 + i;
@@ -165,7 +221,7 @@ __global__ __launch_bounds__(256) void append_kernel(const AppendParams p) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const int pr = lane * 4 + i;
-            if (pr < p.half) {
+            if (FAST ? turn : pr < p.half) {
               const float a = f[2 * i], b = f[2 * i + 1];
               f[2 * i] = rotary_first(a, b, c[pr], s[pr]);
               f[2 * i + 1] = rotary_second(a, b, c[pr], s[pr]);
@@ -187,11 +243,10 @@ __global__ __launch_bounds__(256) void append_kernel(const AppendParams p) {
         continue;
       }
       const int which = kind[n] - 1;
-      const int64_t slot = p.slots[t0 + tok[n]];
       // (unsigned: negative slots are past the end too)
-      const bool live = (uint64_t)slot < (uint64_t)p.slots_all;
-      const uint32_t page = (uint32_t)(slot >> p.page_shift);
-      const int at = (int)(slot & (page_size - 1));
+      const bool live = (uint64_t)slot[n] < (uint64_t)p.slots_all;
+      const uint32_t page = (uint32_t)(slot[n] >> p.page_shift);
+      const int at = (int)(slot[n] & (page_size - 1));
       const KvOffsets<FMT, D> off(which, at, page_size);
       uint8_t* unit = p.cache + (uint64_t)head[n] * p.unit + (uint64_t)page * p.page_stride;
       if (which) kv_store_row<FMT, D, false>(f, lane, unit + off.code + lane * kB, unit + off.scale, off.scale_step, live);
@@ -309,7 +364,9 @@ extern "C" hum_status hum_rotary_kv_write(const hum_rotary_desc* rot, const hum_
     p.offset = norm->weight_offset;
   }
   const bool half = rot->layout == HUM_ROPE_HALF;
-  const bool fast = any % 8 == 0 && p.half % (half ? 8 : 4) == 0;
+  // (strides that pass 32 bits over a workgroup's at most 8 tokens and 4096 heads, q_out's apart, leave the fast path)
+  auto small = [&](int64_t ts, int64_t hs) { return ts < 1 << 26 && ts > -(1 << 26) && hs < 1 << 18 && hs > -(1 << 18); };
+  const bool fast = any % 8 == 0 && p.half % (half ? 8 : 4) == 0 && (!hq || small(q_ts, q_hs)) && small(k_ts, k_hs) && small(v_ts, v_hs);
   // Tokens per workgroup: as many as give 256 threads a coefficient each, as
   // long as that leaves a thousand workgroups; rows are sliced over grid.y
   // where the tokens alone would leave compute units without one.
@@ -327,10 +384,10 @@ extern "C" hum_status hum_rotary_kv_write(const hum_rotary_desc* rot, const hum_
   }
   p.row_step = (int)((all + gy - 1) / gy);
   gy = (all + p.row_step - 1) / p.row_step;
-  const size_t lds = (size_t)tok * p.half * 2 * sizeof(float);
+  const bool normed = p.w[0] || p.w[1];
+  const size_t lds = ((size_t)tok * p.half * 2 + (normed ? 2 * d : 0)) * sizeof(float);
   const dim3 grid((unsigned)gx, (unsigned)gy);
   hipStream_t s = static_cast<hipStream_t>(stream);
-  const bool normed = p.w[0] || p.w[1];
   kv_dispatch(kv, [&](auto fmt, auto dim) {
     constexpr int F = decltype(fmt)::value, D = decltype(dim)::value;
     auto by = [&](auto h, auto f) {
