@@ -38,7 +38,8 @@ struct AppendParams {
   float factor, eps, offset;
 };
 
-constexpr int kAppendRows = 4;  // rows that a thread has in flight at once
+constexpr int kAppendRows = 4;    // rows that a thread has in flight at once
+constexpr int kAppendTokens = 8;  // tokens of a workgroup, at most
 
 // Sum over the N lanes (8, 16 or 32) that hold one row.
 template <int N>
@@ -75,9 +76,11 @@ __device__ __forceinline__ void lds8(const float* at, float (&f)[8]) {
 // another whole piece (half layout: the half a multiple of 8 elements) or
 // within itself (interleaved: rotary_dim a multiple of 8), and the offsets in
 // a workgroup's tokens fit 32 bits.  In the half layout the two lanes of a
-// pair of pieces then load the same two, x0 and x1, and form one result each:
+// pair of pieces exchange them and form one result each:
 //   y0 = x0 c + (-x1) s,   y1 = x0 s + x1 c,
-// the same products with the coefficients exchanged.
+// the same products with the coefficients exchanged.  (Loading both pieces in
+// both lanes instead stalls the vector cache on the line that is on its way:
+// 117 us.)
 template <int FMT, int D, bool HALF, bool FAST, bool NORM>
 __global__ __launch_bounds__(256) void append_kernel(const AppendParams p) {
   using U = KvUnit<FMT, D>;
@@ -86,6 +89,7 @@ __global__ __launch_bounds__(256) void append_kernel(const AppendParams p) {
   constexpr int kStep = 256 / kLanes;  // rows a workgroup moves at once
   constexpr int kB = 8 * U::kRow / D;
   extern __shared__ __attribute__((aligned(16))) float lds[];
+  __shared__ int64_t slots[kAppendTokens];
   const int tid = threadIdx.x, lane = tid % kLanes;
   const int64_t t0 = (int64_t)blockIdx.x * p.tok_per_wg;
   const int nt = (int)(p.tokens - t0 < p.tok_per_wg ? p.tokens - t0 : p.tok_per_wg);
@@ -102,13 +106,13 @@ __global__ __launch_bounds__(256) void append_kernel(const AppendParams p) {
   // a lane's place among the pieces of the turned part
   const int m = p.half / 8;
   const bool first = lane < m, turn = lane < (HALF ? 2 * m : p.half / 4);
-  const int at0 = FAST && HALF && turn ? (first ? lane : lane - m) * 8 : lane * 8;  // x0's piece, or its own
+  const int at0 = HALF && turn ? (first ? lane : lane - m) * 8 : lane * 8;  // where the turn's x0 lies
+  const int partner = ((tid & 63) + (HALF && turn ? (first ? m : -m) : 0)) * 4;
   const uint32_t flip = first ? 0x80008000u : 0u;
-  const uint16_t* const base[3] = {p.x[0] + t0 * p.ts[0] + at0, p.x[1] + t0 * p.ts[1] + at0, p.x[2] + t0 * p.ts[2] + lane * 8};
+  const uint16_t* const base[3] = {p.x[0] + t0 * p.ts[0] + lane * 8, p.x[1] + t0 * p.ts[1] + lane * 8, p.x[2] + t0 * p.ts[2] + lane * 8};
 
   u32x4_t x0[kAppendRows], x1[kAppendRows];
   int tok[kAppendRows], kind[kAppendRows], head[kAppendRows];
-  int64_t slot[kAppendRows];
   auto load = [&](int from) {
 #pragma unroll
     for (int n = 0; n < kAppendRows; ++n) {
@@ -122,10 +126,8 @@ __global__ __launch_bounds__(256) void append_kernel(const AppendParams p) {
       const off_t ts = (off_t)(kind[n] == 0 ? p.ts[0] : kind[n] == 1 ? p.ts[1] : p.ts[2]);
       const off_t hs = (off_t)(kind[n] == 0 ? p.hs[0] : kind[n] == 1 ? p.hs[1] : p.hs[2]);
       const uint16_t* x = (kind[n] == 0 ? base[0] : kind[n] == 1 ? base[1] : base[2]) + (tok[n] * ts + head[n] * hs);
-      if (kind[n]) slot[n] = p.slots[t0 + tok[n]];
       if constexpr (FAST) {
         x0[n] = *reinterpret_cast<const u32x4_t*>(x);
-        if (HALF && kind[n] < 2 && turn) x1[n] = *reinterpret_cast<const u32x4_t*>(x + p.half);
       } else {
         // its own elements, and in the half layout the other one of each pair
 #pragma unroll
@@ -144,6 +146,7 @@ __global__ __launch_bounds__(256) void append_kernel(const AppendParams p) {
   };
   load(0);
 
+  if (tid < nt) slots[tid] = p.slots[t0 + tid];
   if constexpr (NORM) {
     for (int i = tid; i < 2 * D; i += 256) {
       const void* w = i < D ? p.w[0] : p.w[1];
@@ -163,24 +166,26 @@ __global__ __launch_bounds__(256) void append_kernel(const AppendParams p) {
     for (int n = 0; n < kAppendRows; ++n) {
       if (kind[n] < 0) continue;
       float f[8];
-      unpack8(x0[n], f);
       if (kind[n] < 2) {
         float g[8];
+        float sum = 0.0f;  // of the squares of its own elements
+        if constexpr (NORM) {
+          unpack8(x0[n], f);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) sum = __builtin_fmaf(f[i], f[i], sum);
+        }
         if constexpr (HALF && FAST) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) x1[n][i] ^= flip;
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t o = (uint32_t)__builtin_amdgcn_ds_bpermute(partner, (int)x0[n][i]), me = x0[n][i];
+            x0[n][i] = first || !turn ? me : o;
+            x1[n][i] = (first ? o : me) ^ flip;
+          }
         }
+        unpack8(x0[n], f);
         if constexpr (HALF) unpack8(x1[n], g);
         const float* w = wt + (kind[n] ? D : 0);
         if (NORM && p.w[kind[n]]) {
-          float sum = 0.0f;
-          if (FAST && HALF && turn && !first) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) sum = __builtin_fmaf(g[i], g[i], sum);
-          } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) sum = __builtin_fmaf(f[i], f[i], sum);
-          }
           const float r = 1.0f / __builtin_sqrtf(row_sum<kLanes>(sum) * (1.0f / D) + p.eps);
           if constexpr (FAST) {
             float v[8];
@@ -242,11 +247,13 @@ __global__ __launch_bounds__(256) void append_kernel(const AppendParams p) {
         }
         continue;
       }
+      if (kind[n] == 2) unpack8(x0[n], f);
       const int which = kind[n] - 1;
+      const int64_t slot = slots[tok[n]];
       // (unsigned: negative slots are past the end too)
-      const bool live = (uint64_t)slot[n] < (uint64_t)p.slots_all;
-      const uint32_t page = (uint32_t)(slot[n] >> p.page_shift);
-      const int at = (int)(slot[n] & (page_size - 1));
+      const bool live = (uint64_t)slot < (uint64_t)p.slots_all;
+      const uint32_t page = (uint32_t)(slot >> p.page_shift);
+      const int at = (int)(slot & (page_size - 1));
       const KvOffsets<FMT, D> off(which, at, page_size);
       uint8_t* unit = p.cache + (uint64_t)head[n] * p.unit + (uint64_t)page * p.page_stride;
       if (which) kv_store_row<FMT, D, false>(f, lane, unit + off.code + lane * kB, unit + off.scale, off.scale_step, live);
@@ -371,7 +378,7 @@ extern "C" hum_status hum_rotary_kv_write(const hum_rotary_desc* rot, const hum_
   // long as that leaves a thousand workgroups; rows are sliced over grid.y
   // where the tokens alone would leave compute units without one.
   int64_t tok = 256 / p.half;
-  tok = tok < 1 ? 1 : tok > 8 ? 8 : tok;
+  tok = tok < 1 ? 1 : tok > kAppendTokens ? kAppendTokens : tok;
   while (tok > 1 && (num_tokens + tok - 1) / tok < 1024) tok /= 2;
   const int all = hq + 2 * hk, at_once = 256 / (d / 8);
   p.tok_per_wg = (int)tok;
