@@ -32,14 +32,10 @@ struct AppendParams {
   const void* w[2];  // head norms of q, of k
   int64_t tokens;
   int32_t half;        // rotary_dim / 2
-  int32_t tok_per_wg;
-  int32_t row_step;    // rows (q's heads, k's, v's) per workgroup (grid.y slices them)
+  int32_t row_step;    // rows (q's heads, k's, v's) per wave (grid.y slices them)
   int32_t w_f32;
   float factor, eps, offset;
 };
-
-constexpr int kAppendRows = 4;    // rows that a thread has in flight at once
-constexpr int kAppendTokens = 8;  // tokens of a workgroup, at most
 
 // Sum over the N lanes (8, 16 or 32) that hold one row.
 template <int N>
@@ -75,125 +71,129 @@ __device__ __forceinline__ void lds8(const float* at, float (&f)[8]) {
 // FAST: every piece of 8 elements lies at 16 bytes and turns as a whole, with
 // another whole piece (half layout: the half a multiple of 8 elements) or
 // within itself (interleaved: rotary_dim a multiple of 8), and the offsets in
-// a workgroup's tokens fit 32 bits.  In the half layout the two lanes of a
+// a token fit 32 bits.  In the half layout the two lanes of a
 // pair of pieces exchange them and form one result each:
 //   y0 = x0 c + (-x1) s,   y1 = x0 s + x1 c,
 // the same products with the coefficients exchanged.  (Loading both pieces in
 // both lanes instead stalls the vector cache on the line that is on its way:
-// 117 us.)
+// 16384 tokens of 32 + 8 heads of 128 in MXFP8 117 us, with the exchange 107.)
+//
+// A wave has one token (its slot and addresses are scalars) or a slice of its
+// rows, 64 / (D / 8) of them at once; the coefficients lie in its own part of
+// LDS, so the waves of a workgroup do not wait for one another.
 template <int FMT, int D, bool HALF, bool FAST, bool NORM>
 __global__ __launch_bounds__(256) void append_kernel(const AppendParams p) {
   using U = KvUnit<FMT, D>;
   using off_t = std::conditional_t<FAST, int32_t, int64_t>;
   constexpr int kLanes = D / 8;
-  constexpr int kStep = 256 / kLanes;  // rows a workgroup moves at once
+  constexpr int kStep = 64 / kLanes;  // rows a wave moves at once
   constexpr int kB = 8 * U::kRow / D;
   extern __shared__ __attribute__((aligned(16))) float lds[];
-  __shared__ int64_t slots[kAppendTokens];
-  const int tid = threadIdx.x, lane = tid % kLanes;
-  const int64_t t0 = (int64_t)blockIdx.x * p.tok_per_wg;
-  const int nt = (int)(p.tokens - t0 < p.tok_per_wg ? p.tokens - t0 : p.tok_per_wg);
-  float* cs = lds;
-  float* sn = lds + p.tok_per_wg * p.half;
-  float* wt = lds + 2 * p.tok_per_wg * p.half;  // the norms' weights, q's and k's
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), sub = threadIdx.x & 63, lane = sub % kLanes;
+  const int64_t t = (int64_t)blockIdx.x * 4 + wave;
+  const bool have = t < p.tokens;
+  float* cs = lds + wave * 2 * p.half;
+  float* sn = cs + p.half;
+  float* wt = lds + 8 * p.half;  // the norms' weights, q's and k's
   const int hq = p.heads[0], hk = p.heads[1], all = hq + 2 * hk;
-  const int r0 = (int)blockIdx.y * p.row_step;
-  const int nr = all - r0 < p.row_step ? all - r0 : p.row_step;
-  const float inv_nr = 1.0f / (float)nr;  // items below 2^17: (item + 1/2) inv_nr is never a whole step off
-  const int items = nt * nr;
-  const int page_size = 1 << p.page_shift;
+  const int end = ((int)blockIdx.y + 1) * p.row_step < all ? ((int)blockIdx.y + 1) * p.row_step : all;
+  int row = (int)blockIdx.y * p.row_step + sub / kLanes;
+
+  const off_t hs_q = (off_t)p.hs[0], hs_k = (off_t)p.hs[1], hs_v = (off_t)p.hs[2], qo_hs = (off_t)p.qo_hs;
+  const bool norm_q = NORM && p.w[0], norm_k = NORM && p.w[1];
+  const uint32_t unit_bytes = p.unit;
+  const int half = p.half;
+  const float eps = p.eps;
 
   // a lane's place among the pieces of the turned part
   const int m = p.half / 8;
   const bool first = lane < m, turn = lane < (HALF ? 2 * m : p.half / 4);
   const int at0 = HALF && turn ? (first ? lane : lane - m) * 8 : lane * 8;  // where the turn's x0 lies
-  const int partner = ((tid & 63) + (HALF && turn ? (first ? m : -m) : 0)) * 4;
+  const int partner = (sub + (HALF && turn ? (first ? m : -m) : 0)) * 4;
   const uint32_t flip = first ? 0x80008000u : 0u;
-  const uint16_t* const base[3] = {p.x[0] + t0 * p.ts[0] + lane * 8, p.x[1] + t0 * p.ts[1] + lane * 8, p.x[2] + t0 * p.ts[2] + lane * 8};
 
-  u32x4_t x0[kAppendRows], x1[kAppendRows];
-  int tok[kAppendRows], kind[kAppendRows], head[kAppendRows];
-  auto load = [&](int from) {
-#pragma unroll
-    for (int n = 0; n < kAppendRows; ++n) {
-      const int item = from + n * kStep + tid / kLanes;
-      kind[n] = -1;
-      if (item >= items) continue;
-      tok[n] = (int)(((float)item + 0.5f) * inv_nr);
-      const int row = r0 + item - tok[n] * nr;
-      kind[n] = (row >= hq) + (row >= hq + hk);
-      head[n] = row - (kind[n] ? hq : 0) - (kind[n] == 2 ? hk : 0);
-      const off_t ts = (off_t)(kind[n] == 0 ? p.ts[0] : kind[n] == 1 ? p.ts[1] : p.ts[2]);
-      const off_t hs = (off_t)(kind[n] == 0 ? p.hs[0] : kind[n] == 1 ? p.hs[1] : p.hs[2]);
-      const uint16_t* x = (kind[n] == 0 ? base[0] : kind[n] == 1 ? base[1] : base[2]) + (tok[n] * ts + head[n] * hs);
-      if constexpr (FAST) {
-        x0[n] = *reinterpret_cast<const u32x4_t*>(x);
-      } else {
-        // its own elements, and in the half layout the other one of each pair
-#pragma unroll
-        for (int i = 0; i < 4; ++i) x0[n][i] = (uint32_t)x[2 * i] | ((uint32_t)x[2 * i + 1] << 16);
-        x1[n] = u32x4_t{0, 0, 0, 0};
-        if (HALF && kind[n] < 2) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int e = lane * 8 + i;
-            const uint32_t b = e < p.half ? x[i + p.half] : e < 2 * p.half ? x[i - p.half] : 0;
-            x1[n][i / 2] |= b << (16 * (i & 1));
-          }
-        }
-      }
-    }
-  };
-  load(0);
+  const uint16_t *const xq = p.x[0] + t * p.ts[0], *const xk = p.x[1] + t * p.ts[1], *const xv = p.x[2] + t * p.ts[2];
 
-  if (tid < nt) slots[tid] = p.slots[t0 + tid];
   if constexpr (NORM) {
-    for (int i = tid; i < 2 * D; i += 256) {
+    for (int i = threadIdx.x; i < 2 * D; i += 256) {
       const void* w = i < D ? p.w[0] : p.w[1];
       const int e = i < D ? i : i - D;
       if (w) wt[i] = (p.w_f32 ? static_cast<const float*>(w)[e] : bf16_bits_to_f32(static_cast<const uint16_t*>(w)[e])) + p.offset;
     }
+    __syncthreads();
   }
-  for (int i = tid; i < nt * p.half; i += 256) {
-    const int t = i / p.half;
-    rotary_coefficients(p.positions[t0 + t], p.inv_freq[i - t * p.half], p.factor, 1.0f, cs + i, sn + i);
-  }
-  __syncthreads();
+  if (!have) return;
+  const int64_t slot = p.slots[t], position = p.positions[t];
+  for (int i = sub; i < half; i += 64) rotary_coefficients(position, p.inv_freq[i], p.factor, 1.0f, cs + i, sn + i);
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  // (unsigned: negative slots are past the end too)
+  const bool live = (uint64_t)slot < (uint64_t)p.slots_all;
+  const int page_size = 1 << p.page_shift, at = (int)(slot & (page_size - 1));
+  const KvOffsets<FMT, D> off_k(0, at, page_size), off_v(1, at, page_size);
+  uint8_t* const page = p.cache + (uint64_t)(uint32_t)(slot >> p.page_shift) * p.page_stride;
+  uint16_t* const yq = p.q_out + t * p.qo_ts + lane * 8;
 
-  for (int from = 0; from < items; from += kAppendRows * kStep) {
-    if (from) load(from);
+  // One row is loaded while the one before it is worked on.
+  u32x4_t x0_next, x1_next;
+  int kind_next = -1, head_next = 0;
+  const int steps = (end - (int)blockIdx.y * p.row_step + kStep - 1) / kStep;
+  for (int n = -1; n < steps; ++n) {
+    u32x4_t x0 = x0_next, x1 = x1_next;
+    const int kind = kind_next, head = head_next;
+    kind_next = -1;
+    if (row < end) {
+      kind_next = (row >= hq) + (row >= hq + hk);
+      head_next = row - (kind_next ? hq : 0) - (kind_next == 2 ? hk : 0);
+      const uint16_t* x = (kind_next == 0 ? xq : kind_next == 1 ? xk : xv) + head_next * (kind_next == 0 ? hs_q : kind_next == 1 ? hs_k : hs_v) + lane * 8;
+      if constexpr (FAST) {
+        x0_next = *reinterpret_cast<const u32x4_t*>(x);
+      } else {
+        // its own elements, and in the half layout the other one of each pair
 #pragma unroll
-    for (int n = 0; n < kAppendRows; ++n) {
-      if (kind[n] < 0) continue;
+        for (int i = 0; i < 4; ++i) x0_next[i] = (uint32_t)x[2 * i] | ((uint32_t)x[2 * i + 1] << 16);
+        x1_next = u32x4_t{0, 0, 0, 0};
+        if (HALF && kind_next < 2) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const int e = lane * 8 + i;
+            const uint32_t b = e < half ? x[i + half] : e < 2 * half ? x[i - half] : 0;
+            x1_next[i / 2] |= b << (16 * (i & 1));
+          }
+        }
+      }
+    }
+    row += kStep;
+    if (kind >= 0) {
       float f[8];
-      if (kind[n] < 2) {
+      if (kind < 2) {
         float g[8];
         float sum = 0.0f;  // of the squares of its own elements
         if constexpr (NORM) {
-          unpack8(x0[n], f);
+          unpack8(x0, f);
 #pragma unroll
           for (int i = 0; i < 8; ++i) sum = __builtin_fmaf(f[i], f[i], sum);
         }
         if constexpr (HALF && FAST) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const uint32_t o = (uint32_t)__builtin_amdgcn_ds_bpermute(partner, (int)x0[n][i]), me = x0[n][i];
-            x0[n][i] = first || !turn ? me : o;
-            x1[n][i] = (first ? o : me) ^ flip;
+            const uint32_t o = (uint32_t)__builtin_amdgcn_ds_bpermute(partner, (int)x0[i]), me = x0[i];
+            x0[i] = first || !turn ? me : o;
+            x1[i] = (first ? o : me) ^ flip;
           }
         }
-        unpack8(x0[n], f);
-        if constexpr (HALF) unpack8(x1[n], g);
-        const float* w = wt + (kind[n] ? D : 0);
-        if (NORM && p.w[kind[n]]) {
-          const float r = 1.0f / __builtin_sqrtf(row_sum<kLanes>(sum) * (1.0f / D) + p.eps);
+        unpack8(x0, f);
+        if constexpr (HALF) unpack8(x1, g);
+        if (NORM && (kind ? norm_k : norm_q)) {
+          const float* w = wt + (kind ? D : 0);
+          const float r = 1.0f / __builtin_sqrtf(row_sum<kLanes>(sum) * (1.0f / D) + eps);
           if constexpr (FAST) {
             float v[8];
             lds8(w + at0, v);
 #pragma unroll
             for (int i = 0; i < 8; ++i) f[i] = f[i] * r * v[i];
             if (HALF && turn) {
-              lds8(w + at0 + p.half, v);
+              lds8(w + at0 + half, v);
 #pragma unroll
               for (int i = 0; i < 8; ++i) g[i] = g[i] * r * v[i];
             }
@@ -202,16 +202,15 @@ __global__ __launch_bounds__(256) void append_kernel(const AppendParams p) {
             for (int i = 0; i < 8; ++i) {
               const int e = lane * 8 + i;
               f[i] = f[i] * r * w[e];
-              if (HALF && e < 2 * p.half) g[i] = g[i] * r * w[e < p.half ? e + p.half : e - p.half];
+              if (HALF && e < 2 * half) g[i] = g[i] * r * w[e < half ? e + half : e - half];
             }
           }
         }
-        const float *c = cs + tok[n] * p.half, *s = sn + tok[n] * p.half;
         if constexpr (FAST && HALF) {
           if (turn) {
             float ca[8], cb[8];
-            lds8((first ? c : s) + at0, ca);
-            lds8((first ? s : c) + at0, cb);
+            lds8(cs + (at0 + (first ? 0 : half)), ca);
+            lds8(cs + (at0 + (first ? half : 0)), cb);
 #pragma unroll
             for (int i = 0; i < 8; ++i) f[i] = __builtin_fmaf(f[i], ca[i], g[i] * cb[i]);
           }
@@ -219,23 +218,25 @@ __global__ __launch_bounds__(256) void append_kernel(const AppendParams p) {
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             const int e = lane * 8 + i;
-            if (e < p.half) f[i] = rotary_first(f[i], g[i], c[e], s[e]);
-            else if (e < 2 * p.half) f[i] = rotary_second(g[i], f[i], c[e - p.half], s[e - p.half]);
+            if (e < half) f[i] = rotary_first(f[i], g[i], cs[e], sn[e]);
+            else if (e < 2 * half) f[i] = rotary_second(g[i], f[i], cs[e - half], sn[e - half]);
           }
         } else {
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const int pr = lane * 4 + i;
-            if (FAST ? turn : pr < p.half) {
+            if (FAST ? turn : pr < half) {
               const float a = f[2 * i], b = f[2 * i + 1];
-              f[2 * i] = rotary_first(a, b, c[pr], s[pr]);
-              f[2 * i + 1] = rotary_second(a, b, c[pr], s[pr]);
+              f[2 * i] = rotary_first(a, b, cs[pr], sn[pr]);
+              f[2 * i + 1] = rotary_second(a, b, cs[pr], sn[pr]);
             }
           }
         }
+      } else {
+        unpack8(x0, f);
       }
-      if (kind[n] == 0) {
-        uint16_t* y = p.q_out + (t0 + tok[n]) * p.qo_ts + head[n] * p.qo_hs + lane * 8;
+      if (kind == 0) {
+        uint16_t* y = yq + head * qo_hs;
         if constexpr (FAST) {
           u32x4_t o;
 #pragma unroll
@@ -245,19 +246,11 @@ __global__ __launch_bounds__(256) void append_kernel(const AppendParams p) {
 #pragma unroll
           for (int i = 0; i < 8; ++i) y[i] = (uint16_t)f32_to_bf16_bits(f[i]);
         }
-        continue;
+      } else {
+        uint8_t* unit = page + (uint32_t)head * unit_bytes;
+        if (kind == 2) kv_store_row<FMT, D, false>(f, lane, unit + off_v.code + lane * kB, unit + off_v.scale, off_v.scale_step, live);
+        else kv_store_row<FMT, D, true>(f, lane, unit + off_k.code + lane * kB, unit + off_k.scale, off_k.scale_step, live);
       }
-      if (kind[n] == 2) unpack8(x0[n], f);
-      const int which = kind[n] - 1;
-      const int64_t slot = slots[tok[n]];
-      // (unsigned: negative slots are past the end too)
-      const bool live = (uint64_t)slot < (uint64_t)p.slots_all;
-      const uint32_t page = (uint32_t)(slot >> p.page_shift);
-      const int at = (int)(slot & (page_size - 1));
-      const KvOffsets<FMT, D> off(which, at, page_size);
-      uint8_t* unit = p.cache + (uint64_t)head[n] * p.unit + (uint64_t)page * p.page_stride;
-      if (which) kv_store_row<FMT, D, false>(f, lane, unit + off.code + lane * kB, unit + off.scale, off.scale_step, live);
-      else kv_store_row<FMT, D, true>(f, lane, unit + off.code + lane * kB, unit + off.scale, off.scale_step, live);
     }
   }
 }
@@ -371,18 +364,13 @@ extern "C" hum_status hum_rotary_kv_write(const hum_rotary_desc* rot, const hum_
     p.offset = norm->weight_offset;
   }
   const bool half = rot->layout == HUM_ROPE_HALF;
-  // (strides that pass 32 bits over a workgroup's at most 8 tokens and 4096 heads, q_out's apart, leave the fast path)
-  auto small = [&](int64_t ts, int64_t hs) { return ts < 1 << 26 && ts > -(1 << 26) && hs < 1 << 18 && hs > -(1 << 18); };
-  const bool fast = any % 8 == 0 && p.half % (half ? 8 : 4) == 0 && (!hq || small(q_ts, q_hs)) && small(k_ts, k_hs) && small(v_ts, v_hs);
-  // Tokens per workgroup: as many as give 256 threads a coefficient each, as
-  // long as that leaves a thousand workgroups; rows are sliced over grid.y
-  // where the tokens alone would leave compute units without one.
-  int64_t tok = 256 / p.half;
-  tok = tok < 1 ? 1 : tok > kAppendTokens ? kAppendTokens : tok;
-  while (tok > 1 && (num_tokens + tok - 1) / tok < 1024) tok /= 2;
-  const int all = hq + 2 * hk, at_once = 256 / (d / 8);
-  p.tok_per_wg = (int)tok;
-  const int64_t gx = (num_tokens + tok - 1) / tok;
+  // (heads that lie further apart than 2^18 elements leave the fast path, whose offsets are of 32 bits)
+  auto near = [](int64_t hs) { return hs < 1 << 18 && hs > -(1 << 18); };
+  const bool fast = any % 8 == 0 && p.half % (half ? 8 : 4) == 0 && (!hq || (near(q_hs) && near(qo_hs))) && near(k_hs) && near(v_hs);
+  // A token to a wave, four to a workgroup; rows are sliced over grid.y where
+  // the tokens alone would leave compute units without a workgroup.
+  const int all = hq + 2 * hk, at_once = 64 / (d / 8);
+  const int64_t gx = (num_tokens + 3) / 4;
   int64_t gy = 1;
   if (gx < 512) {
     gy = (512 + gx - 1) / gx;
@@ -390,9 +378,10 @@ extern "C" hum_status hum_rotary_kv_write(const hum_rotary_desc* rot, const hum_
     if (gy > most) gy = most;
   }
   p.row_step = (int)((all + gy - 1) / gy);
+  p.row_step = (p.row_step + at_once - 1) / at_once * at_once;
   gy = (all + p.row_step - 1) / p.row_step;
   const bool normed = p.w[0] || p.w[1];
-  const size_t lds = ((size_t)tok * p.half * 2 + (normed ? 2 * d : 0)) * sizeof(float);
+  const size_t lds = ((size_t)p.half * 8 + (normed ? 2 * d : 0)) * sizeof(float);
   const dim3 grid((unsigned)gx, (unsigned)gy);
   hipStream_t s = static_cast<hipStream_t>(stream);
   kv_dispatch(kv, [&](auto fmt, auto dim) {
