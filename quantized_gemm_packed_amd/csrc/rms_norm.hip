@@ -27,7 +27,6 @@ struct NormParams {
   void* scales;
   int64_t m, ld_x, ld_res, ld_res_out, ld_out;
   int32_t k;
-  int32_t vec;     // elements per access where not all are 16 bytes: 4, 2 or 1
   int32_t w_f32;
   float inv_k, eps, offset;
 };
@@ -35,101 +34,76 @@ struct NormParams {
 // What a row's residual is.
 enum { kNoRes = 0, kResBf16 = 1, kResF32 = 2 };
 
+// Eight elements of a row as they lie in memory: 16 bytes of bf16, 32 of f32.
 template <typename T>
-__device__ __forceinline__ float norm_ld(T v) {
-  if constexpr (sizeof(T) == 2) return bf16_bits_to_f32(v);
-  else return v;
-}
-
-// Eight elements at `at` of a row -> f32 (zeros past k).
-template <typename T, bool FAST>
-__device__ __forceinline__ void load8(const T* row, int at, int k, int vec, float (&f)[8]) {
-  if constexpr (FAST) {
-    if (at < k) {
-      if constexpr (sizeof(T) == 2) {
-        const u32x4_t v = *reinterpret_cast<const u32x4_t*>(row + at);
+struct Raw {
+  static constexpr int kWords = sizeof(T) * 2;
+  uint32_t w[kWords];
+  __device__ __forceinline__ void unpack(float (&f)[8]) const {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          f[2 * i] = bf16_bits_to_f32(v[i] & 0xFFFF);
-          f[2 * i + 1] = bf16_bits_to_f32(v[i] >> 16);
-        }
-      } else {
-        const f32x4_t a = *reinterpret_cast<const f32x4_t*>(row + at), b = *reinterpret_cast<const f32x4_t*>(row + at + 4);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          f[i] = a[i];
-          f[4 + i] = b[i];
-        }
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) f[i] = 0.0f;
+    for (int i = 0; i < 8; ++i) {
+      if constexpr (sizeof(T) == 2) f[i] = __uint_as_float(i & 1 ? w[i / 2] & 0xFFFF0000u : w[i / 2] << 16);
+      else f[i] = __uint_as_float(w[i]);
     }
-  } else {
-    auto pieces = [&](auto n) {
-      constexpr int N = decltype(n)::value;
-      typedef T P __attribute__((ext_vector_type(N)));
-#pragma unroll
-      for (int i = 0; i < 8; i += N) {
-        if (at + i < k) {
-          if constexpr (N == 1) {
-            f[i] = norm_ld<T>(row[at + i]);
-          } else {
-            const P v = *reinterpret_cast<const P*>(row + at + i);
-#pragma unroll
-            for (int e = 0; e < N; ++e) f[i + e] = norm_ld<T>((T)v[e]);
-          }
-        } else {
-#pragma unroll
-          for (int e = 0; e < N; ++e) f[i + e] = 0.0f;
-        }
-      }
-    };
-    if (vec == 4) pieces(std::integral_constant<int, 4>{});
-    else if (vec == 2) pieces(std::integral_constant<int, 2>{});
-    else pieces(std::integral_constant<int, 1>{});
   }
-}
-
-template <typename T, bool FAST>
-__device__ __forceinline__ void store8(T* row, int at, int k, int vec, const float (&f)[8]) {
-  if constexpr (FAST) {
-    if (at >= k) return;
-    if constexpr (sizeof(T) == 2) {
-      u32x4_t v;
+  __device__ __forceinline__ void pack(const float (&f)[8]) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) v[i] = f32x2_to_bf16x2_bits(f[2 * i], f[2 * i + 1]);
-      *reinterpret_cast<u32x4_t*>(row + at) = v;
-    } else {
-      *reinterpret_cast<f32x4_t*>(row + at) = f32x4_t{f[0], f[1], f[2], f[3]};
-      *reinterpret_cast<f32x4_t*>(row + at + 4) = f32x4_t{f[4], f[5], f[6], f[7]};
+    for (int i = 0; i < kWords; ++i) {
+      if constexpr (sizeof(T) == 2) w[i] = f32x2_to_bf16x2_bits(f[2 * i], f[2 * i + 1]);
+      else w[i] = __float_as_uint(f[i]);
     }
-  } else {
-    auto pieces = [&](auto n) {
-      constexpr int N = decltype(n)::value;
-      typedef T P __attribute__((ext_vector_type(N)));
+  }
+};
+
+typedef u32x4_t u32x4_at2_t __attribute__((aligned(2)));
+typedef u32x4_t u32x4_at4_t __attribute__((aligned(4)));
+
+// Its loads and stores at `at` (zeros past k): 16 bytes each, of which FAST
+// says that they are aligned and that none lies across the row's end.
+// Otherwise accesses are aligned to their elements, which the vector memory
+// takes at any width, and the row's last piece goes element by element.
+template <typename T, bool FAST>
+__device__ __forceinline__ Raw<T> load8(const T* row, int at, int k) {
+  using V = std::conditional_t<FAST, u32x4_t, std::conditional_t<sizeof(T) == 2, u32x4_at2_t, u32x4_at4_t>>;
+  Raw<T> r;
 #pragma unroll
-      for (int i = 0; i < 8; i += N) {
-        if (at + i >= k) continue;
-        T e[N];
+  for (int i = 0; i < Raw<T>::kWords; ++i) r.w[i] = 0;
+  if (at + 8 <= k) {
 #pragma unroll
-        for (int j = 0; j < N; ++j) {
-          if constexpr (sizeof(T) == 2) e[j] = (T)f32_to_bf16_bits(f[i + j]);
-          else e[j] = f[i + j];
-        }
-        if constexpr (N == 1) {
-          row[at + i] = e[0];
-        } else {
-          P v;
+    for (int i = 0; i < Raw<T>::kWords; i += 4) {
+      const u32x4_t v = *reinterpret_cast<const V*>(row + at + i * 4 / (int)sizeof(T));
 #pragma unroll
-          for (int j = 0; j < N; ++j) v[j] = e[j];
-          *reinterpret_cast<P*>(row + at + i) = v;
-        }
-      }
-    };
-    if (vec == 4) pieces(std::integral_constant<int, 4>{});
-    else if (vec == 2) pieces(std::integral_constant<int, 2>{});
-    else pieces(std::integral_constant<int, 1>{});
+      for (int e = 0; e < 4; ++e) r.w[i + e] = v[e];
+    }
+  } else if (!FAST && at < k) {
+    if constexpr (sizeof(T) == 2) {
+#pragma unroll
+      for (int i = 0; i < 7; ++i)
+        if (at + i < k) r.w[i / 2] |= (uint32_t)row[at + i] << (16 * (i & 1));
+    } else {
+#pragma unroll
+      for (int i = 0; i < 7; ++i)
+        if (at + i < k) r.w[i] = __float_as_uint(row[at + i]);
+    }
+  }
+  return r;
+}
+template <typename T, bool FAST>
+__device__ __forceinline__ void store8(T* row, int at, int k, const float (&f)[8]) {
+  using V = std::conditional_t<FAST, u32x4_t, std::conditional_t<sizeof(T) == 2, u32x4_at2_t, u32x4_at4_t>>;
+  Raw<T> r;
+  r.pack(f);
+  if (at + 8 <= k) {
+#pragma unroll
+    for (int i = 0; i < Raw<T>::kWords; i += 4)
+      *reinterpret_cast<V*>(row + at + i * 4 / (int)sizeof(T)) = u32x4_t{r.w[i], r.w[i + 1], r.w[i + 2], r.w[i + 3]};
+  } else if (!FAST && at < k) {
+#pragma unroll
+    for (int i = 0; i < 7; ++i) {
+      if (at + i >= k) continue;
+      if constexpr (sizeof(T) == 2) row[at + i] = (T)(r.w[i / 2] >> (16 * (i & 1)));
+      else row[at + i] = __uint_as_float(r.w[i]);
+    }
   }
 }
 
@@ -177,25 +151,26 @@ __global__ __launch_bounds__(WAVES == 1 ? 256 : WAVES * 64) void norm_kernel(con
   int turn = 0;  // (the rows' exchanges alternate between two places: one barrier each)
   for (int64_t row = (int64_t)blockIdx.x * rows + (WAVES == 1 ? threadIdx.x >> 6 : 0); row < p.m;
        row += (int64_t)gridDim.x * rows, turn ^= 1) {
-    float h[NV][8];
+    using ResT = std::conditional_t<RES == kResF32, float, uint16_t>;
+    Raw<uint16_t> xr[NV];
+    Raw<ResT> rr[NV];
 #pragma unroll
-    for (int j = 0; j < NV; ++j) load8<uint16_t, FAST>(p.x + row * p.ld_x, (j * kLanes + lane) * 8, k, p.vec, h[j]);
-    if constexpr (RES != kNoRes) {
-#pragma unroll
-      for (int j = 0; j < NV; ++j) {
-        const int at = (j * kLanes + lane) * 8;
-        float b[8];
-        if constexpr (RES == kResBf16) load8<uint16_t, FAST>(static_cast<const uint16_t*>(p.res) + row * p.ld_res, at, k, p.vec, b);
-        else load8<float, FAST>(static_cast<const float*>(p.res) + row * p.ld_res, at, k, p.vec, b);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) h[j][i] += b[i];
-      }
+    for (int j = 0; j < NV; ++j) {
+      xr[j] = load8<uint16_t, FAST>(p.x + row * p.ld_x, (j * kLanes + lane) * 8, k);
+      if constexpr (RES != kNoRes) rr[j] = load8<ResT, FAST>(static_cast<const ResT*>(p.res) + row * p.ld_res, (j * kLanes + lane) * 8, k);
     }
+    float h[NV][8];
     float sum = 0.0f;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      if constexpr (RES == kResBf16) store8<uint16_t, FAST>(static_cast<uint16_t*>(p.res_out) + row * p.ld_res_out, (j * kLanes + lane) * 8, k, p.vec, h[j]);
-      if constexpr (RES == kResF32) store8<float, FAST>(static_cast<float*>(p.res_out) + row * p.ld_res_out, (j * kLanes + lane) * 8, k, p.vec, h[j]);
+      xr[j].unpack(h[j]);
+      if constexpr (RES != kNoRes) {
+        float b[8];
+        rr[j].unpack(b);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) h[j][i] += b[i];
+        store8<ResT, FAST>(static_cast<ResT*>(p.res_out) + row * p.ld_res_out, (j * kLanes + lane) * 8, k, h[j]);
+      }
 #pragma unroll
       for (int i = 0; i < 8; ++i) sum = __builtin_fmaf(h[j][i], h[j][i], sum);
     }
@@ -207,11 +182,11 @@ __global__ __launch_bounds__(WAVES == 1 ? 256 : WAVES * 64) void norm_kernel(con
     for (int j = 0; j < NV; ++j) {
       const int at = (j * kLanes + lane) * 8;
       float w[8];
-      if (p.w_f32) load8<float, FAST>(static_cast<const float*>(p.w), at, k, p.vec, w);
-      else load8<uint16_t, FAST>(static_cast<const uint16_t*>(p.w), at, k, p.vec, w);
+      if (p.w_f32) load8<float, FAST>(static_cast<const float*>(p.w), at, k).unpack(w);
+      else load8<uint16_t, FAST>(static_cast<const uint16_t*>(p.w), at, k).unpack(w);
 #pragma unroll
       for (int i = 0; i < 8; ++i) h[j][i] = h[j][i] * r * (w[i] + p.offset);
-      if (p.out) store8<uint16_t, FAST>(p.out + row * p.ld_out, at, k, p.vec, h[j]);
+      if (p.out) store8<uint16_t, FAST>(p.out + row * p.ld_out, at, k, h[j]);
       if constexpr (FMT == HUM_ACT_FP8_TOKEN) amax = __builtin_fmaxf(amax, max8(h[j]));
     }
     if constexpr (FMT == HUM_ACT_FP8_TOKEN) {
@@ -259,6 +234,7 @@ static void launch_norm(const NormParams& p, hipStream_t s) {
     const int64_t most = (int64_t)1 << 20;
     norm_kernel<FMT, RES, FAST, W, decltype(nv)::value><<<(unsigned)(wgs < most ? wgs : most), W == 1 ? 256 : W * 64, 0, s>>>(p);
   };
+  using I3 = std::integral_constant<int, 3>;
   using I1 = std::integral_constant<int, 1>;
   using I2 = std::integral_constant<int, 2>;
   using I4 = std::integral_constant<int, 4>;
@@ -267,6 +243,7 @@ static void launch_norm(const NormParams& p, hipStream_t s) {
   if (p.k <= 512) go(I1{}, I1{});
   else if (p.k <= 2048) go(I4{}, I1{});
   else if (p.k <= 4096) go(I4{}, I2{});
+  else if (p.k <= 6144) go(I4{}, I3{});
   else if (p.k <= 8192) go(I4{}, I4{});
   else if (p.k <= 16384) go(I16{}, I2{});
   else if (p.k <= 32768) go(I16{}, I4{});
@@ -369,22 +346,13 @@ extern "C" hum_status hum_rms_norm(const hum_norm_desc* d, int64_t m, int64_t k,
   p.inv_k = (float)(1.0 / (double)k);
   p.eps = d->eps;
   p.offset = d->weight_offset;
-  // Elements that every access can take at once: what divides the length, the
-  // strides and the addresses (f32: at most the 16 bytes of four).
-  int64_t all = k | (int64_t)(addr(x) / 2) | (int64_t)(addr(out) / 2);
-  if (m > 1) all |= ld_x | (out ? ld_out : 0);
-  int64_t wide = (int64_t)(addr(weight) / wsize);  // of f32 tensors, in pieces of 4
-  if (wsize == 2) {
-    all |= wide;
-    wide = 0;
+  // Whether every piece of 8 elements is whole and 16-byte aligned.
+  uintptr_t all = addr(x) | addr(out) | addr(weight) | addr(residual) | addr(residual_out);
+  if (m > 1) {
+    all |= (uintptr_t)(ld_x * 2) | (out ? (uintptr_t)(ld_out * 2) : 0);
+    if (residual) all |= (uintptr_t)(ld_res * rsize) | (uintptr_t)(ld_res_out * rsize);
   }
-  if (residual) {
-    const int64_t r = (int64_t)(addr(residual) / rsize) | (int64_t)(addr(residual_out) / rsize) | (m > 1 ? ld_res | ld_res_out : 0);
-    (rsize == 2 ? all : wide) |= r;
-  }
-  const bool fast = all % 8 == 0 && wide % 4 == 0;
-  all |= wide;
-  p.vec = all % 4 == 0 ? 4 : all % 2 == 0 ? 2 : 1;
+  const bool fast = k % 8 == 0 && all % 16 == 0;
   hipStream_t s = static_cast<hipStream_t>(stream);
   auto by_res = [&](auto f) {
     constexpr int F = decltype(f)::value;
