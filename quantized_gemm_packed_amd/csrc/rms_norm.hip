@@ -34,6 +34,9 @@ struct NormParams {
 // What a row's residual is.
 enum { kNoRes = 0, kResBf16 = 1, kResF32 = 2 };
 
+__device__ __forceinline__ float norm_ld(uint16_t v) { return bf16_bits_to_f32(v); }
+__device__ __forceinline__ float norm_ld(float v) { return v; }
+
 // Eight elements of a row as they lie in memory: 16 bytes of bf16, 32 of f32.
 template <typename T>
 struct Raw {
@@ -58,10 +61,9 @@ struct Raw {
 typedef u32x4_t u32x4_at2_t __attribute__((aligned(2)));
 typedef u32x4_t u32x4_at4_t __attribute__((aligned(4)));
 
-// Its loads and stores at `at` (zeros past k): 16 bytes each, of which FAST
-// says that they are aligned and that none lies across the row's end.
-// Otherwise accesses are aligned to their elements, which the vector memory
-// takes at any width, and the row's last piece goes element by element.
+// Its loads and stores at `at`, where all eight lie within k (else zeros): 16
+// bytes each, which FAST says are aligned.  Otherwise they are aligned to
+// their elements, which the vector memory takes at any width.
 template <typename T, bool FAST>
 __device__ __forceinline__ Raw<T> load8(const T* row, int at, int k) {
   using V = std::conditional_t<FAST, u32x4_t, std::conditional_t<sizeof(T) == 2, u32x4_at2_t, u32x4_at4_t>>;
@@ -75,16 +77,6 @@ __device__ __forceinline__ Raw<T> load8(const T* row, int at, int k) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) r.w[i + e] = v[e];
     }
-  } else if (!FAST && at < k) {
-    if constexpr (sizeof(T) == 2) {
-#pragma unroll
-      for (int i = 0; i < 7; ++i)
-        if (at + i < k) r.w[i / 2] |= (uint32_t)row[at + i] << (16 * (i & 1));
-    } else {
-#pragma unroll
-      for (int i = 0; i < 7; ++i)
-        if (at + i < k) r.w[i] = __float_as_uint(row[at + i]);
-    }
   }
   return r;
 }
@@ -97,13 +89,6 @@ __device__ __forceinline__ void store8(T* row, int at, int k, const float (&f)[8
 #pragma unroll
     for (int i = 0; i < Raw<T>::kWords; i += 4)
       *reinterpret_cast<V*>(row + at + i * 4 / (int)sizeof(T)) = u32x4_t{r.w[i], r.w[i + 1], r.w[i + 2], r.w[i + 3]};
-  } else if (!FAST && at < k) {
-#pragma unroll
-    for (int i = 0; i < 7; ++i) {
-      if (at + i >= k) continue;
-      if constexpr (sizeof(T) == 2) row[at + i] = (T)(r.w[i / 2] >> (16 * (i & 1)));
-      else row[at + i] = __uint_as_float(r.w[i]);
-    }
   }
 }
 
@@ -148,31 +133,51 @@ __global__ __launch_bounds__(WAVES == 1 ? 256 : WAVES * 64) void norm_kernel(con
   const int lane = WAVES == 1 ? threadIdx.x & 63 : threadIdx.x;
   const int rows = WAVES == 1 ? 4 : 1;
   const int k = p.k;
+  constexpr bool kLast = FMT == HUM_ACT_BF16 && !FAST;  // (codes have whole pieces only)
   int turn = 0;  // (the rows' exchanges alternate between two places: one barrier each)
   for (int64_t row = (int64_t)blockIdx.x * rows + (WAVES == 1 ? threadIdx.x >> 6 : 0); row < p.m;
        row += (int64_t)gridDim.x * rows, turn ^= 1) {
     using ResT = std::conditional_t<RES == kResF32, float, uint16_t>;
-    Raw<uint16_t> xr[NV];
-    Raw<ResT> rr[NV];
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      xr[j] = load8<uint16_t, FAST>(p.x + row * p.ld_x, (j * kLanes + lane) * 8, k);
-      if constexpr (RES != kNoRes) rr[j] = load8<ResT, FAST>(static_cast<const ResT*>(p.res) + row * p.ld_res, (j * kLanes + lane) * 8, k);
-    }
+    // (long rows in parts: all of their loads at once would not fit the registers)
+    constexpr int kPart = NV > 4 ? 2 : NV;
     float h[NV][8];
     float sum = 0.0f;
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-      xr[j].unpack(h[j]);
+    // the last k % 8 elements: one each of the first threads
+    const int last = (k & ~7) + lane;
+    const bool has_last = kLast && last < k;
+    float h_last = 0.0f;
+    if (has_last) {
+      h_last = norm_ld(p.x[row * p.ld_x + last]);
       if constexpr (RES != kNoRes) {
-        float b[8];
-        rr[j].unpack(b);
+        h_last += norm_ld(static_cast<const ResT*>(p.res)[row * p.ld_res + last]);
+        if constexpr (RES == kResF32) static_cast<float*>(p.res_out)[row * p.ld_res_out + last] = h_last;
+        else static_cast<uint16_t*>(p.res_out)[row * p.ld_res_out + last] = (uint16_t)f32_to_bf16_bits(h_last);
+      }
+      sum = h_last * h_last;
+    }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) h[j][i] += b[i];
-        store8<ResT, FAST>(static_cast<ResT*>(p.res_out) + row * p.ld_res_out, (j * kLanes + lane) * 8, k, h[j]);
+    for (int part = 0; part < NV; part += kPart) {
+      Raw<uint16_t> xr[NV];
+      Raw<ResT> rr[NV];
+#pragma unroll
+      for (int j = part; j < part + kPart; ++j) {
+        xr[j] = load8<uint16_t, FAST>(p.x + row * p.ld_x, (j * kLanes + lane) * 8, k);
+        if constexpr (RES != kNoRes) rr[j] = load8<ResT, FAST>(static_cast<const ResT*>(p.res) + row * p.ld_res, (j * kLanes + lane) * 8, k);
       }
 #pragma unroll
-      for (int i = 0; i < 8; ++i) sum = __builtin_fmaf(h[j][i], h[j][i], sum);
+      for (int j = part; j < part + kPart; ++j) {
+        xr[j].unpack(h[j]);
+        if constexpr (RES != kNoRes) {
+          float b[8];
+          rr[j].unpack(b);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) h[j][i] += b[i];
+          store8<ResT, FAST>(static_cast<ResT*>(p.res_out) + row * p.ld_res_out, (j * kLanes + lane) * 8, k, h[j]);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sum = __builtin_fmaf(h[j][i], h[j][i], sum);
+      }
+      if constexpr (kPart < NV) __builtin_amdgcn_sched_barrier(0);
     }
     sum = over_row<WAVES, false>(sum, red[0][turn]);
     const float r = 1.0f / __builtin_sqrtf(sum * p.inv_k + p.eps);
@@ -181,6 +186,7 @@ __global__ __launch_bounds__(WAVES == 1 ? 256 : WAVES * 64) void norm_kernel(con
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int at = (j * kLanes + lane) * 8;
+      if constexpr (kPart < NV) __builtin_amdgcn_sched_barrier(0);
       float w[8];
       if (p.w_f32) load8<float, FAST>(static_cast<const float*>(p.w), at, k).unpack(w);
       else load8<uint16_t, FAST>(static_cast<const uint16_t*>(p.w), at, k).unpack(w);
@@ -188,6 +194,10 @@ __global__ __launch_bounds__(WAVES == 1 ? 256 : WAVES * 64) void norm_kernel(con
       for (int i = 0; i < 8; ++i) h[j][i] = h[j][i] * r * (w[i] + p.offset);
       if (p.out) store8<uint16_t, FAST>(p.out + row * p.ld_out, at, k, h[j]);
       if constexpr (FMT == HUM_ACT_FP8_TOKEN) amax = __builtin_fmaxf(amax, max8(h[j]));
+    }
+    if (has_last) {
+      const float w = p.w_f32 ? static_cast<const float*>(p.w)[last] : norm_ld(static_cast<const uint16_t*>(p.w)[last]);
+      p.out[row * p.ld_out + last] = (uint16_t)f32_to_bf16_bits(h_last * r * (w + p.offset));
     }
     if constexpr (FMT == HUM_ACT_FP8_TOKEN) {
       amax = over_row<WAVES, true>(amax, red[1][turn]);
@@ -225,7 +235,16 @@ __global__ __launch_bounds__(WAVES == 1 ? 256 : WAVES * 64) void norm_kernel(con
   }
 }
 
-// Waves per row and pieces per thread, by the row's length alone.
+// Waves per row and pieces per thread, by the row's length alone.  Measured
+// (waves x pieces; bf16 residual, FP8 codes, 2^26 elements, and one row):
+//   512   1x1 97 us, 3.6     2x1 124, 3.2
+//   1024  2x1 87, 3.3        1x2 87, 3.4      4x1 122, 3.3
+//   2048  2x2 86, 3.8        4x1 89, 3.4      1x4 95, 4.5
+//   4096  4x2 86, 3.9        8x1 89, 3.9      2x4 95, 4.9
+//   5120  4x3 91, 4.4        8x2 94, 4.2
+//   8192  8x2 87, 4.5        4x4 96, 5.1      16x1 95, 4.7
+//   12288 8x3 91, 5.3        16x2 94, 5.4
+//   16384 16x2 96, 6.1       8x4 101, 6.4
 template <int FMT, int RES, bool FAST>
 static void launch_norm(const NormParams& p, hipStream_t s) {
   auto go = [&](auto waves, auto nv) {
@@ -234,17 +253,19 @@ static void launch_norm(const NormParams& p, hipStream_t s) {
     const int64_t most = (int64_t)1 << 20;
     norm_kernel<FMT, RES, FAST, W, decltype(nv)::value><<<(unsigned)(wgs < most ? wgs : most), W == 1 ? 256 : W * 64, 0, s>>>(p);
   };
-  using I3 = std::integral_constant<int, 3>;
   using I1 = std::integral_constant<int, 1>;
   using I2 = std::integral_constant<int, 2>;
+  using I3 = std::integral_constant<int, 3>;
   using I4 = std::integral_constant<int, 4>;
   using I8 = std::integral_constant<int, 8>;
   using I16 = std::integral_constant<int, 16>;
   if (p.k <= 512) go(I1{}, I1{});
-  else if (p.k <= 2048) go(I4{}, I1{});
+  else if (p.k <= 1024) go(I2{}, I1{});
+  else if (p.k <= 2048) go(I2{}, I2{});
   else if (p.k <= 4096) go(I4{}, I2{});
   else if (p.k <= 6144) go(I4{}, I3{});
-  else if (p.k <= 8192) go(I4{}, I4{});
+  else if (p.k <= 8192) go(I8{}, I2{});
+  else if (p.k <= 12288) go(I8{}, I3{});
   else if (p.k <= 16384) go(I16{}, I2{});
   else if (p.k <= 32768) go(I16{}, I4{});
   else go(I16{}, I8{});
