@@ -117,6 +117,55 @@ __device__ __forceinline__ float mx_inv_scale(int e) {
   return __uint_as_float(0x00400000u);  // 2^-127
 }
 
+// One step towards x / d as an IEEE f32 division rounds it, from an estimate q
+// of it and y = RN(1 / d): with the exact remainder r = q d - x, RN(q - r y)
+// (Markstein, "Computation of elementary functions on the IBM RISC System/6000
+// processor", 1990).  It is the division's own result where q is within one
+// ulp of x / d and nothing over- or underflows.  A zero keeps its sign: r is
+// then +0, and q - 0 is q.
+__device__ __forceinline__ float divide_step(float q, float x, float d, float y) {
+  return __builtin_fmaf(-__builtin_fmaf(q, d, -x), y, q);
+}
+
+// A scale by the FP8 rule, amax / 448 (1 for zeros), and values over it, as
+// IEEE f32 divisions give them (a code can hang on the quotient's last bit) in
+// three or five instructions a value instead of eleven.  Maxima outside
+// [2^-70, 2^120] divide; inside, values below 2^-10 of the scale, whose
+// remainder may underflow, become zero codes either way.  The reciprocal is
+// correctly rounded for every mantissa of a scale, as was the scale itself
+// (all 2^23 of each compared).  x y is within 1.5 ulps of x / s, so that after
+// one step it is within one and after the second right.  Values and a maximum
+// of bf16 need one step: the quotients of all of their mantissas and scales
+// were compared with the division's.  ANY: they may be any f32.
+template <bool ANY>
+struct Fp8Scale {
+  float s, y;
+  bool divides;
+  __device__ __forceinline__ explicit Fp8Scale(float amax) : s(1.0f), y(0.0f), divides(false) {
+    if (amax >= 0x1p-70f && amax <= 0x1p120f) {
+      const float q = divide_step(amax * (1.0f / 448.0f), amax, 448.0f, 1.0f / 448.0f);
+      s = ANY ? divide_step(q, amax, 448.0f, 1.0f / 448.0f) : q;
+      const float y0 = __builtin_amdgcn_rcpf(s);
+      y = __builtin_fmaf(__builtin_fmaf(-s, y0, 1.0f), y0, y0);
+    } else if (amax > 0.0f) {  // (lanes without a row hold zeros)
+      s = amax / 448.0f;
+      divides = true;
+    }
+  }
+  __device__ __forceinline__ void divide(float (&f)[8]) const {
+    if (__builtin_expect(divides, 0)) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) f[i] = f[i] / s;
+    } else if (y > 0.0f) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float q = divide_step(f[i] * y, f[i], s, y);
+        f[i] = ANY ? divide_step(q, f[i], s, y) : q;
+      }
+    }
+  }
+};
+
 // Eight floats over a power of two -> eight codes, nearest even, saturated
 // (the hardware conversions; E2M1 saturates by itself, E4M3 becomes NaN past
 // 448, so what the rule saturates is clamped first).

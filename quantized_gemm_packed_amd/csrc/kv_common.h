@@ -78,41 +78,6 @@ __device__ __forceinline__ float row_max(float v) {
   return v;
 }
 
-// x / d as an IEEE f32 division rounds it, from y = RN(1 / d): with
-// q = RN(x y) and the exact remainder r = q d - x, RN(q - r y) (Markstein,
-// "Computation of elementary functions on the IBM RISC System/6000
-// processor", 1990), three instructions where the division takes eleven.
-// That holds while nothing over- or underflows (fp8_row says where).  A zero
-// keeps its sign: r is then +0, and q - 0 is q.
-__device__ __forceinline__ float divide_by(float x, float d, float y) {
-  const float q = x * y;
-  return __builtin_fmaf(-__builtin_fmaf(q, d, -x), y, q);
-}
-
-// A row's scale by the FP8 rule, amax / 448 (1 for a row of zeros), and the
-// lane's eight values over it, as IEEE f32 divisions give them (a code can
-// hang on the quotient's last bit).  Maxima outside [2^-70, 2^120] divide;
-// inside, values below 2^-10 of the scale, whose remainder may underflow,
-// become zero codes either way.  A bf16 maximum has 128 mantissas, so have
-// the scales: the quotients of all of them were compared with the division's.
-// ANY: of other values only the division itself is known to be right.
-template <bool ANY>
-__device__ __forceinline__ float fp8_row(float (&f)[8], float amax) {
-  float s = 1.0f;
-  if (!ANY && amax >= 0x1p-70f && amax <= 0x1p120f) {
-    s = divide_by(amax, 448.0f, 1.0f / 448.0f);
-    const float y0 = __builtin_amdgcn_rcpf(s);
-    const float y = __builtin_fmaf(__builtin_fmaf(-s, y0, 1.0f), y0, y0);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = divide_by(f[i], s, y);
-  } else if (amax > 0.0f) {  // (lanes without a row hold zeros)
-    s = amax / 448.0f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = f[i] / s;
-  }
-  return s;
-}
-
 // Byte offsets of token `at` of a page inside its (page, head) unit: its code
 // row, and its scale (or the first of them) with the step to the next.
 template <int FMT, int D>
@@ -136,8 +101,8 @@ struct KvOffsets {
 // Quantizes one row, of which the lane has the eight values f, and stores the
 // lane's codes at `code` and the row's scale (of the lane's block of 32:
 // block b's at b * scale_step) at `scale`, where `live`.  Every lane of the
-// row calls it together.  ANY: the values are any f32 (fp8_row says what that
-// changes), not bf16.
+// row calls it together.  ANY: the values are any f32 (Fp8Scale says what
+// that changes), not bf16.
 template <int FMT, int D, bool ANY>
 __device__ __forceinline__ void kv_store_row(float (&f)[8], int lane, uint8_t* code, uint8_t* scale, int32_t scale_step, bool live) {
   if constexpr (FMT == HUM_ACT_BF16) {
@@ -151,7 +116,9 @@ __device__ __forceinline__ void kv_store_row(float (&f)[8], int lane, uint8_t* c
     for (int i = 0; i < 8; ++i) amax = __builtin_fmaxf(amax, __builtin_fabsf(f[i]));
     if constexpr (FMT == HUM_ACT_FP8_TOKEN) {
       amax = row_max<D / 8>(amax);
-      const float sc = fp8_row<ANY>(f, amax);
+      const Fp8Scale<ANY> fs(amax);
+      const float sc = fs.s;
+      fs.divide(f);
       u32x2_t o;
       o[0] = f32x2_to_e4m3x2(f[0], f[1]) | (f32x2_to_e4m3x2(f[2], f[3]) << 16);
       o[1] = f32x2_to_e4m3x2(f[4], f[5]) | (f32x2_to_e4m3x2(f[6], f[7]) << 16);

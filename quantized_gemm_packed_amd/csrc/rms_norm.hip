@@ -109,13 +109,10 @@ __device__ __forceinline__ float over_row(float v, float* red) {
   return v;
 }
 
-// The scale of a maximum by the FP8 rule, and codes of eight values over it.
-__device__ __forceinline__ float fp8_scale(float amax) { return amax > 0.0f ? amax / 448.0f : 1.0f; }
-__device__ __forceinline__ u32x2_t fp8_codes(const float (&f)[8], float s) {
-  u32x2_t o;
-  o[0] = f32x2_to_e4m3x2(f[0] / s, f[1] / s) | (f32x2_to_e4m3x2(f[2] / s, f[3] / s) << 16);
-  o[1] = f32x2_to_e4m3x2(f[4] / s, f[5] / s) | (f32x2_to_e4m3x2(f[6] / s, f[7] / s) << 16);
-  return o;
+__device__ __forceinline__ u32x2_t fp8_codes(float (&f)[8], const Fp8Scale<true>& s) {
+  s.divide(f);
+  return u32x2_t{f32x2_to_e4m3x2(f[0], f[1]) | (f32x2_to_e4m3x2(f[2], f[3]) << 16),
+                 f32x2_to_e4m3x2(f[4], f[5]) | (f32x2_to_e4m3x2(f[6], f[7]) << 16)};
 }
 __device__ __forceinline__ float max8(const float (&f)[8]) {
   float a = 0.0f;
@@ -201,8 +198,8 @@ __global__ __launch_bounds__(WAVES == 1 ? 256 : WAVES * 64) void norm_kernel(con
     }
     if constexpr (FMT == HUM_ACT_FP8_TOKEN) {
       amax = over_row<WAVES, true>(amax, red[1][turn]);
-      const float s = fp8_scale(amax);
-      if (lane == 0) static_cast<float*>(p.scales)[row] = fine ? s : __builtin_nanf("");
+      const Fp8Scale<true> s(amax);
+      if (lane == 0) static_cast<float*>(p.scales)[row] = fine ? s.s : __builtin_nanf("");
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
         const int at = (j * kLanes + lane) * 8;
@@ -213,10 +210,10 @@ __global__ __launch_bounds__(WAVES == 1 ? 256 : WAVES * 64) void norm_kernel(con
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
         const int at = (j * kLanes + lane) * 8;
-        const float s = fp8_scale(row16_max(max8(h[j])));  // 16 lanes have a group of 128
+        const Fp8Scale<true> s(row16_max(max8(h[j])));  // 16 lanes have a group of 128
         if (at < k) {
           *reinterpret_cast<u32x2_t*>(p.q + row * k + at) = fp8_codes(h[j], s);
-          if ((lane & 15) == 0) static_cast<float*>(p.scales)[row * (k / 128) + at / 128] = fine ? s : __builtin_nanf("");
+          if ((lane & 15) == 0) static_cast<float*>(p.scales)[row * (k / 128) + at / 128] = fine ? s.s : __builtin_nanf("");
         }
       }
     }
