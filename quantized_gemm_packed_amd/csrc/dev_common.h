@@ -137,34 +137,36 @@ __device__ __forceinline__ float divide_step(float q, float x, float d, float y)
 // one step it is within one and after the second right.  Values and a maximum
 // of bf16 need one step: the quotients of all of their mantissas and scales
 // were compared with the division's.  ANY: they may be any f32.
+__device__ __forceinline__ bool fp8_in_range(float amax) { return amax >= 0x1p-70f && amax <= 0x1p120f; }
 template <bool ANY>
-struct Fp8Scale {
-  float s, y;
-  bool divides;
-  __device__ __forceinline__ explicit Fp8Scale(float amax) : s(1.0f), y(0.0f), divides(false) {
-    if (amax >= 0x1p-70f && amax <= 0x1p120f) {
-      const float q = divide_step(amax * (1.0f / 448.0f), amax, 448.0f, 1.0f / 448.0f);
-      s = ANY ? divide_step(q, amax, 448.0f, 1.0f / 448.0f) : q;
-      const float y0 = __builtin_amdgcn_rcpf(s);
-      y = __builtin_fmaf(__builtin_fmaf(-s, y0, 1.0f), y0, y0);
-    } else if (amax > 0.0f) {  // (lanes without a row hold zeros)
-      s = amax / 448.0f;
-      divides = true;
-    }
-  }
-  __device__ __forceinline__ void divide(float (&f)[8]) const {
-    if (__builtin_expect(divides, 0)) {
+__device__ __forceinline__ float fp8_scale_in_range(float amax) {
+  const float q = divide_step(amax * (1.0f / 448.0f), amax, 448.0f, 1.0f / 448.0f);
+  return ANY ? divide_step(q, amax, 448.0f, 1.0f / 448.0f) : q;
+}
+template <bool ANY>
+__device__ __forceinline__ void fp8_divide_in_range(float (&f)[8], float s) {
+  const float y0 = __builtin_amdgcn_rcpf(s);
+  const float y = __builtin_fmaf(__builtin_fmaf(-s, y0, 1.0f), y0, y0);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) f[i] = f[i] / s;
-    } else if (y > 0.0f) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float q = divide_step(f[i] * y, f[i], s, y);
-        f[i] = ANY ? divide_step(q, f[i], s, y) : q;
-      }
-    }
+  for (int i = 0; i < 8; ++i) {
+    const float q = divide_step(f[i] * y, f[i], s, y);
+    f[i] = ANY ? divide_step(q, f[i], s, y) : q;
   }
-};
+}
+// The scale of a maximum, and the values over it.
+template <bool ANY>
+__device__ __forceinline__ float fp8_row(float (&f)[8], float amax) {
+  float s = 1.0f;
+  if (fp8_in_range(amax)) {
+    s = fp8_scale_in_range<ANY>(amax);
+    fp8_divide_in_range<ANY>(f, s);
+  } else if (amax > 0.0f) {  // (lanes without a row hold zeros)
+    s = amax / 448.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = f[i] / s;
+  }
+  return s;
+}
 
 // Eight floats over a power of two -> eight codes, nearest even, saturated
 // (the hardware conversions; E2M1 saturates by itself, E4M3 becomes NaN past

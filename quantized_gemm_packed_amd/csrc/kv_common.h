@@ -101,7 +101,7 @@ struct KvOffsets {
 // Quantizes one row, of which the lane has the eight values f, and stores the
 // lane's codes at `code` and the row's scale (of the lane's block of 32:
 // block b's at b * scale_step) at `scale`, where `live`.  Every lane of the
-// row calls it together.  ANY: the values are any f32 (Fp8Scale says what
+// row calls it together.  ANY: the values are any f32 (fp8_row says what
 // that changes), not bf16.
 template <int FMT, int D, bool ANY>
 __device__ __forceinline__ void kv_store_row(float (&f)[8], int lane, uint8_t* code, uint8_t* scale, int32_t scale_step, bool live) {
@@ -116,9 +116,7 @@ __device__ __forceinline__ void kv_store_row(float (&f)[8], int lane, uint8_t* c
     for (int i = 0; i < 8; ++i) amax = __builtin_fmaxf(amax, __builtin_fabsf(f[i]));
     if constexpr (FMT == HUM_ACT_FP8_TOKEN) {
       amax = row_max<D / 8>(amax);
-      const Fp8Scale<ANY> fs(amax);
-      const float sc = fs.s;
-      fs.divide(f);
+      const float sc = fp8_row<ANY>(f, amax);
       u32x2_t o;
       o[0] = f32x2_to_e4m3x2(f[0], f[1]) | (f32x2_to_e4m3x2(f[2], f[3]) << 16);
       o[1] = f32x2_to_e4m3x2(f[4], f[5]) | (f32x2_to_e4m3x2(f[6], f[7]) << 16);

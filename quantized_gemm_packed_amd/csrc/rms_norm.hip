@@ -109,8 +109,7 @@ __device__ __forceinline__ float over_row(float v, float* red) {
   return v;
 }
 
-__device__ __forceinline__ u32x2_t fp8_codes(float (&f)[8], const Fp8Scale<true>& s) {
-  s.divide(f);
+__device__ __forceinline__ u32x2_t e4m3x8(const float (&f)[8]) {
   return u32x2_t{f32x2_to_e4m3x2(f[0], f[1]) | (f32x2_to_e4m3x2(f[2], f[3]) << 16),
                  f32x2_to_e4m3x2(f[4], f[5]) | (f32x2_to_e4m3x2(f[6], f[7]) << 16)};
 }
@@ -198,22 +197,22 @@ __global__ __launch_bounds__(WAVES == 1 ? 256 : WAVES * 64) void norm_kernel(con
     }
     if constexpr (FMT == HUM_ACT_FP8_TOKEN) {
       amax = over_row<WAVES, true>(amax, red[1][turn]);
-      const Fp8Scale<true> s(amax);
-      if (lane == 0) static_cast<float*>(p.scales)[row] = fine ? s.s : __builtin_nanf("");
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
         const int at = (j * kLanes + lane) * 8;
-        if (at < k) *reinterpret_cast<u32x2_t*>(p.q + row * k + at) = fp8_codes(h[j], s);
+        const float s = fp8_row<true>(h[j], amax);
+        if (j == 0 && lane == 0) static_cast<float*>(p.scales)[row] = fine ? s : __builtin_nanf("");
+        if (at < k) *reinterpret_cast<u32x2_t*>(p.q + row * k + at) = e4m3x8(h[j]);
       }
     }
     if constexpr (FMT == HUM_ACT_FP8_GROUP) {
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
         const int at = (j * kLanes + lane) * 8;
-        const Fp8Scale<true> s(row16_max(max8(h[j])));  // 16 lanes have a group of 128
+        const float s = fp8_row<true>(h[j], row16_max(max8(h[j])));  // 16 lanes have a group of 128
         if (at < k) {
-          *reinterpret_cast<u32x2_t*>(p.q + row * k + at) = fp8_codes(h[j], s);
-          if ((lane & 15) == 0) static_cast<float*>(p.scales)[row * (k / 128) + at / 128] = fine ? s.s : __builtin_nanf("");
+          *reinterpret_cast<u32x2_t*>(p.q + row * k + at) = e4m3x8(h[j]);
+          if ((lane & 15) == 0) static_cast<float*>(p.scales)[row * (k / 128) + at / 128] = fine ? s : __builtin_nanf("");
         }
       }
     }
