@@ -123,7 +123,7 @@ __device__ __forceinline__ void route_exactly(const RouteParams& p, int64_t t, d
     // lane g looks at group g (at most 64 of them)
     double a = none, b = none;
     const int from = lane < p.groups ? lane * p.per_group : 0;
-#pragma unroll 4
+#pragma unroll 8
     for (int i = 0; i < p.per_group; ++i) {
       const double v = keys[from + i];
       b = fmax(b, fmin(a, v));
@@ -157,6 +157,7 @@ __device__ __forceinline__ void route_exactly(const RouteParams& p, int64_t t, d
     int at = -1;              // the lowest of those that have it
 #pragma unroll
     for (int j = N - 1; j >= 0; --j) {
+      if (j * 64 >= p.experts) continue;
       const uint64_t have = __ballot(key[j] == best);
       if (have) at = j * 64 + __builtin_ctzll(have);
     }
@@ -430,6 +431,15 @@ __global__ __launch_bounds__(256, NB <= 4 ? 5 : 4) void route_kernel(const Route
   const double after = dpp<kRowShl1>(k);
   const int place_after = (int)dpp<kRowShl1>((uint32_t)place);
   const bool sorted = !inside || k > after || (k == after && place < place_after);
+  // The softmax's sum is an f32 one (a term is off by 2^-23 and 2.6 |x - top|
+  // 2^-24 of itself, |x - top| is at most ln 512 on average, the additions give
+  // 13 times 2^-24: below 2^-19), and with it all scores by one factor: keys
+  // that differ by more than 2^-18 of their scores' difference stand as they
+  // are.  In a sorted row it is enough to look at neighbours.
+  const bool soft = BIAS && !p.sigmoid;
+  auto apart = [](double ka, double sa, double kb, double sb) {
+    return (ka == kb && sa == sb) || __builtin_fabs(ka - kb) > __builtin_fabs(sa - sb) * 0x1p-18;
+  };
   if (__ballot(!sorted)) {
     rank = 0;
     each_lane<0>(n_cand, [&](auto ctrl) {
@@ -437,19 +447,22 @@ __global__ __launch_bounds__(256, NB <= 4 ? 5 : 4) void route_kernel(const Route
       const double o = dpp<C>(k);
       const int other = (int)dpp<C>((uint32_t)place);
       rank += (int)(o > k) | ((int)(o == k) & (int)(other < place));
+      if (soft) {
+        const double so = dpp<C>(s);
+        if (id >= 0 && other < kRouteMaxExperts && !apart(k, s, o, so)) ok = false;
+      }
     });
-  }
-  if (BIAS && !p.sigmoid) {
-    // The softmax's sum is an f32 one, its scores are off by up to 2^-19 of
-    // themselves: neighbours (in cut order; tokens out of it are done again)
-    // have to differ by more.
+  } else if (soft) {
     const double s_after = dpp<kRowShl1>(s);
-    if (inside && place_after < kRouteMaxExperts && !(s == s_after && k == after) && !(k - after > (s + s_after) * 0x1p-18)) ok = false;
+    if (inside && place_after < kRouteMaxExperts && !apart(k, s, after, s_after)) ok = false;
   }
   // What was not taken is below the last candidate's cut key and a step of it.
+  // With a bias its f32 key may be off by 2^-21 (twice a score's 2^-22) and a
+  // rounding of it, and the softmax's factor moves scores, none above 1 / sum,
+  // against one another.
   if (!p.exact_cut) {
     const float hi = from_ordered(mine | low);
-    const double err = BIAS ? ((double)__builtin_fabsf(hi) + 2.0) * 0x1p-18 : 0.0;
+    const double err = !BIAS ? 0.0 : 0x1p-21 + (double)__builtin_fabsf(hi) * 0x1p-22 + (soft ? 0x1p-18 / (double)sum : 0.0);
     // (the last candidate's lane asks for the worst of the chosen)
     const double worst = -row16_max(rank < p.topk && id >= 0 ? -k : -__builtin_inf());
     if (l == n_cand - 1 && id >= 0 && !(worst > (double)hi + err)) ok = false;
