@@ -157,7 +157,6 @@ __device__ __forceinline__ void route_exactly(const RouteParams& p, int64_t t, d
     int at = -1;              // the lowest of those that have it
 #pragma unroll
     for (int j = N - 1; j >= 0; --j) {
-      if (j * 64 >= p.experts) continue;
       const uint64_t have = __ballot(key[j] == best);
       if (have) at = j * 64 + __builtin_ctzll(have);
     }
@@ -218,10 +217,15 @@ __device__ __forceinline__ double reciprocal(double d) {
 // exact order; the first topk stand if the last of them is above whatever was
 // not taken can be, and a token for which that (or the choice of groups) is
 // too near to tell is done again by route_exactly.
-template <typename T, int NB, bool BIAS, bool GROUPS>
-__global__ __launch_bounds__(256, NB <= 4 ? 5 : 4) void route_kernel(const RouteParams p) {
+// What the experts are ordered by: their logits, or scores with a bias.
+enum { kByLogit = 0, kBySigmoid = 1, kBySoftmax = 2 };
+
+template <typename T, int NB, int ORDER, bool GROUPS>
+__global__ __launch_bounds__(256, 4) void route_kernel(const RouteParams p) {
   __shared__ double keys[4][kRouteMaxExperts];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, l = lane & 15;
+  constexpr bool BIAS = ORDER != kByLogit;
+  const bool sigmoid = ORDER == kBySigmoid || (ORDER == kByLogit && p.sigmoid);
   const float none = -__builtin_inff();
   const uint32_t low = p.low_mask;
   const int64_t tw = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 4;
@@ -269,7 +273,7 @@ __global__ __launch_bounds__(256, NB <= 4 ? 5 : 4) void route_kernel(const Route
   bool ok = true;
   // the largest logit, and the sum of exp(x - top)
   float top = none, sum = 0.0f;
-  if (!p.sigmoid) {
+  if (!sigmoid) {
 #pragma unroll
     for (int b = 0; b < NB; ++b)
 #pragma unroll
@@ -287,7 +291,7 @@ __global__ __launch_bounds__(256, NB <= 4 ? 5 : 4) void route_kernel(const Route
   }
   // scores of logits (of -inf: 0)
   auto scores = [&](float (&v)[NB][4]) {
-    if (p.sigmoid) {
+    if (sigmoid) {
 #pragma unroll
       for (int b = 0; b < NB; ++b)
 #pragma unroll
@@ -357,7 +361,7 @@ __global__ __launch_bounds__(256, NB <= 4 ? 5 : 4) void route_kernel(const Route
     // exponential, its argument's rounding, the sum and the reciprocal; a
     // softmax's by its sum's 2^-19 of itself), its sum with the bias by half an
     // ulp.
-    float err = 0x1p-21f + (__builtin_fabsf(a) + (c > none ? __builtin_fabsf(c) : 0.0f)) * (p.sigmoid ? 0x1p-23f : 0x1p-18f);
+    float err = 0x1p-21f + (__builtin_fabsf(a) + (c > none ? __builtin_fabsf(c) : 0.0f)) * (sigmoid ? 0x1p-23f : 0x1p-18f);
     if (p.top2 && c > none) a += c;
     if (l >= p.groups) a = none;
     err = row16_max(a > none ? err : 0.0f);
@@ -419,8 +423,8 @@ __global__ __launch_bounds__(256, NB <= 4 ? 5 : 4) void route_kernel(const Route
     if constexpr (sizeof(T) == 2) v = bf16_bits_to_f32(row[id]);
     else v = row[id];
     const double by = BIAS ? (double)p.bias[id] : 0.0;
-    const double e = exp(p.sigmoid ? -(double)v : (double)v - (double)top);
-    if (!p.sigmoid) s = e * reciprocal((double)sum);
+    const double e = exp(sigmoid ? -(double)v : (double)v - (double)top);
+    if (!sigmoid) s = e * reciprocal((double)sum);
     else s = e < 0x1p1000 ? reciprocal(1.0 + e) : 1.0 / e;
     k = BIAS ? s + by : (double)v;
   }
@@ -436,7 +440,7 @@ __global__ __launch_bounds__(256, NB <= 4 ? 5 : 4) void route_kernel(const Route
   // 13 times 2^-24: below 2^-19), and with it all scores by one factor: keys
   // that differ by more than 2^-18 of their scores' difference stand as they
   // are.  In a sorted row it is enough to look at neighbours.
-  const bool soft = BIAS && !p.sigmoid;
+  constexpr bool soft = ORDER == kBySoftmax;
   auto apart = [](double ka, double sa, double kb, double sb) {
     return (ka == kb && sa == sb) || __builtin_fabs(ka - kb) > __builtin_fabs(sa - sb) * 0x1p-18;
   };
@@ -462,7 +466,7 @@ __global__ __launch_bounds__(256, NB <= 4 ? 5 : 4) void route_kernel(const Route
   // against one another.
   if (!p.exact_cut) {
     const float hi = from_ordered(mine | low);
-    const double err = !BIAS ? 0.0 : 0x1p-21 + (double)__builtin_fabsf(hi) * 0x1p-22 + (soft ? 0x1p-18 / (double)sum : 0.0);
+    const double err = !BIAS ? 0.0 : 0x1p-21 + (double)__builtin_fabsf(hi) * 0x1p-22 + (soft ? (double)(0x1p-17f * __builtin_amdgcn_rcpf(sum)) : 0.0);
     // (the last candidate's lane asks for the worst of the chosen)
     const double worst = -row16_max(rank < p.topk && id >= 0 ? -k : -__builtin_inf());
     if (l == n_cand - 1 && id >= 0 && !(worst > (double)hi + err)) ok = false;
@@ -496,27 +500,30 @@ __global__ __launch_bounds__(256) void route_exact_kernel(const RouteParams p) {
   if (t < p.tokens) route_exactly(p, t, keys[wave]);
 }
 
-template <typename T, bool BIAS, bool GROUPS>
+template <typename T, int ORDER, bool GROUPS>
 static void launch_route(const RouteParams& p, hipStream_t s) {
   const int block = p.tokens >= 4096 ? 256 : 64;
   const unsigned grid = (unsigned)((p.tokens * 16 + block - 1) / block);
   switch ((p.experts + 63) / 64) {
-    case 1: route_kernel<T, 1, BIAS, GROUPS><<<grid, block, 0, s>>>(p); break;
-    case 2: route_kernel<T, 2, BIAS, GROUPS><<<grid, block, 0, s>>>(p); break;
-    case 3: route_kernel<T, 3, BIAS, GROUPS><<<grid, block, 0, s>>>(p); break;
-    case 4: route_kernel<T, 4, BIAS, GROUPS><<<grid, block, 0, s>>>(p); break;
+    case 1: route_kernel<T, 1, ORDER, GROUPS><<<grid, block, 0, s>>>(p); break;
+    case 2: route_kernel<T, 2, ORDER, GROUPS><<<grid, block, 0, s>>>(p); break;
+    case 3: route_kernel<T, 3, ORDER, GROUPS><<<grid, block, 0, s>>>(p); break;
+    case 4: route_kernel<T, 4, ORDER, GROUPS><<<grid, block, 0, s>>>(p); break;
     case 5:
-    case 6: route_kernel<T, 6, BIAS, GROUPS><<<grid, block, 0, s>>>(p); break;
-    default: route_kernel<T, 8, BIAS, GROUPS><<<grid, block, 0, s>>>(p); break;
+    case 6: route_kernel<T, 6, ORDER, GROUPS><<<grid, block, 0, s>>>(p); break;
+    default: route_kernel<T, 8, ORDER, GROUPS><<<grid, block, 0, s>>>(p); break;
   }
 }
-
+template <typename T, int ORDER>
+static void launch_route(const RouteParams& p, hipStream_t s) {
+  if (p.groups > 1) launch_route<T, ORDER, true>(p, s);
+  else launch_route<T, ORDER, false>(p, s);
+}
 template <typename T>
 static void launch_route(const RouteParams& p, hipStream_t s) {
-  if (p.bias && p.groups > 1) launch_route<T, true, true>(p, s);
-  else if (p.bias) launch_route<T, true, false>(p, s);
-  else if (p.groups > 1) launch_route<T, false, true>(p, s);
-  else launch_route<T, false, false>(p, s);
+  if (!p.bias) launch_route<T, kByLogit>(p, s);
+  else if (p.sigmoid) launch_route<T, kBySigmoid>(p, s);
+  else launch_route<T, kBySoftmax>(p, s);
 }
 
 }  // namespace hum
