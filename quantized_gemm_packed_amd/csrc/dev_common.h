@@ -11,6 +11,9 @@ typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
 typedef float f32x4_t __attribute__((ext_vector_type(4)));
 typedef int i32x8_t __attribute__((ext_vector_type(8)));
 typedef uint32_t u32x4_t __attribute__((ext_vector_type(4)));
+// (16 bytes at an address that is aligned to elements of 2 or 4 only)
+typedef u32x4_t u32x4_at2_t __attribute__((aligned(2)));
+typedef u32x4_t u32x4_at4_t __attribute__((aligned(4)));
 typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x3_t __attribute__((ext_vector_type(3)));
 typedef uint32_t u32x1_t __attribute__((ext_vector_type(1)));

@@ -9,6 +9,12 @@
 // elements each.  Memory bound: q is read and written once, k and v are read
 // once and their codes written once; apart, the turned k would be written and
 // read once more, and a launch paid twice.
+//
+// Measured on MI355X, inputs that change from call to call: 16384 tokens of
+// 32 + 8 heads of 128 into MXFP8 78 us, 4.7 TB/s read + written (a large copy
+// reaches 4.9 to 5.2; hum_rotary and hum_kv_write together take 89); 5003
+// tokens of 16 + 4 normed heads of 256, bf16, 26 us, 4.7 TB/s; a decode step of
+// 64 tokens 3.9 us, of which a launch is 3.3.
 #include <cmath>
 
 #include "kv_common.h"
@@ -71,12 +77,16 @@ __device__ __forceinline__ void lds8(const float* at, float (&f)[8]) {
 // FAST: every piece of 8 elements lies at 16 bytes and turns as a whole, with
 // another whole piece (half layout: the half a multiple of 8 elements) or
 // within itself (interleaved: rotary_dim a multiple of 8), and the offsets in
-// a token fit 32 bits.  In the half layout the two lanes of a
-// pair of pieces exchange them and form one result each:
+// a token fit 32 bits.  In the half layout the two lanes of a pair of pieces
+// exchange them and form one result each:
 //   y0 = x0 c + (-x1) s,   y1 = x0 s + x1 c,
 // the same products with the coefficients exchanged.  (Loading both pieces in
 // both lanes instead stalls the vector cache on the line that is on its way:
 // 16384 tokens of 32 + 8 heads of 128 in MXFP8 117 us, with the exchange 107.)
+// Otherwise accesses are aligned to their elements, which the vector memory
+// takes at any width, and the other element of each pair comes from the row's
+// copy in LDS (16384 tokens as above in FP8, 24 of 128 elements turned: 121 us
+// with loads of single elements, 84 so).
 //
 // A wave has one token (its slot and addresses are scalars) or a slice of its
 // rows, 64 / (D / 8) of them at once; the coefficients lie in its own part of
@@ -85,10 +95,12 @@ template <int FMT, int D, bool HALF, bool FAST, bool NORM>
 __global__ __launch_bounds__(256) void append_kernel(const AppendParams p) {
   using U = KvUnit<FMT, D>;
   using off_t = std::conditional_t<FAST, int32_t, int64_t>;
+  using V = std::conditional_t<FAST, u32x4_t, u32x4_at2_t>;
   constexpr int kLanes = D / 8;
   constexpr int kStep = 64 / kLanes;  // rows a wave moves at once
   constexpr int kB = 8 * U::kRow / D;
   extern __shared__ __attribute__((aligned(16))) float lds[];
+  __shared__ __attribute__((aligned(16))) uint16_t copies[HALF && !FAST ? 4 : 1][512];  // of the rows a wave works on
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), sub = threadIdx.x & 63, lane = sub % kLanes;
   const int64_t t = (int64_t)blockIdx.x * 4 + wave;
   const bool have = t < p.tokens;
@@ -135,33 +147,18 @@ __global__ __launch_bounds__(256) void append_kernel(const AppendParams p) {
   uint16_t* const yq = p.q_out + t * p.qo_ts + lane * 8;
 
   // One row is loaded while the one before it is worked on.
-  u32x4_t x0_next, x1_next;
+  u32x4_t x0_next;
   int kind_next = -1, head_next = 0;
   const int steps = (end - (int)blockIdx.y * p.row_step + kStep - 1) / kStep;
   for (int n = -1; n < steps; ++n) {
-    u32x4_t x0 = x0_next, x1 = x1_next;
+    u32x4_t x0 = x0_next;
     const int kind = kind_next, head = head_next;
     kind_next = -1;
     if (row < end) {
       kind_next = (row >= hq) + (row >= hq + hk);
       head_next = row - (kind_next ? hq : 0) - (kind_next == 2 ? hk : 0);
       const uint16_t* x = (kind_next == 0 ? xq : kind_next == 1 ? xk : xv) + head_next * (kind_next == 0 ? hs_q : kind_next == 1 ? hs_k : hs_v) + lane * 8;
-      if constexpr (FAST) {
-        x0_next = *reinterpret_cast<const u32x4_t*>(x);
-      } else {
-        // its own elements, and in the half layout the other one of each pair
-#pragma unroll
-        for (int i = 0; i < 4; ++i) x0_next[i] = (uint32_t)x[2 * i] | ((uint32_t)x[2 * i + 1] << 16);
-        x1_next = u32x4_t{0, 0, 0, 0};
-        if (HALF && kind_next < 2) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const int e = lane * 8 + i;
-            const uint32_t b = e < half ? x[i + half] : e < 2 * half ? x[i - half] : 0;
-            x1_next[i / 2] |= b << (16 * (i & 1));
-          }
-        }
-      }
+      x0_next = *reinterpret_cast<const V*>(x);
     }
     row += kStep;
     if (kind >= 0) {
@@ -173,6 +170,22 @@ __global__ __launch_bounds__(256) void append_kernel(const AppendParams p) {
           unpack8(x0, f);
 #pragma unroll
           for (int i = 0; i < 8; ++i) sum = __builtin_fmaf(f[i], f[i], sum);
+        }
+        u32x4_t x1;
+        if constexpr (HALF && !FAST) {
+          uint16_t* mine = copies[wave] + sub / kLanes * D;
+          *reinterpret_cast<u32x4_t*>(mine + lane * 8) = x0;
+          __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+          __builtin_amdgcn_wave_barrier();
+#pragma unroll
+          for (int i = 0; i < 8; i += 2) {
+            const int e = lane * 8 + i, o = e + 1;
+            const uint32_t a = mine[e < half ? e + half : e < 2 * half ? e - half : e];
+            const uint32_t b = mine[o < half ? o + half : o < 2 * half ? o - half : o];
+            x1[i / 2] = a | b << 16;
+          }
+          __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+          __builtin_amdgcn_wave_barrier();
         }
         if constexpr (HALF && FAST) {
 #pragma unroll
@@ -236,16 +249,10 @@ __global__ __launch_bounds__(256) void append_kernel(const AppendParams p) {
         unpack8(x0, f);
       }
       if (kind == 0) {
-        uint16_t* y = yq + head * qo_hs;
-        if constexpr (FAST) {
-          u32x4_t o;
+        u32x4_t o;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) o[i] = f32x2_to_bf16x2_bits(f[2 * i], f[2 * i + 1]);
-          *reinterpret_cast<u32x4_t*>(y) = o;
-        } else {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) y[i] = (uint16_t)f32_to_bf16_bits(f[i]);
-        }
+        for (int i = 0; i < 4; ++i) o[i] = f32x2_to_bf16x2_bits(f[2 * i], f[2 * i + 1]);
+        *reinterpret_cast<V*>(yq + head * qo_hs) = o;
       } else {
         uint8_t* unit = page + (uint32_t)head * unit_bytes;
         if (kind == 2) kv_store_row<FMT, D, false>(f, lane, unit + off_v.code + lane * kB, unit + off_v.scale, off_v.scale_step, live);

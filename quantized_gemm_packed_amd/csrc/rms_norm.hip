@@ -5,10 +5,17 @@
 // y in f32, rounded once: to bf16, or to the codes of hum_quant_act's rules.
 //
 // Memory bound: x and the residual are read once, everything that is written
-// is written once.  A row stays in the registers of its workgroup between the
-// two passes over it (the sum of squares, then y), 8 elements of a thread side
-// by side.  Which elements a thread has, and so the order of the sums, goes by
-// k alone: a row's bits are the same in every batch and at every alignment.
+// is written once.  A row stays in the registers of its waves between the two
+// passes over it (the sum of squares, then y), 8 elements of a thread side by
+// side; all loads of a row are on their way before the first is used.  Which
+// elements a thread has, and so the order of the sums, goes by k alone: a
+// row's bits are the same in every batch and at every alignment.
+//
+// Measured on MI355X, inputs that change from call to call: 16384 rows of 8192
+// with a bf16 residual to FP8 codes 162 us, 5.8 TB/s read + written (a large
+// copy reaches 4.9 to 5.2); 3001 rows of 4100 with an f32 residual 29 us, 5.0
+// TB/s; 256 rows of 7168 to FP8 codes in groups 5.3 us and one row of 4096 3.8
+// us, of which a launch is 3.3.
 #include <cmath>
 
 #include "dev_common.h"
@@ -57,9 +64,6 @@ struct Raw {
     }
   }
 };
-
-typedef u32x4_t u32x4_at2_t __attribute__((aligned(2)));
-typedef u32x4_t u32x4_at4_t __attribute__((aligned(4)));
 
 // Its loads and stores at `at`, where all eight lie within k (else zeros): 16
 // bytes each, which FAST says are aligned.  Otherwise they are aligned to
