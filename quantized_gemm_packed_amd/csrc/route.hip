@@ -319,7 +319,7 @@ __global__ __launch_bounds__(256, 4) void route_kernel(const RouteParams p) {
 #pragma unroll
   for (int b = 0; b < NB; ++b)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) key[b][i] = x[b][i];
+    for (int i = 0; i < 4; ++i) key[b][i] = x[b][i] + (BIAS ? -0.0f : 0.0f);  // (a zero's sign orders nothing)
   if constexpr (BIAS) {
     scores(key);
 #pragma unroll

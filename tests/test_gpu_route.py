@@ -76,6 +76,18 @@ def test_ties_go_to_the_lowest_index(score):
     assert torch.equal(ids.cpu(), torch.arange(64, dtype=torch.int32).expand(3, 64))
 
 
+def test_zeros_of_either_sign_are_equal():
+    g = np.random.default_rng(3)
+    for e in (8, 64, 200):
+        x = torch.from_numpy(np.where(g.random((60, e)) < 0.5, -1.0, np.copysign(0.0, g.random((60, e)) - 0.5)).astype(np.float32)).cuda()
+        assert (torch.signbit(x) & (x == 0)).any()
+        for dtype in (torch.float32, torch.bfloat16):
+            for k in (1, 2, 5):
+                for kw in ({}, dict(num_groups=4, topk_groups=2), dict(num_groups=4, topk_groups=2, group_score="top2"),
+                           dict(score="sigmoid", bias=torch.full((e,), -0.0, device="cuda"))):
+                    _check(x.to(dtype), k, **kw)
+
+
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 def test_near_scores_are_told_apart(score):
     """Neighbouring f32 logits, at magnitudes where their f32 scores are equal: without a bias the larger logit comes
@@ -186,3 +198,26 @@ def test_many_tokens():
     s = x[:4000].double().cpu().numpy()
     order = np.argsort(-s, axis=1, kind="stable")[:, :8]
     assert (ids[:4000].cpu().numpy() == order).all()
+
+
+@pytest.mark.parametrize("e,k,kw,biased", [(8, 2, {}, False), (64, 6, {}, True), (256, 8, dict(score="sigmoid"), True), (130, 4, dict(score="sigmoid"), False),
+                                           (256, 8, dict(score="sigmoid", num_groups=8, topk_groups=4, group_score="top2", scale=2.5), True),
+                                           (160, 6, dict(num_groups=8, topk_groups=3, renormalize=False), False),
+                                           (512, 14, dict(num_groups=16, topk_groups=5, group_score="top2"), False), (72, 15, dict(num_groups=8, topk_groups=3), True)])
+def test_prompts_are_routed_as_their_tokens_alone(e, k, kw, biased):
+    """Large calls and small ones run on workgroups of other sizes: the same bits, also of tokens that share a wave
+    with others (near and equal logits among them)."""
+    for dtype in (torch.float32, torch.bfloat16):
+        x = _logits(e + k, 6003, e, dtype)
+        x[::7] = x[::7].round()                          # ties
+        x[1::9, : e // 2] = x[1::9, e // 2: e // 2 * 2] * (1 + 2.0 ** -23)
+        x[5::100] = -float("inf")
+        bias = _bias(k, e) if biased else None
+        ids, w = hum.moe_route(x, k, bias=bias, **kw)
+        at = 0
+        for n in (1, 2, 3, 5, 63, 64, 65, 800, 4000, 1000):
+            a, b = hum.moe_route(x[at:at + n], k, bias=bias, **kw)
+            assert torch.equal(a, ids[at:at + n]) and torch.equal(b, w[at:at + n]), n
+            at += n
+        assert at == 6003
+        _check(x[:120], k, bias=bias, **kw)
