@@ -695,7 +695,8 @@ hum_status hum_kv_attention(const hum_kv_desc* desc, const void* cache, size_t c
  *   q_out  : hum_rotary's, bit for bit (without a norm);
  *   cache  : k's and v's rows, quantized as hum_kv_write does.  k is rounded
  *            once, from the f32 turn to its codes (to bf16 and then to codes
- *            by the two calls; in a bf16 cache the same bytes).
+ *            by the two calls; in a bf16 cache the same bytes, but for
+ *            signaling NaNs, which become quiet in q and k).
  * Head norm, where norm and its weights are not NULL: before its turn, each
  * head of q (q_weight) and of k (k_weight), [head_dim] weights, becomes
  *   x * (1 / sqrt(mean(x^2) + eps)) * (w + weight_offset)    in f32.

@@ -255,8 +255,13 @@ __global__ __launch_bounds__(256) void append_kernel(const AppendParams p) {
         *reinterpret_cast<V*>(yq + head * qo_hs) = o;
       } else {
         uint8_t* unit = page + (uint32_t)head * unit_bytes;
-        if (kind == 2) kv_store_row<FMT, D, false>(f, lane, unit + off_v.code + lane * kB, unit + off_v.scale, off_v.scale_step, live);
-        else kv_store_row<FMT, D, true>(f, lane, unit + off_k.code + lane * kB, unit + off_k.scale, off_k.scale_step, live);
+        if (FMT == HUM_ACT_BF16 && kind == 2) {
+          if (live) *reinterpret_cast<u32x4_t*>(unit + off_v.code + lane * kB) = x0;
+        } else if (kind == 2) {
+          kv_store_row<FMT, D, false>(f, lane, unit + off_v.code + lane * kB, unit + off_v.scale, off_v.scale_step, live);
+        } else {
+          kv_store_row<FMT, D, true>(f, lane, unit + off_k.code + lane * kB, unit + off_k.scale, off_k.scale_step, live);
+        }
       }
     }
   }

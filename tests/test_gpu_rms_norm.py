@@ -243,6 +243,24 @@ def test_many_rows():
         assert torch.equal(h, (x.float() + r.float()).to(torch.bfloat16))
 
 
+@pytest.mark.parametrize("m,k,fmt", [((4 << 20) + 5, 8, "fp8_token"), ((4 << 20) + 5, 9, "bf16"), ((1 << 20) + 3, 544, "mxfp8")])
+def test_more_rows_than_a_grid_has(m, k, fmt):
+    """Workgroups that take several rows: the same bits as those rows alone."""
+    g = torch.Generator("cuda").manual_seed(m)
+    x = torch.randn(m, k, generator=g, device="cuda").to(torch.bfloat16)
+    w = torch.randn(k, generator=g, device="cuda").to(torch.bfloat16)
+    y = hum.rms_norm(x, w, residual=x, act_fmt=fmt)
+    at = torch.cat([torch.arange(300), torch.arange(m - 300, m), torch.randint(0, m, (2000,), generator=torch.Generator().manual_seed(1))]).cuda()
+    z = hum.rms_norm(x[at], w, residual=x[at], act_fmt=fmt)
+    assert torch.equal(y[1][at], z[1])
+    for a, b in zip(y[0] if fmt != "bf16" else y[:1], z[0] if fmt != "bf16" else z[:1]):
+        assert torch.equal(a[at], b)
+    part = 1 << 18
+    for i in (0, m - part):                               # every row of both ends: sums of squares near one
+        v = hum.rms_norm(x[i:i + part], torch.ones_like(w), residual=x[i:i + part])[0].float()
+        assert ((v * v).mean(1) - 1).abs().max() < 0.02
+
+
 def test_empty():
     x, r, w = _inputs(1, 0, 256)
     y, h = hum.rms_norm(x, w, residual=r)

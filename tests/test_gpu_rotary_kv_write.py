@@ -229,6 +229,17 @@ def test_infinities_and_nans_stay_in_their_rows():
         assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
 
 
+def test_every_bit_pattern_of_v_reaches_a_bf16_cache():
+    """Signaling NaNs too: v is copied there, as by the two calls."""
+    c = Case(17, "bf16", 256, 1, 2, 128, 128, skip=False)
+    c.qkv.view(torch.int16)[:, 3:] = torch.arange(-32768, 32768, dtype=torch.int32).view(256, 2, 128).to(torch.int16).cuda()
+    cache, two = c.cache(), c.cache()
+    c.run(cache)
+    c.apart(two)
+    assert torch.equal(cache, two)
+    assert torch.equal(hum.kv_read(c.desc, cache, c.slots)[1].view(torch.int16), c.split()[2].contiguous().view(torch.int16))
+
+
 def test_pages_at_the_far_end_of_a_large_cache():
     """Slots whose bytes lie past 4 GiB."""
     c = Case(15, "bf16", 6, 2, 8, 128, 128, 256)
