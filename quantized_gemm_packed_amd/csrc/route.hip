@@ -369,11 +369,17 @@ __global__ __launch_bounds__(256, 4) void route_kernel(const RouteParams p) {
     // How far a group's f32 score may be off: each score by 2^-22 (the
     // exponential, its argument's rounding, the sum and the reciprocal; a
     // softmax's by its sum's 2^-19 of itself), its sum with the bias by half an
-    // ulp.
-    float err = 0x1p-21f + (__builtin_fabsf(a) + (c > none ? __builtin_fabsf(c) : 0.0f)) * (sigmoid ? 0x1p-23f : 0x1p-18f);
-    if (p.top2 && c > none) a += c;
+    // ulp, and so the sum of two and the bounds.
+    const float part = sigmoid ? 0x1.9p-23f : 0x1p-18f;
+    float err = __builtin_fmaf(__builtin_fabsf(a), part, 0x1p-21f);
+    float down = a;
+    if (p.top2 && c > none) {
+      err = __builtin_fmaf(__builtin_fabsf(c), part, err);
+      down = a + c;
+      a = __builtin_fmaxf(down, -0x1.fffffep127f);  // (two lowest values: not an empty group yet)
+    }
     if (l >= p.groups) a = none;
-    err = row16_max(a > none ? err : 0.0f);
+    const float lowest = a > none ? down - err : __builtin_inff(), highest = a + err;
     int rank = 0;
     each_lane<0>(p.groups, [&](auto ctrl) {
       constexpr int C = decltype(ctrl)::value;
@@ -381,10 +387,10 @@ __global__ __launch_bounds__(256, 4) void route_kernel(const RouteParams p) {
       rank += (int)(o > a) | ((int)(o == a) & (int)(C - 0x150 < l));
     });
     const bool keep = l < p.groups && rank < p.topk_groups;
-    // the worst that stays and the best that does not
-    const float worst = -row16_max(keep ? -a : none), best = row16_max(keep ? none : a);
-    // (by logits the comparison is exact)
-    if ((BIAS || p.top2) && worst > none) ok = worst - best > 2.0f * err;
+    // the least of those that stay and the most of the others (by logits the
+    // comparison is exact; where an empty group stays, the others are empty)
+    const float least = -row16_max(keep ? -lowest : none), most = row16_max(keep ? none : highest);
+    if (BIAS || p.top2) ok = least > most;
     const uint32_t kept = (uint32_t)(__ballot(keep) >> (lane & 48)) & 0xFFFFu;
 #pragma unroll
     for (int b = 0; b < NB; ++b) {

@@ -135,6 +135,28 @@ def test_masked_experts_and_rows(score, dtype):
     assert (ids != 7).all()
 
 
+@pytest.mark.parametrize("gs", ["max", "top2"])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_biases_of_the_lowest_value(score, gs):
+    """float32's lowest value as a mask: two of them pass it in a group's sum,
+    and yet such a group comes before one without experts."""
+    low = torch.finfo(torch.float32).min
+    for e, groups, kept, k in ((256, 8, 4, 8), (64, 8, 3, 6), (16, 4, 2, 6), (60, 4, 3, 20)):
+        n = e // groups
+        x = _logits(e, 80, e, torch.float32)
+        g = torch.Generator().manual_seed(e)
+        empty = torch.rand(80, groups, generator=g) < 0.3       # of each token
+        x = x.masked_fill(empty.repeat_interleave(n, 1).cuda(), float("-inf"))
+        x[3] = float("-inf")
+        single = torch.rand(80, e, generator=g) < 0.2
+        x = x.masked_fill(single.cuda(), float("-inf"))
+        for masked in (torch.rand(e, generator=g) < 0.5, torch.arange(e) // n < groups - kept + 1, torch.arange(e) // n >= 1, torch.ones(e, dtype=torch.bool)):
+            bias = torch.where(masked.cuda(), torch.full((e,), low, device="cuda"), _bias(e, e))
+            _check(x, k, score=score, bias=bias, num_groups=groups, topk_groups=kept, group_score=gs)
+            bias = torch.where(masked.cuda(), -(2.0 + torch.rand(e, generator=g).cuda()) * 1e38, _bias(e, e))
+            _check(x, k, score=score, bias=bias, num_groups=groups, topk_groups=kept, group_score=gs)
+
+
 def test_far_logits():
     """Scores far below f32's range: sigmoids renormalise all the same."""
     x = torch.full((4, 16), -200.0, device="cuda")
