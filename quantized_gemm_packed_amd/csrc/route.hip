@@ -14,7 +14,7 @@
 // four tokens of a wave, 250 experts each).  Measured on MI355X: 16384 tokens
 // of 128 bf16 experts 5.6 us and 16381 of 256 f32 experts in groups, with a
 // bias, 11 us, 15 where a token is done again; in f64 throughout they took 54
-// and 80.  Memory alone would take 1.1 and 3.6 us, a launch 3.3.
+// and 80.  16384 of 72 experts in groups of 9: 7.6 us, in f64 34.  Memory alone would take 1.1 and 3.6 us, a launch 3.3.
 #include <cmath>
 
 #include "dev_common.h"
@@ -38,7 +38,7 @@ struct RouteParams {
   int32_t candidates;  // topk, and two more where a cut key is not exact
   int32_t exact_cut;   // a cut key holds the whole of its key
   uint32_t low_mask;   // of a cut key: the expert's number
-  float inv_quads, scale;
+  float inv_group, scale;  // 1 / (per_group, or per_group / 4 where groups are of whole quads)
 };
 
 template <int CTRL>
@@ -221,6 +221,8 @@ __device__ __forceinline__ double reciprocal(double d) {
 
 // What the experts are ordered by: their logits, or scores with a bias.
 enum { kByLogit = 0, kBySigmoid = 1, kBySoftmax = 2 };
+// Groups: none, of a multiple of 4 experts, of any number of them.
+enum { kNoGroups = 0, kQuadGroups = 1, kAnyGroups = 2 };
 
 // 16 lanes per token, four tokens per wave.  Lane l has the experts 64 b + 4 l
 // .. + 3 of NB blocks.  Keys are formed in f32 and cut to what leaves room for
@@ -229,9 +231,10 @@ enum { kByLogit = 0, kBySigmoid = 1, kBySoftmax = 2 };
 // exact order; the first topk stand if the last of them is above whatever was
 // not taken can be, and a token for which that (or the choice of groups) is
 // too near to tell is done again by route_exactly.
-template <typename T, int NB, int ORDER, bool GROUPS>
+template <typename T, int NB, int ORDER, int GROUPS>
 __global__ __launch_bounds__(256, 4) void route_kernel(const RouteParams p) {
-  __shared__ double keys[4][kRouteMaxExperts];
+  constexpr int kOfGroups = GROUPS == kAnyGroups ? NB * 64 * 2 : 0;  // four tokens' f32 keys
+  __shared__ double keys[4][kOfGroups > kRouteMaxExperts ? kOfGroups : kRouteMaxExperts];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, l = lane & 15;
   constexpr bool BIAS = ORDER != kByLogit;
   const bool sigmoid = ORDER == kBySigmoid || (ORDER == kByLogit && p.sigmoid);
@@ -332,10 +335,7 @@ __global__ __launch_bounds__(256, 4) void route_kernel(const RouteParams p) {
   for (int b = 0; b < NB; ++b)
 #pragma unroll
     for (int i = 0; i < 4; ++i) odd = odd || !(key[b][i] < __builtin_inff());
-  if constexpr (GROUPS) {
-    // each lane's four experts to LDS: their best two
-    typedef float f32x2_t __attribute__((ext_vector_type(2)));
-    f32x2_t* mine = reinterpret_cast<f32x2_t*>(keys[wave]) + (lane >> 4) * (kRouteMaxExperts / 4);
+  if constexpr (GROUPS != kNoGroups) {
     float v[NB][4];
 #pragma unroll
     for (int b = 0; b < NB; ++b)
@@ -348,21 +348,39 @@ __global__ __launch_bounds__(256, 4) void route_kernel(const RouteParams p) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) v[b][i] = key[b][i] > none ? v[b][i] : none;
     }
-#pragma unroll
-    for (int b = 0; b < NB; ++b) {
-      const float a0 = __builtin_fmaxf(v[b][0], v[b][1]), c0 = __builtin_fminf(v[b][0], v[b][1]);
-      const float a1 = __builtin_fmaxf(v[b][2], v[b][3]), c1 = __builtin_fminf(v[b][2], v[b][3]);
-      mine[b * 16 + l] = f32x2_t{__builtin_fmaxf(a0, a1), __builtin_fmaxf(__builtin_fminf(a0, a1), __builtin_fmaxf(c0, c1))};
-    }
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();
     float a = none, c = none;  // lane g: group g's best two
-    const int quads = p.per_group / 4, mine0 = l < p.groups ? l * quads : 0;
+    if constexpr (GROUPS == kQuadGroups) {
+      // each lane's four experts to LDS: their best two
+      typedef float f32x2_t __attribute__((ext_vector_type(2)));
+      f32x2_t* mine = reinterpret_cast<f32x2_t*>(keys[wave]) + (lane >> 4) * (kRouteMaxExperts / 4);
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        const float a0 = __builtin_fmaxf(v[b][0], v[b][1]), c0 = __builtin_fminf(v[b][0], v[b][1]);
+        const float a1 = __builtin_fmaxf(v[b][2], v[b][3]), c1 = __builtin_fminf(v[b][2], v[b][3]);
+        mine[b * 16 + l] = f32x2_t{__builtin_fmaxf(a0, a1), __builtin_fmaxf(__builtin_fminf(a0, a1), __builtin_fmaxf(c0, c1))};
+      }
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+      const int quads = p.per_group / 4, mine0 = l < p.groups ? l * quads : 0;
 #pragma unroll 4
-    for (int i = 0; i < quads; ++i) {
-      const f32x2_t v = mine[mine0 + i];
-      c = __builtin_fmaxf(__builtin_fmaxf(c, v[1]), __builtin_fminf(a, v[0]));
-      a = __builtin_fmaxf(a, v[0]);
+      for (int i = 0; i < quads; ++i) {
+        const f32x2_t v = mine[mine0 + i];
+        c = __builtin_fmaxf(__builtin_fmaxf(c, v[1]), __builtin_fminf(a, v[0]));
+        a = __builtin_fmaxf(a, v[0]);
+      }
+    } else {
+      float* mine = reinterpret_cast<float*>(keys[wave]) + (lane >> 4) * (NB * 64);
+#pragma unroll
+      for (int b = 0; b < NB; ++b) *reinterpret_cast<f32x4_t*>(mine + b * 64 + l * 4) = f32x4_t{v[b][0], v[b][1], v[b][2], v[b][3]};
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+      const int mine0 = l < p.groups ? l * p.per_group : 0;
+#pragma unroll 4
+      for (int i = 0; i < p.per_group; ++i) {
+        const float v = mine[mine0 + i];
+        c = __builtin_fmaxf(c, __builtin_fminf(a, v));
+        a = __builtin_fmaxf(a, v);
+      }
     }
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     __builtin_amdgcn_wave_barrier();
@@ -394,10 +412,12 @@ __global__ __launch_bounds__(256, 4) void route_kernel(const RouteParams p) {
     const uint32_t kept = (uint32_t)(__ballot(keep) >> (lane & 48)) & 0xFFFFu;
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
-      const int g = (int)(((float)(b * 16 + l) + 0.5f) * p.inv_quads);
-      const bool out = !((kept >> (g & 31)) & 1);
+      int g = (int)(((float)(b * 16 + l) + 0.5f) * p.inv_group);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) key[b][i] = out ? none : key[b][i];
+      for (int i = 0; i < 4; ++i) {
+        if constexpr (GROUPS == kAnyGroups) g = (int)(((float)(b * 64 + l * 4 + i) + 0.5f) * p.inv_group);
+        key[b][i] = (kept >> (g & 31)) & 1 ? key[b][i] : none;
+      }
     }
   }
   // Cut keys: what takes no part lies below kNoKey.
@@ -515,7 +535,7 @@ __global__ __launch_bounds__(256) void route_exact_kernel(const RouteParams p) {
   if (t < p.tokens) route_exactly(p, t, keys[wave]);
 }
 
-template <typename T, int ORDER, bool GROUPS>
+template <typename T, int ORDER, int GROUPS>
 static void launch_route(const RouteParams& p, hipStream_t s) {
   const int block = p.tokens >= 4096 ? 256 : 64;
   const unsigned grid = (unsigned)((p.tokens * 16 + block - 1) / block);
@@ -531,8 +551,9 @@ static void launch_route(const RouteParams& p, hipStream_t s) {
 }
 template <typename T, int ORDER>
 static void launch_route(const RouteParams& p, hipStream_t s) {
-  if (p.groups > 1) launch_route<T, ORDER, true>(p, s);
-  else launch_route<T, ORDER, false>(p, s);
+  if (p.groups == 1) launch_route<T, ORDER, kNoGroups>(p, s);
+  else if (p.per_group % 4 == 0) launch_route<T, ORDER, kQuadGroups>(p, s);
+  else launch_route<T, ORDER, kAnyGroups>(p, s);
 }
 template <typename T>
 static void launch_route(const RouteParams& p, hipStream_t s) {
@@ -601,11 +622,10 @@ extern "C" hum_status hum_moe_route(const hum_route_desc* d, int64_t num_tokens,
   int bits = 0;
   while (1 << bits < d->num_experts) ++bits;
   p.low_mask = (1u << bits) - 1u;
-  p.inv_quads = 4.0f / (float)p.per_group;
+  p.inv_group = (p.per_group % 4 == 0 ? 4.0f : 1.0f) / (float)p.per_group;
   hipStream_t s = static_cast<hipStream_t>(stream);
-  // The fast kernel holds topk + 2 candidates in 16 lanes, and groups of whole
-  // lanes' experts in 16 more.
-  if (d->topk <= 14 && (p.groups == 1 || (p.groups <= 16 && p.per_group % 4 == 0))) {
+  // The fast kernel holds topk + 2 candidates in 16 lanes, and the groups too.
+  if (d->topk <= 14 && p.groups <= 16) {
     if (p.bf16) launch_route<uint16_t>(p, s);
     else launch_route<float>(p, s);
   } else {

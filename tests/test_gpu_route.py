@@ -63,6 +63,21 @@ def test_route_groups(e, groups, kept, k, score, gs):
             _check(x, k, score=score, bias=bias, num_groups=groups, topk_groups=kept, group_score=gs)
 
 
+@pytest.mark.parametrize("gs", ["max", "top2"])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("e,groups,kept,k", [(15, 15, 4, 3), (30, 15, 3, 6), (36, 12, 5, 8), (72, 8, 3, 6), (72, 4, 1, 14), (170, 10, 3, 8),
+                                             (266, 14, 2, 10), (500, 4, 2, 8), (510, 2, 1, 12)])
+def test_route_groups_of_any_size(e, groups, kept, k, score, gs):
+    g = torch.Generator().manual_seed(e)
+    for dtype in (torch.float32, torch.bfloat16):
+        x = _logits(e + groups, 75, e, dtype)
+        x = x.masked_fill((torch.rand(75, e, generator=g) < 0.1).cuda(), float("-inf"))
+        x = x.masked_fill((torch.rand(75, groups, generator=g) < 0.3).repeat_interleave(e // groups, 1).cuda(), float("-inf"))
+        low = torch.where(torch.rand(e, generator=g).cuda() < 0.5, torch.finfo(torch.float32).min, _bias(4, e))
+        for bias in (None, _bias(3, e), low):
+            _check(x, k, score=score, bias=bias, num_groups=groups, topk_groups=kept, group_score=gs)
+
+
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 def test_ties_go_to_the_lowest_index(score):
     g = np.random.default_rng(0)
