@@ -85,11 +85,11 @@ __device__ __forceinline__ double wave_sum(double v) {
   return (lane_of(v, 0) + lane_of(v, 16)) + (lane_of(v, 32) + lane_of(v, 48));
 }
 
-// One token by one wave, all in f64; lane l has the experts l, l + 64, ...
+// One token by one wave, all in f64; lane l has the experts l, l + 64, ... (N of them)
 // keys: LDS of this wave alone.  What calls exp stays rolled: it runs seldom,
 // and what it holds in registers the kernel around it does not have.
+template <int N>
 __device__ __forceinline__ void route_exactly(const RouteParams& p, int64_t t, double* keys) {
-  constexpr int N = kRouteMaxExperts / 64;
   const int lane = threadIdx.x & 63;
   const double none = -__builtin_inf();
   auto logit = [&](int e) {
@@ -523,16 +523,17 @@ __global__ __launch_bounds__(256, 4) void route_kernel(const RouteParams p) {
   if (__builtin_expect(bad != 0, 0)) {  // (so that the loop's invariants are formed in here)
 #pragma unroll 1
     for (int n = 0; n < 4; ++n)
-      if ((bad >> (16 * n)) & 0xFFFF) route_exactly(p, tw - (lane >> 4) + n, keys[wave]);
+      if ((bad >> (16 * n)) & 0xFFFF) route_exactly<NB>(p, tw - (lane >> 4) + n, keys[wave]);
   }
 }
 
 // Whatever the kernel above does not take: one wave per token.
+template <int N>
 __global__ __launch_bounds__(256) void route_exact_kernel(const RouteParams p) {
-  __shared__ double keys[4][kRouteMaxExperts];
+  __shared__ double keys[4][N * 64];
   const int wave = threadIdx.x >> 6;
   const int64_t t = (int64_t)blockIdx.x * 4 + wave;
-  if (t < p.tokens) route_exactly(p, t, keys[wave]);
+  if (t < p.tokens) route_exactly<N>(p, t, keys[wave]);
 }
 
 template <typename T, int ORDER, int GROUPS>
@@ -629,7 +630,12 @@ extern "C" hum_status hum_moe_route(const hum_route_desc* d, int64_t num_tokens,
     if (p.bf16) launch_route<uint16_t>(p, s);
     else launch_route<float>(p, s);
   } else {
-    route_exact_kernel<<<(unsigned)((num_tokens + 3) / 4), 256, 0, s>>>(p);
+    const unsigned grid = (unsigned)((num_tokens + 3) / 4);
+    const int blocks = (d->num_experts + 63) / 64;
+    if (blocks <= 1) route_exact_kernel<1><<<grid, 256, 0, s>>>(p);
+    else if (blocks <= 2) route_exact_kernel<2><<<grid, 256, 0, s>>>(p);
+    else if (blocks <= 4) route_exact_kernel<4><<<grid, 256, 0, s>>>(p);
+    else route_exact_kernel<8><<<grid, 256, 0, s>>>(p);
   }
   hipError_t err = hipGetLastError();
   if (err != hipSuccess) return set_error(HUM_ERR_HIP, "moe_route launch: %s", hipGetErrorString(err));
