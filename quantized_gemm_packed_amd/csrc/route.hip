@@ -93,20 +93,27 @@ __device__ __forceinline__ void route_exactly(const RouteParams& p, int64_t t, d
   const int lane = threadIdx.x & 63;
   const double none = -__builtin_inf();
   auto logit = [&](int e) {
-    return (double)(p.bf16 ? bf16_bits_to_f32(static_cast<const uint16_t*>(p.logits)[t * p.ld + e]) : static_cast<const float*>(p.logits)[t * p.ld + e]);
+    return p.bf16 ? bf16_bits_to_f32(static_cast<const uint16_t*>(p.logits)[t * p.ld + e]) : static_cast<const float*>(p.logits)[t * p.ld + e];
   };
   auto fence = [] {
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     __builtin_amdgcn_wave_barrier();
   };
   double top = none, sum = 0.0;
+  // (the rolled loops read the logits from LDS: one latency for four loads)
+#pragma unroll 4
+  for (int j = 0; j < N; ++j) {
+    const int e = j * 64 + lane;
+    const float x = logit(e < p.experts ? e : 0);
+    keys[e] = x;
+    if (e < p.experts) top = fmax(top, (double)x);
+  }
+  fence();
   if (!p.sigmoid) {
-#pragma unroll 1
-    for (int e = lane; e < p.experts; e += 64) top = fmax(top, logit(e));
     top = wave_max(top);
 #pragma unroll 1
     for (int e = lane; e < p.experts; e += 64) {
-      const double x = logit(e);
+      const double x = keys[e];
       if (x != none) sum += exp(x - top);
     }
     sum = wave_sum(sum);
@@ -120,7 +127,7 @@ __device__ __forceinline__ void route_exactly(const RouteParams& p, int64_t t, d
   // what an expert is ordered by, and its group (by its score then); a NaN first
 #pragma unroll 2
   for (int e = lane; e < p.experts; e += 64) {
-    double k = logit(e);
+    double k = keys[e];
     if (k != none && (by_bias || by_score)) k = score(k) + (by_bias ? (double)p.bias[e] : 0.0);
     keys[e] = k == k ? k : -none;
   }
