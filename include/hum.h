@@ -437,7 +437,7 @@ size_t hum_moe_masked_workspace_bytes(const hum_weight_desc* w13, const hum_weig
  * Scores are compared in f64.  Ids come best first.  An expert whose logit (or
  * bias) is -inf takes no part; where fewer than topk are left, the other ids
  * are -1 with weight 0, which hum_moe_gemm skips: a row of -inf (a padding
- * token) routes nowhere.  A NaN logit comes first of all and its weight is NaN
+ * token) routes nowhere.  Else a NaN logit comes first of all and its weight is NaN
  * (with softmax or renormalize, every weight of its row; so it is where the
  * softmax of a row meets an infinity, and the logits alone then order it); ids
  * stay valid.

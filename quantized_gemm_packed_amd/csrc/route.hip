@@ -14,7 +14,8 @@
 // four tokens of a wave, 250 experts each).  Measured on MI355X: 16384 tokens
 // of 128 bf16 experts 5.6 us and 16381 of 256 f32 experts in groups, with a
 // bias, 11 us, 15 where a token is done again; in f64 throughout they took 54
-// and 80.  16384 of 72 experts in groups of 9: 7.6 us, in f64 34.  Memory alone would take 1.1 and 3.6 us, a launch 3.3.
+// and 80.  Memory alone would take 1.1 and 3.6 us, a launch 3.3.  16384 of 72
+// experts in groups of 9: 7.6 us, in f64 34.
 #include <cmath>
 
 #include "dev_common.h"
@@ -127,8 +128,9 @@ __device__ __forceinline__ void route_exactly(const RouteParams& p, int64_t t, d
   // what an expert is ordered by, and its group (by its score then); a NaN first
 #pragma unroll 2
   for (int e = lane; e < p.experts; e += 64) {
-    double k = keys[e];
-    if (k != none && (by_bias || by_score)) k = score(k) + (by_bias ? (double)p.bias[e] : 0.0);
+    const double by = p.bias ? (double)p.bias[e] : 0.0;
+    double k = by == none ? none : keys[e];
+    if (k != none && (by_bias || by_score)) k = score(k) + by;
     keys[e] = k == k ? k : -none;
   }
   fence();

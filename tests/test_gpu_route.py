@@ -210,6 +210,26 @@ def test_nan_and_infinity_stay_visible_and_ids_valid(score):
                 assert not torch.isnan(w[2]).any()
 
 
+@pytest.mark.parametrize("groups", [1, 4])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+def test_switched_off_experts_stay_off_beside_nans_and_infinities(score, groups):
+    for e, k in ((16, 4), (256, 8), (64, 20)):
+        x = _logits(e, 12, e, torch.float32)
+        bias = _bias(7, e)
+        off = torch.rand(e, generator=torch.Generator().manual_seed(e)) < 0.3
+        off[5], off[6] = True, False
+        bias[off.cuda()] = float("-inf")
+        x[1, 6], x[2, 6], x[3, 5], x[4, 5] = float("inf"), float("nan"), float("inf"), float("nan")
+        x[5, :] = float("nan")
+        ids, _ = hum.moe_route(x, k, score=score, bias=bias, num_groups=groups, topk_groups=max(1, groups // 2))
+        ids = ids.cpu()
+        assert (ids < e).all() and not off[ids.clamp(min=0).long()][ids >= 0].any()
+        assert ids[2, 0] == 6
+        if score == "softmax":  # (a sigmoid of infinity is 1, and a bias may put another before it)
+            assert ids[1, 0] == 6
+        assert torch.equal(ids[5][ids[5] >= 0], torch.arange(e)[~off][:int((ids[5] >= 0).sum())].int())
+
+
 def test_strided_logits_and_given_outputs():
     for dtype in (torch.float32, torch.bfloat16):
         wide = _logits(3, 21, 300, dtype)
