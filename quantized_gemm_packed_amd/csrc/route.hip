@@ -393,20 +393,23 @@ __global__ __launch_bounds__(256, 4) void route_kernel(const RouteParams p) {
     }
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     __builtin_amdgcn_wave_barrier();
-    // How far a group's f32 score may be off: each score by 2^-22 (the
-    // exponential, its argument's rounding, the sum and the reciprocal; a
-    // softmax's by its sum's 2^-19 of itself), its sum with the bias by half an
-    // ulp, and so the sum of two and the bounds.
-    const float part = sigmoid ? 0x1.9p-23f : 0x1p-18f;
-    float err = __builtin_fmaf(__builtin_fabsf(a), part, 0x1p-21f);
+    // How far a group's f32 score may be off.  A sigmoid by 2^-22 (the
+    // exponential, its argument's rounding, the sum and the reciprocal); a
+    // softmax, d below the top one, by (2.25 d + 3) 2^-24 of itself, which is
+    // below 2^-22 of the largest, 1 / sum, and by the sum's 2^-19 and the
+    // reciprocal's 2^-23, one factor for all scores, which orders nothing where
+    // there is no bias; the sum with the bias by half an ulp, and so the sum of
+    // two and the bounds.
+    float err = sigmoid ? 0x1p-21f : __builtin_amdgcn_rcpf(sum) * (BIAS ? 0x1p-21f + 0x1.2p-18f : 0x1p-21f);
+    err = __builtin_fmaf(__builtin_fabsf(a), 0x1.9p-23f, err);
     float down = a;
     if (p.top2 && c > none) {
-      err = __builtin_fmaf(__builtin_fabsf(c), part, err);
+      err = __builtin_fmaf(__builtin_fabsf(c), 0x1.9p-23f, err);
       down = a + c;
       a = __builtin_fmaxf(down, -0x1.fffffep127f);  // (two lowest values: not an empty group yet)
     }
     if (l >= p.groups) a = none;
-    const float lowest = a > none ? down - err : __builtin_inff(), highest = a + err;
+    const float lowest = a > none ? down - err : __builtin_inff(), highest = a > none ? a + err : none;
     int rank = 0;
     each_lane<0>(p.groups, [&](auto ctrl) {
       constexpr int C = decltype(ctrl)::value;
@@ -482,11 +485,11 @@ __global__ __launch_bounds__(256, 4) void route_kernel(const RouteParams p) {
   // The softmax's sum is an f32 one (a term is off by 2^-23 and 2.6 |x - top|
   // 2^-24 of itself, |x - top| is at most ln 512 on average, the additions give
   // 13 times 2^-24: below 2^-19), and with it all scores by one factor: keys
-  // that differ by more than 2^-18 of their scores' difference stand as they
+  // that differ by more of their scores' difference than that stand as they
   // are.  In a sorted row it is enough to look at neighbours.
   constexpr bool soft = ORDER == kBySoftmax;
   auto apart = [](double ka, double sa, double kb, double sb) {
-    return (ka == kb && sa == sb) || __builtin_fabs(ka - kb) > __builtin_fabs(sa - sb) * 0x1p-18;
+    return (ka == kb && sa == sb) || __builtin_fabs(ka - kb) > __builtin_fabs(sa - sb) * 0x1.1p-19;
   };
   if (__ballot(!sorted)) {
     rank = 0;
@@ -505,12 +508,12 @@ __global__ __launch_bounds__(256, 4) void route_kernel(const RouteParams p) {
     if (inside && place_after < kRouteMaxExperts && !apart(k, s, after, s_after)) ok = false;
   }
   // What was not taken is below the last candidate's cut key and a step of it.
-  // With a bias its f32 key may be off by 2^-21 (twice a score's 2^-22) and a
-  // rounding of it, and the softmax's factor moves scores, none above 1 / sum,
-  // against one another.
+  // With a bias its f32 key may be off by 2^-21 (twice a score's 2^-22; of a
+  // softmax's largest score, 1 / sum) and a rounding of it, and the softmax's
+  // factor moves scores, none above 1 / sum, against one another.
   if (!p.exact_cut) {
     const float hi = from_ordered(mine | low);
-    const double err = !BIAS ? 0.0 : 0x1p-21 + (double)__builtin_fabsf(hi) * 0x1p-22 + (soft ? (double)(0x1p-17f * __builtin_amdgcn_rcpf(sum)) : 0.0);
+    const double err = !BIAS ? 0.0 : (double)__builtin_fabsf(hi) * 0x1p-22 + (soft ? (double)((0x1p-21f + 0x1.2p-19f) * __builtin_amdgcn_rcpf(sum)) : 0x1p-21);
     // (the last candidate's lane asks for the worst of the chosen)
     const double worst = -row16_max(rank < p.topk && id >= 0 ? -k : -__builtin_inf());
     if (l == n_cand - 1 && id >= 0 && !(worst > (double)hi + err)) ok = false;
