@@ -216,7 +216,8 @@ typedef struct hum_norm_desc {
  * alone, not on m or on alignment.
  * Magnitudes up to 2^55 are in range.  Past that the sum of squares may be
  * infinite: such a row, and one that holds an infinity or NaN, gets y of
- * zeros and NaN, and scales of NaN. */
+ * zeros and NaN, and scales of NaN.  Where y alone is infinite or NaN (by its
+ * weight), the scale of its row, group or block is NaN. */
 hum_status hum_rms_norm(const hum_norm_desc* desc, int64_t m, int64_t k, const void* x_bf16, int64_t ld_x,
                         const void* residual, int64_t ld_residual, void* residual_out, int64_t ld_residual_out,
                         const void* weight, void* out_bf16, int64_t ld_out, void* q, void* scales, void* stream);

@@ -117,11 +117,13 @@ __device__ __forceinline__ u32x2_t e4m3x8(const float (&f)[8]) {
   return u32x2_t{f32x2_to_e4m3x2(f[0], f[1]) | (f32x2_to_e4m3x2(f[2], f[3]) << 16),
                  f32x2_to_e4m3x2(f[4], f[5]) | (f32x2_to_e4m3x2(f[6], f[7]) << 16)};
 }
+// The largest magnitude of eight; infinity where one is a NaN (the maximum
+// that keeps NaNs takes as many instructions as the one that drops them).
 __device__ __forceinline__ float max8(const float (&f)[8]) {
   float a = 0.0f;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) a = __builtin_fmaxf(a, __builtin_fabsf(f[i]));
-  return a;
+  for (int i = 0; i < 8; ++i) a = __builtin_elementwise_maximum(a, __builtin_fabsf(f[i]));
+  return a == a ? a : __builtin_inff();
 }
 
 // WAVES waves have a row (one: a workgroup has four rows), NV pieces of 8
@@ -181,7 +183,10 @@ __global__ __launch_bounds__(WAVES == 1 ? 256 : WAVES * 64) void norm_kernel(con
     }
     sum = over_row<WAVES, false>(sum, red[0][turn]);
     const float r = 1.0f / __builtin_sqrtf(sum * p.inv_k + p.eps);
-    const bool fine = sum < __builtin_inff();  // (false for a NaN too)
+    // Codes hold no infinity and no NaN, so a scale of NaN shows them: in all of
+    // a row whose squares have no finite sum, and where y alone is not finite
+    // (by its weight), `amax` infinite then.
+    auto fine = [&](float amax) { return sum < __builtin_inff() && amax < __builtin_inff(); };
     float amax = 0.0f;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
@@ -205,7 +210,7 @@ __global__ __launch_bounds__(WAVES == 1 ? 256 : WAVES * 64) void norm_kernel(con
       for (int j = 0; j < NV; ++j) {
         const int at = (j * kLanes + lane) * 8;
         const float s = fp8_row<true>(h[j], amax);
-        if (j == 0 && lane == 0) static_cast<float*>(p.scales)[row] = fine ? s : __builtin_nanf("");
+        if (j == 0 && lane == 0) static_cast<float*>(p.scales)[row] = fine(amax) ? s : __builtin_nanf("");
         if (at < k) *reinterpret_cast<u32x2_t*>(p.q + row * k + at) = e4m3x8(h[j]);
       }
     }
@@ -213,10 +218,11 @@ __global__ __launch_bounds__(WAVES == 1 ? 256 : WAVES * 64) void norm_kernel(con
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
         const int at = (j * kLanes + lane) * 8;
-        const float s = fp8_row<true>(h[j], row16_max(max8(h[j])));  // 16 lanes have a group of 128
+        amax = row16_max(max8(h[j]));  // 16 lanes have a group of 128
+        const float s = fp8_row<true>(h[j], amax);
         if (at < k) {
           *reinterpret_cast<u32x2_t*>(p.q + row * k + at) = e4m3x8(h[j]);
-          if ((lane & 15) == 0) static_cast<float*>(p.scales)[row * (k / 128) + at / 128] = fine ? s : __builtin_nanf("");
+          if ((lane & 15) == 0) static_cast<float*>(p.scales)[row * (k / 128) + at / 128] = fine(amax) ? s : __builtin_nanf("");
         }
       }
     }
@@ -224,12 +230,13 @@ __global__ __launch_bounds__(WAVES == 1 ? 256 : WAVES * 64) void norm_kernel(con
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
         const int at = (j * kLanes + lane) * 8;
-        const int e = mx_scale_code_emax(quad_max(max8(h[j])), FMT == HUM_ACT_MXFP8 ? 8 : 2);  // 4 lanes have a block of 32
+        amax = quad_max(max8(h[j]));  // 4 lanes have a block of 32
+        const int e = mx_scale_code_emax(amax, FMT == HUM_ACT_MXFP8 ? 8 : 2);
         if (at >= k) continue;
         const float sc = e8m0_to_f32((uint32_t)e);
         if constexpr (FMT == HUM_ACT_MXFP8) *reinterpret_cast<u32x2_t*>(p.q + row * k + at) = mx_e4m3x8(h[j], sc);
         else *reinterpret_cast<uint32_t*>(p.q + (row * k + at) / 2) = mx_e2m1x8(h[j], sc);
-        if ((lane & 3) == 0) static_cast<uint8_t*>(p.scales)[row * (k / 32) + at / 32] = fine ? (uint8_t)e : 255;
+        if ((lane & 3) == 0) static_cast<uint8_t*>(p.scales)[row * (k / 32) + at / 32] = fine(amax) ? (uint8_t)e : 255;
       }
     }
   }
