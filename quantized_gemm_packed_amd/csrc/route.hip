@@ -228,6 +228,26 @@ __device__ __forceinline__ double reciprocal(double d) {
   return __builtin_fma(__builtin_fma(-d, y, 1.0), y, y);
 }
 
+// exp(d), d <= 0, to 2^-33 of itself (0 from -690 down, to 2^-995): d log2(e)
+// is a whole number n, which the sum with 1.5 * 2^52 holds in its low bits, and
+// a rest f in [-1/2, 1/2]; 2^f by the polynomial through its values at the
+// eight Chebyshev points (2^-34 off at most); n goes to the exponent's bits.
+__device__ __forceinline__ double exp_of(double d) {
+  constexpr double kLog2e = 1.4426950408889634, kWhole = 0x1.8p52;
+  d = fmax(d, -690.0);
+  const double m = __builtin_fma(d, kLog2e, kWhole);
+  const double f = __builtin_fma(d, kLog2e, kWhole - m);
+  double y = 1.5303700711365693e-05;
+  y = __builtin_fma(y, f, 0.00015469729214118296);
+  y = __builtin_fma(y, f, 0.0013333478473685416);
+  y = __builtin_fma(y, f, 0.009618025613318034);
+  y = __builtin_fma(y, f, 0.055504109063258665);
+  y = __builtin_fma(y, f, 0.24022651213498092);
+  y = __builtin_fma(y, f, 0.6931471805568324);
+  y = __builtin_fma(y, f, 0.9999999999595618);
+  return __builtin_bit_cast(double, __builtin_bit_cast(uint64_t, y) + (__builtin_bit_cast(uint64_t, m) << 52));
+}
+
 // What the experts are ordered by: their logits, or scores with a bias.
 enum { kByLogit = 0, kBySigmoid = 1, kBySoftmax = 2 };
 // Groups: none, of a multiple of 4 experts, of any number of them.
@@ -292,23 +312,40 @@ __global__ __launch_bounds__(256, 4) void route_kernel(const RouteParams p) {
       }
   }
   bool ok = true;
-  // the largest logit, and the sum of exp(x - top)
+  // The largest logit, and the sum of exp(x - top): in f32, which the margins
+  // below and renormalised weights (they do not depend on it) allow.  Other
+  // weights are quotients by it, and an f32 one would move them by up to 7 times
+  // what their rounding does: they have the sum of f64 terms, here or, where the
+  // biases leave too few registers here, behind the choice (16384 tokens, 8 of
+  // 256 experts: 9.6 us, renormalised 8.1; with a bias 11.7 and 9.2).
+  constexpr bool kSumLater = ORDER == kBySoftmax;
   float top = none, sum = 0.0f;
+  double total = 0.0;
   if (!sigmoid) {
 #pragma unroll
     for (int b = 0; b < NB; ++b)
 #pragma unroll
       for (int i = 0; i < 4; ++i) top = __builtin_fmaxf(top, x[b][i]);
     top = row16_max(top);
-    const float shift = top > none ? top : 0.0f;
+    if (kSumLater || p.renormalize) {
+      const float shift = top > none ? top : 0.0f;
 #pragma unroll
-    for (int b = 0; b < NB; ++b) {
-      float e[4];
+      for (int b = 0; b < NB; ++b) {
+        float e[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) e[i] = __builtin_amdgcn_exp2f((x[b][i] - shift) * 1.44269504f);
-      sum += (e[0] + e[1]) + (e[2] + e[3]);
+        for (int i = 0; i < 4; ++i) e[i] = __builtin_amdgcn_exp2f((x[b][i] - shift) * 1.44269504f);
+        sum += (e[0] + e[1]) + (e[2] + e[3]);
+      }
+      sum = row16_sum(sum);
+      total = sum;
+    } else {
+#pragma unroll
+      for (int b = 0; b < NB; ++b)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) total += exp_of((double)x[b][i] - (double)top);
+      total = row16_sum(total);
+      sum = (float)total;
     }
-    sum = row16_sum(sum);
   }
   // scores of logits (of -inf: 0)
   auto scores = [&](float (&v)[NB][4]) {
@@ -462,6 +499,17 @@ __global__ __launch_bounds__(256, 4) void route_kernel(const RouteParams p) {
     next = row16_max(next);
     best = best < kNoKey ? best : best + next;
   }
+  if (kSumLater && !p.renormalize) {
+    total = 0.0;
+#pragma unroll 2
+    for (int e = l; e < p.experts; e += 16) {
+      float v;
+      if constexpr (sizeof(T) == 2) v = bf16_bits_to_f32(row[e]);
+      else v = row[e];
+      total += exp_of((double)v - (double)top);
+    }
+    total = row16_sum(total);
+  }
   // their exact keys
   const int id = mine >= kNoKey ? (int)(low - (mine & low)) : -1;
   double s = 0.0, k = -__builtin_inf();
@@ -471,7 +519,7 @@ __global__ __launch_bounds__(256, 4) void route_kernel(const RouteParams p) {
     else v = row[id];
     const double by = BIAS ? (double)p.bias[id] : 0.0;
     const double e = exp(sigmoid ? -(double)v : (double)v - (double)top);
-    if (!sigmoid) s = e * reciprocal((double)sum);
+    if (!sigmoid) s = e * reciprocal(total);
     else s = e < 0x1p1000 ? reciprocal(1.0 + e) : 1.0 / e;
     k = BIAS ? s + by : (double)v;
   }
