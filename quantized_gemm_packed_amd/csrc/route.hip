@@ -86,6 +86,13 @@ __device__ __forceinline__ double wave_sum(double v) {
   return (lane_of(v, 0) + lane_of(v, 16)) + (lane_of(v, 32) + lane_of(v, 48));
 }
 
+// 2^1023 for infinity; smaller numbers as they are.
+__device__ __forceinline__ double below_nan(double v) {
+  const uint64_t b = __builtin_bit_cast(uint64_t, v);
+  const int32_t hi = (int32_t)(b >> 32);
+  return __builtin_bit_cast(double, (uint64_t)(uint32_t)(hi < 0x7FE00000 ? hi : 0x7FE00000) << 32 | (uint32_t)b);
+}
+
 // One token by one wave, all in f64; lane l has the experts l, l + 64, ... (N of them)
 // keys: LDS of this wave alone.  What calls exp stays rolled: it runs seldom,
 // and what it holds in registers the kernel around it does not have.
@@ -125,13 +132,14 @@ __device__ __forceinline__ void route_exactly(const RouteParams& p, int64_t t, d
   };
   // (where a NaN leaves no softmax, the logits order)
   const bool by_bias = p.bias && sum == sum, by_score = p.groups > 1 && p.top2 && !p.bias && sum == sum;
-  // what an expert is ordered by, and its group (by its score then); a NaN first
+  // What an expert is ordered by, and its group (by its score then).  NaNs come
+  // first: infinity is theirs, what is infinite of itself becomes 2^1023.
 #pragma unroll 2
   for (int e = lane; e < p.experts; e += 64) {
     const double by = p.bias ? (double)p.bias[e] : 0.0;
     double k = by == none ? none : keys[e];
     if (k != none && (by_bias || by_score)) k = score(k) + by;
-    keys[e] = k == k ? k : -none;
+    keys[e] = k == k ? below_nan(k) : -none;
   }
   fence();
   double key[N];
@@ -147,7 +155,7 @@ __device__ __forceinline__ void route_exactly(const RouteParams& p, int64_t t, d
       b = fmax(b, fmin(a, v));
       a = fmax(a, v);
     }
-    if (p.top2 && b != none) a += b;
+    if (p.top2 && b != none && a != -none) a = below_nan(a + b);
     int rank = 0;
     for (int g = 0; g < p.groups; ++g) {
       const double o = lane_of(a, g);
@@ -160,7 +168,7 @@ __device__ __forceinline__ void route_exactly(const RouteParams& p, int64_t t, d
       if (e >= p.experts) continue;
       if (by_score && key[j] != none) {  // (their own order is that of the logits)
         const double x = logit(e);
-        key[j] = x == x ? x : -none;
+        key[j] = x == x ? below_nan(x) : -none;
       }
       if (!((kept >> (e / p.per_group)) & 1)) key[j] = none;
     }
