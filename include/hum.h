@@ -435,13 +435,14 @@ size_t hum_moe_masked_workspace_bytes(const hum_weight_desc* w13, const hum_weig
  *   without a bias of their s), the lowest first among equal ones.
  *   weights = s of the chosen (without the bias), divided by their sum where
  *   renormalize, times scale.
- * Scores are compared in f64; weights are formed in f64 and rounded once.  Ids come best first.  An expert whose logit (or
- * bias) is -inf takes no part; where fewer than topk are left, the other ids
- * are -1 with weight 0, which hum_moe_gemm skips: a row of -inf (a padding
- * token) routes nowhere.  Else a NaN logit comes first of all and its weight is NaN
- * (with softmax or renormalize, every weight of its row; so it is where the
- * softmax of a row meets an infinity, and the logits alone then order it); ids
- * stay valid.
+ * Scores are compared in f64; weights are formed in f64 and rounded once.
+ * Ids come best first.  An expert whose logit (or bias) is -inf takes no part;
+ * where fewer than topk are left, the other ids are -1 with weight 0, which
+ * hum_moe_gemm skips: a row of -inf (a padding token) routes nowhere.  Else a
+ * NaN logit comes first of all, before infinity too, and its weight is NaN
+ * (with softmax or renormalize, so is that of every other expert chosen; and
+ * where the softmax of a row meets an infinity: the logits alone then order
+ * it); ids stay valid.
  *   logits : [T][E], ld_logits elements from row to row
  *   bias   : f32 [E] or NULL
  *   topk_ids, topk_weights: contiguous [T][topk]

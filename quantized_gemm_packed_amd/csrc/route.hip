@@ -194,7 +194,7 @@ __device__ __forceinline__ void route_exactly(const RouteParams& p, int64_t t, d
   double w = id < 0 ? 0.0 : score(logit(id));
   if (p.renormalize) {
     const double all = wave_sum(w);
-    if (all != 0.0) w /= all;
+    if (all != 0.0 && id >= 0) w /= all;  // (ids of -1 keep 0 where the others' sum is a NaN)
   }
   if (lane < p.topk) {
     p.ids[t * p.topk + lane] = id;
