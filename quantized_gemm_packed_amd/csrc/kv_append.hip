@@ -10,11 +10,11 @@
 // once and their codes written once; apart, the turned k would be written and
 // read once more, and a launch paid twice.
 //
-// Measured on MI355X, inputs that change from call to call: 16384 tokens of
-// 32 + 8 heads of 128 into MXFP8 78 us, 4.7 TB/s read + written (a large copy
-// reaches 4.9 to 5.2; hum_rotary and hum_kv_write together take 89); 5003
-// tokens of 16 + 4 normed heads of 256, bf16, 26 us, 4.7 TB/s; a decode step of
-// 64 tokens 3.9 us, of which a launch is 3.3.
+// Measured on MI355X, in a captured graph, inputs that change from call to call:
+// 16384 tokens of 32 + 8 heads of 128 into MXFP8 78 us, 4.7 TB/s read + written
+// (a large copy reaches 5.1, the norm 5.8; hum_rotary and hum_kv_write together
+// take 89), into MXFP4 74; 5003 tokens of 16 + 4 normed heads of 256, bf16, 25
+// to 28 us; a decode step of 64 tokens 3.2 us, of which an empty launch is 1.9.
 #include <cmath>
 
 #include "kv_common.h"
@@ -380,7 +380,10 @@ extern "C" hum_status hum_rotary_kv_write(const hum_rotary_desc* rot, const hum_
   auto near = [](int64_t hs) { return hs < 1 << 18 && hs > -(1 << 18); };
   const bool fast = any % 8 == 0 && p.half % (half ? 8 : 4) == 0 && (!hq || (near(q_hs) && near(qo_hs))) && near(k_hs) && near(v_hs);
   // A token to a wave, four to a workgroup; rows are sliced over grid.y where
-  // the tokens alone would leave compute units without a workgroup.
+  // the tokens alone would leave compute units without a workgroup (32 + 8 heads
+  // of 128 into FP8: 64 tokens 3.2 us, unsliced 9.1; 512 tokens 5.8 and 10.2.
+  // Slices for 2048 workgroups in place of 512 would take 5.4 there and 3.9
+  // instead of 4.5 for 256 tokens; below that the two are alike).
   const int all = hq + 2 * hk, at_once = 64 / (d / 8);
   const int64_t gx = (num_tokens + 3) / 4;
   int64_t gy = 1;

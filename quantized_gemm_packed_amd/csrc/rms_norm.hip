@@ -11,11 +11,12 @@
 // elements a thread has, and so the order of the sums, goes by k alone: a
 // row's bits are the same in every batch and at every alignment.
 //
-// Measured on MI355X, inputs that change from call to call: 16384 rows of 8192
-// with a bf16 residual to FP8 codes 162 us, 5.8 TB/s read + written (a large
-// copy reaches 4.9 to 5.2); 3001 rows of 4100 with an f32 residual 29 us, 5.0
-// TB/s; 256 rows of 7168 to FP8 codes in groups 5.3 us and one row of 4096 3.8
-// us, of which a launch is 3.3.
+// Measured on MI355X, in a captured graph, inputs that change from call to call:
+// 16384 rows of 8192 with a bf16 residual to FP8 codes 161 us, 5.8 TB/s read +
+// written (a large copy reaches 5.1), to MXFP4 151, to FP8 codes and bf16 with
+// f32 weights 212; 3001 rows of 4100 with an f32 residual 29 us, 5.1 TB/s; 256
+// rows of 7168 to FP8 codes in groups 5.0 us and one row of 4096 3.3 us, of
+// which an empty launch is 1.9.  Rows past 16384 elements: 3.9 to 4.3 TB/s.
 #include <cmath>
 
 #include "dev_common.h"
@@ -252,6 +253,10 @@ __global__ __launch_bounds__(WAVES == 1 ? 256 : WAVES * 64) void norm_kernel(con
 //   8192  8x2 87, 4.5        4x4 96, 5.1      16x1 95, 4.7
 //   12288 8x3 91, 5.3        16x2 94, 5.4
 //   16384 16x2 96, 6.1       8x4 101, 6.4
+// (and in a captured graph:)
+//   20480 16x4 115, 7.0      8x8 132, 8.0
+//   32768 16x4 110, 7.5      8x8 118, 8.9
+//   65536 16x8 121, 12.4     (the only one that holds it; 4 to 26 registers spill)
 template <int FMT, int RES, bool FAST>
 static void launch_norm(const NormParams& p, hipStream_t s) {
   auto go = [&](auto waves, auto nv) {

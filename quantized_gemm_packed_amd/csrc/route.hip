@@ -7,15 +7,19 @@
 // The choice is that of f64 scores: f32 makes near ones equal.  Nearly all of
 // the work is done in f32 all the same, with bounds on what it may be off by;
 // the few candidates that are left are ordered by f64 scores, and a token that
-// the bounds do not decide (0.005 % of them with 8 of 256 experts in groups) is
-// done again in f64 throughout.
+// the bounds do not decide is done again in f64 throughout: 0.005 % of them with
+// 8 of 256 experts in groups and f32 logits of any values, 0.1 to 1 % where f32
+// logits hold bf16 values, half and more of them where the logits are so coarse
+// that most rows tie at the last choice.
 //
-// Bound by instructions and latency (about 1000 vector instructions for the
-// four tokens of a wave, 250 experts each).  Measured on MI355X: 16384 tokens
-// of 128 bf16 experts 5.6 us and 16381 of 256 f32 experts in groups, with a
-// bias, 11 us, 15 where a token is done again; in f64 throughout they took 54
-// and 80.  Memory alone would take 1.1 and 3.6 us, a launch 3.3.  16384 of 72
-// experts in groups of 9: 7.6 us, in f64 34.
+// Bound by instructions and latency (980 vector instructions for the four
+// tokens of a wave with 256 experts in groups, 450 with 128 bf16 ones).
+// Measured on MI355X, in a captured graph: 16384 tokens of 128 bf16 experts 5.0
+// us and 16381 of 256 f32 experts in groups, with a bias, 11.5 us, 14.5 where a
+// token is done again; in f64 throughout they took 54 and 80.  Memory alone
+// would take 0.9 and 3.0 us, an empty launch 1.9.  16384 of 128 f32 experts: 5.9
+// us, with bf16 values 9.4, with multiples of a half 28.  16384 of 72 experts in
+// groups of 9: 6.8 us, in f64 34.
 #include <cmath>
 
 #include "dev_common.h"
@@ -606,6 +610,10 @@ __global__ __launch_bounds__(256) void route_exact_kernel(const RouteParams p) {
 
 template <typename T, int ORDER, int GROUPS>
 static void launch_route(const RouteParams& p, hipStream_t s) {
+  // Four waves to a workgroup where the chip is full (16384 tokens, 8 of 128 bf16
+  // experts: 4.8 us, with one wave 6.6), one where it is not (1024 tokens: 3.0,
+  // with four 3.3); at 4096 tokens they are even (3.4 and 3.2; in groups of 256
+  // experts 7.8 and 7.7).
   const int block = p.tokens >= 4096 ? 256 : 64;
   const unsigned grid = (unsigned)((p.tokens * 16 + block - 1) / block);
   switch ((p.experts + 63) / 64) {

@@ -1,8 +1,8 @@
 """GPU: routing weights are float64's, rounded once.
 
 Bounds: a score is an exponential over a sum (or one over one and an
-exponential), both in float64: the sum's terms are off by 2^-32 of themselves
-(their series ends there), all else by a few 2^-53.  The weight's one rounding
+exponential), both in float64: the sum's terms are off by less than 2^-32 of
+themselves (the polynomial in them), all else by a few 2^-53.  The weight's one rounding
 to float32 adds half a step: 2^-24 of the value, below 2^-126 half of the
 subnormals' 2^-149.  Together less than (2^-24 + 2^-30) of the weight, 2^-150."""
 import numpy as np
